@@ -1,0 +1,496 @@
+"""The operators around and inside one MoE layer, as a user's program calls them:
+
+* ``norm``    residual addition + root-mean-square norm + quantisation into the expert FFN's activation format;
+* ``router``  router logits of normalised tokens;
+* ``layer``   the routed experts' whole layer (routing, gate_up, SwiGLU, requantisation, down, combine) for few tokens.
+
+``run`` computes them in plain fp32 torch operations where ``own`` is false and through the framework's entry
+points where it is true.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+E4M3_MAX = 448.0
+FP32_MIN_NORMAL = 2.0 ** -126
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+# ------------------------------------------------------------------------------------------------ cases
+def listed():
+    return [
+        # decode of one token: the norm ahead of the experts, where only latency counts
+        {"name": "norm fp8 1", "op": "norm", "T": 1, "H": 7168, "fmt": "fp8_block128", "f32": False, "res": True},
+        # prefill: 8192 tokens stream through memory
+        {"name": "norm fp8 8192", "op": "norm", "T": 8192, "H": 7168, "fmt": "fp8_block128", "f32": False, "res": True},
+        # a residual stream kept in fp32, MX activations, a hidden size that no power of two divides
+        {"name": "norm mx f32 2048", "op": "norm", "T": 2048, "H": 2880, "fmt": "w4a8_mx", "f32": True, "res": True},
+        # router of one token: 256 rows of weights to read, latency
+        {"name": "router 1", "op": "router", "T": 1, "H": 7168, "E": 256, "w32": False},
+        # router of a decode batch
+        {"name": "router 256", "op": "router", "T": 256, "H": 7168, "E": 256, "w32": False},
+        # router of a prefill
+        {"name": "router 8192", "op": "router", "T": 8192, "H": 7168, "E": 256, "w32": False},
+        # router weights kept in fp32, a ragged batch
+        {"name": "router f32 2047", "op": "router", "T": 2047, "H": 2880, "E": 128, "w32": True},
+        # one user's decode step, FP8 experts
+        {"name": "layer fp8 1", "op": "layer", "T": 1, "H": 7168, "I": 2048, "E": 32, "k": 8, "fmt": "fp8_block128",
+         "route": "precomputed", "mask": 0.0, "add": True},
+        # a small batch of users, FP8 experts: every expert is active
+        {"name": "layer fp8 16", "op": "layer", "T": 16, "H": 7168, "I": 2048, "E": 32, "k": 8, "fmt": "fp8_block128",
+         "route": "precomputed", "mask": 0.0, "add": True},
+        # bf16 experts, few and wide
+        {"name": "layer bf16 4", "op": "layer", "T": 4, "H": 4096, "I": 14336, "E": 8, "k": 2, "fmt": "bf16",
+         "route": "precomputed", "mask": 0.0, "add": False},
+        # 4-bit weights, routing from logits, the largest batch of the few-token form
+        {"name": "layer w4a8 32", "op": "layer", "T": 32, "H": 2880, "I": 2880, "E": 128, "k": 4, "fmt": "w4a8_mx",
+         "route": "from_logits", "mask": 0.0, "add": True},
+        # NVFP4 weights, an odd batch with slots that belong to another device's experts
+        {"name": "layer nvfp4 3", "op": "layer", "T": 3, "H": 7168, "I": 2048, "E": 32, "k": 8, "fmt": "nvfp4_w4a16",
+         "route": "precomputed", "mask": 0.25, "add": False},
+    ]
+
+
+def _log_uniform(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "router", "layer"])
+    if op == "norm":
+        fmt = rng.choice(["fp8_block128", "w4a8_mx", "bf16"])
+        step = {"fp8_block128": 128, "w4a8_mx": 32, "bf16": 64}[fmt]
+        H = max(1, _log_uniform(rng, 256, 8192) // step) * step
+        return {"op": op, "T": _log_uniform(rng, 1, 8192), "H": H, "fmt": fmt, "f32": rng.random() < 0.3,
+                "res": rng.random() < 0.8}
+    if op == "router":
+        return {"op": op, "T": _log_uniform(rng, 1, 8192), "H": max(1, _log_uniform(rng, 256, 7168) // 32) * 32,
+                "E": _log_uniform(rng, 4, 256), "w32": rng.random() < 0.3}
+    fmt = rng.choice(["fp8_block128", "bf16", "w4a8_mx", "nvfp4_w4a16", "nvfp4"])
+    step = {"fp8_block128": 128, "w4a8_mx": 32}.get(fmt, 64)
+    H = max(1, _log_uniform(rng, 256, 7168) // step) * step
+    I = max(1, _log_uniform(rng, 128, 4096) // step) * step
+    E = max(2, min(_log_uniform(rng, 2, 160), int(6e8 / (3.0 * H * I))))
+    route = rng.choice(["precomputed", "from_logits"])
+    return {"op": op, "T": _log_uniform(rng, 1, 32), "H": H, "I": I, "E": E, "k": rng.randint(1, min(8, E)),
+            "fmt": fmt, "route": route, "mask": rng.choice([0.0, 0.25]) if route == "precomputed" else 0.0,
+            "add": rng.random() < 0.5}
+
+
+def work(case):
+    T, H = case["T"], case["H"]
+    if case["op"] == "norm":
+        stream = 4 if case["f32"] else 2
+        moved = stream * (3 if case["res"] else 1) + 2
+        sf = {"fp8_block128": 4 * (H // 128), "w4a8_mx": H // 32, "bf16": 0}[case["fmt"]]
+        if case["fmt"] != "bf16":
+            moved += 1
+        return {"bytes": T * (H * moved + sf) + 2 * H, "flops": 6 * T * H}
+    if case["op"] == "router":
+        E = case["E"]
+        return {"bytes": 2 * T * H + (4 if case["w32"] else 2) * E * H + 4 * T * E, "flops": 2 * T * E * H}
+    I, E, k = case["I"], case["E"], case["k"]
+    bits = {"fp8_block128": 8 + 32 / 16384, "bf16": 16, "w4a8_mx": 4 + 8 / 32}.get(case["fmt"], 4 + 8 / 16)
+    share = k / E * (1.0 - case["mask"])
+    active = E * (1.0 - (1.0 - share) ** T)  # experts that some token chose
+    moved = active * 3 * H * I * bits / 8 + T * H * (2 + 2 + (4 if case["add"] else 0))
+    return {"bytes": moved, "flops": 6 * T * k * (1.0 - case["mask"]) * H * I}
+
+
+# ------------------------------------------------------------------------------------------------ inputs
+def _generator(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed & 0x7FFFFFFF)
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV, dtype=torch.float32)
+
+
+def _pow2_at_least(amax, top):
+    """The smallest e with top * 2**e >= amax, in [-127, 127]; -127 for amax = 0."""
+    m, e = torch.frexp(amax.double() / top)
+    e = torch.where(m == 0.5, e - 1, e)
+    return torch.where(amax == 0, torch.full_like(e, -127), e).clamp(-127, 127)
+
+
+def _e2m1_codes(v):
+    """The nearest E2M1 code, ties to the even code, saturated."""
+    a = v.abs()
+    code = torch.zeros_like(v, dtype=torch.uint8)
+    for mid, up in ((0.25, False), (0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True), (5.0, False)):
+        code += ((a >= mid) if up else (a > mid)).to(torch.uint8)
+    return code | ((v < 0) & (code > 0)).to(torch.uint8) << 3
+
+
+def _pack(codes):
+    return codes[..., 0::2] | (codes[..., 1::2] << 4)
+
+
+def _quant_fp8(v, rows):
+    R, C = v.shape
+    b = v.view(R // rows, rows, C // 128, 128)
+    amax = b.abs().amax((1, 3))
+    s = torch.where(amax > 0, amax / E4M3_MAX, torch.ones_like(amax))
+    q = (b / s[:, None, :, None]).clamp(-E4M3_MAX, E4M3_MAX).view(R, C)
+    return q.to(torch.float8_e4m3fn).view(torch.uint8), s
+
+
+def _quant_mx(v, top):
+    R, C = v.shape
+    b = v.view(R, C // 32, 32)
+    e = _pow2_at_least(b.abs().amax(2), top)
+    q = (b / torch.exp2(e.float())[..., None]).view(R, C)
+    return q, (e + 127).to(torch.uint8)
+
+
+def _quant_nv(v, gs):
+    R, C = v.shape
+    b = v.view(R, C // 16, 16)
+    sc = (b.abs().amax(2) / (6.0 * gs)).clamp(max=E4M3_MAX).to(torch.float8_e4m3fn)
+    den = (sc.float() * gs)[..., None]
+    q = torch.where(den > 0, b / torch.where(den > 0, den, torch.ones_like(den)), torch.zeros_like(b))
+    return _pack(_e2m1_codes(q.view(R, C))), sc.view(torch.uint8)
+
+
+def _weight(g, fmt, R, C):
+    """One expert's matrix of N(0, 1/C) values in the format: (codes, scales, global scale)."""
+    v = _randn(g, R, C) * (1.0 / math.sqrt(C))
+    if fmt == "fp8_block128":
+        return (*_quant_fp8(v, 128), None)
+    if fmt == "bf16":
+        return v.to(torch.bfloat16), None, None
+    if fmt == "w4a8_mx":
+        q, sf = _quant_mx(v, 6.0)
+        return _pack(_e2m1_codes(q)), sf, None
+    gs = (v.abs().max() / (6.0 * E4M3_MAX)).float()
+    return (*_quant_nv(v, gs), gs)
+
+
+def _layer_inputs(case, seed):
+    g = _generator(seed)
+    T, H, I, E, k, fmt = (case[n] for n in ("T", "H", "I", "E", "k", "fmt"))
+    s = {"logits": _randn(g, T, E)}
+    order = s["logits"].sort(dim=1, descending=True, stable=True)[1][:, :k]
+    s["topk_idx"] = order.contiguous()
+    s["topk_weights"] = torch.softmax(s["logits"].gather(1, order), 1)
+    if case["route"] == "precomputed" and case["mask"] > 0:
+        off = torch.rand((T, k), generator=g, device=DEV) < case["mask"]
+        s["topk_idx"] = torch.where(off, torch.full_like(order, -1), order).contiguous()
+    x = _randn(g, T, H)
+    x_gs = None
+    if fmt == "fp8_block128":
+        s["x"], s["x_sf"] = _quant_fp8(x, 1)
+    elif fmt == "w4a8_mx":
+        q, s["x_sf"] = _quant_mx(x, E4M3_MAX)
+        s["x"] = q.clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn).view(torch.uint8)
+    elif fmt == "nvfp4":
+        x_gs = (x.abs().max() / (6.0 * E4M3_MAX)).float()
+        s["x"], s["x_sf"] = _quant_nv(x, x_gs)
+    else:
+        s["x"], s["x_sf"] = x.to(torch.bfloat16), None
+    w13, w2 = [], []
+    for _ in range(E):
+        w13.append(_weight(g, fmt, 2 * I, H))
+        w2.append(_weight(g, fmt, H, I))
+    w = {}
+    for name, parts in (("w13", w13), ("w2", w2)):
+        w[name] = torch.stack([p[0] for p in parts])
+        w[name + "_sf"] = None if parts[0][1] is None else torch.stack([p[1] for p in parts])
+        w[name + "_gs"] = None if parts[0][2] is None else torch.stack([p[2] for p in parts])
+    w["c_input_scales"] = None
+    if fmt == "nvfp4":  # the legs' output scales, and the scale of the requantised intermediate
+        c = (12.0 + 8.0 * torch.rand(E, generator=g, device=DEV)) / (6.0 * E4M3_MAX)
+        w["c_input_scales"] = c
+        w["w13_gs"] = w["w13_gs"] * x_gs
+        w["w2_gs"] = w["w2_gs"] * c
+    s["weights"] = w
+    s["shared"] = _randn(g, T, H).mul_(0.5).to(torch.bfloat16) if case["add"] else None
+    s["residual"] = _randn(g, T, H).to(torch.bfloat16) if case["add"] else None
+    return s
+
+
+def _inputs(case, seed):
+    if case["op"] == "layer":
+        return _layer_inputs(case, seed)
+    g = _generator(seed)
+    T, H = case["T"], case["H"]
+    if case["op"] == "router":
+        w = _randn(g, case["E"], H) * (1.0 / math.sqrt(H))
+        return {"x": _randn(g, T, H).to(torch.bfloat16), "w": w if case["w32"] else w.to(torch.bfloat16)}
+    kind = torch.float32 if case["f32"] else torch.bfloat16
+    # a residual stream grows with depth and has a few large channels
+    channel = 1.0 + 20.0 * (torch.rand(H, generator=g, device=DEV) < 0.005).float()
+    return {"x": _randn(g, T, H).to(kind), "residual": (4.0 * channel * _randn(g, T, H)).to(kind) if case["res"] else None,
+            "weight": (1.0 + 0.2 * _randn(g, H)).to(torch.bfloat16), "eps": 1e-6}
+
+
+def prepare(case, seed):
+    s = _inputs(case, seed)
+    s["case"] = case
+    if not own:
+        return s
+    from mixture_experts_ffn_topk_amd import MoEFFN
+    T, H = case["T"], case["H"]
+    if case["op"] == "layer":
+        s["moe"] = MoEFFN(H, case["I"], case["E"], case["k"], T, fmt=case["fmt"], route_mode=case["route"])
+        s["weights"] = s["moe"].prepare_weights(s["weights"])  # laid out once, as for every other call of the framework
+        s["ws"] = s["moe"].alloc_few_workspace(T)
+        s["out"] = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+        return s
+    if case["op"] == "router":
+        s["moe"] = MoEFFN(H, 64, case["E"], 1, T, fmt="w4a8_mx", route_mode="from_logits")
+        s["logits"] = torch.empty((T, case["E"]), dtype=torch.float32, device=DEV)
+        return s
+    s["moe"] = MoEFFN(H, 128, 8, 2, T, fmt=case["fmt"])
+    s["residual_out"] = torch.empty_like(s["x"]) if case["res"] else None
+    s["x_norm"] = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+    s["x_q"] = s["x_sf"] = None
+    if case["fmt"] != "bf16":
+        s["x_q"] = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=DEV)
+        s["x_sf"] = (torch.empty((T, H // 128), dtype=torch.float32, device=DEV) if case["fmt"] == "fp8_block128" else
+                     torch.empty((T, H // 32), dtype=torch.float8_e8m0fnu, device=DEV))
+    return s
+
+
+# ------------------------------------------------------------------------------------------------ one pass
+def run(state):
+    case = state["case"]
+    if case["op"] == "norm":
+        if own:
+            state["moe"].add_rmsnorm(case["T"], state["x"], state["residual"], state["weight"], state["eps"],
+                                     residual_out=state["residual_out"], x_norm=state["x_norm"], x_q=state["x_q"],
+                                     x_sf=state["x_sf"])
+            return {n: state[n] for n in ("residual_out", "x_norm", "x_q", "x_sf")}
+        return _plain_norm(case, state)
+    if case["op"] == "router":
+        if own:
+            state["moe"].router_logits(case["T"], state["x"], state["w"], state["logits"])
+            return state["logits"]
+        return state["x"].float() @ state["w"].float().t()
+    if own:
+        state["moe"].forward_few(case["T"], state["x"], state["x_sf"], state["topk_idx"], state["topk_weights"],
+                                 state["logits"] if case["route"] == "from_logits" else None, state["weights"],
+                                 state["out"], state["ws"], shared=state["shared"], residual=state["residual"])
+        return {"out": state["out"], "topk_idx": state["topk_idx"], "topk_weights": state["topk_weights"]}
+    return _plain_layer(case, state)
+
+
+def _plain_norm(case, s):
+    z = s["x"].float()
+    if s["residual"] is not None:
+        z = z + s["residual"].float()
+    n = z * torch.rsqrt(z.square().mean(1, keepdim=True) + s["eps"]) * s["weight"].float()
+    out = {"residual_out": z.to(s["x"].dtype) if s["residual"] is not None else None, "x_norm": n.to(torch.bfloat16),
+           "x_q": None, "x_sf": None}
+    if case["fmt"] == "bf16":
+        return out
+    T, H = n.shape
+    if case["fmt"] == "fp8_block128":
+        b = n.view(T, H // 128, 128)
+        amax = b.abs().amax(2)
+        sf = torch.where(amax > 0, (amax / E4M3_MAX).clamp(min=FP32_MIN_NORMAL), torch.ones_like(amax))
+        out["x_sf"] = sf
+    else:
+        b = n.view(T, H // 32, 32)
+        m, e = torch.frexp(b.abs().amax(2))  # amax = m * 2**e; 448 = 0.875 * 2**9
+        e = torch.where(m > 0.875, e - 8, e - 9)
+        e = torch.where(m == 0, torch.full_like(e, -127), e).clamp(-127, 127)
+        sf = torch.exp2(e.float())
+        out["x_sf"] = (e + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
+    out["x_q"] = (b / sf[..., None]).clamp(-E4M3_MAX, E4M3_MAX).view(T, H).to(torch.float8_e4m3fn)
+    return out
+
+
+def _fp8(codes):
+    return codes.view(torch.float8_e4m3fn).float()
+
+
+def _fp4(packed):
+    """Packed E2M1 [..., C/2] -> fp32 [..., C]."""
+    one = torch.tensor(E2M1 + tuple(-v for v in E2M1), device=packed.device)
+    both = torch.stack([one.repeat(16), one.repeat_interleave(16)], 1)  # byte -> (low nibble, high nibble)
+    return both[packed.int()].flatten(-2)
+
+
+def _spread(sf, n):
+    return sf.repeat_interleave(n, -1)
+
+
+def _plain_weights(fmt, w, name, pick):
+    """The picked experts' matrices in fp32 [A, R, C]."""
+    q = w[name][pick]
+    if fmt == "bf16":
+        return q.float()
+    sf = w[name + "_sf"][pick]
+    if fmt == "fp8_block128":
+        A, R, C = q.shape
+        return (_fp8(q).view(A, R // 128, 128, C // 128, 128) * sf[:, :, None, :, None]).view(A, R, C)
+    v = _fp4(q)
+    if fmt == "w4a8_mx":
+        return v * _spread(torch.exp2(sf.float() - 127.0), 32)
+    return v * _spread(_fp8(sf), 16) * w[name + "_gs"][pick][:, None, None]
+
+
+def _plain_x(fmt, x, sf):
+    if fmt == "fp8_block128":
+        return _fp8(x) * _spread(sf, 128)
+    if fmt == "w4a8_mx":
+        return _fp8(x) * _spread(torch.exp2(sf.float() - 127.0), 32)
+    if fmt == "nvfp4":
+        return _fp4(x) * _spread(_fp8(sf), 16)
+    return x.float()
+
+
+def _plain_requant(fmt, h, c):
+    """The intermediate as the down product reads it (c: the experts' NVFP4 scales)."""
+    if fmt in ("bf16", "nvfp4_w4a16"):
+        return h.to(torch.bfloat16).float()
+    n = {"fp8_block128": 128, "w4a8_mx": 32, "nvfp4": 16}[fmt]
+    b = h.unflatten(-1, (h.shape[-1] // n, n))
+    amax = b.abs().amax(-1, keepdim=True)
+    if fmt == "nvfp4":
+        c = c.view(-1, 1, 1, 1)
+        sf = (amax / (6.0 * c)).clamp(max=E4M3_MAX).to(torch.float8_e4m3fn).float()
+        a = torch.where(sf > 0, b / (sf * c), torch.zeros_like(b))
+        m = a.abs().clamp(max=6.0)
+        step = torch.where(m < 2.0, 0.5, torch.where(m < 4.0, 1.0, 2.0))
+        return (torch.round(m / step) * step * torch.sign(a) * sf).flatten(-2)
+    if fmt == "fp8_block128":
+        sf = torch.where(amax > 0, amax / E4M3_MAX, torch.ones_like(amax))
+    else:
+        m, e = torch.frexp(amax)
+        e = torch.where(m == 0, torch.full_like(e, -127), torch.where(m > 0.875, e - 8, e - 9)).clamp(-127, 127)
+        sf = torch.exp2(e.float())
+    return ((b / sf).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn).float() * sf).flatten(-2)
+
+
+def _plain_layer(case, s):
+    T, H, I, E, k, fmt, w = (*(case[n] for n in ("T", "H", "I", "E", "k", "fmt")), s["weights"])
+    ids, tw = s["topk_idx"], s["topk_weights"]
+    if case["route"] == "from_logits":
+        top, ids = s["logits"].sort(dim=1, descending=True, stable=True)
+        top, ids = top[:, :k], ids[:, :k].contiguous()
+        ex = torch.exp(top - top.amax(1, keepdim=True))
+        tw = ex / ex.sum(1, keepdim=True)
+    ok = ids >= 0
+    at = torch.where(ok, ids, torch.zeros_like(ids))
+    x = _plain_x(fmt, s["x"], s["x_sf"])
+    by_pair = T * k <= E  # one product for each (token, slot), or all tokens through every expert
+    if by_pair:
+        pick, rows = at.reshape(-1), x.repeat_interleave(k, 0).unsqueeze(1)
+    else:
+        pick, rows = torch.arange(E, device=x.device), x.expand(E, T, H)
+    gu = rows @ _plain_weights(fmt, w, "w13", pick).transpose(1, 2)
+    gate, up = gu[..., :I].clamp(max=10.0), gu[..., I:].clamp(-10.0, 10.0)
+    h = gate / (1.0 + torch.exp(-gate)) * up
+    c = w["c_input_scales"]
+    y = _plain_requant(fmt, h, None if c is None else c[pick]) @ _plain_weights(fmt, w, "w2", pick).transpose(1, 2)
+    y = y.view(T, k, H) if by_pair else y[at, torch.arange(T, device=x.device)[:, None]]
+    out = (torch.where(ok, tw, torch.zeros_like(tw))[..., None] * y).sum(1)
+    if s["shared"] is not None:
+        out = out + s["shared"].float() + s["residual"].float()
+    return {"out": out.to(torch.bfloat16), "topk_idx": ids, "topk_weights": tw}
+
+
+# ------------------------------------------------------------------------------------------------ 64 bits
+def _round64(v, mantissa, emin, top):
+    """Float64 values on the grid of a format with so many mantissa bits, ties to even, saturated."""
+    a = v.abs()
+    _, e = torch.frexp(a)
+    q = torch.ldexp(torch.ones_like(a), (e - 1).clamp(min=emin) - mantissa)
+    return torch.copysign((torch.round(a / q) * q).clamp(max=top), v)
+
+
+def _exponent64(amax):
+    """The smallest e with 448 * 2**e >= amax."""
+    e = torch.ceil(torch.log2(torch.where(amax > 0, amax, torch.ones_like(amax)) / E4M3_MAX))
+    e = torch.where(E4M3_MAX * torch.exp2(e - 1) >= amax, e - 1, e)
+    e = torch.where(E4M3_MAX * torch.exp2(e) < amax, e + 1, e)
+    return torch.where(amax > 0, e, torch.full_like(e, -127.0)).clamp(-127, 127)
+
+
+def _exact_norm(case, s):
+    z = s["x"].double()
+    if s["residual"] is not None:
+        z = z + s["residual"].double()
+    n = z / torch.sqrt((z * z).sum(1, keepdim=True) / case["H"] + s["eps"]) * s["weight"].double()
+    q = sf = None
+    if case["fmt"] != "bf16":
+        blocks = n.reshape(n.shape[0], -1, 128 if case["fmt"] == "fp8_block128" else 32)
+        amax = blocks.abs().max(2)[0]
+        if case["fmt"] == "fp8_block128":
+            sf = (amax / E4M3_MAX).clamp(min=FP32_MIN_NORMAL)
+            sf[amax == 0] = 1.0
+        else:
+            sf = torch.exp2(_exponent64(amax))
+        q = _round64(blocks / sf[:, :, None], 3, -6, E4M3_MAX).reshape(n.shape)
+    return {"residual_out": z if s["residual"] is not None else None, "x_norm": n, "x_q": q, "x_sf": sf}
+
+
+def _value64(fmt, q, sf, block):
+    """A matrix of the format's codes in float64; block: its scales' span (rows, columns)."""
+    if sf is None:
+        return q.double()
+    if fmt == "fp8_block128" or (fmt == "w4a8_mx" and q.shape[-1] == 32 * sf.shape[-1]):
+        v = q.view(torch.float8_e4m3fn).to(torch.float64)
+    else:
+        grid = torch.tensor(E2M1, dtype=torch.float64, device=q.device)
+        nibbles = torch.stack([q & 15, q >> 4], 2).reshape(q.shape[0], -1).long()
+        v = grid[nibbles & 7] * (1.0 - 2.0 * (nibbles >> 3).double())
+    if fmt == "fp8_block128":
+        f = sf.double()
+    else:
+        f = torch.exp2(sf.double() - 127.0) if fmt == "w4a8_mx" else sf.view(torch.float8_e4m3fn).double()
+    return v * torch.kron(f, torch.ones(block, dtype=torch.float64, device=q.device))
+
+
+def _requant64(fmt, h, c):
+    if fmt in ("bf16", "nvfp4_w4a16"):
+        return _round64(h, 7, -126, 3.3e38)
+    n = {"fp8_block128": 128, "w4a8_mx": 32, "nvfp4": 16}[fmt]
+    b = h.reshape(h.shape[0], -1, n)
+    amax = b.abs().max(2, keepdim=True)[0]
+    if fmt == "nvfp4":
+        sf = _round64(amax / (6.0 * c), 3, -6, E4M3_MAX)
+        safe = torch.where(sf > 0, sf * c, torch.ones_like(sf))
+        return (torch.where(sf > 0, _round64(b / safe, 1, 0, 6.0), torch.zeros_like(b)) * sf).reshape(h.shape)
+    sf = torch.where(amax > 0, amax / E4M3_MAX, torch.ones_like(amax)) if n == 128 else torch.exp2(_exponent64(amax))
+    return (_round64(b / sf, 3, -6, E4M3_MAX) * sf).reshape(h.shape)
+
+
+def _exact_layer(case, s):
+    T, I, E, k, fmt, w = (*(case[n] for n in ("T", "I", "E", "k", "fmt")), s["weights"])
+    ids, tw = s["topk_idx"], s["topk_weights"].double()
+    if case["route"] == "from_logits":
+        lg = s["logits"].double()
+        ids = torch.argsort(lg, dim=1, descending=True, stable=True)[:, :k]
+        tw = torch.softmax(lg.gather(1, ids), 1)
+    rows, cols = {"fp8_block128": (128, 128), "w4a8_mx": (1, 32)}.get(fmt, (1, 16))
+    x = _value64(fmt if fmt != "nvfp4_w4a16" else "bf16", s["x"], s["x_sf"], (1, cols))
+    out = torch.zeros((T, case["H"]), dtype=torch.float64, device=x.device)
+    for e in sorted(set(ids.flatten().tolist()) - {-1}):
+        t, j = (ids == e).nonzero(as_tuple=True)
+        part = lambda name: _value64(fmt, w[name][e], None if w[name + "_sf"] is None else w[name + "_sf"][e], (rows, cols))  # noqa: E731
+        scale = lambda name: 1.0 if w[name + "_gs"] is None else w[name + "_gs"][e].double()  # noqa: E731
+        gu = x[t] @ part("w13").T * scale("w13")
+        gate, up = gu[:, :I].clamp(max=10.0), gu[:, I:].clamp(-10.0, 10.0)
+        c = None if w["c_input_scales"] is None else w["c_input_scales"][e].double()
+        h = _requant64(fmt, gate * torch.sigmoid(gate) * up, c)
+        out.index_add_(0, t, tw[t, j][:, None] * (h @ part("w2").T * scale("w2")))
+    if s["shared"] is not None:
+        out = out + s["shared"].double() + s["residual"].double()
+    return {"out": out, "topk_idx": ids, "topk_weights": tw}
+
+
+def exact(case, seed):
+    s = _inputs(case, seed)
+    if case["op"] == "norm":
+        return _exact_norm(case, s)
+    if case["op"] == "router":
+        return s["x"].double() @ s["w"].double().t()
+    return _exact_layer(case, s)
