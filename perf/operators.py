@@ -244,6 +244,7 @@ def prepare(case, seed):
         return s
     if case["op"] == "router":
         s["moe"] = MoEFFN(H, 64, case["E"], 1, T, fmt="w4a8_mx", route_mode="from_logits")
+        s["ws"] = s["moe"].alloc_router_workspace(T)
         s["logits"] = torch.empty((T, case["E"]), dtype=torch.float32, device=DEV)
         return s
     s["moe"] = MoEFFN(H, 128, 8, 2, T, fmt=case["fmt"])
@@ -269,7 +270,7 @@ def run(state):
         return _plain_norm(case, state)
     if case["op"] == "router":
         if own:
-            state["moe"].router_logits(case["T"], state["x"], state["w"], state["logits"])
+            state["moe"].router_logits(case["T"], state["x"], state["w"], state["logits"], state["ws"])
             return state["logits"]
         return state["x"].float() @ state["w"].float().t()
     if own:
