@@ -413,6 +413,77 @@ moe_status moe_forward_static(const moe_handle* h, int32_t num_tokens, const voi
                               void* topk_idx, float* topk_weights, const float* routing_logits,
                               const moe_weights* w /* host struct */, void* out, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+   Around the expert FFN: the norm that makes its activations and the router
+   whose logits FROM_LOGITS takes; and the whole layer for few tokens. */
+
+/* Residual addition, root-mean-square norm and quantisation into the handle's
+   activation format, in one launch ([SymmBuffer] x / x_sf staging views; [ActPack]
+   encodings).  Per token, with H = hidden:
+     z            = x + residual                (fp32; residual NULL: z = x)
+     residual_out = z rounded to residual's type
+     n            = z * (1 / sqrt(mean over H of z^2 + eps)) * weight   (of the unrounded z)
+     x_norm       = bf16(n)
+     x_q, x_sf    = n in the handle's format, moe_format's x and x_sf:
+       FP8 block-128  scale s = fp32(amax / 448) per 128 columns (1 for an all-zero block, at
+                      least 2^-126), codes E4M3_RNE_sat(n / s)
+       W4A8 (MX)      per 32 columns the smallest power of two s = 2^e with 448 s >= amax,
+                      codes E4M3_RNE_sat(n / s), x_sf the UE8M0 byte e + 127
+       NVFP4 x NVFP4  per 16 columns s = E4M3_RNE_sat(amax / (6 x_global_scale)), codes
+                      E2M1_RNE_sat(n / (s x_global_scale)), zero where s = 0
+     A block that holds a NaN gets a NaN scale.
+   x [T,H] and weight [H] are bf16 or, with x_fp32 / weight_fp32 = 1, fp32; residual and
+   residual_out [T,H] are both given or both NULL, bf16 or fp32 (residual_fp32).
+   x_norm [T,H] bf16 and the pair x_q, x_sf may be NULL, not all three; BF16 and NVFP4 x
+   BF16 handles take x_norm as their activations, and x_q and x_sf must be NULL.
+   x_global_scale (NVFP4 x NVFP4 only) must be finite and > 0.  eps must be finite and
+   >= 0 (with 0 a row of zeros is NaN).  An output may be an input's own buffer when
+   their elements have the same size (residual_out = residual updates the stream in
+   place); any other overlap is MOE_ERR_INVALID_ARGUMENT.  hidden above 32768 or T of 2^25 and more
+   is MOE_ERR_UNSUPPORTED.  x, residual, weight and the outputs 16-byte aligned, x_sf 4. */
+moe_status moe_add_rmsnorm(const moe_handle* h, int32_t num_tokens, const void* x, int32_t x_fp32,
+                           const void* residual, int32_t residual_fp32, const void* weight, int32_t weight_fp32,
+                           float eps, void* residual_out, void* x_norm, void* x_q, void* x_sf, float x_global_scale,
+                           hipStream_t stream);
+
+/* Bytes of workspace moe_router_logits needs (0 for many sizes, and if num_tokens is
+   out of range or the call would not be supported). */
+size_t moe_router_workspace_size(const moe_handle* h, int32_t num_tokens);
+
+/* Router logits ([ActPack] routing_input_mode FromLogits: the routing_logits it takes):
+   logits[t,e] = sum over hidden of x[t,:] * router_w[e,:], x [T,H] bf16 (x_norm of
+   moe_add_rmsnorm), router_w [E,H] bf16 or fp32 (router_w_fp32), logits [T,E] fp32.  The sums
+   are fp32, of exact products for bf16 weights and of products exact to 2^-24 for fp32
+   ones; their order depends on the sizes alone.  x, router_w and logits 16-byte aligned; ws as for
+   moe_plan.  hidden above 32768 or T x E above 2^31 is MOE_ERR_UNSUPPORTED. */
+moe_status moe_router_logits(const moe_handle* h, int32_t num_tokens, const void* x, const void* router_w,
+                             int32_t router_w_fp32, float* logits, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Largest num_tokens of moe_forward_few. */
+#define MOE_FEW_MAX_TOKENS 32
+
+/* Bytes of workspace moe_forward_few needs for num_tokens tokens; 0 if num_tokens is
+   out of range or above MOE_FEW_MAX_TOKENS. */
+size_t moe_few_workspace_size(const moe_handle* h, int32_t num_tokens);
+
+/* The routed layer for few tokens: moe_forward_ex's operator, formats and arguments in two
+   launches ([EPConfig] fused_moe_ready: as few launches as there are steps) -- routing,
+   gate_up, SwiGLU; then down, combine, addends -- that read each active expert's weights once
+   and build no plan.  (FROM_LOGITS with more than 4 tokens: the top-k is a launch of its own
+   before them.)  The intermediate is requantised exactly as in moe_forward; the expert outputs are
+   not rounded to bf16 before the router weights (moe_forward stores them as y), and the fp32
+   sums are in another order, fixed by the sizes and the routing.  A token that lists an expert twice
+   gets it by the sum of both weights.  Masked slots and ids outside [0,E) contribute
+   nothing; a token with no valid slot gets the addends (or zeros).  A NaN or infinity in one token's activations
+   stays in that token's output.  out may be shared or residual itself when it is bf16.
+   Handles of any tile_regime, fuse_combine and fuse_plan (which do not apply).  num_tokens
+   above MOE_FEW_MAX_TOKENS is MOE_ERR_UNSUPPORTED; ws as for moe_forward, of
+   moe_few_workspace_size bytes, its contents neither read nor kept. */
+moe_status moe_forward_few(const moe_handle* h, int32_t num_tokens, const void* x, const void* x_sf,
+                           void* topk_idx, float* topk_weights, const float* routing_logits,
+                           const float* routing_bias, const moe_weights* w /* host struct */, const void* shared,
+                           const void* residual, void* out, void* ws, size_t ws_bytes, hipStream_t stream);
+
 const char* moe_status_string(moe_status s);
 int32_t moe_abi_version(void);
 

@@ -63,7 +63,9 @@ EXPORTED = ["moe_create", "moe_destroy", "moe_workspace_size", "moe_down_split_s
             "moe_plan", "moe_ffn", "moe_ffn_gate_up", "moe_ffn_down", "moe_combine", "moe_forward",
             "moe_plan_ex", "moe_combine_ex", "moe_forward_ex", "moe_ffn_gate_up_timed", "moe_ffn_down_timed",
             "moe_ffn_down_combine", "moe_ffn_down_combine_timed", "moe_plan_ffn_gate_up", "moe_plan_ffn_gate_up_timed",
-            "moe_forward_static", "moe_status_string", "moe_abi_version"]
+            "moe_forward_static", "moe_add_rmsnorm", "moe_router_workspace_size", "moe_router_logits",
+            "moe_few_workspace_size", "moe_forward_few", "moe_status_string", "moe_abi_version"]
+FEW_MAX_TOKENS = 32  # MOE_FEW_MAX_TOKENS
 STATIC_SCRATCH_BYTES = 64 << 20  # MOE_STATIC_SCRATCH_BYTES
 
 _lib = None
@@ -126,6 +128,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_forward_ex.restype = i32
     lib.moe_forward_static.argtypes = [vp, i32, vp, vp, vp, vp, vp, ctypes.POINTER(_Weights), vp, vp]
     lib.moe_forward_static.restype = i32
+    f32 = ctypes.c_float
+    lib.moe_add_rmsnorm.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, f32, vp, vp, vp, vp, f32, vp]
+    lib.moe_add_rmsnorm.restype = i32
+    lib.moe_router_workspace_size.argtypes = [vp, i32]
+    lib.moe_router_workspace_size.restype = sz
+    lib.moe_router_logits.argtypes = [vp, i32, vp, vp, i32, vp, vp, sz, vp]
+    lib.moe_router_logits.restype = i32
+    lib.moe_few_workspace_size.argtypes = [vp, i32]
+    lib.moe_few_workspace_size.restype = sz
+    lib.moe_forward_few.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, ctypes.POINTER(_Weights), vp, vp, vp, vp, sz, vp]
+    lib.moe_forward_few.restype = i32
     lib.moe_status_string.argtypes = [i32]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_abi_version.argtypes = []
@@ -196,6 +209,21 @@ def _on_gpu(**tensors):
             _on_gpu(**{f"{what}['{k}']": v for k, v in t.items()})
         elif t is not None and not isinstance(t, int) and t.device.type != "cuda":
             raise ValueError(f"{what} must be a GPU tensor (got {t.device})")
+
+
+def _on_current_gpu(**tensors):
+    """_on_gpu, and on the current device: the one whose stream the call uses."""
+    _on_gpu(**tensors)
+    import torch
+    cur = None
+    for what, t in tensors.items():
+        for v in t.values() if isinstance(t, dict) else (t,):
+            if v is None or isinstance(v, int):
+                continue
+            if cur is None:
+                cur = torch.cuda.current_device()
+            if v.get_device() != cur:
+                raise ValueError(f"{what} is on {v.device}; the current device is cuda:{cur}")
 
 
 class MoEFFN:
@@ -566,5 +594,83 @@ class MoEFFN:
                                            _ptr(topk_weights), _ptr(routing_logits), ctypes.byref(ws_), _ptr(out),
                                            _stream(stream)), "moe_forward_static")
 
+    # ---------------------------------------------------------------- around the FFN, and the layer for few tokens
+    def add_rmsnorm(self, num_tokens, x, residual, weight, eps, residual_out=None, x_norm=None, x_q=None, x_sf=None,
+                    x_global_scale=1.0, stream=None):
+        """moe_add_rmsnorm: residual addition, root-mean-square norm, and the norm as bf16
+        (x_norm) and in the handle's activation format (x_q, x_sf).  x, residual and
+        weight are bf16 or fp32 tensors (raw addresses: bf16); residual_out has residual's type and may be
+        residual itself."""
+        import torch
+        T, H = num_tokens, self.hidden
+        kinds = (torch.bfloat16, torch.float32)
+        f32 = [t is not None and not isinstance(t, int) and t.dtype == torch.float32 for t in (x, residual, weight)]
+        size = [4 if f else 2 for f in f32]
+        _need(x, "x", T * H * size[0], kinds)
+        _need(weight, "weight", H * size[2], kinds)
+        _need(residual, "residual", T * H * size[1], kinds, required=False)
+        _need(residual_out, "residual_out", T * H * size[1], (kinds[f32[1]],), required=residual is not None)
+        _need(x_norm, "x_norm", T * H * 2, kinds[:1], required=x_q is None)
+        if self._x_sf_row() > 0:
+            _need(x_q, "x_q", T * self._x_bytes(H), elem=1, required=x_sf is not None)
+            _need(x_sf, "x_sf", T * self._x_sf_row(), elem=4 if self.fmt == "fp8_block128" else 1,
+                  required=x_q is not None)
+        _on_current_gpu(x=x, residual=residual, weight=weight, residual_out=residual_out, x_norm=x_norm, x_q=x_q,
+                        x_sf=x_sf)
+        _check(self.lib.moe_add_rmsnorm(self._h, T, _ptr(x), f32[0], _ptr(residual), f32[1], _ptr(weight), f32[2],
+                                        eps, _ptr(residual_out), _ptr(x_norm), _ptr(x_q), _ptr(x_sf), x_global_scale,
+                                        _stream(stream)), "moe_add_rmsnorm")
 
-__all__ = ["MoEFFN", "MoEError", "load_library", "LIB_PATH", "EXPORTED", "FORMATS", "ROUTE_MODES", "TILE_REGIMES"]
+    def router_workspace_size(self, num_tokens: int) -> int:
+        return int(self.lib.moe_router_workspace_size(self._h, num_tokens))
+
+    def alloc_router_workspace(self, num_tokens: int, device="cuda"):
+        import torch
+        return torch.empty(max(1, self.router_workspace_size(num_tokens)), dtype=torch.uint8, device=device)
+
+    def router_logits(self, num_tokens, x, router_w, logits, ws=None, stream=None):
+        """moe_router_logits: logits [T,E] fp32 of x [T,H] bf16 and router_w [E,H] bf16 or
+        fp32 (a raw address: bf16); ws from alloc_router_workspace."""
+        import torch
+        T, H, E = num_tokens, self.hidden, self.experts
+        w32 = not isinstance(router_w, int) and router_w is not None and router_w.dtype == torch.float32
+        _need(x, "x", T * H * 2, (torch.bfloat16,))
+        _need(router_w, "router_w", E * H * (4 if w32 else 2), (torch.bfloat16, torch.float32))
+        _need(logits, "logits", T * E * 4, (torch.float32,))
+        _need(ws, "ws", 0, required=False)
+        _on_current_gpu(x=x, router_w=router_w, logits=logits, ws=ws)
+        _check(self.lib.moe_router_logits(self._h, T, _ptr(x), _ptr(router_w), w32, _ptr(logits), _ptr(ws),
+                                          self._nbytes(ws), _stream(stream)), "moe_router_logits")
+
+    def few_workspace_size(self, num_tokens: int) -> int:
+        return int(self.lib.moe_few_workspace_size(self._h, num_tokens))
+
+    def alloc_few_workspace(self, num_tokens: int, device="cuda"):
+        import torch
+        return torch.empty(max(1, self.few_workspace_size(num_tokens)), dtype=torch.uint8, device=device)
+
+    def forward_few(self, num_tokens, x, x_sf, topk_idx, topk_weights, routing_logits, weights: dict, out, ws,
+                    stream=None, routing_bias=None, shared=None, residual=None):
+        """moe_forward_few: forward() for at most FEW_MAX_TOKENS tokens in two launches; ws
+        from alloc_few_workspace."""
+        import torch
+        T = num_tokens
+        self._check_x(x, x_sf, T)
+        self._check_weights(weights)
+        self._check_routing_in(T, topk_idx, routing_logits, routing_bias)
+        _need(topk_idx, "topk_idx", T * self.topk * self.topk_idx_bits // 8, self._idx_dtypes())
+        _need(topk_weights, "topk_weights", T * self.topk * 4, (torch.float32,))
+        self._check_out(T, out, shared, residual)
+        _need(ws, "ws", 0, required=False)
+        _on_current_gpu(x=x, x_sf=x_sf, weights=weights, topk_idx=topk_idx, topk_weights=topk_weights,
+                        routing_logits=routing_logits, routing_bias=routing_bias, out=out, ws=ws, shared=shared,
+                        residual=residual)
+        ws_ = self._weights_struct(weights)
+        _check(self.lib.moe_forward_few(self._h, T, _ptr(x), _ptr(x_sf), _ptr(topk_idx), _ptr(topk_weights),
+                                        _ptr(routing_logits), _ptr(routing_bias), ctypes.byref(ws_), _ptr(shared),
+                                        _ptr(residual), _ptr(out), _ptr(ws), self._nbytes(ws), _stream(stream)),
+               "moe_forward_few")
+
+
+__all__ = ["MoEFFN", "MoEError", "load_library", "LIB_PATH", "EXPORTED", "FORMATS", "ROUTE_MODES", "TILE_REGIMES",
+           "FEW_MAX_TOKENS"]

@@ -8,6 +8,7 @@
 #include <new>
 
 #include "launch.h"
+#include "layer.h"
 
 struct moe_handle {
   moe_config cfg;
@@ -238,6 +239,35 @@ bool sizes_supported(const moe_config& c) {
   // the fused combine addresses y [T*k, H] bf16 through a buffer resource
   if (c.fuse_combine && T * k * H * 2 > kMaxBytes) return false;
   return true;
+}
+
+// Host ranges of device buffers, for the overlap rules of moe_add_rmsnorm.
+struct Span {
+  const void* p;
+  size_t bytes;
+  size_t elem;
+};
+// Disjoint, or the very same elements.
+bool apart_or_same(const Span& a, const Span& b) {
+  if (!a.p || !b.p) return true;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  if (x == y && a.elem == b.elem) return true;
+  return x + a.bytes <= y || y + b.bytes <= x;
+}
+
+struct FewLayout {
+  size_t hsf, total;  // h at 0
+};
+FewLayout few_layout(const moe_config& c, int T) {
+  const moe::Fmt f = to_fmt(c.format);
+  FewLayout L;
+  L.hsf = align_up(moe::few_h_bytes(f, T, c.num_topk, c.num_experts, c.intermediate_hidden));
+  L.total = L.hsf + align_up(moe::few_hsf_bytes(f, T * c.num_topk, c.intermediate_hidden));
+  return L;
+}
+
+bool router_supported(const moe_config& c, int T) {
+  return c.hidden <= moe::kNormMaxHidden && (long long)T * c.num_experts <= (1LL << 31);
 }
 
 }  // namespace
@@ -539,6 +569,139 @@ moe_status moe_forward(const moe_handle* h, int32_t T, const void* x, const void
                        size_t ws_bytes, hipStream_t stream) {
   return moe_forward_ex(h, T, x, x_sf, topk_idx, topk_weights, routing_logits, nullptr, w, nullptr, nullptr, out, ws,
                         ws_bytes, stream);
+}
+
+moe_status moe_add_rmsnorm(const moe_handle* h, int32_t T, const void* x, int32_t x_fp32, const void* residual,
+                           int32_t residual_fp32, const void* weight, int32_t weight_fp32, float eps,
+                           void* residual_out, void* x_norm, void* x_q, void* x_sf, float x_global_scale,
+                           hipStream_t stream) {
+  if (!valid_T(h, T)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_config& c = h->cfg;
+  for (int32_t f : {x_fp32, residual_fp32, weight_fp32})
+    if (f != 0 && f != 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARGUMENT;
+  if (c.format == MOE_FMT_NVFP4 && (!(x_global_scale > 0.0f) || !std::isfinite(x_global_scale)))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (T > 0) {
+    if (!x || !weight || (!x_norm && !x_q)) return MOE_ERR_INVALID_ARGUMENT;
+    if (!residual != !residual_out || !x_q != !x_sf) return MOE_ERR_INVALID_ARGUMENT;
+    if (x_q && bf16_acts(c.format)) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  if (!al(x, 16) || !al(residual, 16) || !al(weight, 16) || !al(residual_out, 16) || !al(x_norm, 16) || !al(x_q, 16) ||
+      !al(x_sf, 4))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (c.hidden > moe::kNormMaxHidden || T >= 1 << 25) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const size_t H = (size_t)c.hidden, n = (size_t)T * H, res = residual_fp32 ? 4 : 2, xe = x_fp32 ? 4 : 2;
+  const bool nv = c.format == MOE_FMT_NVFP4;
+  const size_t sf = c.format == MOE_FMT_FP8_BLOCK128 ? n / 128 * 4 : n / (nv ? 16 : 32);
+  const Span in[3] = {{x, n * xe, xe}, {residual, n * res, res}, {weight, H * (weight_fp32 ? 4 : 2), 0}};
+  // (element size 0: never the same elements)
+  const Span out[4] = {{residual_out, n * res, res}, {x_norm, n * 2, 2}, {x_q, nv ? n / 2 : n, 1}, {x_sf, sf, 3}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& s : in)
+      if (!apart_or_same(out[i], s)) return MOE_ERR_INVALID_ARGUMENT;
+    for (int j = 0; j < i; ++j)
+      if (out[i].p && out[i].p == out[j].p) return MOE_ERR_INVALID_ARGUMENT;
+      else if (!apart_or_same(out[i], out[j])) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  moe::NormArgs a{};
+  a.fmt = to_fmt(c.format);
+  a.T = T;
+  a.H = c.hidden;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.x_f32 = x_fp32 != 0;
+  a.residual_f32 = residual_fp32 != 0;
+  a.weight_f32 = weight_fp32 != 0;
+  a.eps = eps;
+  a.x_gs = x_global_scale;
+  a.residual_out = residual_out;
+  a.x_norm = x_norm;
+  a.x_q = x_q;
+  a.x_sf = x_sf;
+  return hip_status(moe::launch_add_rmsnorm(a, stream));
+}
+
+size_t moe_router_workspace_size(const moe_handle* h, int32_t T) {
+  if (!valid_T(h, T) || !router_supported(h->cfg, T)) return 0;
+  return align_up(moe::router_workspace_bytes(T, h->cfg.hidden, h->cfg.num_experts));
+}
+
+moe_status moe_router_logits(const moe_handle* h, int32_t T, const void* x, const void* router_w,
+                             int32_t router_w_fp32, float* logits, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!valid_T(h, T) || (router_w_fp32 != 0 && router_w_fp32 != 1)) return MOE_ERR_INVALID_ARGUMENT;
+  if (T > 0 && (!x || !router_w || !logits)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al(x, 16) || !al(router_w, 16) || !al(logits, 16) || !al(ws, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!router_supported(h->cfg, T)) return MOE_ERR_UNSUPPORTED;
+  const size_t need = moe_router_workspace_size(h, T);
+  if (ws_bytes < need || (need > 0 && !ws)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const moe::RouterArgs a{T, h->cfg.hidden, h->cfg.num_experts, x, router_w, router_w_fp32 != 0, logits, (float*)ws};
+  return hip_status(moe::launch_router_logits(a, stream));
+}
+
+size_t moe_few_workspace_size(const moe_handle* h, int32_t T) {
+  static_assert(MOE_FEW_MAX_TOKENS == moe::kFewMaxTokens, "the header's limit");
+  if (!valid_T(h, T) || T > MOE_FEW_MAX_TOKENS) return 0;
+  return few_layout(h->cfg, T).total;
+}
+
+moe_status moe_forward_few(const moe_handle* h, int32_t T, const void* x, const void* x_sf, void* topk_idx,
+                           float* topk_weights, const float* routing_logits, const float* routing_bias,
+                           const moe_weights* w, const void* shared, const void* residual, void* out, void* ws,
+                           size_t ws_bytes, hipStream_t stream) {
+  if (!valid_T(h, T) || !weights_ok(h->cfg, w)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_config& c = h->cfg;
+  const bool from_logits = c.route_mode == MOE_ROUTE_FROM_LOGITS;
+  if (T > 0) {
+    if (!x_ok(c, x, x_sf) || !out || !topk_idx || !topk_weights) return MOE_ERR_INVALID_ARGUMENT;
+    if (from_logits && !routing_logits) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  if (!from_logits && routing_bias) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al(x, 16) || !al(x_sf, 4) || !al(out, 16) || !al(shared, 16) || !al(residual, 16) || !al(ws, 256) ||
+      !al(w->w13, 16) || !al(w->w2, 16) || !al(w->w13_sf, 4) || !al(w->w2_sf, 4))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  const FewLayout L = few_layout(c, T);
+  if (ws_bytes < L.total || (L.total > 0 && !ws)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (T == 0) return MOE_OK;
+  const bool in_launch = from_logits && moe::few_routes_in_launch(T);
+  if (from_logits && !in_launch) {
+    const void* ids = nullptr;
+    const moe_status st = do_route(h, T, topk_idx, routing_logits, routing_bias, topk_idx, topk_weights, stream, &ids);
+    if (st != MOE_OK) return st;
+  }
+  moe::FewArgs a{};
+  a.fmt = to_fmt(c.format);
+  a.T = T;
+  a.E = c.num_experts;
+  a.topk = c.num_topk;
+  a.H = c.hidden;
+  a.I = c.intermediate_hidden;
+  a.clamp = c.activation_clamp;
+  a.fast = c.fast_math != 0;
+  a.ids = topk_idx;
+  a.ids64 = c.topk_idx_bits == 64;
+  a.topk_w = topk_weights;
+  a.logits = in_launch ? routing_logits : nullptr;
+  a.bias = in_launch ? routing_bias : nullptr;
+  a.x = x;
+  a.x_sf = x_sf;
+  a.w13 = w->w13;
+  a.w13_sf = w->w13_sf;
+  a.w2 = w->w2;
+  a.w2_sf = w->w2_sf;
+  a.w13_gs = w->w13_gs;
+  a.w2_gs = w->w2_gs;
+  a.c_scales = w->c_input_scales;
+  a.h = ws;
+  a.h_sf = (char*)ws + L.hsf;
+  a.shared = shared;
+  a.residual = residual;
+  a.out = out;
+  a.out_f32 = c.out_fp32 != 0;
+  return hip_status(moe::launch_few(a, stream));
 }
 
 }  // extern "C"

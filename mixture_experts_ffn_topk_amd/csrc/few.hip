@@ -1,0 +1,843 @@
+// The routed layer for few tokens (at most kFewMaxTokens) in two launches:
+//
+//   few_gate_up: routing (from logits, or the caller's ids) -> gate/up product of
+//                every active expert -> clamped SwiGLU -> h
+//   few_down:    requantised h -> down product -> router-weighted combine with the
+//                addends -> out
+//
+// The same operator as moe_forward on the same prepared weights, for batches so
+// small that the step is one pass over the active experts' weights.  What differs
+// from the grouped GEMMs:
+//   * Columns are tokens, not gathered rows: the weights are the first MFMA
+//     operand (16 rows), the second is a 16-token slice in which the tokens not
+//     routed to the expert are zeros.  A token's outputs of all experts then
+//     share a lane, so the down launch sums the experts in registers: no plan, no
+//     y rows, no combine launch.
+//   * Weights go straight from HBM into registers, each byte read once, non-temporal,
+//     and nothing is staged in LDS: a wave is on its own until its sums are complete.
+//   * gate_up: a wave owns 16 columns of h (MX: 32, one scale block) of one expert,
+//     or 1/KSP of their K-steps where that would leave the part underfilled.
+//   * down: a workgroup owns 16 R output columns and all experts; its waves split
+//     the (expert, K-step) sequence evenly.
+//   * The FP8 intermediate needs the maximum over 128 columns.  Where whole 128-column
+//     blocks make enough workgroups, the eight waves of a gate_up workgroup hold one
+//     block and quantise it; otherwise (one token, small I) h stays fp32 between the
+//     launches and every down workgroup quantises all of it into LDS first.  The
+//     other formats' blocks lie inside one wave and are quantised there.
+//
+// Every expert's term is a fresh MFMA partial scaled by (router weight x block
+// scales) in fp32, so the output is one fp32 sum per element, rounded once; the
+// order of the sum is fixed by the sizes and the routing alone.
+#include <type_traits>
+
+#include "gemm_common.h"
+#include "layer.h"
+#include "topk.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kFewMaxPairs = kFewMaxTokens * 32;  // num_topk <= 32
+constexpr int kFewMaxExperts = 1024;
+constexpr int kDownWaves = 8;
+// FP8: the most bytes of h (with 16 spare ones per row) that the down launch quantises into LDS: two
+// workgroups still share a CU.
+constexpr int kFewLdsH = 48 * 1024;
+
+constexpr bool bf16_mma(Fmt f) { return f == Fmt::BF16 || f == Fmt::NV4 || f == Fmt::NVF4; }
+constexpr bool nv4w(Fmt f) { return f == Fmt::NV4 || f == Fmt::NVF4; }
+
+struct FewParams {
+  int T, topk, E, H, I;
+  int fast;
+  float clamp;
+  const void* ids;  // [T, k]
+  int ids64;
+  const float* topk_w;
+  const float* logits;  // gate_up: route here (nullptr: ids are given)
+  const float* bias;
+  int* idx32_out;       // where the routing goes (one of them), and its weights
+  long long* idx64_out;
+  float* w_out;
+  const uint8_t* x;
+  const uint8_t* x_sf;
+  uint32_t x_row, x_sf_row;  // bytes
+  const uint8_t* w;     // the leg's prepared weights
+  const uint8_t* w_sf;
+  uint32_t w_expert, w_sf_expert;  // bytes per expert
+  const float* w_gs;
+  const float* c_gs;
+  int ksteps;           // K-steps of the prepared layout
+  int steps;            // K-steps of the kernel (NVFP4: pairs of the layout's)
+  void* h;
+  void* h_sf;
+  const uint16_t* shared;
+  const uint16_t* residual;
+  void* out;
+  int out_f32;
+};
+
+// ---------------------------------------------------------------- operands
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+MOE_DEV int pack2(f32x2 v) { return (int)bf16x2_rne(v[0], v[1]); }
+// 8 E2M1 values (element 2i in the low nibble of byte i) times their E4M3 block
+// scale, as bf16: the product of a 2-bit and a 4-bit significand is exact.
+MOE_DEV i32x4 e2m1_bf16x8(uint32_t d, float s) {
+  i32x4 r;
+  r[0] = pack2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 0) * s);
+  r[1] = pack2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 1) * s);
+  r[2] = pack2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 2) * s);
+  r[3] = pack2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 3) * s);
+  return r;
+}
+template <int B>
+MOE_DEV float e4m3_byte(int v) {
+  return __builtin_amdgcn_cvt_f32_fp8(v, B);
+}
+MOE_DEV i32x8 join(i32x4 a, i32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+MOE_DEV f32x4 mma_bf16(i32x4 w, i32x4 x, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), c, 0, 0, 0);
+}
+
+// One K-step of a 16-row weight tile in registers.
+//   FP8: q[0], q[1] the two 16-byte pieces; BF16: likewise, the two 32-element halves;
+//   MX: q[0], s the scale byte; NVFP4: q[0] two of the layout's K-steps (lanes g = 0, 1
+//   the first, 2, 3 the second), s the four E4M3 block scales of the lane's row.
+template <Fmt F>
+struct WFrag {
+  i32x4 q[F == Fmt::FP8 || F == Fmt::BF16 ? 2 : 1];
+  int s;
+};
+// The lane's part of a weight tile's address: row block rb (16 rows; the 32-row
+// tiles of the bf16 formats: tile rb / 2, half rb % 2), relative to the expert.
+template <Fmt F>
+struct WAddr {
+  uint32_t q, s;
+};
+template <Fmt F>
+MOE_DEV WAddr<F> w_addr(int tile32, int half, int rb, int ksteps, int g, int r16, bool ok) {
+  WAddr<F> a{};
+  if constexpr (F == Fmt::FP8) {
+    a.q = (uint32_t)rb * (uint32_t)ksteps * 2048u + 16u * (16 * g + r16);
+  } else if constexpr (F == Fmt::MX) {
+    a.q = (uint32_t)rb * (uint32_t)ksteps * 1024u + 16u * (16 * g + r16);
+    a.s = (uint32_t)rb * (uint32_t)ksteps * 64u + (uint32_t)(16 * g + r16);
+  } else if constexpr (F == Fmt::BF16) {
+    // lane (g, r) of the 16x16x32 operand: sub-step 2q + g / 2, half-step g % 2 of tile row r
+    a.q = (uint32_t)tile32 * (uint32_t)ksteps * 4096u + 1024u * (g >> 1) + 16u * (32 * (g & 1) + 16 * half + r16);
+  } else {
+    a.q = ((uint32_t)tile32 * (uint32_t)ksteps + (g >> 1)) * 1024u + 16u * (32 * (g & 1) + 16 * half + r16);
+    a.s = ((uint32_t)tile32 * (uint32_t)ksteps + (g >> 1)) * 128u + 4u * (16 * half + r16);
+  }
+  if (!ok) a.q = a.s = kOOB;
+  return a;
+}
+template <Fmt F>
+MOE_DEV void w_load(WFrag<F>& f, const WAddr<F>& a, __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t srs, int k,
+                    uint32_t dead, int ksteps, int g) {
+  if constexpr (F == Fmt::FP8) {
+    f.q[0] = bload16_nt(rs, a.q | dead, (uint32_t)k * 2048u);
+    f.q[1] = bload16_nt(rs, (a.q + 1024u) | dead, (uint32_t)k * 2048u);
+  } else if constexpr (F == Fmt::MX) {
+    f.q[0] = bload16_nt(rs, a.q | dead, (uint32_t)k * 1024u);
+    f.s = (int)__builtin_amdgcn_raw_buffer_load_b8(srs, a.s | dead, (uint32_t)k * 64u, 0);
+  } else if constexpr (F == Fmt::BF16) {
+    f.q[0] = bload16_nt(rs, a.q | dead, (uint32_t)k * 4096u);
+    f.q[1] = bload16_nt(rs, (a.q + 2048u) | dead, (uint32_t)k * 4096u);
+  } else {
+    dead |= oob_if(2 * k + (g >> 1) >= ksteps);  // an odd count of the layout's K-steps
+    f.q[0] = bload16_nt(rs, a.q | dead, (uint32_t)k * 2048u);
+    f.s = (int)__builtin_amdgcn_raw_buffer_load_b32(srs, a.s | dead, (uint32_t)k * 256u, 0);
+  }
+}
+
+// One K-step of a 16-token activation slice.  v: FP8 / MX E4M3 bytes [16g, 16g+16) and
+// [64+16g, ..) of the step's 128; BF16 the two 32-element halves; NVFP4 x BF16 the four
+// sub-steps' 8 elements; NVFP4 x NVFP4 their packed codes in v[0].  s: the FP8 scale's
+// bits, the MX scale byte, or NVFP4's four block scales.
+template <Fmt F, bool GATEUP>
+struct XFrag {
+  static constexpr bool kPacked = F == Fmt::NVF4 && GATEUP;
+  i32x4 v[nv4w(F) && !kPacked ? 4 : (kPacked ? 1 : 2)];
+  int s;
+};
+
+// acc += (weights x activations) of one K-step; FP8: a partial, its scales are the caller's.
+template <Fmt F, bool GATEUP>
+MOE_DEV f32x4 mma_step(const WFrag<F>& w, const XFrag<F, GATEUP>& x, f32x4 acc) {
+  if constexpr (F == Fmt::FP8) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w.q[0], w.q[1]), join(x.v[0], x.v[1]), acc, 0, 0, 0,
+                                                            127, 0, 127);
+  } else if constexpr (F == Fmt::MX) {
+    const i32x8 b8 = {w.q[0][0], w.q[0][1], w.q[0][2], w.q[0][3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b8, join(x.v[0], x.v[1]), acc, 4, 0, 0, w.s, 0, x.s);
+  } else if constexpr (F == Fmt::BF16) {
+    acc = mma_bf16(w.q[0], x.v[0], acc);
+    return mma_bf16(w.q[1], x.v[1], acc);
+  } else {
+    auto xs = [&](int sub) {
+      if constexpr (XFrag<F, GATEUP>::kPacked) {
+        const float s = sub == 0 ? e4m3_byte<0>(x.s) : sub == 1 ? e4m3_byte<1>(x.s) : sub == 2 ? e4m3_byte<2>(x.s) : e4m3_byte<3>(x.s);
+        return e2m1_bf16x8((uint32_t)x.v[0][sub], s);
+      } else {
+        return x.v[sub];
+      }
+    };
+    acc = mma_bf16(e2m1_bf16x8((uint32_t)w.q[0][0], e4m3_byte<0>(w.s)), xs(0), acc);
+    acc = mma_bf16(e2m1_bf16x8((uint32_t)w.q[0][1], e4m3_byte<1>(w.s)), xs(1), acc);
+    acc = mma_bf16(e2m1_bf16x8((uint32_t)w.q[0][2], e4m3_byte<2>(w.s)), xs(2), acc);
+    return mma_bf16(e2m1_bf16x8((uint32_t)w.q[0][3], e4m3_byte<3>(w.s)), xs(3), acc);
+  }
+}
+
+// ---------------------------------------------------------------- routing in LDS
+struct RouteLds {
+  short ids[kFewMaxPairs];             // expert of each pair, -1: no valid expert
+  uint32_t bits[kFewMaxExperts / 32];  // the active experts
+};
+
+// The pairs' experts and the active set, by the whole workgroup (ends with a barrier).
+// logits given (gate_up): each wave routes tokens wave, wave + WAVES, ...; workgroup 0 stores the result.
+template <int WAVES>
+MOE_DEV void route_to_lds(const FewParams& p, RouteLds& L, bool from_logits) {
+  const int tid = threadIdx.x, lane = lane_id(), np = p.T * p.topk;
+  if (tid < kFewMaxExperts / 32) L.bits[tid] = 0;
+  __syncthreads();
+  if (from_logits) {
+    for (int t = tid >> 6; t < p.T; t += WAVES) {
+      int e;
+      float w;
+      const float* row = p.logits + (size_t)t * p.E;
+      if (p.fast) route_token_topk<true>(row, p.bias, p.E, p.topk, e, w);
+      else route_token_topk<false>(row, p.bias, p.E, p.topk, e, w);
+      if (lane < p.topk) {
+        const int q = t * p.topk + lane;
+        L.ids[q] = (short)e;
+        atomicOr(&L.bits[e >> 5], 1u << (e & 31));
+        if (blockIdx.x == 0) {
+          if (p.idx64_out != nullptr) p.idx64_out[q] = e;
+          else p.idx32_out[q] = e;
+          p.w_out[q] = w;
+        }
+      }
+    }
+  } else {
+    for (int q = tid; q < np; q += 64 * WAVES) {
+      const long long v = p.ids64 ? ((const long long*)p.ids)[q] : (long long)((const int*)p.ids)[q];
+      const bool ok = v >= 0 && v < p.E;
+      L.ids[q] = ok ? (short)v : (short)-1;
+      if (ok) atomicOr(&L.bits[(int)v >> 5], 1u << ((int)v & 31));
+    }
+  }
+  __syncthreads();
+}
+// Active experts before word `lane` (lanes 0..31) of the active set, and in it.
+MOE_DEV int active_before(const RouteLds& L, int& mine) {
+  const int lane = lane_id();
+  mine = lane < kFewMaxExperts / 32 ? __popc(L.bits[lane]) : 0;
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
+  }
+  return incl - mine;
+}
+// The first slot of token t routed to expert e, -1 if none.
+MOE_DEV int slot_of(const RouteLds& L, int T, int topk, int t, int e) {
+  int slot = -1;
+  if (t < T)
+    for (int j = topk - 1; j >= 0; --j)
+      if (L.ids[t * topk + j] == e) slot = j;
+  return slot;
+}
+
+// ---------------------------------------------------------------- gate_up
+// min and max that keep a NaN
+MOE_DEV float clamp_hi(float v, float c) { return v > c ? c : v; }
+MOE_DEV float clamp_both(float v, float c) { return v > c ? c : (v < -c ? -c : v); }
+MOE_DEV f32x4 swiglu4(f32x4 g, f32x4 u, float c, int fast) {
+  f32x4 h;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float gc = clamp_hi(g[i], c), uc = clamp_both(u[i], c);
+    h[i] = (fast ? silu_f32<true>(gc) : silu_f32<false>(gc)) * uc;
+  }
+  return h;
+}
+MOE_DEV uint32_t amax_bits4(f32x4 v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);  // a NaN is the largest
+  return m;
+}
+MOE_DEV uint32_t max_over_g(uint32_t m) {  // the four lanes of one token
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+  return max(m, (uint32_t)__shfl_xor((int)m, 32));
+}
+
+// The FP8 block scale amax / 448 (1 for an all-zero block) and its reciprocal; never below
+// the smallest normal number, whose reciprocal is finite.  A NaN maximum is a NaN scale.
+MOE_DEV float fp8_scale(uint32_t amax, float& inv) {
+  const float s = __uint_as_float(amax) / 448.0f;
+  const float sc = amax == 0 ? 1.0f : (s < 1.17549435e-38f ? 1.17549435e-38f : s);
+  inv = 1.0f / sc;
+  return sc;
+}
+// Four values of magnitude at most 448 (1 + 2^-22) to E4M3 codes: they round to 448 at most, so
+// they need no saturation, and a NaN stays one.
+MOE_DEV int e4m3x4(f32x4 v) {
+  return __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false), true);
+}
+
+// NT: 16-token slices.  KSP: waves that share one slice of columns.  D: K-steps in flight per wave.
+// FP8: 8 waves hold (and quantise) a 128-column block, 4 leave h in fp32.
+template <Fmt F, int NT, int WAVES, int KSP, int D>
+__global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
+  constexpr int CT = F == Fmt::MX ? 2 : 1;  // 16-column groups per wave
+  constexpr int kSlices = WAVES / KSP;
+  constexpr bool kBlock = F == Fmt::FP8 && WAVES == 8;
+  static_assert(!kBlock || KSP == 1, "a wave of a block has its columns' whole sums");
+  __shared__ RouteLds route;
+  __shared__ f32x4 red[KSP > 1 ? WAVES : 1][KSP > 1 ? CT * 2 * NT : 1][KSP > 1 ? 64 : 1];
+  __shared__ uint32_t amax[kBlock ? NT : 1][kBlock ? WAVES : 1][16];
+  const int tid = threadIdx.x, lane = lane_id(), g = lane >> 4, r16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  route_to_lds<WAVES>(p, route, p.logits != nullptr);
+
+  // this workgroup's expert: the a-th active one
+  const int n_slices = p.I / (16 * CT), blocks = (n_slices + kSlices - 1) / kSlices;
+  const int a = (int)blockIdx.x / blocks, slice = ((int)blockIdx.x % blocks) * kSlices + wave / KSP;
+  int mine;
+  const int before = active_before(route, mine);
+  const uint64_t hit = __ballot(lane < kFewMaxExperts / 32 && a >= before && a < before + mine);
+  if (hit == 0) return;  // (uniform: fewer active experts than workgroup rows)
+  const int word = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+  uint32_t bits = route.bits[word];
+  for (int n = a - __shfl(before, word); n > 0; --n) bits &= bits - 1;
+  const int e = __builtin_amdgcn_readfirstlane(word * 32 + __ffs(bits) - 1);
+
+  // the slice's tokens
+  int slot[NT];
+  uint32_t xo[NT], xso[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int t = 16 * n + r16;
+    slot[n] = slot_of(route, p.T, p.topk, t, e);
+    // the lane's first byte of a K-step, as XFrag describes
+    const uint32_t at = F == Fmt::NV4 ? 128u * (g >> 1) + 16u * (g & 1) : F == Fmt::NVF4 ? 32u * (g >> 1) + 4u * (g & 1) : 16u * g;
+    const uint32_t sat = F == Fmt::MX ? (uint32_t)g : F == Fmt::NVF4 ? 4u * (g >> 1) : 0u;
+    xo[n] = slot[n] >= 0 ? (uint32_t)t * p.x_row + at : kOOB;
+    xso[n] = slot[n] >= 0 ? (uint32_t)t * p.x_sf_row + sat : kOOB;
+  }
+  const __amdgpu_buffer_rsrc_t x_rs = make_rsrc(p.x, (uint32_t)p.T * p.x_row);
+  const __amdgpu_buffer_rsrc_t xs_rs = make_rsrc(p.x_sf, (uint32_t)p.T * p.x_sf_row);
+  const __amdgpu_buffer_rsrc_t w_rs = make_rsrc(p.w + (size_t)e * p.w_expert, p.w_expert);
+  const __amdgpu_buffer_rsrc_t ws_rs = make_rsrc(p.w_sf + (size_t)e * p.w_sf_expert, p.w_sf_expert);
+  const bool live = slice < n_slices;
+  const int col0 = slice * 16 * CT;
+  WAddr<F> wa[CT][2];  // gate, up
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      wa[c][u] = w_addr<F>(slice, u, slice * CT + c + u * (p.I / 16), p.ksteps, g, r16, live);
+  // FP8: the 128-row blocks' scales
+  const float* sbg = (const float*)(p.w_sf + (size_t)e * p.w_sf_expert) + (size_t)((live ? col0 : 0) / 128) * p.ksteps;
+  const float* sbu = sbg + (size_t)(p.I / 128) * p.ksteps;
+
+  struct Stage {
+    WFrag<F> w[CT][2];
+    XFrag<F, true> x[NT];
+    float sg, su;
+  } st[D];
+  auto load = [&](Stage& s, int k) {
+    const uint32_t dead = oob_if(k >= p.steps);
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) w_load<F>(s.w[c][u], wa[c][u], w_rs, ws_rs, k, dead, p.ksteps, g);
+    if constexpr (F == Fmt::FP8) {
+      const int kc = min(k, p.steps - 1);
+      s.sg = sbg[kc];
+      s.su = sbu[kc];
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t o = xo[n] | dead;
+      if constexpr (F == Fmt::FP8) {
+        s.x[n].v[0] = bload16(x_rs, o, (uint32_t)k * 128u);
+        s.x[n].v[1] = bload16(x_rs, o + 64u, (uint32_t)k * 128u);
+        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_rs, xso[n] | dead, (uint32_t)k * 4u, 0);
+      } else if constexpr (F == Fmt::MX) {
+        // K tail: rows of any multiple of 32 elements
+        s.x[n].v[0] = bload16(x_rs, o | oob_if(k * 128 + 16 * g >= p.H), (uint32_t)k * 128u);
+        s.x[n].v[1] = bload16(x_rs, (o + 64u) | oob_if(k * 128 + 64 + 16 * g >= p.H), (uint32_t)k * 128u);
+        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b8(
+            xs_rs, xso[n] | dead | oob_if(k * 128 + 32 * g >= p.H), (uint32_t)k * 4u, 0);
+      } else if constexpr (F == Fmt::BF16) {
+        s.x[n].v[0] = bload16(x_rs, o, (uint32_t)k * 128u);
+        s.x[n].v[1] = bload16(x_rs, o + 64u, (uint32_t)k * 128u);
+      } else if constexpr (F == Fmt::NV4) {
+        const uint32_t o2 = o | oob_if(2 * k + (g >> 1) >= p.ksteps);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s.x[n].v[q] = bload16(x_rs, o2 + 32u * q, (uint32_t)k * 256u);
+      } else {
+        const uint32_t odd = oob_if(2 * k + (g >> 1) >= p.ksteps);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          s.x[n].v[0][q] = (int)__builtin_amdgcn_raw_buffer_load_b32(x_rs, (o | odd) + 8u * q, (uint32_t)k * 64u, 0);
+        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_rs, xso[n] | dead | odd, (uint32_t)k * 8u, 0);
+      }
+    }
+  };
+  f32x4 acc[CT][2][NT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[c][u][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto mul = [&](const Stage& s) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if constexpr (F == Fmt::FP8) {
+            const float sc = __builtin_bit_cast(float, s.x[n].s) * (u ? s.su : s.sg);
+            const f32x4 part = mma_step<F, true>(s.w[c][u], s.x[n], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[c][u][n][i] = fmaf(part[i], sc, acc[c][u][n][i]);
+          } else {
+            acc[c][u][n] = mma_step<F, true>(s.w[c][u], s.x[n], acc[c][u][n]);
+          }
+        }
+  };
+  int k = wave % KSP;
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(st[d], k + d * KSP);
+  for (; k < p.steps; k += D * KSP) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      mul(st[d]);
+      __builtin_amdgcn_sched_barrier(0);
+      load(st[d], k + (D + d) * KSP);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  // the K parts, in order
+  if constexpr (KSP > 1) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) red[wave][(c * 2 + u) * NT + n][lane] = acc[c][u][n];
+    __syncthreads();
+    if (wave % KSP != 0) return;
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int w = 1; w < KSP; ++w) acc[c][u][n] += red[wave + w][(c * 2 + u) * NT + n][lane];
+  }
+  if (!live) return;  // (never in a block of FP8: I is a multiple of 128)
+
+  // lane (g, token): columns col0 + 16 c + 4 g ... of the token's row
+  const float gs = nv4w(F) ? p.w_gs[e] : 1.0f;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const size_t row = (size_t)(16 * n + r16) * p.topk + slot[n];
+    f32x4 h[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      f32x4 gt = acc[c][0][n], up = acc[c][1][n];
+      if constexpr (nv4w(F)) gt *= gs, up *= gs;
+      h[c] = swiglu4(gt, up, p.clamp, p.fast);
+    }
+    if constexpr (kBlock) {
+      const uint32_t m = max_over_g(amax_bits4(h[0]));
+      if (g == 0) amax[n][wave][r16] = m;
+      acc[0][0][n] = h[0];  // quantised below, once all the waves' maxima are there
+    } else if constexpr (F == Fmt::FP8) {
+      if (slot[n] >= 0) *(f32x4*)((float*)p.h + row * p.I + col0 + 4 * g) = h[0];
+    } else if constexpr (F == Fmt::MX) {
+      const uint32_t m = max_over_g(max(amax_bits4(h[0]), amax_bits4(h[1])));
+      const int ex = mx_exponent_for_amax(__uint_as_float(m));
+      const float inv = exp2i(-ex);
+      if (slot[n] >= 0) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+          *(uint32_t*)((uint8_t*)p.h + row * p.I + col0 + 16 * c + 4 * g) =
+              f32x2_to_e4m3_sat(h[c][0] * inv, h[c][1] * inv) | f32x2_to_e4m3_sat(h[c][2] * inv, h[c][3] * inv) << 16;
+        // (a NaN in the block: UE8M0's NaN)
+        if (g == 0) ((uint8_t*)p.h_sf)[row * (p.I / 32) + slice] = m > 0x7F800000u ? (uint8_t)255 : (uint8_t)(ex + 127);
+      }
+    } else {
+      f32x4 v = h[0];
+      if constexpr (F == Fmt::NVF4) {
+        // block scale E4M3(amax / (6 c)), codes E2M1(h / (scale c)); kept as code x scale, exact in bf16
+        const uint32_t m = max_over_g(amax_bits4(v));
+        const float c = p.c_gs[e], s6 = __uint_as_float(m) / (6.0f * c);
+        const float sc = e4m3_byte<0>(__builtin_amdgcn_cvt_pk_fp8_f32(s6 > 448.0f ? 448.0f : s6, 0.0f, 0, false));
+        const float den = sc * c, inv = den > 0.0f ? 1.0f / den : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = e2m1_rne_sat(v[i] * inv) * sc;  // (a NaN in the block: sc is NaN)
+      }
+      if (slot[n] >= 0)
+        *(uint2*)((uint16_t*)p.h + row * p.I + col0 + 4 * g) = uint2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+    }
+  }
+  if constexpr (kBlock) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) m = max(m, amax[n][w][r16]);
+      float inv;
+      const float sc = fp8_scale(m, inv);
+      if (slot[n] < 0) continue;
+      const size_t row = (size_t)(16 * n + r16) * p.topk + slot[n];
+      const f32x4 q = acc[0][0][n] * inv;
+      *(int*)((uint8_t*)p.h + row * p.I + col0 + 4 * g) = e4m3x4(q);
+      if (wave == 0 && g == 0) ((float*)p.h_sf)[row * (p.I / 128) + col0 / 128] = sc;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- down
+// R: 16-row weight tiles (output column groups) per workgroup.  HL (FP8): h is fp32 and
+// quantised into LDS here.
+template <Fmt F, int NT, int R, int D, bool HL>
+__global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewParams p) {
+  static_assert(!HL || F == Fmt::FP8, "only FP8 leaves h in fp32");
+  struct Lds {
+    RouteLds route;
+    float w[kFewMaxPairs];
+    short act[kFewMaxExperts];
+    int n_act;
+  };
+  __shared__ Lds L;
+  __shared__ f32x4 red[kDownWaves][R * NT][64];
+  // HL: 128 zero bytes, then the rows' codes (row stride I + 16: rows in other banks); their scales
+  __shared__ __attribute__((aligned(16))) uint8_t hq[HL ? 128 + kFewLdsH : 16];
+  __shared__ float hsc[HL ? kFewLdsH / 128 : 1];
+  const int tid = threadIdx.x, lane = lane_id(), g = lane >> 4, r16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if constexpr (HL) {
+    // 16 lanes a 128-column block, 8 columns a lane (rows of masked slots hold anything and are not read)
+    const int cpr = p.I / 8, n = p.T * p.topk * cpr;
+    if (tid < 32) ((uint32_t*)hq)[tid] = 0;
+    for (int c = tid; c < n; c += 64 * kDownWaves) {
+      const f32x4 a = *(const f32x4*)((const float*)p.h + (size_t)c * 8), b = *(const f32x4*)((const float*)p.h + (size_t)c * 8 + 4);
+      uint32_t m = max(amax_bits4(a), amax_bits4(b));
+      m = dpp_max_u32<0xB1>(m);
+      m = dpp_max_u32<0x4E>(m);
+      m = dpp_max_u32<0x141>(m);
+      m = dpp_max_u32<0x140>(m);
+      float inv;
+      const float sc = fp8_scale(m, inv);
+      const int row = c / cpr, col = c - row * cpr;
+      *(uint2*)(hq + 128 + row * (p.I + 16) + col * 8) = uint2{(uint32_t)e4m3x4(a * inv), (uint32_t)e4m3x4(b * inv)};
+      if ((lane & 15) == 0) hsc[c >> 4] = sc;
+    }
+  }
+  for (int q = tid; q < p.T * p.topk; q += 64 * kDownWaves) L.w[q] = p.topk_w[q];
+  route_to_lds<kDownWaves>(p, L.route, false);
+  if (wave == 0) {
+    int mine;
+    int at = active_before(L.route, mine);
+    if (lane < kFewMaxExperts / 32)
+      for (uint32_t b = L.route.bits[lane]; b != 0; b &= b - 1) L.act[at++] = (short)(lane * 32 + __ffs(b) - 1);
+    if (lane == kFewMaxExperts / 32 - 1) L.n_act = at;
+  }
+  __syncthreads();
+
+  // this wave's part of the (active expert, K-step) sequence
+  const int n_act = __builtin_amdgcn_readfirstlane(L.n_act);
+  const long long total = (long long)n_act * p.steps;
+  const int lo = (int)(total * wave / kDownWaves), hi = (int)(total * (wave + 1) / kDownWaves);
+  const int rb0 = (int)blockIdx.x * R;  // first 16-row block
+  const int n_rb = p.H / 16;
+  WAddr<F> wa[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) wa[r] = w_addr<F>((rb0 + r) >> 1, (rb0 + r) & 1, rb0 + r, p.ksteps, g, r16, rb0 + r < n_rb);
+
+  const uint32_t h_row = HL ? (uint32_t)p.I + 16u : (uint32_t)p.I * (bf16_mma(F) ? 2u : 1u);
+  const uint32_t hs_row = F == Fmt::FP8 ? (uint32_t)(p.I / 128) * (HL ? 1u : 4u) : (uint32_t)(p.I / 32);
+  const uint32_t rows = (uint32_t)(p.T * p.topk);
+  const __amdgpu_buffer_rsrc_t h_rs = make_rsrc(p.h, rows * h_row);
+  const __amdgpu_buffer_rsrc_t hs_rs = make_rsrc(p.h_sf, rows * hs_row);
+
+  // the load side's position: expert, its resources, the tokens' rows and weights
+  int la = lo / p.steps, lk = lo % p.steps, lf = lo;
+  __amdgpu_buffer_rsrc_t w_rs, ws_rs;
+  const float* sb = nullptr;
+  uint32_t ho[NT], hso[NT];
+  float wt[NT];
+  auto set_expert = [&]() {
+    const int e = __builtin_amdgcn_readfirstlane((int)L.act[min(la, max(n_act - 1, 0))]);
+    w_rs = make_rsrc(p.w + (size_t)e * p.w_expert, p.w_expert);
+    ws_rs = make_rsrc(p.w_sf + (size_t)e * p.w_sf_expert, p.w_sf_expert);
+    if constexpr (F == Fmt::FP8)
+      sb = (const float*)(p.w_sf + (size_t)e * p.w_sf_expert) + (size_t)(rb0 / 8) * p.ksteps;
+    const float gs = nv4w(F) ? p.w_gs[e] : 1.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = 16 * n + r16;
+      int slot = -1;
+      float s = 0.0f;  // a token that lists the expert twice weighs it by both, in slot order
+      if (t < p.T)
+        for (int j = 0; j < p.topk; ++j)
+          if (L.route.ids[t * p.topk + j] == e) {
+            s += L.w[t * p.topk + j];
+            if (slot < 0) slot = j;
+          }
+      wt[n] = s * gs;
+      const uint32_t row = (uint32_t)(t * p.topk + slot);
+      const uint32_t at = nv4w(F) ? 128u * (g >> 1) + 16u * (g & 1) : 16u * g;
+      ho[n] = slot >= 0 ? row * h_row + at : kOOB;
+      hso[n] = slot >= 0 ? row * hs_row + (F == Fmt::MX ? (uint32_t)g : 0u) : kOOB;
+    }
+  };
+  struct Stage {
+    WFrag<F> w[R];
+    XFrag<F, false> x[NT];
+    float wt[NT], sb;
+    uint32_t off[NT], soff[NT];  // bit 31: not routed (or past the end); HL: the row's place in LDS
+    int k;
+  } st[D];
+  auto load = [&](Stage& s) {
+    const uint32_t dead = oob_if(lf >= hi);
+    const int k = lk;
+#pragma unroll
+    for (int r = 0; r < R; ++r) w_load<F>(s.w[r], wa[r], w_rs, ws_rs, k, dead, p.ksteps, g);
+    if constexpr (F == Fmt::FP8) s.sb = sb[k];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t o = ho[n] | dead;
+      s.wt[n] = wt[n];
+      s.off[n] = o;
+      if constexpr (HL) {
+        s.soff[n] = hso[n];
+        s.k = k;
+      } else if constexpr (F == Fmt::FP8) {
+        s.x[n].v[0] = bload16(h_rs, o, (uint32_t)k * 128u);
+        s.x[n].v[1] = bload16(h_rs, o + 64u, (uint32_t)k * 128u);
+        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b32(hs_rs, hso[n] | dead, (uint32_t)k * 4u, 0);
+      } else if constexpr (F == Fmt::MX) {
+        s.x[n].v[0] = bload16(h_rs, o | oob_if(k * 128 + 16 * g >= p.I), (uint32_t)k * 128u);
+        s.x[n].v[1] = bload16(h_rs, (o + 64u) | oob_if(k * 128 + 64 + 16 * g >= p.I), (uint32_t)k * 128u);
+        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b8(
+            hs_rs, hso[n] | dead | oob_if(k * 128 + 32 * g >= p.I), (uint32_t)k * 4u, 0);
+      } else if constexpr (F == Fmt::BF16) {
+        s.x[n].v[0] = bload16(h_rs, o, (uint32_t)k * 128u);
+        s.x[n].v[1] = bload16(h_rs, o + 64u, (uint32_t)k * 128u);
+      } else {
+        const uint32_t o2 = o | oob_if(2 * k + (g >> 1) >= p.ksteps);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s.x[n].v[q] = bload16(h_rs, o2 + 32u * q, (uint32_t)k * 256u);
+      }
+    }
+    ++lf;
+    if (++lk == p.steps) {  // (uniform)
+      lk = 0;
+      ++la;
+      set_expert();
+    }
+  };
+  f32x4 acc[R][NT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto mul = [&](Stage& s) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float c = s.wt[n];
+      if constexpr (HL) {
+        const bool ok = !(s.off[n] & kOOB);
+        const uint32_t at = ok ? 128u + s.off[n] + (uint32_t)s.k * 128u : 16u * g;
+        s.x[n].v[0] = *(const i32x4*)(hq + at);
+        s.x[n].v[1] = *(const i32x4*)(hq + at + 64);
+        c *= hsc[ok ? s.soff[n] + (uint32_t)s.k : 0u] * s.sb;
+      } else if constexpr (F == Fmt::FP8) {
+        c *= __builtin_bit_cast(float, s.x[n].s) * s.sb;
+      }
+      const bool routed = !(s.off[n] & kOOB);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const f32x4 part = mma_step<F, false>(s.w[r], s.x[n], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // (an infinite or NaN weight times the zeros of a token that is not routed here stays out)
+          const float v = fmaf(part[i], c, acc[r][n][i]);
+          acc[r][n][i] = routed ? v : acc[r][n][i];
+        }
+      }
+    }
+  };
+  if (lo < hi) {  // (uniform per wave)
+    set_expert();
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(st[d]);
+    for (int f = lo; f < hi; f += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        mul(st[d]);
+        __builtin_amdgcn_sched_barrier(0);
+        load(st[d]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) red[wave][r * NT + n][lane] = acc[r][n];
+  __syncthreads();
+  for (int i = tid; i < R * NT * 64; i += 64 * kDownWaves) {
+    const int rn = i >> 6, l = i & 63, t = 16 * (rn % NT) + (l & 15), rb = rb0 + rn / NT;
+    if (t >= p.T || rb >= n_rb) continue;
+    f32x4 s = red[0][rn][l];
+#pragma unroll
+    for (int w = 1; w < kDownWaves; ++w) s += red[w][rn][l];
+    const size_t at = (size_t)t * p.H + 16 * rb + 4 * (l >> 4);
+    const uint16_t* add[2] = {p.shared, p.residual};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (add[q] == nullptr) continue;
+      const uint2 v = *(const uint2*)(add[q] + at);
+      s += f32x4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                 __uint_as_float(v.y & 0xFFFF0000u)};
+    }
+    if (p.out_f32) *(f32x4*)((float*)p.out + at) = s;
+    else *(uint2*)((uint16_t*)p.out + at) = uint2{bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3])};
+  }
+}
+
+}  // namespace
+
+bool few_routes_in_launch(int T) { return T <= 4; }
+
+// FP8: h in fp32 between the launches (see above).  Whole 128-column blocks need about as many
+// workgroups as the part has CUs to stream at full rate.
+static bool few_h_fp32(Fmt f, int T, int topk, int E, int I) {
+  const int pairs = T * topk, active = min(E, pairs);
+  return f == Fmt::FP8 && (long long)active * (I / 128) < 256 && (long long)pairs * (I + 16) <= kFewLdsH;
+}
+size_t few_h_bytes(Fmt f, int T, int topk, int E, int I) {
+  return (size_t)T * topk * I * (few_h_fp32(f, T, topk, E, I) ? 4 : bf16_mma(f) ? 2 : 1);
+}
+size_t few_hsf_bytes(Fmt f, int pairs, int I) {
+  return f == Fmt::FP8 ? (size_t)pairs * (I / 128) * 4 : f == Fmt::MX ? (size_t)pairs * (I / 32) : 0;
+}
+
+hipError_t launch_few(const FewArgs& a, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  const Fmt wf = a.fmt == Fmt::NVF4 ? Fmt::NV4 : a.fmt;
+  FewParams p{};
+  p.T = a.T;
+  p.topk = a.topk;
+  p.E = a.E;
+  p.H = a.H;
+  p.I = a.I;
+  p.fast = a.fast ? 1 : 0;
+  p.clamp = a.clamp;
+  p.ids = a.ids;
+  p.ids64 = a.ids64 ? 1 : 0;
+  p.topk_w = a.topk_w;
+  p.h = a.h;
+  p.h_sf = a.h_sf;
+  p.shared = (const uint16_t*)a.shared;
+  p.residual = (const uint16_t*)a.residual;
+  p.out = a.out;
+  p.out_f32 = a.out_f32 ? 1 : 0;
+
+  FewParams u = p;  // gate_up
+  u.logits = a.logits;
+  u.bias = a.bias;
+  if (a.logits != nullptr) {
+    if (a.ids64) u.idx64_out = (long long*)a.ids;
+    else u.idx32_out = (int*)a.ids;
+    u.w_out = (float*)a.topk_w;
+  }
+  u.x = (const uint8_t*)a.x;
+  u.x_sf = (const uint8_t*)a.x_sf;
+  u.x_row = a.fmt == Fmt::NVF4 ? a.H / 2 : bf16_mma(a.fmt) ? 2 * a.H : a.H;
+  u.x_sf_row = a.fmt == Fmt::FP8 ? a.H / 128 * 4 : a.fmt == Fmt::MX ? a.H / 32 : a.fmt == Fmt::NVF4 ? a.H / 16 : 0;
+  u.w = (const uint8_t*)a.w13;
+  u.w_sf = (const uint8_t*)a.w13_sf;
+  u.w_expert = (uint32_t)prepared_expert_bytes(wf, 2 * a.I, a.H);
+  u.w_sf_expert = a.fmt == Fmt::FP8 ? (uint32_t)(2 * a.I / 128 * (a.H / 128) * 4)
+                                    : (uint32_t)prepared_scale_expert_bytes(wf, 2 * a.I, a.H);
+  u.w_gs = a.w13_gs;
+  u.c_gs = a.c_scales;
+  u.ksteps = prepared_ksteps(wf, a.H);
+  u.steps = nv4w(a.fmt) ? (u.ksteps + 1) / 2 : u.ksteps;
+
+  FewParams d = p;  // down
+  d.w = (const uint8_t*)a.w2;
+  d.w_sf = (const uint8_t*)a.w2_sf;
+  d.w_expert = (uint32_t)prepared_expert_bytes(wf, a.H, a.I);
+  d.w_sf_expert = a.fmt == Fmt::FP8 ? (uint32_t)(a.H / 128 * (a.I / 128) * 4)
+                                    : (uint32_t)prepared_scale_expert_bytes(wf, a.H, a.I);
+  d.w_gs = a.w2_gs;
+  d.ksteps = prepared_ksteps(wf, a.I);
+  d.steps = nv4w(a.fmt) ? (d.ksteps + 1) / 2 : d.ksteps;
+
+  const int active = a.E < a.T * a.topk ? a.E : a.T * a.topk;  // at most
+  auto go = [&](auto fmt, auto nt) {
+    constexpr Fmt F = decltype(fmt)::value;
+    constexpr int NT = decltype(nt)::value;
+    constexpr int CT = F == Fmt::MX ? 2 : 1;
+    const int n_slices = a.I / (16 * CT);
+    auto up = [&](auto waves, auto ksp) {
+      constexpr int W = decltype(waves)::value, KSP = decltype(ksp)::value;
+      constexpr int per = W / KSP;
+      const int grid = (n_slices + per - 1) / per * active;
+      hipLaunchKernelGGL((few_gate_up_kernel<F, NT, W, KSP, 3>), dim3((unsigned)grid), dim3(64 * W), 0, s, u);
+    };
+    auto down = [&](auto lds_h) {
+      hipLaunchKernelGGL((few_down_kernel<F, NT, 1, 3, decltype(lds_h)::value>), dim3((unsigned)(a.H / 16)),
+                         dim3(64 * kDownWaves), 0, s, d);
+    };
+    using C1 = std::integral_constant<int, 1>;
+    using C4 = std::integral_constant<int, 4>;
+    using C8 = std::integral_constant<int, 8>;
+    if constexpr (F == Fmt::FP8) {
+      if (!few_h_fp32(a.fmt, a.T, a.topk, a.E, a.I)) {
+        up(C8{}, C1{});
+        down(std::false_type{});
+      } else {
+        up(C4{}, C4{});
+        down(std::true_type{});
+      }
+    } else {
+      up(C4{}, C4{});
+      down(std::false_type{});
+    }
+  };
+  auto by_tokens = [&](auto fmt) {
+    if (a.T <= 16) go(fmt, std::integral_constant<int, 1>{});
+    else go(fmt, std::integral_constant<int, 2>{});
+  };
+  switch (a.fmt) {
+    case Fmt::FP8: by_tokens(std::integral_constant<Fmt, Fmt::FP8>{}); break;
+    case Fmt::BF16: by_tokens(std::integral_constant<Fmt, Fmt::BF16>{}); break;
+    case Fmt::MX: by_tokens(std::integral_constant<Fmt, Fmt::MX>{}); break;
+    case Fmt::NV4: by_tokens(std::integral_constant<Fmt, Fmt::NV4>{}); break;
+    case Fmt::NVF4: by_tokens(std::integral_constant<Fmt, Fmt::NVF4>{}); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe

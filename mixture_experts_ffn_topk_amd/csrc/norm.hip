@@ -1,0 +1,217 @@
+// Residual addition, root-mean-square norm and quantisation into the expert
+// FFN's activation format, in one pass over the rows:
+//
+//   z = x + residual                     (fp32, not rounded before the norm)
+//   residual_out = round(z)              (bf16, or fp32 as it is)
+//   n = z * 1/sqrt(mean(z^2) + eps) * weight
+//   x_norm = bf16(n)
+//   x_q, x_sf = n quantised per block of 128 (E4M3, fp32 scale amax/448), 32
+//               (E4M3, the smallest power of two 2^e with 448 * 2^e >= amax) or
+//               16 columns (E2M1, E4M3 scale of amax / (6 x_gs))
+//
+// The formats are those of the MoEActivationPack page's encodings list and the
+// quantisation rules those of the FFN's own intermediate.  A block that holds a
+// NaN gets a NaN scale (the codes of such a block mean nothing), so that a NaN
+// is never turned into a number on the way into the experts.
+//
+// A workgroup owns one row, which stays in registers between the sum of squares
+// and the outputs: thread i holds the 8-column chunks i, i + threads, ....  Each
+// quantisation block then lies in 16, 4 or 2 neighbouring lanes, and its maximum
+// takes DPP moves only.
+#include <type_traits>
+
+#include "layer.h"
+#include "topk.h"
+
+namespace moe {
+
+namespace {
+
+constexpr float kMinNormal = 1.17549435e-38f;
+
+struct NormParams {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* residual_out;
+  void* x_norm;
+  void* x_q;
+  void* x_sf;
+  int H;
+  int weight_f32;
+  float eps, inv_h, x_gs;
+};
+
+MOE_DEV void unpack8(i32x4 v, float (&f)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = __uint_as_float((uint32_t)v[q] << 16);
+    f[2 * q + 1] = __uint_as_float((uint32_t)v[q] & 0xFFFF0000u);
+  }
+}
+template <bool F32>
+MOE_DEV void load8(const void* base, size_t i, float (&f)[8]) {
+  if constexpr (F32) {
+    const f32x4 a = *(const f32x4*)((const float*)base + i), b = *(const f32x4*)((const float*)base + i + 4);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f[q] = a[q], f[4 + q] = b[q];
+  } else {
+    unpack8(*(const i32x4*)((const uint16_t*)base + i), f);
+  }
+}
+MOE_DEV i32x4 pack8(const float (&f)[8]) {
+  i32x4 o;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = (int)bf16x2_rne(f[2 * q], f[2 * q + 1]);
+  return o;
+}
+
+// The largest |f| of 8 values, as bits: unsigned order puts NaN above infinity, so a NaN survives.
+MOE_DEV uint32_t amax_bits8(const float (&f)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  return m;
+}
+// What one row's chunk writes of the format's activations: n the 8 values, c the chunk.
+template <Fmt F>
+MOE_DEV void quantise8(const NormParams& p, size_t t, int c, const float (&n)[8], bool live) {
+  const int lane = lane_id(), C = p.H >> 3;
+  uint32_t m = amax_bits8(n);
+  m = dpp_max_u32<0xB1>(m);  // lanes l, l ^ 1
+  if constexpr (F == Fmt::NVF4) {
+    const float a = __uint_as_float(m);
+    // v_cvt_pk_fp8_f32 past the E4M3 maximum would give NaN: the scale saturates; a NaN maximum stays one
+    const float s6 = a / (6.0f * p.x_gs);
+    const uint32_t code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s6 > 448.0f ? 448.0f : s6, 0.0f, 0, false) & 0xFFu;
+    const float den = __builtin_amdgcn_cvt_f32_fp8((int)code, 0) * p.x_gs;
+    const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float r = e2m1_rne_sat(n[i] * inv), b = fabsf(r);
+      // magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 -> codes 0 .. 7
+      const uint32_t k = b < 2.0f ? (uint32_t)(b * 2.0f) : (b < 4.0f ? (uint32_t)b + 2u : (b < 6.0f ? 6u : 7u));
+      v |= (k | (k != 0 && r < 0.0f ? 8u : 0u)) << (4 * i);
+    }
+    if (live) {
+      ((uint32_t*)p.x_q)[t * C + c] = v;
+      if ((lane & 1) == 0) ((uint8_t*)p.x_sf)[t * (C >> 1) + (c >> 1)] = (uint8_t)code;
+    }
+    return;
+  }
+  m = dpp_max_u32<0x4E>(m);  // 4 lanes: 32 columns
+  float inv;
+  if constexpr (F == Fmt::FP8) {
+    m = dpp_max_u32<0x141>(m);
+    m = dpp_max_u32<0x140>(m);  // 16 lanes: 128 columns
+    const float a = __uint_as_float(m);
+    // an all-zero block has scale 1; a scale below the smallest normal number would have no finite reciprocal
+    const float s = a / 448.0f;
+    const float sc = m == 0 ? 1.0f : (s < kMinNormal ? kMinNormal : s);
+    inv = 1.0f / sc;
+    if (live && (lane & 15) == 0) ((float*)p.x_sf)[t * (C >> 4) + (c >> 4)] = sc;
+  } else {
+    const bool nan = m > 0x7F800000u;
+    const int e = mx_exponent_for_amax(__uint_as_float(m));
+    inv = exp2i(-e);
+    if (live && (lane & 3) == 0) ((uint8_t*)p.x_sf)[t * (C >> 2) + (c >> 2)] = nan ? (uint8_t)255 : (uint8_t)(e + 127);
+  }
+  uint2 v;
+  v.x = f32x2_to_e4m3_sat(n[0] * inv, n[1] * inv) | f32x2_to_e4m3_sat(n[2] * inv, n[3] * inv) << 16;
+  v.y = f32x2_to_e4m3_sat(n[4] * inv, n[5] * inv) | f32x2_to_e4m3_sat(n[6] * inv, n[7] * inv) << 16;
+  if (live) ((uint2*)p.x_q)[t * C + c] = v;
+}
+
+// NV: chunks a thread holds.  RES: 0 no residual, 1 bf16, 2 fp32.
+template <Fmt F, int NV, bool XF32, int RES>
+__global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
+  __shared__ float part[16];
+  const size_t t = blockIdx.x;
+  const int tid = threadIdx.x, C = p.H >> 3, nthr = blockDim.x;
+  float z[NV][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = tid + v * nthr;
+    const size_t at = t * p.H + (size_t)c * 8;
+    if (c < C) {
+      load8<XF32>(p.x, at, z[v]);
+      if constexpr (RES != 0) {
+        float r[8];
+        load8<RES == 2>(p.residual, at, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[v][i] += r[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[v][i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(z[v][i], z[v][i], ss);
+  }
+  ss = wave_sum_f32(ss);
+  if (nthr > 64) {
+    if ((tid & 63) == 0) part[tid >> 6] = ss;
+    __syncthreads();
+    ss = 0.0f;
+    for (int w = 0; w < nthr >> 6; ++w) ss += part[w];
+  }
+  const float r = 1.0f / sqrtf(fmaf(ss, p.inv_h, p.eps));
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = tid + v * nthr;
+    const bool live = c < C;
+    const size_t at = t * p.H + (size_t)c * 8;
+    float w[8] = {};
+    if (live) {
+      if (p.weight_f32) load8<true>(p.weight, (size_t)c * 8, w);
+      else load8<false>(p.weight, (size_t)c * 8, w);
+      if constexpr (RES == 1) *(i32x4*)((uint16_t*)p.residual_out + at) = pack8(z[v]);
+      if constexpr (RES == 2) {
+        *(f32x4*)((float*)p.residual_out + at) = f32x4{z[v][0], z[v][1], z[v][2], z[v][3]};
+        *(f32x4*)((float*)p.residual_out + at + 4) = f32x4{z[v][4], z[v][5], z[v][6], z[v][7]};
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[v][i] = z[v][i] * r * w[i];
+    if (live && p.x_norm != nullptr) *(i32x4*)((uint16_t*)p.x_norm + at) = pack8(z[v]);
+    if constexpr (F != Fmt::BF16) quantise8<F>(p, t, c, z[v], live);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  NormParams p{a.x, a.residual, a.weight, a.residual_out, a.x_norm, a.x_q, a.x_sf, a.H, a.weight_f32 ? 1 : 0,
+               a.eps, 1.0f / (float)a.H, a.x_gs};
+  const int chunks = a.H / 8;
+  const int nv = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  const int threads = ((chunks + nv - 1) / nv + 63) / 64 * 64;
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)a.T), dim3((unsigned)threads), 0, s, p); };
+  auto by_nv = [&](auto f, auto xf, auto res) {
+    constexpr Fmt F = decltype(f)::value;
+    constexpr bool X = decltype(xf)::value;
+    constexpr int R = decltype(res)::value;
+    if (nv == 1) go(add_rmsnorm_kernel<F, 1, X, R>);
+    else if (nv == 2) go(add_rmsnorm_kernel<F, 2, X, R>);
+    else go(add_rmsnorm_kernel<F, 4, X, R>);
+  };
+  auto by_type = [&](auto f) {
+    auto by_res = [&](auto xf) {
+      if (a.residual == nullptr) by_nv(f, xf, std::integral_constant<int, 0>{});
+      else if (!a.residual_f32) by_nv(f, xf, std::integral_constant<int, 1>{});
+      else by_nv(f, xf, std::integral_constant<int, 2>{});
+    };
+    if (a.x_f32) by_res(std::true_type{});
+    else by_res(std::false_type{});
+  };
+  if (a.x_q == nullptr) by_type(std::integral_constant<Fmt, Fmt::BF16>{});
+  else if (a.fmt == Fmt::FP8) by_type(std::integral_constant<Fmt, Fmt::FP8>{});
+  else if (a.fmt == Fmt::MX) by_type(std::integral_constant<Fmt, Fmt::MX>{});
+  else by_type(std::integral_constant<Fmt, Fmt::NVF4>{});
+  return hipGetLastError();
+}
+
+}  // namespace moe

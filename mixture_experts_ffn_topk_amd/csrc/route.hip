@@ -14,6 +14,7 @@
 // order could leak into the result).
 #include "device.h"
 #include "launch.h"
+#include "topk.h"
 
 namespace moe {
 
@@ -21,72 +22,7 @@ constexpr int kPlanThreads = 1024;  // 16 waves; also the largest expert count
 constexpr int kPlanWaves = kPlanThreads / 64;
 
 // ------------------------------------------------------------------ top-k
-// Order-preserving map of a float key to 32 bits (larger key, larger value;
-// -0 and +0 equal, as the float comparison has them).
-MOE_DEV uint32_t key_bits(float f) {
-  const uint32_t u = __float_as_uint(f + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-// The wave's largest 64-bit (key, ~index) word, uniform: butterflies inside each
-// row of 16 lanes by DPP (quad swaps, half-row and row mirrors), then the four
-// row results read into scalars.  (Cross-lane shuffles through the LDS crossbar
-// made each of the k selection rounds a chain of 18 round trips.)
-template <int CTRL>
-MOE_DEV uint64_t dpp_max_u64(uint64_t x) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)x, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(x >> 32), CTRL, 0xF, 0xF, false);
-  const uint64_t y = ((uint64_t)hi << 32) | lo;
-  return y > x ? y : x;
-}
-MOE_DEV uint64_t wave_max_u64(uint64_t x) {
-  x = dpp_max_u64<0xB1>(x);   // quad_perm [1,0,3,2]
-  x = dpp_max_u64<0x4E>(x);   // quad_perm [2,3,0,1]
-  x = dpp_max_u64<0x141>(x);  // row_half_mirror
-  x = dpp_max_u64<0x140>(x);  // row_mirror
-  uint64_t m = 0;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const uint64_t v = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), 16 * r) << 32) |
-                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, 16 * r);
-    m = v > m ? v : m;
-  }
-  return m;
-}
-
-// The wave's maximum and sum of a float (uniform), by the same DPP butterflies
-// and row read-outs; the sum adds the four row sums in row order.
-template <int CTRL>
-MOE_DEV float dpp_f32(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
-}
-MOE_DEV float wave_max_f32(float x) {
-  x = fmaxf(x, dpp_f32<0xB1>(x));
-  x = fmaxf(x, dpp_f32<0x4E>(x));
-  x = fmaxf(x, dpp_f32<0x141>(x));
-  x = fmaxf(x, dpp_f32<0x140>(x));
-  float m = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 0));
-#pragma unroll
-  for (int r = 1; r < 4; ++r)
-    m = fmaxf(m, __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 16 * r)));
-  return m;
-}
-MOE_DEV float wave_sum_f32(float x) {
-  x += dpp_f32<0xB1>(x);
-  x += dpp_f32<0x4E>(x);
-  x += dpp_f32<0x141>(x);
-  x += dpp_f32<0x140>(x);
-  float m = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 0));
-#pragma unroll
-  for (int r = 1; r < 4; ++r) m += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 16 * r));
-  return m;
-}
-
-// One wavefront per token.  Each lane holds logits e = lane + 64*i (i < 8),
-// k rounds of wave-wide argmax with key (logit + bias desc, index asc), then a
-// softmax over the k selected logits.  The optional per-expert bias (the
-// routing_bias of bias-aware methods on the MoEActivationPack page) only ranks
-// the experts: the weights come from the logits themselves.
+// One wavefront per token (route_token_topk).
 template <typename IdxT, bool FAST>
 __global__ __launch_bounds__(256) void route_logits_topk_kernel(const float* __restrict__ logits,
                                                                 const float* __restrict__ bias, int T, int E, int k,
@@ -95,51 +31,12 @@ __global__ __launch_bounds__(256) void route_logits_topk_kernel(const float* __r
   const int lane = lane_id();
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
-  float v[8], key[8];
-  const float* row = logits + (size_t)t * E;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    int e = lane + 64 * i;
-    float x = e < E ? row[e] : -INFINITY;
-    v[i] = (x != x) ? -INFINITY : x;  // NaN ranks as -inf
-    const float kb = (bias != nullptr && e < E) ? v[i] + bias[e] : v[i];
-    key[i] = (kb != kb) ? -INFINITY : kb;
-  }
-  unsigned taken = 0;
-  float my_v = -INFINITY;
-  int my_i = 0;
-  for (int s = 0; s < k; ++s) {
-    float bk = -INFINITY, bv = -INFINITY;
-    int bi = 0x7FFFFFFF;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int e = lane + 64 * i;
-      bool ok = e < E && !((taken >> i) & 1u);
-      if (ok && (key[i] > bk || (key[i] == bk && e < bi))) {
-        bk = key[i];
-        bv = v[i];
-        bi = e;
-      }
-    }
-    // the wave's winner: largest key, then smallest index (a lane without a
-    // candidate, ~0x7FFFFFFF, loses to any expert at an equal key)
-    const uint64_t w = wave_max_u64(((uint64_t)key_bits(bk) << 32) | (uint32_t)~bi);
-    bi = (int)~(uint32_t)w;
-    bv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, bv), bi & 63));
-    if ((bi & 63) == lane) taken |= 1u << (bi >> 6);
-    if (lane == s) {
-      my_v = bv;
-      my_i = bi;
-    }
-  }
-  // the largest selected logit (the first one when there is no bias)
-  const float vmax = wave_max_f32(lane < k ? my_v : -INFINITY);
-  float ex = 0.0f;
-  if (lane < k) ex = FAST ? __builtin_amdgcn_exp2f((my_v - vmax) * 1.4426950408889634f) : expf(my_v - vmax);
-  const float sum = wave_sum_f32(ex);
+  int my_i;
+  float my_w;
+  route_token_topk<FAST>(logits + (size_t)t * E, bias, E, k, my_i, my_w);
   if (lane < k) {
     idx_out[(size_t)t * k + lane] = (IdxT)my_i;
-    w_out[(size_t)t * k + lane] = FAST ? ex * __builtin_amdgcn_rcpf(sum) : ex / sum;
+    w_out[(size_t)t * k + lane] = my_w;
   }
 }
 
