@@ -215,15 +215,51 @@ def _on_current_gpu(**tensors):
     """_on_gpu, and on the current device: the one whose stream the call uses."""
     _on_gpu(**tensors)
     import torch
-    cur = None
+    cur = torch.cuda.current_device()
     for what, t in tensors.items():
         for v in t.values() if isinstance(t, dict) else (t,):
-            if v is None or isinstance(v, int):
-                continue
-            if cur is None:
-                cur = torch.cuda.current_device()
-            if v.get_device() != cur:
+            if v is not None and not isinstance(v, int) and v.get_device() != cur:
                 raise ValueError(f"{what} is on {v.device}; the current device is cuda:{cur}")
+
+
+_byte_kinds = None
+
+
+def _byte_types():
+    """The one-byte dtypes that raw codes and scales may travel in."""
+    global _byte_kinds
+    if _byte_kinds is None:
+        import torch
+        _byte_kinds = tuple(getattr(torch, n) for n in ("uint8", "int8", "float8_e4m3fn", "float8_e8m0fnu",
+                                                        "float4_e2m1fn_x2") if hasattr(torch, n))
+    return _byte_kinds
+
+
+def _fit(*args) -> bool:
+    """Whether every (tensor, bytes, dtypes) given is a contiguous GPU tensor of one of the
+    dtypes (None: of any), on the current device, with at least so many bytes: the checks of _need and
+    _on_current_gpu in one pass, without their messages (a call of a few microseconds
+    should not spend more on them).  False says nothing about which check failed, nor
+    that one did: raw addresses take the slow checks too."""
+    import torch
+    cur = None
+    for t, nbytes, dtypes in args:
+        if t is None or t.__class__ is int or (dtypes is not None and t.dtype not in dtypes) or t.nbytes < nbytes:
+            return False
+        if not t.is_contiguous():
+            return False
+        d = t.get_device()
+        if d != cur:
+            if cur is not None or d < 0 or d != torch.cuda.current_device():
+                return False
+            cur = d
+    return True
+
+
+def _current_stream() -> int:
+    """The current stream's handle (_stream(None) without making a Stream object)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 class MoEFFN:
@@ -603,23 +639,32 @@ class MoEFFN:
         residual itself."""
         import torch
         T, H = num_tokens, self.hidden
-        kinds = (torch.bfloat16, torch.float32)
-        f32 = [t is not None and not isinstance(t, int) and t.dtype == torch.float32 for t in (x, residual, weight)]
-        size = [4 if f else 2 for f in f32]
-        _need(x, "x", T * H * size[0], kinds)
-        _need(weight, "weight", H * size[2], kinds)
-        _need(residual, "residual", T * H * size[1], kinds, required=False)
-        _need(residual_out, "residual_out", T * H * size[1], (kinds[f32[1]],), required=residual is not None)
-        _need(x_norm, "x_norm", T * H * 2, kinds[:1], required=x_q is None)
-        if self._x_sf_row() > 0:
-            _need(x_q, "x_q", T * self._x_bytes(H), elem=1, required=x_sf is not None)
-            _need(x_sf, "x_sf", T * self._x_sf_row(), elem=4 if self.fmt == "fp8_block128" else 1,
-                  required=x_q is not None)
-        _on_current_gpu(x=x, residual=residual, weight=weight, residual_out=residual_out, x_norm=x_norm, x_q=x_q,
-                        x_sf=x_sf)
-        _check(self.lib.moe_add_rmsnorm(self._h, T, _ptr(x), f32[0], _ptr(residual), f32[1], _ptr(weight), f32[2],
-                                        eps, _ptr(residual_out), _ptr(x_norm), _ptr(x_q), _ptr(x_sf), x_global_scale,
-                                        _stream(stream)), "moe_add_rmsnorm")
+        n, bf16, f32 = T * H, torch.bfloat16, torch.float32
+        xf, rf, wf = (getattr(t, "dtype", None) is f32 for t in (x, residual, weight))
+        kinds, res = (bf16, f32), n * (4 if rf else 2)
+        sf_bytes = T * self._x_sf_row()
+        sf_kinds = (f32,) if self.fmt == "fp8_block128" else _byte_types()
+        fast = [(x, n * (4 if xf else 2), kinds), (weight, H * (4 if wf else 2), kinds)]
+        if residual is not None and residual_out is not None:
+            fast += ((residual, res, kinds), (residual_out, res, (f32 if rf else bf16,)))
+        if x_norm is not None:
+            fast.append((x_norm, n * 2, (bf16,)))
+        if x_q is not None and x_sf is not None:
+            fast += ((x_q, T * self._x_bytes(H), _byte_types()), (x_sf, sf_bytes, sf_kinds))
+        if len(fast) != 2 + sum(t is not None for t in (residual, residual_out, x_norm, x_q, x_sf)) or not _fit(*fast):
+            _need(x, "x", n * (4 if xf else 2), kinds)
+            _need(weight, "weight", H * (4 if wf else 2), kinds)
+            _need(residual, "residual", res, kinds, required=False)
+            _need(residual_out, "residual_out", res, (f32 if rf else bf16,), required=residual is not None)
+            _need(x_norm, "x_norm", n * 2, (bf16,), required=x_q is None)
+            if sf_bytes > 0:
+                _need(x_q, "x_q", T * self._x_bytes(H), _byte_types(), required=x_sf is not None)
+                _need(x_sf, "x_sf", sf_bytes, sf_kinds, required=x_q is not None)
+            _on_current_gpu(x=x, residual=residual, weight=weight, residual_out=residual_out, x_norm=x_norm, x_q=x_q,
+                            x_sf=x_sf)
+        _check(self.lib.moe_add_rmsnorm(self._h, T, _ptr(x), xf, _ptr(residual), rf, _ptr(weight), wf, eps,
+                                        _ptr(residual_out), _ptr(x_norm), _ptr(x_q), _ptr(x_sf), x_global_scale,
+                                        _current_stream() if stream is None else _stream(stream)), "moe_add_rmsnorm")
 
     def router_workspace_size(self, num_tokens: int) -> int:
         return int(self.lib.moe_router_workspace_size(self._h, num_tokens))
@@ -633,14 +678,20 @@ class MoEFFN:
         fp32 (a raw address: bf16); ws from alloc_router_workspace."""
         import torch
         T, H, E = num_tokens, self.hidden, self.experts
-        w32 = not isinstance(router_w, int) and router_w is not None and router_w.dtype == torch.float32
-        _need(x, "x", T * H * 2, (torch.bfloat16,))
-        _need(router_w, "router_w", E * H * (4 if w32 else 2), (torch.bfloat16, torch.float32))
-        _need(logits, "logits", T * E * 4, (torch.float32,))
-        _need(ws, "ws", 0, required=False)
-        _on_current_gpu(x=x, router_w=router_w, logits=logits, ws=ws)
+        w32 = getattr(router_w, "dtype", None) is torch.float32
+        fast = [(x, T * H * 2, (torch.bfloat16,)), (router_w, E * H * (4 if w32 else 2), (torch.bfloat16, torch.float32)),
+                (logits, T * E * 4, (torch.float32,))]
+        if ws is not None:
+            fast.append((ws, 0, (torch.uint8,)))
+        if not _fit(*fast):
+            _need(x, "x", T * H * 2, (torch.bfloat16,))
+            _need(router_w, "router_w", E * H * (4 if w32 else 2), (torch.bfloat16, torch.float32))
+            _need(logits, "logits", T * E * 4, (torch.float32,))
+            _need(ws, "ws", 0, required=False)
+            _on_current_gpu(x=x, router_w=router_w, logits=logits, ws=ws)
         _check(self.lib.moe_router_logits(self._h, T, _ptr(x), _ptr(router_w), w32, _ptr(logits), _ptr(ws),
-                                          self._nbytes(ws), _stream(stream)), "moe_router_logits")
+                                          self._nbytes(ws), _current_stream() if stream is None else _stream(stream)),
+               "moe_router_logits")
 
     def few_workspace_size(self, num_tokens: int) -> int:
         return int(self.lib.moe_few_workspace_size(self._h, num_tokens))
@@ -654,22 +705,35 @@ class MoEFFN:
         """moe_forward_few: forward() for at most FEW_MAX_TOKENS tokens in two launches; ws
         from alloc_few_workspace."""
         import torch
-        T = num_tokens
-        self._check_x(x, x_sf, T)
-        self._check_weights(weights)
-        self._check_routing_in(T, topk_idx, routing_logits, routing_bias)
-        _need(topk_idx, "topk_idx", T * self.topk * self.topk_idx_bits // 8, self._idx_dtypes())
-        _need(topk_weights, "topk_weights", T * self.topk * 4, (torch.float32,))
-        self._check_out(T, out, shared, residual)
-        _need(ws, "ws", 0, required=False)
-        _on_current_gpu(x=x, x_sf=x_sf, weights=weights, topk_idx=topk_idx, topk_weights=topk_weights,
-                        routing_logits=routing_logits, routing_bias=routing_bias, out=out, ws=ws, shared=shared,
-                        residual=residual)
+        T, n, f32 = num_tokens, num_tokens * self.hidden, (torch.float32,)
+        if not hasattr(self, "_psizes"):
+            self._psizes = self.prepared_weights_size()
+        fast = [(x, T * self._x_bytes(self.hidden), None), (ws, 0, None),
+                (topk_idx, T * self.topk * self.topk_idx_bits // 8, self._idx_dtypes()), (topk_weights, T * self.topk * 4, f32),
+                (out, n * (4 if self.out_fp32 else 2), f32 if self.out_fp32 else (torch.bfloat16,))]
+        fast += [(weights.get(name), size, None) for name, size in self._psizes.items() if size]
+        if self._x_sf_row() > 0:
+            fast.append((x_sf, T * self._x_sf_row(), None))
+        if self.route_mode != "precomputed":
+            fast.append((routing_logits, T * self.experts * 4, f32))
+        fast += [(t, n * 2, (torch.bfloat16,)) for t in (shared, residual) if t is not None]
+        # (a routing bias and NVFP4's per-expert scales take the slow checks)
+        if routing_bias is not None or self.fmt in ("nvfp4_w4a16", "nvfp4") or not _fit(*fast):
+            self._check_x(x, x_sf, T)
+            self._check_weights(weights)
+            self._check_routing_in(T, topk_idx, routing_logits, routing_bias)
+            _need(topk_idx, "topk_idx", T * self.topk * self.topk_idx_bits // 8, self._idx_dtypes())
+            _need(topk_weights, "topk_weights", T * self.topk * 4, f32)
+            self._check_out(T, out, shared, residual)
+            _need(ws, "ws", 0, required=False)
+            _on_current_gpu(x=x, x_sf=x_sf, weights=weights, topk_idx=topk_idx, topk_weights=topk_weights,
+                            routing_logits=routing_logits, routing_bias=routing_bias, out=out, ws=ws, shared=shared,
+                            residual=residual)
         ws_ = self._weights_struct(weights)
         _check(self.lib.moe_forward_few(self._h, T, _ptr(x), _ptr(x_sf), _ptr(topk_idx), _ptr(topk_weights),
                                         _ptr(routing_logits), _ptr(routing_bias), ctypes.byref(ws_), _ptr(shared),
-                                        _ptr(residual), _ptr(out), _ptr(ws), self._nbytes(ws), _stream(stream)),
-               "moe_forward_few")
+                                        _ptr(residual), _ptr(out), _ptr(ws), self._nbytes(ws),
+                                        _current_stream() if stream is None else _stream(stream)), "moe_forward_few")
 
 
 __all__ = ["MoEFFN", "MoEError", "load_library", "LIB_PATH", "EXPORTED", "FORMATS", "ROUTE_MODES", "TILE_REGIMES",

@@ -7,14 +7,15 @@
 // holds all 24 bits of the weight (w = w0 + w1 + w2 exactly, barring underflow),
 // each multiplied on the matrix cores: bf16 products are exact in fp32, so the
 // result has the error of an fp32 sum.
+#include <type_traits>
+
 #include "gemm_common.h"
 #include "layer.h"
+#include "topk.h"
 
 namespace moe {
 
 namespace {
-
-constexpr int kRouterWaves = 8;
 
 struct RouterParams {
   const uint8_t* x;
@@ -26,113 +27,247 @@ struct RouterParams {
   int splits;    // workgroups that share a tile's K-steps
 };
 
-// Three bf16 terms of 8 fp32 values: each is the rounding of what the ones before leave.
+// Three bf16 terms of 8 fp32 values: the upper half of each word, then of what that
+// leaves, then the rest (24 significand bits are 3 x 8, so nothing is lost).  An
+// infinite weight is its first term alone; a NaN reaches the second.
+MOE_DEV uint32_t high_halves(float lo, float hi) {  // (bf16 of lo, bf16 of hi), truncated
+  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+MOE_DEV float high_half(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
 MOE_DEV void split3(const f32x4 a, const f32x4 b, i32x4 (&o)[3]) {
-  float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 #pragma unroll
-  for (int s = 0; s < 3; ++s)
+  for (int q = 0; q < 4; ++q) {
+    float r[2], s[2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t r = bf16x2_rne(v[2 * q], v[2 * q + 1]);
-      o[s][q] = (int)r;
-      const float lo = __uint_as_float(r << 16), hi = __uint_as_float(r & 0xFFFF0000u);
-      // an infinite or NaN weight is its first term alone
-      v[2 * q] = s > 0 || fabsf(lo) < INFINITY ? v[2 * q] - lo : 0.0f;
-      v[2 * q + 1] = s > 0 || fabsf(hi) < INFINITY ? v[2 * q + 1] - hi : 0.0f;
+    for (int i = 0; i < 2; ++i) {
+      const float h = high_half(v[2 * q + i]);
+      r[i] = v[2 * q + i] == h ? 0.0f : v[2 * q + i] - h;
+      s[i] = r[i] - high_half(r[i]);
     }
+    o[0][q] = (int)high_halves(v[2 * q], v[2 * q + 1]);
+    o[1][q] = (int)high_halves(r[0], r[1]);
+    o[2][q] = (int)high_halves(s[0], s[1]);
+  }
 }
 
-// A workgroup computes 16 MT tokens x 16 NT experts; its waves (and the workgroups
-// of a split) take every kRouterWaves-th K-step of 64, and their sums are added
-// in wave order.
-template <int MT, int NT, bool W32>
-__global__ __launch_bounds__(64 * kRouterWaves) void router_mfma_kernel(RouterParams p) {
-  constexpr int kFrag = W32 ? 2 : 1;  // 16-byte pieces of 8 weights
-  __shared__ f32x4 red[kRouterWaves][MT * NT][64];
-  const int tid = threadIdx.x, lane = lane_id(), g = lane >> 4, r16 = lane & 15;
+// ---------------------------------------------------------------- few tokens
+// A workgroup per expert, TT >= T tokens: dot products in fp32 on rows read
+// in whole lines by all four waves.
+template <int TT, bool W32>
+__global__ __launch_bounds__(256) void router_dot_kernel(RouterParams p) {
+  __shared__ float part[4][TT];
+  const int tid = threadIdx.x, e = blockIdx.x, C = p.H >> 3;
+  float acc[TT] = {};
+  for (int c = tid; c < C; c += 256) {
+    float w[8];
+    if constexpr (W32) {
+      const f32x4* q = (const f32x4*)((const float*)p.w + (size_t)e * p.H + c * 8);
+      const f32x4 a = q[0], b = q[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = a[i], w[4 + i] = b[i];
+    } else {
+      const i32x4 a = *(const i32x4*)((const uint16_t*)p.w + (size_t)e * p.H + c * 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[2 * i] = __uint_as_float((uint32_t)a[i] << 16);
+        w[2 * i + 1] = __uint_as_float((uint32_t)a[i] & 0xFFFF0000u);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      // (past the last token: the last one again, not stored)
+      const i32x4 x = *(const i32x4*)((const uint16_t*)p.x + (size_t)min(t, p.T - 1) * p.H + c * 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[t] = fmaf(__uint_as_float((uint32_t)x[i] << 16), w[2 * i], acc[t]);
+        acc[t] = fmaf(__uint_as_float((uint32_t)x[i] & 0xFFFF0000u), w[2 * i + 1], acc[t]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const float s = wave_sum_f32(acc[t]);
+    if ((tid & 63) == 0) part[tid >> 6][t] = s;
+  }
+  __syncthreads();
+  if (tid < TT && tid < p.T)
+    p.out[(size_t)tid * p.E + e] = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+}
+
+// ---------------------------------------------------------------- tiles
+// A workgroup computes BM tokens x BN experts.  Rows of x and W are staged in LDS by
+// direct-to-LDS loads of whole 128-byte lines (8 lanes a line: MFMA-order loads straight
+// into registers put every lane of a quarter wave on another line and ran at 17 bytes per
+// cycle and CU), 16-byte chunks XOR-swizzled by row, K-step 64, STG buffers.
+// WT waves share a stage, each its part of the tile (1: a wave on its own, no
+// barriers); WK such groups, and the workgroups of a split, take the K-steps in
+// turn, and their sums are added in order.
+template <int BM, int BN, int WT, int WK, int STG, bool W32>
+struct RouterTile {
+  static constexpr int kF = W32 ? 2 : 1;
+  static constexpr int kXBytes = BM * 128, kStage = kXBytes + BN * 128 * kF;
+  static constexpr int kThreads = 64 * WT * WK;
+  static constexpr int kLds = WK * STG * kStage;
+  static constexpr int kLoads = (BM * 8 + BN * 8 * kF) / (64 * WT);  // per lane and stage
+};
+// (rows r and r + 16 of a 32-row operand are read together: they take different chunks too)
+template <int B>
+MOE_HOST_DEV constexpr int router_swz(int r) {
+  return (r & 7) ^ (B >= 32 ? (r >> 4) & 1 : 0);
+}
+
+template <int BM, int BN, int WT, int WK, int STG, bool REMAP, bool W32>
+__global__ __launch_bounds__(64 * WT * WK) void router_tile_kernel(RouterParams p) {
+  using TL = RouterTile<BM, BN, WT, WK, STG, W32>;
+  constexpr int F = TL::kF;
+  constexpr bool k32 = BM >= 32;           // 32x32x16 MFMA, else 16x16x32
+  constexpr int WM = WT >= 4 ? 2 : 1, WN = WT / WM;  // waves over the tile
+  constexpr int R = k32 ? 32 : 16;
+  constexpr int MT = BM / WM / R, NT = BN / WN / R;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[TL::kLds];
+  const int tid = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x % p.splits, tile = blockIdx.x / p.splits;
-  const int t0 = tile / p.n_tiles * (16 * MT), e0 = tile % p.n_tiles * (16 * NT);
-  const uint32_t xrow = (uint32_t)p.H * 2, wrow = (uint32_t)p.H * (W32 ? 4 : 2);
-  const __amdgpu_buffer_rsrc_t x_rs = make_rsrc(p.x + (size_t)t0 * xrow, (uint32_t)min(16 * MT, p.T - t0) * xrow);
-  const __amdgpu_buffer_rsrc_t w_rs = make_rsrc(p.w + (size_t)e0 * wrow, (uint32_t)min(16 * NT, p.E - e0) * wrow);
-  uint32_t xo[MT], wo[NT];  // rows past the last one lie past the resource: zeros
+  const int kg = wave / WT, wt = wave % WT, gl = wt * 64 + lane;  // K group, wave and lane of it
+  // (REMAP: neighbouring tiles, which share rows of x, on one XCD's L2)
+  const int id = REMAP ? xcd_remap(blockIdx.x, gridDim.x) : (int)blockIdx.x;
+  const int split = id % p.splits, tile = id / p.splits;
+  const int t0 = tile / p.n_tiles * BM, e0 = tile % p.n_tiles * BN;
+  const uint32_t xrow = (uint32_t)p.H * 2, wrow = (uint32_t)p.H * 2 * F;
+  // rows past the last one lie past the resource: zeros
+  const __amdgpu_buffer_rsrc_t x_rs = make_rsrc(p.x + (size_t)t0 * xrow, (uint32_t)min(BM, p.T - t0) * xrow);
+  const __amdgpu_buffer_rsrc_t w_rs = make_rsrc(p.w + (size_t)e0 * wrow, (uint32_t)min(BN, p.E - e0) * wrow);
+  uint8_t* mine = lds + kg * STG * TL::kStage;
+
+  auto issue = [&](int k, int buf) {
+    const uint32_t dead = oob_if(k >= p.steps);
+    const bool half = k * 64 + 32 >= p.H;  // H is a multiple of 32: the last K-step may hold 32 elements
+    uint8_t* base = mine + buf * TL::kStage;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) xo[m] = (uint32_t)(16 * m + r16) * xrow + 16u * g;
+    for (int i = 0; i < BM * 8 / (64 * WT); ++i) {
+      const int s = i * 64 * WT + gl, row = s >> 3, c = (s & 7) ^ router_swz<BM>(row);
+      lds_load16(x_rs, base + (i * 64 * WT + wt * 64) * 16, ((uint32_t)row * xrow + 16u * c) | dead | oob_if(half && c >= 4),
+                 (uint32_t)k * 128u);
+    }
 #pragma unroll
-  for (int n = 0; n < NT; ++n) wo[n] = (uint32_t)(16 * n + r16) * wrow + 16u * kFrag * g;
-  f32x4 acc[MT][NT];
+    for (int i = 0; i < BN * 8 * F / (64 * WT); ++i) {
+      const int s = i * 64 * WT + gl, row = s / (8 * F), q = s % (8 * F), c = (q & 8) | ((q & 7) ^ router_swz<BN>(row));
+      lds_load16(w_rs, base + TL::kXBytes + (i * 64 * WT + wt * 64) * 16,
+                 ((uint32_t)row * wrow + 16u * c) | dead | oob_if(half && c >= 4 * F), (uint32_t)k * 128u * F);
+    }
+  };
+  typedef float accv __attribute__((ext_vector_type(k32 ? 16 : 4)));
+  accv acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  struct Stage {
-    i32x4 x[MT][2], w[NT][2][kFrag];
-  };
-  auto load = [&](Stage& s, int k) {
-    const uint32_t dead = oob_if(k >= p.steps);
-    // H is a multiple of 32: the last K-step may hold 32 elements
-    const uint32_t dead2 = oob_if(k * 64 + 32 >= p.H) | dead;
+    for (int n = 0; n < NT; ++n) acc[m][n] = accv{};
+  const int r = lane % R, g = lane / R;  // operand row, K group of the lane
+  const int m0 = wt / WN * (BM / WM), n0 = wt % WN * (BN / WN);
+  auto mul = [&](int buf) {
+    const uint8_t* xb = mine + buf * TL::kStage;
+    const uint8_t* wb = xb + TL::kXBytes;
+    constexpr int kSub = k32 ? 4 : 2, kG = k32 ? 2 : 4;  // MFMAs of a K-step, lanes of a row
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      s.x[m][0] = bload16(x_rs, xo[m] | dead, (uint32_t)k * 128u);
-      s.x[m][1] = bload16(x_rs, (xo[m] + 64u) | dead2, (uint32_t)k * 128u);
-    }
+    for (int sub = 0; sub < kSub; ++sub) {
+      const int c = kG * sub + g;  // the lane's 8 elements
+      i32x4 xf[MT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int f = 0; f < kFrag; ++f) {
-        s.w[n][0][f] = bload16(w_rs, (wo[n] + 16u * f) | dead, (uint32_t)k * 128u * kFrag);
-        s.w[n][1][f] = bload16(w_rs, (wo[n] + 64u * kFrag + 16u * f) | dead2, (uint32_t)k * 128u * kFrag);
+      for (int m = 0; m < MT; ++m) {
+        const int row = m0 + m * R + r;
+        xf[m] = *(const i32x4*)(xb + row * 128 + ((c ^ router_swz<BM>(row)) << 4));
       }
-  };
-  auto mul = [&](const Stage& s) {
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        const int row = n0 + n * R + r, sw = router_swz<BN>(row);
         i32x4 wf[W32 ? 3 : 1];
         if constexpr (W32) {
-          split3(__builtin_bit_cast(f32x4, s.w[n][hh][0]), __builtin_bit_cast(f32x4, s.w[n][hh][1]), wf);
+          const int c0 = 2 * c, c1 = 2 * c + 1;
+          const uint8_t* at = wb + row * 256;
+          split3(*(const f32x4*)(at + (((c0 & 8) | ((c0 & 7) ^ sw)) << 4)),
+                 *(const f32x4*)(at + (((c1 & 8) | ((c1 & 7) ^ sw)) << 4)), wf);
         } else {
-          wf[0] = s.w[n][hh][0];
+          wf[0] = *(const i32x4*)(wb + row * 128 + ((c ^ sw) << 4));
         }
 #pragma unroll
         for (int q = (W32 ? 2 : 0); q >= 0; --q)  // the smallest term first
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-            acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wf[q]),
-                                                                __builtin_bit_cast(bf16x8, s.x[m][hh]), acc[m][n], 0, 0, 0);
+          for (int m = 0; m < MT; ++m) {
+            const bf16x8 a = __builtin_bit_cast(bf16x8, wf[q]), b = __builtin_bit_cast(bf16x8, xf[m]);
+            if constexpr (k32) acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[m][n], 0, 0, 0);
+            else acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc[m][n], 0, 0, 0);
+          }
       }
+    }
   };
-  const int stride = kRouterWaves * p.splits;
-  int k = split * kRouterWaves + wave;
-  Stage a, b;
-  load(a, k);
-  while (k < p.steps) {
-    load(b, k + stride);
-    mul(a);
-    load(a, k + 2 * stride);
-    mul(b);
-    k += 2 * stride;
+  const int stride = WK * p.splits;
+  int k = split * WK + kg;
+#pragma unroll
+  for (int s = 0; s < STG - 1; ++s) issue(k + s * stride, s);
+  // Every wave of the workgroup runs the same number of trips.  A stage's loads have landed when
+  // only those of the STG - 2 later stages are outstanding (the counter retires in order); the
+  // barrier publishes it to the group and frees the buffer read one stage earlier.
+  const int trips = (p.steps - split * WK + stride - 1) / stride;
+  for (int i = 0; i < trips; i += STG) {
+#pragma unroll
+    for (int s = 0; s < STG; ++s) {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((STG - 2) * TL::kLoads));
+      if constexpr (WT > 1) __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      issue(k + (STG - 1) * stride, (s + STG - 1) % STG);
+      __builtin_amdgcn_sched_barrier(0);
+      mul(s);
+      k += stride;
+    }
   }
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) red[wave][m * NT + n][lane] = acc[m][n];
-  __syncthreads();
-  // lane l of tile (m, n): token 16 m + l % 16, experts 16 n + 4 (l / 16) ...
+  __builtin_amdgcn_s_waitcnt(0);  // the trailing loads (zeros) have landed
+  // lane l of a tile: token l % R, experts 8 (i / 4) + 4 (l / 32) + i % 4 (32x32) or 4 (l / 16) + i (16x16)
   float* out = p.out + (size_t)split * p.T * p.E;
-  for (int i = tid; i < MT * NT * 64; i += 64 * kRouterWaves) {
-    const int mn = i >> 6, l = i & 63;
-    f32x4 s = red[0][mn][l];
+  constexpr int Q = k32 ? 4 : 1;  // runs of 4 experts per lane
+  auto store = [&](int m, int n, int q, f32x4 v) {
+    const int t = t0 + m0 + m * R + r, e = e0 + n0 + n * R + 8 * q + 4 * g;
+    if (t >= p.T) return;
+    float* at = out + (size_t)t * p.E + e;
+    if (e + 3 < p.E && (p.E & 3) == 0) {
+      *(f32x4*)at = v;
+    } else {
 #pragma unroll
-    for (int w = 1; w < kRouterWaves; ++w) s += red[w][mn][l];
-    const int t = t0 + mn / NT * 16 + (l & 15), e = e0 + mn % NT * 16 + 4 * (l >> 4);
-    if (t >= p.T) continue;
+      for (int j = 0; j < 4; ++j)
+        if (e + j < p.E) at[j] = v[j];
+    }
+  };
+  if constexpr (WK == 1) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (e + q < p.E) out[(size_t)t * p.E + e + q] = s[q];
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          store(m, n, q, f32x4{acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]});
+  } else {
+    static_assert(WK * BM * BN * 4 <= TL::kLds, "the sums fit the stages' space");
+    __syncthreads();
+    f32x4* red = (f32x4*)lds;  // [WK][WT][MT][NT][Q][64]
+    constexpr int kRuns = MT * NT * Q;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          red[(wave * kRuns + (m * NT + n) * Q + q) * 64 + lane] =
+              f32x4{acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
+    __syncthreads();
+    // each group finishes its share of the runs
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      if (i % WK != kg) continue;
+      f32x4 v = red[(wt * kRuns + i) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < WK; ++w) v += red[((w * WT + wt) * kRuns + i) * 64 + lane];
+      store(i / Q / NT, i / Q % NT, i % Q, v);
+    }
   }
 }
 
@@ -147,10 +282,25 @@ __global__ __launch_bounds__(256) void router_sum_kernel(const float* __restrict
 }
 
 struct RouterPlan {
-  int tile;  // tokens and experts of a tile: 16, 32 or 64
+  int kind;  // 0: dot products, 16 and 32: square tiles of one wave per K group, 64: 64 x 128 tiles
   int splits;
 };
-RouterPlan router_plan(int, int, int) { return RouterPlan{16, 1}; }
+// The smallest tile that leaves no CU a second workgroup (small tiles have the most
+// bytes per flop and the shortest way through K).  Measured, bf16, H 7168, E 256:
+//   T 1: dot 2.6 us, 16-tiles 5.8; T 4: 3.2 / 5.8; T 8: 7.2 / 5.8
+//   T 256 (256 / 64 / 8 workgroups): 16-tiles 7.7 us, 32-tiles 12.6, 64-tiles 38
+//   T 1024: 16-tiles 22 us, 32-tiles 12.8, 64-tiles in 4 splits 15.5
+//   T 2048: 32-tiles 24 us, 64-tiles in 4 splits 18.2; T 8192: 123 and (1 split) 51
+// With E <= 32 a 32-tile reads x once as it is: T 8192, E 32: 23.5 us against 27.
+RouterPlan router_plan(int T, int H, int E) {
+  if (T <= 4) return RouterPlan{0, 1};
+  auto tiles = [&](int m, int n) { return (long long)((T + m - 1) / m) * ((E + n - 1) / n); };
+  if (tiles(16, 16) <= 256) return RouterPlan{16, 1};
+  if (tiles(32, 32) <= 256 || E <= 32) return RouterPlan{32, 1};
+  int splits = 1;
+  while (splits < 8 && tiles(64, 128) * splits * 2 <= 256 && splits * 16 * 64 <= H) splits *= 2;
+  return RouterPlan{64, splits};
+}
 
 }  // namespace
 
@@ -162,12 +312,30 @@ size_t router_workspace_bytes(int T, int H, int E) {
 hipError_t launch_router_logits(const RouterArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
   const RouterPlan r = router_plan(a.T, a.H, a.E);
-  const int m_tiles = (a.T + r.tile - 1) / r.tile, n_tiles = (a.E + r.tile - 1) / r.tile;
-  RouterParams p{(const uint8_t*)a.x, (const uint8_t*)a.w, r.splits > 1 ? a.partial : a.logits, a.T, a.H, a.E, n_tiles,
+  RouterParams p{(const uint8_t*)a.x, (const uint8_t*)a.w, r.splits > 1 ? a.partial : a.logits, a.T, a.H, a.E, 0,
                  (a.H + 63) / 64, r.splits};
-  const dim3 grid((unsigned)(m_tiles * n_tiles * r.splits)), block(64 * kRouterWaves);
-  if (a.w_f32) hipLaunchKernelGGL((router_mfma_kernel<1, 1, true>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((router_mfma_kernel<1, 1, false>), grid, block, 0, s, p);
+  if (r.kind == 0) {
+    auto go = [&](auto tt) {
+      constexpr int TT = decltype(tt)::value;
+      const dim3 grid((unsigned)a.E);
+      if (a.w_f32) hipLaunchKernelGGL((router_dot_kernel<TT, true>), grid, dim3(256), 0, s, p);
+      else hipLaunchKernelGGL((router_dot_kernel<TT, false>), grid, dim3(256), 0, s, p);
+    };
+    if (a.T == 1) go(std::integral_constant<int, 1>{});
+    else if (a.T == 2) go(std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 4>{});
+    return hipGetLastError();
+  }
+  const int bm = r.kind, bn = r.kind == 64 ? 128 : r.kind;
+  p.n_tiles = (a.E + bn - 1) / bn;
+  const dim3 grid((unsigned)((a.T + bm - 1) / bm * p.n_tiles * r.splits));
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, p); };
+  if (r.kind == 16)
+    a.w_f32 ? go(router_tile_kernel<16, 16, 1, 4, 4, false, true>) : go(router_tile_kernel<16, 16, 1, 4, 4, false, false>);
+  else if (r.kind == 32)
+    a.w_f32 ? go(router_tile_kernel<32, 32, 1, 4, 3, true, true>) : go(router_tile_kernel<32, 32, 1, 4, 4, true, false>);
+  else
+    a.w_f32 ? go(router_tile_kernel<64, 128, 4, 1, 3, true, true>) : go(router_tile_kernel<64, 128, 4, 1, 4, true, false>);
   if (r.splits > 1) {
     const size_t n = (size_t)a.T * a.E;
     hipLaunchKernelGGL(router_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.partial, a.logits, n,
