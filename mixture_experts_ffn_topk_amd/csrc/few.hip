@@ -8,17 +8,17 @@
 // The same operator as moe_forward on the same prepared weights, for batches so
 // small that the step is one pass over the active experts' weights.  What differs
 // from the grouped GEMMs:
-//   * Columns are tokens, not gathered rows: the weights are the first MFMA
-//     operand (16 rows), the second is a 16-token slice in which the tokens not
-//     routed to the expert are zeros.  A token's outputs of all experts then
-//     share a lane, so the down launch sums the experts in registers: no plan, no
-//     y rows, no combine launch.
+//   * The weights are the first MFMA operand (16 rows), an expert's tokens (in token
+//     order, found from one 32-bit mask per expert in LDS) the 16 columns of the
+//     second: no plan, no gathered rows.  An expert with more than 16 tokens is two
+//     units of work that read its weights twice.
 //   * Weights go straight from HBM into registers, each byte read once, non-temporal,
 //     and nothing is staged in LDS: a wave is on its own until its sums are complete.
 //   * gate_up: a wave owns 16 columns of h (MX: 32, one scale block) of one expert,
 //     or 1/KSP of their K-steps where that would leave the part underfilled.
 //   * down: a workgroup owns 16 R output columns and all experts; its waves split
-//     the (expert, K-step) sequence evenly.
+//     the (unit, K-step) sequence evenly and add each unit's result to their own
+//     sums per token in LDS: no y rows, no combine launch.
 //   * The FP8 intermediate needs the maximum over 128 columns.  Where whole 128-column
 //     blocks make enough workgroups, the eight waves of a gate_up workgroup hold one
 //     block and quantise it; otherwise (one token, small I) h stays fp32 between the
@@ -40,7 +40,11 @@ namespace {
 
 constexpr int kFewMaxPairs = kFewMaxTokens * 32;  // num_topk <= 32
 constexpr int kFewMaxExperts = 1024;
-constexpr int kDownWaves = 8;
+// (an expert with more than 16 of T <= 32 tokens is two units: at most one such per 17 pairs)
+constexpr int kFewMaxUnits = kFewMaxExperts + kFewMaxPairs / 17;
+constexpr int few_max_units(int E, int T, int topk) {
+  return (E < T * topk ? E : T * topk) + (T > 16 ? T * topk / 17 : 0);
+}
 // FP8: the most bytes of h (with 16 spare ones per row) that the down launch quantises into LDS: two
 // workgroups still share a CU.
 constexpr int kFewLdsH = 48 * 1024;
@@ -193,16 +197,16 @@ MOE_DEV f32x4 mma_step(const WFrag<F>& w, const XFrag<F, GATEUP>& x, f32x4 acc) 
 
 // ---------------------------------------------------------------- routing in LDS
 struct RouteLds {
-  short ids[kFewMaxPairs];             // expert of each pair, -1: no valid expert
-  uint32_t bits[kFewMaxExperts / 32];  // the active experts
+  short ids[kFewMaxPairs];        // expert of each pair, -1: no valid expert
+  uint32_t mask[kFewMaxExperts];  // the tokens of each expert
 };
 
-// The pairs' experts and the active set, by the whole workgroup (ends with a barrier).
-// logits given (gate_up): each wave routes tokens wave, wave + WAVES, ...; workgroup 0 stores the result.
+// The pairs' experts and the experts' tokens, by the whole workgroup (ends with a barrier).
+// from_logits (gate_up): each wave routes tokens wave, wave + WAVES, ...; workgroup 0 stores the result.
 template <int WAVES>
 MOE_DEV void route_to_lds(const FewParams& p, RouteLds& L, bool from_logits) {
   const int tid = threadIdx.x, lane = lane_id(), np = p.T * p.topk;
-  if (tid < kFewMaxExperts / 32) L.bits[tid] = 0;
+  for (int e = tid; e < p.E; e += 64 * WAVES) L.mask[e] = 0;
   __syncthreads();
   if (from_logits) {
     for (int t = tid >> 6; t < p.T; t += WAVES) {
@@ -214,7 +218,7 @@ MOE_DEV void route_to_lds(const FewParams& p, RouteLds& L, bool from_logits) {
       if (lane < p.topk) {
         const int q = t * p.topk + lane;
         L.ids[q] = (short)e;
-        atomicOr(&L.bits[e >> 5], 1u << (e & 31));
+        atomicOr(&L.mask[e], 1u << t);
         if (blockIdx.x == 0) {
           if (p.idx64_out != nullptr) p.idx64_out[q] = e;
           else p.idx32_out[q] = e;
@@ -227,30 +231,33 @@ MOE_DEV void route_to_lds(const FewParams& p, RouteLds& L, bool from_logits) {
       const long long v = p.ids64 ? ((const long long*)p.ids)[q] : (long long)((const int*)p.ids)[q];
       const bool ok = v >= 0 && v < p.E;
       L.ids[q] = ok ? (short)v : (short)-1;
-      if (ok) atomicOr(&L.bits[(int)v >> 5], 1u << ((int)v & 31));
+      if (ok) atomicOr(&L.mask[(int)v], 1u << (q / p.topk));
     }
   }
   __syncthreads();
 }
-// Active experts before word `lane` (lanes 0..31) of the active set, and in it.
-MOE_DEV int active_before(const RouteLds& L, int& mine) {
-  const int lane = lane_id();
-  mine = lane < kFewMaxExperts / 32 ? __popc(L.bits[lane]) : 0;
-  int incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-  }
-  return incl - mine;
+MOE_DEV int bits_below(uint64_t b) {  // set bits of the lanes below this one
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(b >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)b, 0));
 }
-// The first slot of token t routed to expert e, -1 if none.
-MOE_DEV int slot_of(const RouteLds& L, int T, int topk, int t, int e) {
-  int slot = -1;
-  if (t < T)
-    for (int j = topk - 1; j >= 0; --j)
-      if (L.ids[t * topk + j] == e) slot = j;
-  return slot;
+// Units of work: an active expert, or each half of one with more than 16 tokens, in expert order.
+// Calls f(units before the lane's expert, the lane's expert, its units) for 64 experts at a time
+// until f returns true; returns the number of units seen.
+template <typename Fn>
+MOE_DEV int for_units(const RouteLds& L, int E, Fn f) {
+  int base = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane_id(), n = e < E ? __popc(L.mask[e]) : 0;
+    const uint64_t b1 = __ballot(n > 0), b2 = __ballot(n > 16);
+    if (f(base + bits_below(b1) + bits_below(b2), e, (n > 0 ? 1 : 0) + (n > 16 ? 1 : 0))) break;
+    base += __popcll(b1) + __popcll(b2);
+  }
+  return base;
+}
+// The token of the lane's column r of a unit (-1: none): the r-th (+ 16) of the expert's tokens.
+MOE_DEV int token_of(uint32_t mask, int half, int r) {
+  for (int i = half ? 16 : 0; i > 0; --i) mask &= mask - 1;
+  for (int i = r; i > 0; --i) mask &= mask - 1;
+  return mask != 0 ? __ffs(mask) - 1 : -1;
 }
 
 // ---------------------------------------------------------------- gate_up
@@ -291,46 +298,44 @@ MOE_DEV int e4m3x4(f32x4 v) {
   return __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false), true);
 }
 
-// NT: 16-token slices.  KSP: waves that share one slice of columns.  D: K-steps in flight per wave.
+// KSP: waves that share one slice of columns.  D: K-steps in flight per wave.
 // FP8: 8 waves hold (and quantise) a 128-column block, 4 leave h in fp32.
-template <Fmt F, int NT, int WAVES, int KSP, int D>
+template <Fmt F, int WAVES, int KSP, int D>
 __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   constexpr int CT = F == Fmt::MX ? 2 : 1;  // 16-column groups per wave
   constexpr int kSlices = WAVES / KSP;
   constexpr bool kBlock = F == Fmt::FP8 && WAVES == 8;
   static_assert(!kBlock || KSP == 1, "a wave of a block has its columns' whole sums");
   __shared__ RouteLds route;
-  __shared__ f32x4 red[KSP > 1 ? WAVES : 1][KSP > 1 ? CT * 2 * NT : 1][KSP > 1 ? 64 : 1];
-  __shared__ uint32_t amax[kBlock ? NT : 1][kBlock ? WAVES : 1][16];
+  __shared__ f32x4 red[KSP > 1 ? WAVES : 1][KSP > 1 ? CT * 2 : 1][KSP > 1 ? 64 : 1];
+  __shared__ uint32_t amax[kBlock ? WAVES : 1][16];
   const int tid = threadIdx.x, lane = lane_id(), g = lane >> 4, r16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   route_to_lds<WAVES>(p, route, p.logits != nullptr);
 
-  // this workgroup's expert: the a-th active one
+  // this workgroup's unit
   const int n_slices = p.I / (16 * CT), blocks = (n_slices + kSlices - 1) / kSlices;
   const int a = (int)blockIdx.x / blocks, slice = ((int)blockIdx.x % blocks) * kSlices + wave / KSP;
-  int mine;
-  const int before = active_before(route, mine);
-  const uint64_t hit = __ballot(lane < kFewMaxExperts / 32 && a >= before && a < before + mine);
-  if (hit == 0) return;  // (uniform: fewer active experts than workgroup rows)
-  const int word = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
-  uint32_t bits = route.bits[word];
-  for (int n = a - __shfl(before, word); n > 0; --n) bits &= bits - 1;
-  const int e = __builtin_amdgcn_readfirstlane(word * 32 + __ffs(bits) - 1);
+  int e = -1, half = 0;
+  for_units(route, p.E, [&](int before, int le, int n) {
+    const uint64_t hit = __ballot(a >= before && a < before + n);
+    if (hit == 0) return false;
+    const int src = __ffsll((unsigned long long)hit) - 1;
+    e = __builtin_amdgcn_readlane(le, src);
+    half = a - __builtin_amdgcn_readlane(before, src);
+    return true;
+  });
+  if (e < 0) return;  // (uniform: fewer units than workgroup rows)
 
-  // the slice's tokens
-  int slot[NT];
-  uint32_t xo[NT], xso[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int t = 16 * n + r16;
-    slot[n] = slot_of(route, p.T, p.topk, t, e);
-    // the lane's first byte of a K-step, as XFrag describes
-    const uint32_t at = F == Fmt::NV4 ? 128u * (g >> 1) + 16u * (g & 1) : F == Fmt::NVF4 ? 32u * (g >> 1) + 4u * (g & 1) : 16u * g;
-    const uint32_t sat = F == Fmt::MX ? (uint32_t)g : F == Fmt::NVF4 ? 4u * (g >> 1) : 0u;
-    xo[n] = slot[n] >= 0 ? (uint32_t)t * p.x_row + at : kOOB;
-    xso[n] = slot[n] >= 0 ? (uint32_t)t * p.x_sf_row + sat : kOOB;
-  }
+  // the lane's token, its first slot of this expert, and its first byte of a K-step, as XFrag describes
+  const int t = token_of(route.mask[e], half, r16);
+  int slot = 0;
+  if (t >= 0)
+    while (route.ids[t * p.topk + slot] != e) ++slot;  // (the mask says that there is one)
+  const uint32_t at = F == Fmt::NV4 ? 128u * (g >> 1) + 16u * (g & 1) : F == Fmt::NVF4 ? 32u * (g >> 1) + 4u * (g & 1) : 16u * g;
+  const uint32_t sat = F == Fmt::MX ? (uint32_t)g : F == Fmt::NVF4 ? 4u * (g >> 1) : 0u;
+  const uint32_t xo = t >= 0 ? (uint32_t)t * p.x_row + at : kOOB;
+  const uint32_t xso = t >= 0 ? (uint32_t)t * p.x_sf_row + sat : kOOB;
   const __amdgpu_buffer_rsrc_t x_rs = make_rsrc(p.x, (uint32_t)p.T * p.x_row);
   const __amdgpu_buffer_rsrc_t xs_rs = make_rsrc(p.x_sf, (uint32_t)p.T * p.x_sf_row);
   const __amdgpu_buffer_rsrc_t w_rs = make_rsrc(p.w + (size_t)e * p.w_expert, p.w_expert);
@@ -349,7 +354,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
 
   struct Stage {
     WFrag<F> w[CT][2];
-    XFrag<F, true> x[NT];
+    XFrag<F, true> x;
     float sg, su;
   } st[D];
   auto load = [&](Stage& s, int k) {
@@ -363,58 +368,50 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
       s.sg = sbg[kc];
       s.su = sbu[kc];
     }
+    const uint32_t o = xo | dead;
+    if constexpr (F == Fmt::FP8) {
+      s.x.v[0] = bload16(x_rs, o, (uint32_t)k * 128u);
+      s.x.v[1] = bload16(x_rs, o + 64u, (uint32_t)k * 128u);
+      s.x.s = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_rs, xso | dead, (uint32_t)k * 4u, 0);
+    } else if constexpr (F == Fmt::MX) {
+      // K tail: rows of any multiple of 32 elements
+      s.x.v[0] = bload16(x_rs, o | oob_if(k * 128 + 16 * g >= p.H), (uint32_t)k * 128u);
+      s.x.v[1] = bload16(x_rs, (o + 64u) | oob_if(k * 128 + 64 + 16 * g >= p.H), (uint32_t)k * 128u);
+      s.x.s = (int)__builtin_amdgcn_raw_buffer_load_b8(xs_rs, xso | dead | oob_if(k * 128 + 32 * g >= p.H), (uint32_t)k * 4u, 0);
+    } else if constexpr (F == Fmt::BF16) {
+      s.x.v[0] = bload16(x_rs, o, (uint32_t)k * 128u);
+      s.x.v[1] = bload16(x_rs, o + 64u, (uint32_t)k * 128u);
+    } else if constexpr (F == Fmt::NV4) {
+      const uint32_t o2 = o | oob_if(2 * k + (g >> 1) >= p.ksteps);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint32_t o = xo[n] | dead;
-      if constexpr (F == Fmt::FP8) {
-        s.x[n].v[0] = bload16(x_rs, o, (uint32_t)k * 128u);
-        s.x[n].v[1] = bload16(x_rs, o + 64u, (uint32_t)k * 128u);
-        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_rs, xso[n] | dead, (uint32_t)k * 4u, 0);
-      } else if constexpr (F == Fmt::MX) {
-        // K tail: rows of any multiple of 32 elements
-        s.x[n].v[0] = bload16(x_rs, o | oob_if(k * 128 + 16 * g >= p.H), (uint32_t)k * 128u);
-        s.x[n].v[1] = bload16(x_rs, (o + 64u) | oob_if(k * 128 + 64 + 16 * g >= p.H), (uint32_t)k * 128u);
-        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b8(
-            xs_rs, xso[n] | dead | oob_if(k * 128 + 32 * g >= p.H), (uint32_t)k * 4u, 0);
-      } else if constexpr (F == Fmt::BF16) {
-        s.x[n].v[0] = bload16(x_rs, o, (uint32_t)k * 128u);
-        s.x[n].v[1] = bload16(x_rs, o + 64u, (uint32_t)k * 128u);
-      } else if constexpr (F == Fmt::NV4) {
-        const uint32_t o2 = o | oob_if(2 * k + (g >> 1) >= p.ksteps);
+      for (int q = 0; q < 4; ++q) s.x.v[q] = bload16(x_rs, o2 + 32u * q, (uint32_t)k * 256u);
+    } else {
+      const uint32_t odd = oob_if(2 * k + (g >> 1) >= p.ksteps);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s.x[n].v[q] = bload16(x_rs, o2 + 32u * q, (uint32_t)k * 256u);
-      } else {
-        const uint32_t odd = oob_if(2 * k + (g >> 1) >= p.ksteps);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          s.x[n].v[0][q] = (int)__builtin_amdgcn_raw_buffer_load_b32(x_rs, (o | odd) + 8u * q, (uint32_t)k * 64u, 0);
-        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_rs, xso[n] | dead | odd, (uint32_t)k * 8u, 0);
-      }
+      for (int q = 0; q < 4; ++q)
+        s.x.v[0][q] = (int)__builtin_amdgcn_raw_buffer_load_b32(x_rs, (o | odd) + 8u * q, (uint32_t)k * 64u, 0);
+      s.x.s = (int)__builtin_amdgcn_raw_buffer_load_b32(xs_rs, xso | dead | odd, (uint32_t)k * 8u, 0);
     }
   };
-  f32x4 acc[CT][2][NT];
+  f32x4 acc[CT][2];
 #pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[c][u][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < 2; ++u) acc[c][u] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto mul = [&](const Stage& s) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int c = 0; c < CT; ++c)
 #pragma unroll
-      for (int c = 0; c < CT; ++c)
+      for (int u = 0; u < 2; ++u) {
+        if constexpr (F == Fmt::FP8) {
+          const float sc = __builtin_bit_cast(float, s.x.s) * (u ? s.su : s.sg);
+          const f32x4 part = mma_step<F, true>(s.w[c][u], s.x, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if constexpr (F == Fmt::FP8) {
-            const float sc = __builtin_bit_cast(float, s.x[n].s) * (u ? s.su : s.sg);
-            const f32x4 part = mma_step<F, true>(s.w[c][u], s.x[n], f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[c][u][n][i] = fmaf(part[i], sc, acc[c][u][n][i]);
-          } else {
-            acc[c][u][n] = mma_step<F, true>(s.w[c][u], s.x[n], acc[c][u][n]);
-          }
+          for (int i = 0; i < 4; ++i) acc[c][u][i] = fmaf(part[i], sc, acc[c][u][i]);
+        } else {
+          acc[c][u] = mma_step<F, true>(s.w[c][u], s.x, acc[c][u]);
         }
+      }
   };
   int k = wave % KSP;
 #pragma unroll
@@ -434,9 +431,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) red[wave][(c * 2 + u) * NT + n][lane] = acc[c][u][n];
+      for (int u = 0; u < 2; ++u) red[wave][c * 2 + u][lane] = acc[c][u];
     __syncthreads();
     if (wave % KSP != 0) return;
 #pragma unroll
@@ -444,89 +439,76 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int w = 1; w < KSP; ++w) acc[c][u][n] += red[wave + w][(c * 2 + u) * NT + n][lane];
+        for (int w = 1; w < KSP; ++w) acc[c][u] += red[wave + w][c * 2 + u][lane];
   }
   if (!live) return;  // (never in a block of FP8: I is a multiple of 128)
 
   // lane (g, token): columns col0 + 16 c + 4 g ... of the token's row
   const float gs = nv4w(F) ? p.w_gs[e] : 1.0f;
+  const size_t row = (size_t)max(t, 0) * p.topk + slot;
+  f32x4 h[CT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const size_t row = (size_t)(16 * n + r16) * p.topk + slot[n];
-    f32x4 h[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      f32x4 gt = acc[c][0][n], up = acc[c][1][n];
-      if constexpr (nv4w(F)) gt *= gs, up *= gs;
-      h[c] = swiglu4(gt, up, p.clamp, p.fast);
-    }
-    if constexpr (kBlock) {
-      const uint32_t m = max_over_g(amax_bits4(h[0]));
-      if (g == 0) amax[n][wave][r16] = m;
-      acc[0][0][n] = h[0];  // quantised below, once all the waves' maxima are there
-    } else if constexpr (F == Fmt::FP8) {
-      if (slot[n] >= 0) *(f32x4*)((float*)p.h + row * p.I + col0 + 4 * g) = h[0];
-    } else if constexpr (F == Fmt::MX) {
-      const uint32_t m = max_over_g(max(amax_bits4(h[0]), amax_bits4(h[1])));
-      const int ex = mx_exponent_for_amax(__uint_as_float(m));
-      const float inv = exp2i(-ex);
-      if (slot[n] >= 0) {
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-          *(uint32_t*)((uint8_t*)p.h + row * p.I + col0 + 16 * c + 4 * g) =
-              f32x2_to_e4m3_sat(h[c][0] * inv, h[c][1] * inv) | f32x2_to_e4m3_sat(h[c][2] * inv, h[c][3] * inv) << 16;
-        // (a NaN in the block: UE8M0's NaN)
-        if (g == 0) ((uint8_t*)p.h_sf)[row * (p.I / 32) + slice] = m > 0x7F800000u ? (uint8_t)255 : (uint8_t)(ex + 127);
-      }
-    } else {
-      f32x4 v = h[0];
-      if constexpr (F == Fmt::NVF4) {
-        // block scale E4M3(amax / (6 c)), codes E2M1(h / (scale c)); kept as code x scale, exact in bf16
-        const uint32_t m = max_over_g(amax_bits4(v));
-        const float c = p.c_gs[e], s6 = __uint_as_float(m) / (6.0f * c);
-        const float sc = e4m3_byte<0>(__builtin_amdgcn_cvt_pk_fp8_f32(s6 > 448.0f ? 448.0f : s6, 0.0f, 0, false));
-        const float den = sc * c, inv = den > 0.0f ? 1.0f / den : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = e2m1_rne_sat(v[i] * inv) * sc;  // (a NaN in the block: sc is NaN)
-      }
-      if (slot[n] >= 0)
-        *(uint2*)((uint16_t*)p.h + row * p.I + col0 + 4 * g) = uint2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
-    }
+  for (int c = 0; c < CT; ++c) {
+    f32x4 gt = acc[c][0], up = acc[c][1];
+    if constexpr (nv4w(F)) gt *= gs, up *= gs;
+    h[c] = swiglu4(gt, up, p.clamp, p.fast);
   }
   if constexpr (kBlock) {
+    const uint32_t mw = max_over_g(amax_bits4(h[0]));
+    if (g == 0) amax[wave][r16] = mw;
     __syncthreads();
+    uint32_t m = 0;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      uint32_t m = 0;
+    for (int w = 0; w < WAVES; ++w) m = max(m, amax[w][r16]);
+    float inv;
+    const float sc = fp8_scale(m, inv);
+    if (t < 0) return;
+    *(int*)((uint8_t*)p.h + row * p.I + col0 + 4 * g) = e4m3x4(h[0] * inv);
+    if (wave == 0 && g == 0) ((float*)p.h_sf)[row * (p.I / 128) + col0 / 128] = sc;
+  } else if constexpr (F == Fmt::FP8) {
+    if (t >= 0) *(f32x4*)((float*)p.h + row * p.I + col0 + 4 * g) = h[0];
+  } else if constexpr (F == Fmt::MX) {
+    const uint32_t m = max_over_g(max(amax_bits4(h[0]), amax_bits4(h[1])));
+    const int ex = mx_exponent_for_amax(__uint_as_float(m));
+    const float inv = exp2i(-ex);
+    if (t < 0) return;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) m = max(m, amax[n][w][r16]);
-      float inv;
-      const float sc = fp8_scale(m, inv);
-      if (slot[n] < 0) continue;
-      const size_t row = (size_t)(16 * n + r16) * p.topk + slot[n];
-      const f32x4 q = acc[0][0][n] * inv;
-      *(int*)((uint8_t*)p.h + row * p.I + col0 + 4 * g) = e4m3x4(q);
-      if (wave == 0 && g == 0) ((float*)p.h_sf)[row * (p.I / 128) + col0 / 128] = sc;
+    for (int c = 0; c < CT; ++c)
+      *(uint32_t*)((uint8_t*)p.h + row * p.I + col0 + 16 * c + 4 * g) =
+          f32x2_to_e4m3_sat(h[c][0] * inv, h[c][1] * inv) | f32x2_to_e4m3_sat(h[c][2] * inv, h[c][3] * inv) << 16;
+    // (a NaN in the block: UE8M0's NaN)
+    if (g == 0) ((uint8_t*)p.h_sf)[row * (p.I / 32) + slice] = m > 0x7F800000u ? (uint8_t)255 : (uint8_t)(ex + 127);
+  } else {
+    f32x4 v = h[0];
+    if constexpr (F == Fmt::NVF4) {
+      // block scale E4M3(amax / (6 c)), codes E2M1(h / (scale c)); kept as code x scale, exact in bf16
+      const uint32_t m = max_over_g(amax_bits4(v));
+      const float c = p.c_gs[e], s6 = __uint_as_float(m) / (6.0f * c);
+      const float sc = e4m3_byte<0>(__builtin_amdgcn_cvt_pk_fp8_f32(s6 > 448.0f ? 448.0f : s6, 0.0f, 0, false));
+      const float den = sc * c, inv = den > 0.0f ? 1.0f / den : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = e2m1_rne_sat(v[i] * inv) * sc;  // (a NaN in the block: sc is NaN)
     }
+    if (t >= 0)
+      *(uint2*)((uint16_t*)p.h + row * p.I + col0 + 4 * g) = uint2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
   }
 }
 
 // ---------------------------------------------------------------- down
 // R: 16-row weight tiles (output column groups) per workgroup.  HL (FP8): h is fp32 and
 // quantised into LDS here.
-template <Fmt F, int NT, int R, int D, bool HL>
-__global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewParams p) {
+template <Fmt F, int WAVES, int R, int D, bool HL>
+__global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
   static_assert(!HL || F == Fmt::FP8, "only FP8 leaves h in fp32");
   struct Lds {
     RouteLds route;
     float w[kFewMaxPairs];
-    short act[kFewMaxExperts];
-    int n_act;
+    short unit[kFewMaxUnits];  // expert, + kHalf: its second 16 tokens
+    int n_units;
   };
+  constexpr int kHalf = 0x4000;
   __shared__ Lds L;
-  __shared__ f32x4 red[kDownWaves][R * NT][64];
+  __shared__ f32x4 sum[WAVES][R][kFewMaxTokens][4];  // a wave's sums: token, rows 4 g ...
   // HL: 128 zero bytes, then the rows' codes (row stride I + 16: rows in other banks); their scales
   __shared__ __attribute__((aligned(16))) uint8_t hq[HL ? 128 + kFewLdsH : 16];
   __shared__ float hsc[HL ? kFewLdsH / 128 : 1];
@@ -536,7 +518,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewParams p) 
     // 16 lanes a 128-column block, 8 columns a lane (rows of masked slots hold anything and are not read)
     const int cpr = p.I / 8, n = p.T * p.topk * cpr;
     if (tid < 32) ((uint32_t*)hq)[tid] = 0;
-    for (int c = tid; c < n; c += 64 * kDownWaves) {
+    for (int c = tid; c < n; c += 64 * WAVES) {
       const f32x4 a = *(const f32x4*)((const float*)p.h + (size_t)c * 8), b = *(const f32x4*)((const float*)p.h + (size_t)c * 8 + 4);
       uint32_t m = max(amax_bits4(a), amax_bits4(b));
       m = dpp_max_u32<0xB1>(m);
@@ -550,21 +532,25 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewParams p) 
       if ((lane & 15) == 0) hsc[c >> 4] = sc;
     }
   }
-  for (int q = tid; q < p.T * p.topk; q += 64 * kDownWaves) L.w[q] = p.topk_w[q];
-  route_to_lds<kDownWaves>(p, L.route, false);
+  for (int q = tid; q < p.T * p.topk; q += 64 * WAVES) L.w[q] = p.topk_w[q];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    for (int i = lane; i < p.T * 4; i += 64) sum[wave][r][i >> 2][i & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
+  route_to_lds<WAVES>(p, L.route, false);
   if (wave == 0) {
-    int mine;
-    int at = active_before(L.route, mine);
-    if (lane < kFewMaxExperts / 32)
-      for (uint32_t b = L.route.bits[lane]; b != 0; b &= b - 1) L.act[at++] = (short)(lane * 32 + __ffs(b) - 1);
-    if (lane == kFewMaxExperts / 32 - 1) L.n_act = at;
+    const int n = for_units(L.route, p.E, [&](int before, int e, int units) {
+      if (units > 0) L.unit[before] = (short)e;
+      if (units > 1) L.unit[before + 1] = (short)(e | kHalf);
+      return false;
+    });
+    if (lane == 0) L.n_units = n;
   }
   __syncthreads();
 
-  // this wave's part of the (active expert, K-step) sequence
-  const int n_act = __builtin_amdgcn_readfirstlane(L.n_act);
-  const long long total = (long long)n_act * p.steps;
-  const int lo = (int)(total * wave / kDownWaves), hi = (int)(total * (wave + 1) / kDownWaves);
+  // this wave's part of the (unit, K-step) sequence
+  const int n_units = __builtin_amdgcn_readfirstlane(L.n_units);
+  const long long total = (long long)n_units * p.steps;
+  const int lo = (int)(total * wave / WAVES), hi = (int)(total * (wave + 1) / WAVES);
   const int rb0 = (int)blockIdx.x * R;  // first 16-row block
   const int n_rb = p.H / 16;
   WAddr<F> wa[R];
@@ -577,43 +563,41 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewParams p) 
   const __amdgpu_buffer_rsrc_t h_rs = make_rsrc(p.h, rows * h_row);
   const __amdgpu_buffer_rsrc_t hs_rs = make_rsrc(p.h_sf, rows * hs_row);
 
-  // the load side's position: expert, its resources, the tokens' rows and weights
-  int la = lo / p.steps, lk = lo % p.steps, lf = lo;
+  // the load side's position: unit, its expert's resources, the lane's token, row and router weight
+  int lu = lo / p.steps, lk = lo % p.steps, lf = lo;
   __amdgpu_buffer_rsrc_t w_rs, ws_rs;
   const float* sb = nullptr;
-  uint32_t ho[NT], hso[NT];
-  float wt[NT];
-  auto set_expert = [&]() {
-    const int e = __builtin_amdgcn_readfirstlane((int)L.act[min(la, max(n_act - 1, 0))]);
+  uint32_t ho, hso;
+  float wt;
+  int tok;
+  auto set_unit = [&]() {
+    const int u = __builtin_amdgcn_readfirstlane((int)L.unit[min(lu, n_units - 1)]), e = u & (kHalf - 1);
     w_rs = make_rsrc(p.w + (size_t)e * p.w_expert, p.w_expert);
     ws_rs = make_rsrc(p.w_sf + (size_t)e * p.w_sf_expert, p.w_sf_expert);
     if constexpr (F == Fmt::FP8)
       sb = (const float*)(p.w_sf + (size_t)e * p.w_sf_expert) + (size_t)(rb0 / 8) * p.ksteps;
-    const float gs = nv4w(F) ? p.w_gs[e] : 1.0f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int t = 16 * n + r16;
-      int slot = -1;
-      float s = 0.0f;  // a token that lists the expert twice weighs it by both, in slot order
-      if (t < p.T)
-        for (int j = 0; j < p.topk; ++j)
-          if (L.route.ids[t * p.topk + j] == e) {
-            s += L.w[t * p.topk + j];
-            if (slot < 0) slot = j;
-          }
-      wt[n] = s * gs;
-      const uint32_t row = (uint32_t)(t * p.topk + slot);
-      const uint32_t at = nv4w(F) ? 128u * (g >> 1) + 16u * (g & 1) : 16u * g;
-      ho[n] = slot >= 0 ? row * h_row + at : kOOB;
-      hso[n] = slot >= 0 ? row * hs_row + (F == Fmt::MX ? (uint32_t)g : 0u) : kOOB;
-    }
+    tok = token_of(L.route.mask[e], u & kHalf, r16);
+    int slot = -1;
+    wt = 0.0f;  // a token that lists the expert twice weighs it by both, in slot order
+    if (tok >= 0)
+      for (int j = 0; j < p.topk; ++j)
+        if (L.route.ids[tok * p.topk + j] == e) {
+          wt += L.w[tok * p.topk + j];
+          if (slot < 0) slot = j;
+        }
+    if constexpr (nv4w(F)) wt *= p.w_gs[e];
+    const uint32_t row = (uint32_t)(tok * p.topk + slot);
+    const uint32_t at = nv4w(F) ? 128u * (g >> 1) + 16u * (g & 1) : 16u * g;
+    ho = tok >= 0 ? row * h_row + at : kOOB;
+    hso = tok >= 0 ? row * hs_row + (F == Fmt::MX ? (uint32_t)g : 0u) : kOOB;
   };
   struct Stage {
     WFrag<F> w[R];
-    XFrag<F, false> x[NT];
-    float wt[NT], sb;
-    uint32_t off[NT], soff[NT];  // bit 31: not routed (or past the end); HL: the row's place in LDS
-    int k;
+    XFrag<F, false> x;
+    float wt, sb;
+    uint32_t off, soff;  // HL: the row's place in LDS
+    int k, tok;
+    bool last;  // of the unit, or of the wave's part
   } st[D];
   auto load = [&](Stage& s) {
     const uint32_t dead = oob_if(lf >= hi);
@@ -621,72 +605,78 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewParams p) 
 #pragma unroll
     for (int r = 0; r < R; ++r) w_load<F>(s.w[r], wa[r], w_rs, ws_rs, k, dead, p.ksteps, g);
     if constexpr (F == Fmt::FP8) s.sb = sb[k];
+    const uint32_t o = ho | dead;
+    s.wt = wt;
+    s.tok = tok;
+    if constexpr (HL) {
+      s.off = ho;
+      s.soff = hso;
+      s.k = k;
+    } else if constexpr (F == Fmt::FP8) {
+      s.x.v[0] = bload16(h_rs, o, (uint32_t)k * 128u);
+      s.x.v[1] = bload16(h_rs, o + 64u, (uint32_t)k * 128u);
+      s.x.s = (int)__builtin_amdgcn_raw_buffer_load_b32(hs_rs, hso | dead, (uint32_t)k * 4u, 0);
+    } else if constexpr (F == Fmt::MX) {
+      s.x.v[0] = bload16(h_rs, o | oob_if(k * 128 + 16 * g >= p.I), (uint32_t)k * 128u);
+      s.x.v[1] = bload16(h_rs, (o + 64u) | oob_if(k * 128 + 64 + 16 * g >= p.I), (uint32_t)k * 128u);
+      s.x.s = (int)__builtin_amdgcn_raw_buffer_load_b8(hs_rs, hso | dead | oob_if(k * 128 + 32 * g >= p.I), (uint32_t)k * 4u, 0);
+    } else if constexpr (F == Fmt::BF16) {
+      s.x.v[0] = bload16(h_rs, o, (uint32_t)k * 128u);
+      s.x.v[1] = bload16(h_rs, o + 64u, (uint32_t)k * 128u);
+    } else {
+      const uint32_t o2 = o | oob_if(2 * k + (g >> 1) >= p.ksteps);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint32_t o = ho[n] | dead;
-      s.wt[n] = wt[n];
-      s.off[n] = o;
-      if constexpr (HL) {
-        s.soff[n] = hso[n];
-        s.k = k;
-      } else if constexpr (F == Fmt::FP8) {
-        s.x[n].v[0] = bload16(h_rs, o, (uint32_t)k * 128u);
-        s.x[n].v[1] = bload16(h_rs, o + 64u, (uint32_t)k * 128u);
-        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b32(hs_rs, hso[n] | dead, (uint32_t)k * 4u, 0);
-      } else if constexpr (F == Fmt::MX) {
-        s.x[n].v[0] = bload16(h_rs, o | oob_if(k * 128 + 16 * g >= p.I), (uint32_t)k * 128u);
-        s.x[n].v[1] = bload16(h_rs, (o + 64u) | oob_if(k * 128 + 64 + 16 * g >= p.I), (uint32_t)k * 128u);
-        s.x[n].s = (int)__builtin_amdgcn_raw_buffer_load_b8(
-            hs_rs, hso[n] | dead | oob_if(k * 128 + 32 * g >= p.I), (uint32_t)k * 4u, 0);
-      } else if constexpr (F == Fmt::BF16) {
-        s.x[n].v[0] = bload16(h_rs, o, (uint32_t)k * 128u);
-        s.x[n].v[1] = bload16(h_rs, o + 64u, (uint32_t)k * 128u);
-      } else {
-        const uint32_t o2 = o | oob_if(2 * k + (g >> 1) >= p.ksteps);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) s.x[n].v[q] = bload16(h_rs, o2 + 32u * q, (uint32_t)k * 256u);
-      }
+      for (int q = 0; q < 4; ++q) s.x.v[q] = bload16(h_rs, o2 + 32u * q, (uint32_t)k * 256u);
     }
+    s.last = lf < hi && (lk + 1 == p.steps || lf + 1 == hi);
     ++lf;
     if (++lk == p.steps) {  // (uniform)
       lk = 0;
-      ++la;
-      set_expert();
+      ++lu;
+      set_unit();
     }
   };
-  f32x4 acc[R][NT];
+  f32x4 acc[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto mul = [&](Stage& s) {
+    float c = s.wt;
+    if constexpr (HL) {
+      const bool ok = s.tok >= 0;
+      const uint32_t at = ok ? 128u + s.off + (uint32_t)s.k * 128u : 16u * g;
+      s.x.v[0] = *(const i32x4*)(hq + at);
+      s.x.v[1] = *(const i32x4*)(hq + at + 64);
+      c *= hsc[ok ? s.soff + (uint32_t)s.k : 0u] * s.sb;
+    } else if constexpr (F == Fmt::FP8) {
+      c *= __builtin_bit_cast(float, s.x.s) * s.sb;
+    }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float c = s.wt[n];
-      if constexpr (HL) {
-        const bool ok = !(s.off[n] & kOOB);
-        const uint32_t at = ok ? 128u + s.off[n] + (uint32_t)s.k * 128u : 16u * g;
-        s.x[n].v[0] = *(const i32x4*)(hq + at);
-        s.x[n].v[1] = *(const i32x4*)(hq + at + 64);
-        c *= hsc[ok ? s.soff[n] + (uint32_t)s.k : 0u] * s.sb;
-      } else if constexpr (F == Fmt::FP8) {
-        c *= __builtin_bit_cast(float, s.x[n].s) * s.sb;
+    for (int r = 0; r < R; ++r) {
+      // FP8: each K-step's partial has its own scales; the others scale the unit's sum
+      if constexpr (F == Fmt::FP8) {
+        const f32x4 part = mma_step<F, false>(s.w[r], s.x, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(part[i], c, acc[r][i]);
+      } else {
+        acc[r] = mma_step<F, false>(s.w[r], s.x, acc[r]);
       }
-      const bool routed = !(s.off[n] & kOOB);
+    }
+    if (s.last) {  // (uniform)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const f32x4 part = mma_step<F, false>(s.w[r], s.x[n], f32x4{0.f, 0.f, 0.f, 0.f});
+        if (s.tok >= 0) {
+          f32x4& at = sum[wave][r][s.tok][g];
+          f32x4 v = at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // (an infinite or NaN weight times the zeros of a token that is not routed here stays out)
-          const float v = fmaf(part[i], c, acc[r][n][i]);
-          acc[r][n][i] = routed ? v : acc[r][n][i];
+          for (int i = 0; i < 4; ++i) v[i] = F == Fmt::FP8 ? v[i] + acc[r][i] : fmaf(acc[r][i], c, v[i]);
+          at = v;
         }
+        acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
     }
   };
   if (lo < hi) {  // (uniform per wave)
-    set_expert();
+    set_unit();
 #pragma unroll
     for (int d = 0; d < D; ++d) load(st[d]);
     for (int f = lo; f < hi; f += D) {
@@ -699,18 +689,14 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewParams p) 
       }
     }
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) red[wave][r * NT + n][lane] = acc[r][n];
   __syncthreads();
-  for (int i = tid; i < R * NT * 64; i += 64 * kDownWaves) {
-    const int rn = i >> 6, l = i & 63, t = 16 * (rn % NT) + (l & 15), rb = rb0 + rn / NT;
-    if (t >= p.T || rb >= n_rb) continue;
-    f32x4 s = red[0][rn][l];
+  for (int i = tid; i < R * p.T * 4; i += 64 * WAVES) {
+    const int r = i / (p.T * 4), t = (i >> 2) % p.T, gg = i & 3, rb = rb0 + r;
+    if (rb >= n_rb) continue;
+    f32x4 s = sum[0][r][t][gg];
 #pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) s += red[w][rn][l];
-    const size_t at = (size_t)t * p.H + 16 * rb + 4 * (l >> 4);
+    for (int w = 1; w < WAVES; ++w) s += sum[w][r][t][gg];
+    const size_t at = (size_t)t * p.H + 16 * rb + 4 * gg;
     const uint16_t* add[2] = {p.shared, p.residual};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -794,49 +780,50 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   d.ksteps = prepared_ksteps(wf, a.I);
   d.steps = nv4w(a.fmt) ? (d.ksteps + 1) / 2 : d.ksteps;
 
-  const int active = a.E < a.T * a.topk ? a.E : a.T * a.topk;  // at most
-  auto go = [&](auto fmt, auto nt) {
+  const int units = few_max_units(a.E, a.T, a.topk);
+  auto up = [&](auto fmt, auto waves, auto ksp, auto depth) {
     constexpr Fmt F = decltype(fmt)::value;
-    constexpr int NT = decltype(nt)::value;
-    constexpr int CT = F == Fmt::MX ? 2 : 1;
-    const int n_slices = a.I / (16 * CT);
-    auto up = [&](auto waves, auto ksp) {
-      constexpr int W = decltype(waves)::value, KSP = decltype(ksp)::value;
-      constexpr int per = W / KSP;
-      const int grid = (n_slices + per - 1) / per * active;
-      hipLaunchKernelGGL((few_gate_up_kernel<F, NT, W, KSP, 3>), dim3((unsigned)grid), dim3(64 * W), 0, s, u);
-    };
-    auto down = [&](auto lds_h) {
-      hipLaunchKernelGGL((few_down_kernel<F, NT, 1, 3, decltype(lds_h)::value>), dim3((unsigned)(a.H / 16)),
-                         dim3(64 * kDownWaves), 0, s, d);
-    };
-    using C1 = std::integral_constant<int, 1>;
-    using C4 = std::integral_constant<int, 4>;
-    using C8 = std::integral_constant<int, 8>;
-    if constexpr (F == Fmt::FP8) {
-      if (!few_h_fp32(a.fmt, a.T, a.topk, a.E, a.I)) {
-        up(C8{}, C1{});
-        down(std::false_type{});
-      } else {
-        up(C4{}, C4{});
-        down(std::true_type{});
-      }
-    } else {
-      up(C4{}, C4{});
-      down(std::false_type{});
-    }
+    constexpr int W = decltype(waves)::value, KSP = decltype(ksp)::value, D = decltype(depth)::value;
+    constexpr int per = W / KSP * (F == Fmt::MX ? 32 : 16);  // columns of h per workgroup
+    hipLaunchKernelGGL((few_gate_up_kernel<F, W, KSP, D>), dim3((unsigned)((a.I + per - 1) / per * units)), dim3(64 * W), 0, s, u);
   };
-  auto by_tokens = [&](auto fmt) {
-    if (a.T <= 16) go(fmt, std::integral_constant<int, 1>{});
-    else go(fmt, std::integral_constant<int, 2>{});
+  auto down = [&](auto fmt, auto waves, auto rows, auto depth, auto lds_h) {
+    constexpr Fmt F = decltype(fmt)::value;
+    constexpr int W = decltype(waves)::value, R = decltype(rows)::value, D = decltype(depth)::value;
+    hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)((a.H / 16 + R - 1) / R)),
+                       dim3(64 * W), 0, s, d);
   };
+#define C_(v) std::integral_constant<int, v>{}
+#define F_(v) std::integral_constant<Fmt, v>{}
   switch (a.fmt) {
-    case Fmt::FP8: by_tokens(std::integral_constant<Fmt, Fmt::FP8>{}); break;
-    case Fmt::BF16: by_tokens(std::integral_constant<Fmt, Fmt::BF16>{}); break;
-    case Fmt::MX: by_tokens(std::integral_constant<Fmt, Fmt::MX>{}); break;
-    case Fmt::NV4: by_tokens(std::integral_constant<Fmt, Fmt::NV4>{}); break;
-    case Fmt::NVF4: by_tokens(std::integral_constant<Fmt, Fmt::NVF4>{}); break;
+    case Fmt::FP8:
+      if (few_h_fp32(a.fmt, a.T, a.topk, a.E, a.I)) {
+        up(F_(Fmt::FP8), C_(4), C_(4), C_(3));
+        down(F_(Fmt::FP8), C_(8), C_(1), C_(3), std::true_type{});
+      } else {
+        up(F_(Fmt::FP8), C_(8), C_(1), C_(3));
+        down(F_(Fmt::FP8), C_(8), C_(1), C_(3), std::false_type{});
+      }
+      break;
+    case Fmt::BF16:
+      up(F_(Fmt::BF16), C_(4), C_(4), C_(3));
+      down(F_(Fmt::BF16), C_(8), C_(1), C_(3), std::false_type{});
+      break;
+    case Fmt::MX:
+      up(F_(Fmt::MX), C_(4), C_(4), C_(3));
+      down(F_(Fmt::MX), C_(8), C_(1), C_(4), std::false_type{});
+      break;
+    case Fmt::NV4:
+      up(F_(Fmt::NV4), C_(4), C_(4), C_(3));
+      down(F_(Fmt::NV4), C_(8), C_(1), C_(3), std::false_type{});
+      break;
+    case Fmt::NVF4:
+      up(F_(Fmt::NVF4), C_(4), C_(4), C_(3));
+      down(F_(Fmt::NVF4), C_(8), C_(1), C_(3), std::false_type{});
+      break;
   }
+#undef C_
+#undef F_
   return hipGetLastError();
 }
 
