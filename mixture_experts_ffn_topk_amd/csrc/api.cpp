@@ -256,13 +256,16 @@ bool apart_or_same(const Span& a, const Span& b) {
 }
 
 struct FewLayout {
-  size_t hsf, total;  // h at 0
+  size_t hsf, arrived, part, total;  // h at 0
 };
 FewLayout few_layout(const moe_config& c, int T) {
-  const moe::Fmt f = to_fmt(c.format);
+  const moe::FewBuffers b =
+      moe::few_buffers(to_fmt(c.format), T, c.num_topk, c.num_experts, c.hidden, c.intermediate_hidden);
   FewLayout L;
-  L.hsf = align_up(moe::few_h_bytes(f, T, c.num_topk, c.num_experts, c.intermediate_hidden));
-  L.total = L.hsf + align_up(moe::few_hsf_bytes(f, T * c.num_topk, c.intermediate_hidden));
+  L.hsf = align_up(b.h);
+  L.arrived = L.hsf + align_up(b.h_sf);
+  L.part = L.arrived + align_up(b.arrived);
+  L.total = L.part + align_up(b.part);
   return L;
 }
 
@@ -697,6 +700,8 @@ moe_status moe_forward_few(const moe_handle* h, int32_t T, const void* x, const 
   a.c_scales = w->c_input_scales;
   a.h = ws;
   a.h_sf = (char*)ws + L.hsf;
+  a.arrived = (char*)ws + L.arrived;
+  a.part = (char*)ws + L.part;
   a.shared = shared;
   a.residual = residual;
   a.out = out;

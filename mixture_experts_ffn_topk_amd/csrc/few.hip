@@ -16,9 +16,11 @@
 //     and nothing is staged in LDS: a wave is on its own until its sums are complete.
 //   * gate_up: a wave owns 16 columns of h (MX: 32, one scale block) of one expert,
 //     or 1/KSP of their K-steps where that would leave the part underfilled.
-//   * down: a workgroup owns 16 R output columns and all experts; its waves split
-//     the (unit, K-step) sequence evenly and add each unit's result to their own
-//     sums per token in LDS: no y rows, no combine launch.
+//   * down: a workgroup owns 16 R output columns and all units, or one of `splits`
+//     parts of them; its waves split its (unit, K-step) sequence evenly and add each
+//     unit's result to their own sums per token in LDS: no y rows, no combine launch.
+//     The splits' sums meet in the workspace: the last to arrive at a counter (which
+//     gate_up zeroed) adds them in order.
 //   * The FP8 intermediate needs the maximum over 128 columns.  Where whole 128-column
 //     blocks make enough workgroups, the eight waves of a gate_up workgroup hold one
 //     block and quantise it; otherwise (one token, small I) h stays fp32 between the
@@ -45,6 +47,7 @@ constexpr int kFewMaxUnits = kFewMaxExperts + kFewMaxPairs / 17;
 constexpr int few_max_units(int E, int T, int topk) {
   return (E < T * topk ? E : T * topk) + (T > 16 ? T * topk / 17 : 0);
 }
+constexpr int kFewMaxSplits = 8;
 // FP8: the most bytes of h (with 16 spare ones per row) that the down launch quantises into LDS: two
 // workgroups still share a CU.
 constexpr int kFewLdsH = 48 * 1024;
@@ -76,6 +79,10 @@ struct FewParams {
   int steps;            // K-steps of the kernel (NVFP4: pairs of the layout's)
   void* h;
   void* h_sf;
+  int splits;           // down: workgroups that share a block of columns
+  int n_blocks;         // down: blocks of 16 R columns
+  int* arrived;         // [n_blocks]
+  float* part;          // [splits][n_blocks][R][T][16]
   const uint16_t* shared;
   const uint16_t* residual;
   void* out;
@@ -311,6 +318,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   __shared__ uint32_t amax[kBlock ? WAVES : 1][16];
   const int tid = threadIdx.x, lane = lane_id(), g = lane >> 4, r16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (blockIdx.x == 0 && p.splits > 1)  // the down launch's counters
+    for (int i = tid; i < p.n_blocks; i += 64 * WAVES) p.arrived[i] = 0;
   route_to_lds<WAVES>(p, route, p.logits != nullptr);
 
   // this workgroup's unit
@@ -504,11 +513,11 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
     RouteLds route;
     float w[kFewMaxPairs];
     short unit[kFewMaxUnits];  // expert, + kHalf: its second 16 tokens
-    int n_units;
+    int n_units, last;
   };
   constexpr int kHalf = 0x4000;
   __shared__ Lds L;
-  __shared__ f32x4 sum[WAVES][R][kFewMaxTokens][4];  // a wave's sums: token, rows 4 g ...
+  extern __shared__ f32x4 sum[];  // [WAVES][R][T][4]: a wave's sums per token and run of 4 rows
   // HL: 128 zero bytes, then the rows' codes (row stride I + 16: rows in other banks); their scales
   __shared__ __attribute__((aligned(16))) uint8_t hq[HL ? 128 + kFewLdsH : 16];
   __shared__ float hsc[HL ? kFewLdsH / 128 : 1];
@@ -533,9 +542,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
     }
   }
   for (int q = tid; q < p.T * p.topk; q += 64 * WAVES) L.w[q] = p.topk_w[q];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    for (int i = lane; i < p.T * 4; i += 64) sum[wave][r][i >> 2][i & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int entries = R * p.T * 4;
+  for (int i = lane; i < entries; i += 64) sum[wave * entries + i] = f32x4{0.f, 0.f, 0.f, 0.f};
   route_to_lds<WAVES>(p, L.route, false);
   if (wave == 0) {
     const int n = for_units(L.route, p.E, [&](int before, int e, int units) {
@@ -549,9 +557,11 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
 
   // this wave's part of the (unit, K-step) sequence
   const int n_units = __builtin_amdgcn_readfirstlane(L.n_units);
+  const int blk = (int)blockIdx.x % p.n_blocks, split = (int)blockIdx.x / p.n_blocks;
   const long long total = (long long)n_units * p.steps;
-  const int lo = (int)(total * wave / WAVES), hi = (int)(total * (wave + 1) / WAVES);
-  const int rb0 = (int)blockIdx.x * R;  // first 16-row block
+  const int at = split * WAVES + wave, parts = p.splits * WAVES;
+  const int lo = (int)(total * at / parts), hi = (int)(total * (at + 1) / parts);
+  const int rb0 = blk * R;  // first 16-row block
   const int n_rb = p.H / 16;
   WAddr<F> wa[R];
 #pragma unroll
@@ -665,7 +675,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (s.tok >= 0) {
-          f32x4& at = sum[wave][r][s.tok][g];
+          f32x4& at = sum[wave * entries + (r * p.T + s.tok) * 4 + g];
           f32x4 v = at;
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = F == Fmt::FP8 ? v[i] + acc[r][i] : fmaf(acc[r][i], c, v[i]);
@@ -690,23 +700,52 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
     }
   }
   __syncthreads();
-  for (int i = tid; i < R * p.T * 4; i += 64 * WAVES) {
-    const int r = i / (p.T * 4), t = (i >> 2) % p.T, gg = i & 3, rb = rb0 + r;
-    if (rb >= n_rb) continue;
-    f32x4 s = sum[0][r][t][gg];
+  auto wave_sum = [&](int i) {
+    f32x4 v = sum[i];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) s += sum[w][r][t][gg];
-    const size_t at = (size_t)t * p.H + 16 * rb + 4 * gg;
+    for (int w = 1; w < WAVES; ++w) v += sum[w * entries + i];
+    return v;
+  };
+  auto finish = [&](int i, f32x4 v) {
+    const int t = (i >> 2) % p.T, rb = rb0 + i / (p.T * 4);
+    if (rb >= n_rb) return;
+    const size_t at = (size_t)t * p.H + 16 * rb + 4 * (i & 3);
     const uint16_t* add[2] = {p.shared, p.residual};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (add[q] == nullptr) continue;
-      const uint2 v = *(const uint2*)(add[q] + at);
-      s += f32x4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                 __uint_as_float(v.y & 0xFFFF0000u)};
+      const uint2 a = *(const uint2*)(add[q] + at);
+      v += f32x4{__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u), __uint_as_float(a.y << 16),
+                 __uint_as_float(a.y & 0xFFFF0000u)};
     }
-    if (p.out_f32) *(f32x4*)((float*)p.out + at) = s;
-    else *(uint2*)((uint16_t*)p.out + at) = uint2{bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3])};
+    if (p.out_f32) *(f32x4*)((float*)p.out + at) = v;
+    else *(uint2*)((uint16_t*)p.out + at) = uint2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+  };
+  if (p.splits == 1) {
+    for (int i = tid; i < entries; i += 64 * WAVES) finish(i, wave_sum(i));
+    return;
+  }
+  // Device-scope stores, completed before the workgroup arrives; device-scope loads by the last one.
+  // No waiting, no data atomics.
+  const __amdgpu_buffer_rsrc_t p_rs = make_rsrc(p.part, (uint32_t)(p.splits * p.n_blocks * entries) * 16u);
+  for (int i = tid; i < entries; i += 64 * WAVES)
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, wave_sum(i)), p_rs,
+                                           (uint32_t)((split * p.n_blocks + blk) * entries + i) * 16u, 0, kCpolDevice);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (tid == 0) L.last = atomicAdd(p.arrived + blk, 1) == p.splits - 1;
+  __syncthreads();
+  if (!L.last) return;
+  for (int i = tid; i < entries; i += 64 * WAVES) {
+    f32x4 v[kFewMaxSplits];
+#pragma unroll
+    for (int q = 0; q < kFewMaxSplits; ++q)  // (all in flight at once; past the last split: zeros)
+      v[q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                           p_rs, q < p.splits ? (uint32_t)((q * p.n_blocks + blk) * entries + i) * 16u : kOOB,
+                                           0, kCpolDevice));
+#pragma unroll
+    for (int q = 1; q < kFewMaxSplits; ++q) v[0] += v[q];
+    finish(i, v[0]);
   }
 }
 
@@ -720,11 +759,27 @@ static bool few_h_fp32(Fmt f, int T, int topk, int E, int I) {
   const int pairs = T * topk, active = min(E, pairs);
   return f == Fmt::FP8 && (long long)active * (I / 128) < 256 && (long long)pairs * (I + 16) <= kFewLdsH;
 }
-size_t few_h_bytes(Fmt f, int T, int topk, int E, int I) {
-  return (size_t)T * topk * I * (few_h_fp32(f, T, topk, E, I) ? 4 : bf16_mma(f) ? 2 : 1);
+// The down launch's blocks: 16 rows per wave's weight tile, tiles per workgroup, splits.
+struct DownPlan {
+  int rows, n_blocks, splits;
+};
+static DownPlan down_plan(Fmt f, int H) {
+  DownPlan d;
+  d.rows = f == Fmt::BF16 ? 1 : f == Fmt::MX ? 4 : 2;
+  d.n_blocks = (H / 16 + d.rows - 1) / d.rows;
+  d.splits = 1;
+  while (d.n_blocks * d.splits < 160 && d.splits < kFewMaxSplits) d.splits *= 2;
+  return d;
 }
-size_t few_hsf_bytes(Fmt f, int pairs, int I) {
-  return f == Fmt::FP8 ? (size_t)pairs * (I / 128) * 4 : f == Fmt::MX ? (size_t)pairs * (I / 32) : 0;
+FewBuffers few_buffers(Fmt f, int T, int topk, int E, int H, int I) {
+  FewBuffers b;
+  const size_t pairs = (size_t)T * topk;
+  b.h = pairs * I * (few_h_fp32(f, T, topk, E, I) ? 4 : bf16_mma(f) ? 2 : 1);
+  b.h_sf = f == Fmt::FP8 ? pairs * (I / 128) * 4 : f == Fmt::MX ? pairs * (I / 32) : 0;
+  const DownPlan d = down_plan(f, H);
+  b.arrived = d.splits > 1 ? (size_t)d.n_blocks * 4 : 0;
+  b.part = d.splits > 1 ? (size_t)d.splits * d.n_blocks * d.rows * T * 64 : 0;
+  return b;
 }
 
 hipError_t launch_few(const FewArgs& a, hipStream_t s) {
@@ -747,6 +802,12 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   p.residual = (const uint16_t*)a.residual;
   p.out = a.out;
   p.out_f32 = a.out_f32 ? 1 : 0;
+
+  const DownPlan dp = down_plan(a.fmt, a.H);
+  p.splits = dp.splits;
+  p.n_blocks = dp.n_blocks;
+  p.arrived = (int*)a.arrived;
+  p.part = (float*)a.part;
 
   FewParams u = p;  // gate_up
   u.logits = a.logits;
@@ -790,36 +851,35 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   auto down = [&](auto fmt, auto waves, auto rows, auto depth, auto lds_h) {
     constexpr Fmt F = decltype(fmt)::value;
     constexpr int W = decltype(waves)::value, R = decltype(rows)::value, D = decltype(depth)::value;
-    hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)((a.H / 16 + R - 1) / R)),
-                       dim3(64 * W), 0, s, d);
+    hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)(dp.n_blocks * dp.splits)), dim3(64 * W), (size_t)W * R * a.T * 64, s, d);
   };
 #define C_(v) std::integral_constant<int, v>{}
 #define F_(v) std::integral_constant<Fmt, v>{}
   switch (a.fmt) {
     case Fmt::FP8:
       if (few_h_fp32(a.fmt, a.T, a.topk, a.E, a.I)) {
-        up(F_(Fmt::FP8), C_(4), C_(4), C_(3));
-        down(F_(Fmt::FP8), C_(8), C_(1), C_(3), std::true_type{});
+        up(F_(Fmt::FP8), C_(4), C_(4), C_(2));
+        down(F_(Fmt::FP8), C_(8), C_(2), C_(2), std::true_type{});
       } else {
-        up(F_(Fmt::FP8), C_(8), C_(1), C_(3));
-        down(F_(Fmt::FP8), C_(8), C_(1), C_(3), std::false_type{});
+        up(F_(Fmt::FP8), C_(8), C_(1), C_(2));
+        down(F_(Fmt::FP8), C_(8), C_(2), C_(2), std::false_type{});
       }
       break;
     case Fmt::BF16:
-      up(F_(Fmt::BF16), C_(4), C_(4), C_(3));
-      down(F_(Fmt::BF16), C_(8), C_(1), C_(3), std::false_type{});
+      up(F_(Fmt::BF16), C_(4), C_(4), C_(2));
+      down(F_(Fmt::BF16), C_(8), C_(1), C_(2), std::false_type{});
       break;
     case Fmt::MX:
-      up(F_(Fmt::MX), C_(4), C_(4), C_(3));
-      down(F_(Fmt::MX), C_(8), C_(1), C_(4), std::false_type{});
+      up(F_(Fmt::MX), C_(4), C_(4), C_(2));
+      down(F_(Fmt::MX), C_(8), C_(4), C_(2), std::false_type{});
       break;
     case Fmt::NV4:
-      up(F_(Fmt::NV4), C_(4), C_(4), C_(3));
-      down(F_(Fmt::NV4), C_(8), C_(1), C_(3), std::false_type{});
+      up(F_(Fmt::NV4), C_(4), C_(4), C_(2));
+      down(F_(Fmt::NV4), C_(8), C_(2), C_(2), std::false_type{});
       break;
     case Fmt::NVF4:
-      up(F_(Fmt::NVF4), C_(4), C_(4), C_(3));
-      down(F_(Fmt::NVF4), C_(8), C_(1), C_(3), std::false_type{});
+      up(F_(Fmt::NVF4), C_(4), C_(4), C_(2));
+      down(F_(Fmt::NVF4), C_(8), C_(2), C_(2), std::false_type{});
       break;
   }
 #undef C_

@@ -57,8 +57,10 @@ struct FewArgs {
   const float* w13_gs;
   const float* w2_gs;
   const float* c_scales;
-  void* h;     // few_h_bytes
-  void* h_sf;  // few_hsf_bytes
+  void* h;        // the buffers of few_buffers
+  void* h_sf;
+  void* arrived;
+  void* part;
   const void* shared;
   const void* residual;
   void* out;
@@ -67,8 +69,10 @@ struct FewArgs {
 // Whether the first launch can route from logits itself (else the top-k launch
 // comes before it).
 bool few_routes_in_launch(int T);
-size_t few_h_bytes(Fmt f, int T, int topk, int E, int I);
-size_t few_hsf_bytes(Fmt f, int pairs, int I);
+struct FewBuffers {
+  size_t h, h_sf, arrived, part;  // bytes
+};
+FewBuffers few_buffers(Fmt f, int T, int topk, int E, int H, int I);
 hipError_t launch_few(const FewArgs& a, hipStream_t s);
 
 }  // namespace moe
