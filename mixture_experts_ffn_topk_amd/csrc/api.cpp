@@ -256,14 +256,15 @@ bool apart_or_same(const Span& a, const Span& b) {
 }
 
 struct FewLayout {
-  size_t hsf, arrived, part, total;  // h at 0
+  size_t hsf, tables, arrived, part, total;  // h at 0
 };
 FewLayout few_layout(const moe_config& c, int T) {
   const moe::FewBuffers b =
       moe::few_buffers(to_fmt(c.format), T, c.num_topk, c.num_experts, c.hidden, c.intermediate_hidden);
   FewLayout L;
   L.hsf = align_up(b.h);
-  L.arrived = L.hsf + align_up(b.h_sf);
+  L.tables = L.hsf + align_up(b.h_sf);
+  L.arrived = L.tables + align_up(b.tables);
   L.part = L.arrived + align_up(b.arrived);
   L.total = L.part + align_up(b.part);
   return L;
@@ -700,6 +701,7 @@ moe_status moe_forward_few(const moe_handle* h, int32_t T, const void* x, const 
   a.c_scales = w->c_input_scales;
   a.h = ws;
   a.h_sf = (char*)ws + L.hsf;
+  a.tables = (char*)ws + L.tables;
   a.arrived = (char*)ws + L.arrived;
   a.part = (char*)ws + L.part;
   a.shared = shared;

@@ -11,7 +11,9 @@
 //   * The weights are the first MFMA operand (16 rows), an expert's tokens (in token
 //     order, found from one 32-bit mask per expert in LDS) the 16 columns of the
 //     second: no plan, no gathered rows.  An expert with more than 16 tokens is two
-//     units of work that read its weights twice.
+//     units of work that read its weights twice.  gate_up's workgroups each find
+//     their unit from the ids; one more workgroup writes all units' tables for the
+//     down launch, whose start is then one load away.
 //   * Weights go straight from HBM into registers, each byte read once, non-temporal,
 //     and nothing is staged in LDS: a wave is on its own until its sums are complete.
 //   * gate_up: a wave owns 16 columns of h (MX: 32, one scale block) of one expert,
@@ -43,7 +45,6 @@ namespace {
 constexpr int kFewMaxPairs = kFewMaxTokens * 32;  // num_topk <= 32
 constexpr int kFewMaxExperts = 1024;
 // (an expert with more than 16 of T <= 32 tokens is two units: at most one such per 17 pairs)
-constexpr int kFewMaxUnits = kFewMaxExperts + kFewMaxPairs / 17;
 constexpr int few_max_units(int E, int T, int topk) {
   return (E < T * topk ? E : T * topk) + (T > 16 ? T * topk / 17 : 0);
 }
@@ -79,6 +80,8 @@ struct FewParams {
   int steps;            // K-steps of the kernel (NVFP4: pairs of the layout's)
   void* h;
   void* h_sf;
+  uint32_t* tables;     // the units (FewTables)
+  int max_units;
   int splits;           // down: workgroups that share a block of columns
   int n_blocks;         // down: blocks of 16 R columns
   int* arrived;         // [n_blocks]
@@ -207,38 +210,46 @@ struct RouteLds {
   short ids[kFewMaxPairs];        // expert of each pair, -1: no valid expert
   uint32_t mask[kFewMaxExperts];  // the tokens of each expert
 };
+constexpr int kCol(int t, int j) { return t << 5 | j; }  // a column: token and slot (both below 32)
 
 // The pairs' experts and the experts' tokens, by the whole workgroup (ends with a barrier).
-// from_logits (gate_up): each wave routes tokens wave, wave + WAVES, ...; workgroup 0 stores the result.
+// from_logits (gate_up): each wave routes tokens wave, wave + WAVES, ...; w (the tables' workgroup,
+// else nullptr) receives the router weights, and the caller's arrays the result.
 template <int WAVES>
-MOE_DEV void route_to_lds(const FewParams& p, RouteLds& L, bool from_logits) {
+MOE_DEV void route_to_lds(const FewParams& p, RouteLds& L, float* w) {
   const int tid = threadIdx.x, lane = lane_id(), np = p.T * p.topk;
+  auto id_of = [&](int q) { return p.ids64 ? ((const long long*)p.ids)[q] : (long long)((const int*)p.ids)[q]; };
+  const bool routes = p.logits != nullptr;
+  long long first = -1;  // (in flight while the masks are cleared)
+  if (!routes && tid < np) first = id_of(tid);
   for (int e = tid; e < p.E; e += 64 * WAVES) L.mask[e] = 0;
   __syncthreads();
-  if (from_logits) {
+  if (routes) {
     for (int t = tid >> 6; t < p.T; t += WAVES) {
       int e;
-      float w;
+      float wt;
       const float* row = p.logits + (size_t)t * p.E;
-      if (p.fast) route_token_topk<true>(row, p.bias, p.E, p.topk, e, w);
-      else route_token_topk<false>(row, p.bias, p.E, p.topk, e, w);
+      if (p.fast) route_token_topk<true>(row, p.bias, p.E, p.topk, e, wt);
+      else route_token_topk<false>(row, p.bias, p.E, p.topk, e, wt);
       if (lane < p.topk) {
         const int q = t * p.topk + lane;
         L.ids[q] = (short)e;
         atomicOr(&L.mask[e], 1u << t);
-        if (blockIdx.x == 0) {
+        if (w != nullptr) {
           if (p.idx64_out != nullptr) p.idx64_out[q] = e;
           else p.idx32_out[q] = e;
-          p.w_out[q] = w;
+          p.w_out[q] = wt;
+          w[q] = wt;
         }
       }
     }
   } else {
     for (int q = tid; q < np; q += 64 * WAVES) {
-      const long long v = p.ids64 ? ((const long long*)p.ids)[q] : (long long)((const int*)p.ids)[q];
+      const long long v = q == tid ? first : id_of(q);
       const bool ok = v >= 0 && v < p.E;
       L.ids[q] = ok ? (short)v : (short)-1;
       if (ok) atomicOr(&L.mask[(int)v], 1u << (q / p.topk));
+      if (w != nullptr) w[q] = p.topk_w[q];
     }
   }
   __syncthreads();
@@ -260,11 +271,50 @@ MOE_DEV int for_units(const RouteLds& L, int E, Fn f) {
   }
   return base;
 }
-// The token of the lane's column r of a unit (-1: none): the r-th (+ 16) of the expert's tokens.
-MOE_DEV int token_of(uint32_t mask, int half, int r) {
-  for (int i = half ? 16 : 0; i > 0; --i) mask &= mask - 1;
-  for (int i = r; i > 0; --i) mask &= mask - 1;
-  return mask != 0 ? __ffs(mask) - 1 : -1;
+MOE_DEV int rank_in(uint32_t mask, int t) { return __popc(mask & ((1u << t) - 1u)); }
+
+// The tables of the units for the down launch: the pairs' router weights (of a token's first slot
+// of an expert: the sum over its slots of that expert, in slot order), each unit's expert and number of
+// columns, and their columns.
+struct FewTables {
+  uint32_t *n, *w, *unit, *col;  // [4] (one used), [pairs] floats, [max_units], [max_units][8] pairs of shorts
+};
+MOE_HOST_DEV inline size_t few_table_words(int pairs, int max_units) { return 4 + (size_t)pairs + 9 * (size_t)max_units; }
+MOE_DEV FewTables few_tables(uint32_t* base, int pairs, int max_units) {
+  return FewTables{base, base + 4, base + 4 + pairs, base + 4 + pairs + max_units};
+}
+template <int WAVES>
+MOE_DEV void write_tables(const FewParams& p, const RouteLds& L, const float* w, short* ustart) {
+  const int tid = threadIdx.x, np = p.T * p.topk;
+  const FewTables tb = few_tables(p.tables, np, p.max_units);
+  if (tid < 64) {
+    const int n = for_units(L, p.E, [&](int before, int e, int units) {
+      const int cnt = units > 0 ? __popc(L.mask[e]) : 0;
+      if (units > 0) {
+        ustart[e] = (short)before;
+        tb.unit[before] = (uint32_t)(e | min(cnt, 16) << 16);
+      }
+      if (units > 1) tb.unit[before + 1] = (uint32_t)(e | (cnt - 16) << 16);
+      return false;
+    });
+    if (tid == 0) *tb.n = (uint32_t)n;
+  }
+  __syncthreads();
+  for (int q = tid; q < np; q += 64 * WAVES) {
+    const int e = L.ids[q], t = q / p.topk, j = q - t * p.topk;
+    if (e < 0) continue;
+    float s = 0.0f;
+    bool first = true;
+    for (int i = 0; i < p.topk; ++i)
+      if (L.ids[t * p.topk + i] == e) {
+        first = first && i >= j;
+        s += w[t * p.topk + i];
+      }
+    if (!first) continue;
+    const int r = rank_in(L.mask[e], t);
+    ((float*)tb.w)[q] = s;
+    ((short*)tb.col)[(ustart[e] + (r >> 4)) * 16 + (r & 15)] = (short)kCol(t, j);
+  }
 }
 
 // ---------------------------------------------------------------- gate_up
@@ -318,9 +368,18 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   __shared__ uint32_t amax[kBlock ? WAVES : 1][16];
   const int tid = threadIdx.x, lane = lane_id(), g = lane >> 4, r16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (blockIdx.x == 0 && p.splits > 1)  // the down launch's counters
-    for (int i = tid; i < p.n_blocks; i += 64 * WAVES) p.arrived[i] = 0;
-  route_to_lds<WAVES>(p, route, p.logits != nullptr);
+  __shared__ int col[32];  // the columns of this workgroup's expert
+  if (blockIdx.x == gridDim.x - 1) {  // the down launch's tables and counters
+    __shared__ float tw[kFewMaxPairs];
+    __shared__ short ustart[kFewMaxExperts];
+    if (p.splits > 1)
+      for (int i = tid; i < p.n_blocks; i += 64 * WAVES) p.arrived[i] = 0;
+    route_to_lds<WAVES>(p, route, tw);
+    write_tables<WAVES>(p, route, tw, ustart);
+    return;
+  }
+  if (tid < 32) col[tid] = 0x7FFF;
+  route_to_lds<WAVES>(p, route, nullptr);
 
   // this workgroup's unit
   const int n_slices = p.I / (16 * CT), blocks = (n_slices + kSlices - 1) / kSlices;
@@ -336,11 +395,17 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   });
   if (e < 0) return;  // (uniform: fewer units than workgroup rows)
 
-  // the lane's token, its first slot of this expert, and its first byte of a K-step, as XFrag describes
-  const int t = token_of(route.mask[e], half, r16);
-  int slot = 0;
-  if (t >= 0)
-    while (route.ids[t * p.topk + slot] != e) ++slot;  // (the mask says that there is one)
+  // the columns of the expert: each of its tokens, with the token's first slot of it
+  const uint32_t mask = route.mask[e];
+  for (int q = tid; q < p.T * p.topk; q += 64 * WAVES)
+    if (route.ids[q] == e) {
+      const int tq = q / p.topk;
+      atomicMin(&col[rank_in(mask, tq)], kCol(tq, q - tq * p.topk));
+    }
+  __syncthreads();
+  const int c = col[16 * half + r16];
+  const int t = c == 0x7FFF ? -1 : c >> 5, slot = c & 31;
+  // the lane's first byte of a K-step, as XFrag describes
   const uint32_t at = F == Fmt::NV4 ? 128u * (g >> 1) + 16u * (g & 1) : F == Fmt::NVF4 ? 32u * (g >> 1) + 4u * (g & 1) : 16u * g;
   const uint32_t sat = F == Fmt::MX ? (uint32_t)g : F == Fmt::NVF4 ? 4u * (g >> 1) : 0u;
   const uint32_t xo = t >= 0 ? (uint32_t)t * p.x_row + at : kOOB;
@@ -454,7 +519,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
 
   // lane (g, token): columns col0 + 16 c + 4 g ... of the token's row
   const float gs = nv4w(F) ? p.w_gs[e] : 1.0f;
-  const size_t row = (size_t)max(t, 0) * p.topk + slot;
+  const size_t row = (size_t)max(t, 0) * p.topk + slot;  // (not used without a token)
   f32x4 h[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
@@ -504,59 +569,70 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
 }
 
 // ---------------------------------------------------------------- down
+// A workgroup barrier that waits for this wave's LDS accesses only.
+MOE_DEV void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // R: 16-row weight tiles (output column groups) per workgroup.  HL (FP8): h is fp32 and
 // quantised into LDS here.
 template <Fmt F, int WAVES, int R, int D, bool HL>
 __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
   static_assert(!HL || F == Fmt::FP8, "only FP8 leaves h in fp32");
-  struct Lds {
-    RouteLds route;
-    float w[kFewMaxPairs];
-    short unit[kFewMaxUnits];  // expert, + kHalf: its second 16 tokens
-    int n_units, last;
-  };
-  constexpr int kHalf = 0x4000;
-  __shared__ Lds L;
+  __shared__ int last;
   extern __shared__ f32x4 sum[];  // [WAVES][R][T][4]: a wave's sums per token and run of 4 rows
   // HL: 128 zero bytes, then the rows' codes (row stride I + 16: rows in other banks); their scales
   __shared__ __attribute__((aligned(16))) uint8_t hq[HL ? 128 + kFewLdsH : 16];
   __shared__ float hsc[HL ? kFewLdsH / 128 : 1];
   const int tid = threadIdx.x, lane = lane_id(), g = lane >> 4, r16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if constexpr (HL) {
-    // 16 lanes a 128-column block, 8 columns a lane (rows of masked slots hold anything and are not read)
-    const int cpr = p.I / 8, n = p.T * p.topk * cpr;
-    if (tid < 32) ((uint32_t*)hq)[tid] = 0;
-    for (int c = tid; c < n; c += 64 * WAVES) {
-      const f32x4 a = *(const f32x4*)((const float*)p.h + (size_t)c * 8), b = *(const f32x4*)((const float*)p.h + (size_t)c * 8 + 4);
-      uint32_t m = max(amax_bits4(a), amax_bits4(b));
-      m = dpp_max_u32<0xB1>(m);
-      m = dpp_max_u32<0x4E>(m);
-      m = dpp_max_u32<0x141>(m);
-      m = dpp_max_u32<0x140>(m);
-      float inv;
-      const float sc = fp8_scale(m, inv);
-      const int row = c / cpr, col = c - row * cpr;
-      *(uint2*)(hq + 128 + row * (p.I + 16) + col * 8) = uint2{(uint32_t)e4m3x4(a * inv), (uint32_t)e4m3x4(b * inv)};
-      if ((lane & 15) == 0) hsc[c >> 4] = sc;
+  const int np = p.T * p.topk;
+  // HL: 16 lanes a 128-column block, 8 columns a lane (rows of masked slots hold anything and are not
+  // read).  The first kHB chunks of a thread are in flight during the set-up below.
+  constexpr int kHB = 4;
+  const int cpr = p.I / 8, n_chunks = HL ? np * cpr : 0;
+  f32x4 hv[HL ? kHB : 1][2];
+  const __amdgpu_buffer_rsrc_t hf_rs = make_rsrc(p.h, (uint32_t)n_chunks * 32u);  // (past the end: zeros)
+  auto load_h = [&](int c0) {
+    if constexpr (HL) {
+#pragma unroll
+      for (int i = 0; i < kHB; ++i) {
+        const uint32_t o = (uint32_t)(c0 + tid + i * 64 * WAVES) * 32u;
+        hv[i][0] = __builtin_bit_cast(f32x4, bload16(hf_rs, o, 0));
+        hv[i][1] = __builtin_bit_cast(f32x4, bload16(hf_rs, o + 16u, 0));
+      }
     }
-  }
-  for (int q = tid; q < p.T * p.topk; q += 64 * WAVES) L.w[q] = p.topk_w[q];
+  };
+  auto quantise_h = [&](int c0) {
+    if constexpr (HL) {
+#pragma unroll
+      for (int i = 0; i < kHB; ++i) {
+        const int c = c0 + tid + i * 64 * WAVES;
+        uint32_t m = max(amax_bits4(hv[i][0]), amax_bits4(hv[i][1]));
+        m = dpp_max_u32<0xB1>(m);
+        m = dpp_max_u32<0x4E>(m);
+        m = dpp_max_u32<0x141>(m);
+        m = dpp_max_u32<0x140>(m);
+        float inv;
+        const float sc = fp8_scale(m, inv);
+        if (c < n_chunks) {
+          const int row = c / cpr, col = c - row * cpr;
+          *(uint2*)(hq + 128 + row * (p.I + 16) + col * 8) =
+              uint2{(uint32_t)e4m3x4(hv[i][0] * inv), (uint32_t)e4m3x4(hv[i][1] * inv)};
+          if ((lane & 15) == 0) hsc[c >> 4] = sc;
+        }
+      }
+    }
+  };
+  load_h(0);
   const int entries = R * p.T * 4;
   for (int i = lane; i < entries; i += 64) sum[wave * entries + i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  route_to_lds<WAVES>(p, L.route, false);
-  if (wave == 0) {
-    const int n = for_units(L.route, p.E, [&](int before, int e, int units) {
-      if (units > 0) L.unit[before] = (short)e;
-      if (units > 1) L.unit[before + 1] = (short)(e | kHalf);
-      return false;
-    });
-    if (lane == 0) L.n_units = n;
-  }
+  // the units' tables
+  uint32_t* tables = (uint32_t*)(sum + WAVES * entries);
+  const FewTables tb = few_tables(tables, np, p.max_units);
+  for (int i = tid; i < (int)few_table_words(np, p.max_units); i += 64 * WAVES) tables[i] = p.tables[i];
+  const int n_units = (int)*p.tables;
   __syncthreads();
 
   // this wave's part of the (unit, K-step) sequence
-  const int n_units = __builtin_amdgcn_readfirstlane(L.n_units);
   const int blk = (int)blockIdx.x % p.n_blocks, split = (int)blockIdx.x / p.n_blocks;
   const long long total = (long long)n_units * p.steps;
   const int at = split * WAVES + wave, parts = p.splits * WAVES;
@@ -581,22 +657,18 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
   float wt;
   int tok;
   auto set_unit = [&]() {
-    const int u = __builtin_amdgcn_readfirstlane((int)L.unit[min(lu, n_units - 1)]), e = u & (kHalf - 1);
+    const int lc = max(min(lu, n_units - 1), 0);
+    const int u = __builtin_amdgcn_readfirstlane((int)tb.unit[lc]), e = u & 0xFFFF;
+    const int c = ((const unsigned short*)tb.col)[lc * 16 + r16];
     w_rs = make_rsrc(p.w + (size_t)e * p.w_expert, p.w_expert);
     ws_rs = make_rsrc(p.w_sf + (size_t)e * p.w_sf_expert, p.w_sf_expert);
     if constexpr (F == Fmt::FP8)
       sb = (const float*)(p.w_sf + (size_t)e * p.w_sf_expert) + (size_t)(rb0 / 8) * p.ksteps;
-    tok = token_of(L.route.mask[e], u & kHalf, r16);
-    int slot = -1;
-    wt = 0.0f;  // a token that lists the expert twice weighs it by both, in slot order
-    if (tok >= 0)
-      for (int j = 0; j < p.topk; ++j)
-        if (L.route.ids[tok * p.topk + j] == e) {
-          wt += L.w[tok * p.topk + j];
-          if (slot < 0) slot = j;
-        }
+    const bool mine = r16 < u >> 16;
+    tok = mine ? c >> 5 : -1;
+    const uint32_t row = mine ? (uint32_t)((c >> 5) * p.topk + (c & 31)) : 0u;
+    wt = __builtin_bit_cast(float, tb.w[row]);
     if constexpr (nv4w(F)) wt *= p.w_gs[e];
-    const uint32_t row = (uint32_t)(tok * p.topk + slot);
     const uint32_t at = nv4w(F) ? 128u * (g >> 1) + 16u * (g & 1) : 16u * g;
     ho = tok >= 0 ? row * h_row + at : kOOB;
     hso = tok >= 0 ? row * hs_row + (F == Fmt::MX ? (uint32_t)g : 0u) : kOOB;
@@ -685,10 +757,22 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
       }
     }
   };
-  if (lo < hi) {  // (uniform per wave)
+  const bool busy = lo < hi;  // (uniform per wave)
+  if (busy) {
     set_unit();
 #pragma unroll
     for (int d = 0; d < D; ++d) load(st[d]);
+  }
+  if constexpr (HL) {
+    if (tid < 32) ((uint32_t*)hq)[tid] = 0;
+    quantise_h(0);
+    for (int c0 = kHB * 64 * WAVES; c0 < n_chunks; c0 += kHB * 64 * WAVES) {
+      load_h(c0);
+      quantise_h(c0);
+    }
+    lds_barrier();  // (the weights stay in flight)
+  }
+  if (busy) {
     for (int f = lo; f < hi; f += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
@@ -733,9 +817,9 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
                                            (uint32_t)((split * p.n_blocks + blk) * entries + i) * 16u, 0, kCpolDevice);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (tid == 0) L.last = atomicAdd(p.arrived + blk, 1) == p.splits - 1;
+  if (tid == 0) last = atomicAdd(p.arrived + blk, 1) == p.splits - 1;
   __syncthreads();
-  if (!L.last) return;
+  if (!last) return;
   for (int i = tid; i < entries; i += 64 * WAVES) {
     f32x4 v[kFewMaxSplits];
 #pragma unroll
@@ -772,11 +856,13 @@ static DownPlan down_plan(Fmt f, int H) {
   return d;
 }
 FewBuffers few_buffers(Fmt f, int T, int topk, int E, int H, int I) {
-  FewBuffers b;
+  FewBuffers b{};
+  if (T == 0) return b;
   const size_t pairs = (size_t)T * topk;
   b.h = pairs * I * (few_h_fp32(f, T, topk, E, I) ? 4 : bf16_mma(f) ? 2 : 1);
   b.h_sf = f == Fmt::FP8 ? pairs * (I / 128) * 4 : f == Fmt::MX ? pairs * (I / 32) : 0;
   const DownPlan d = down_plan(f, H);
+  b.tables = few_table_words(T * topk, few_max_units(E, T, topk)) * 4;
   b.arrived = d.splits > 1 ? (size_t)d.n_blocks * 4 : 0;
   b.part = d.splits > 1 ? (size_t)d.splits * d.n_blocks * d.rows * T * 64 : 0;
   return b;
@@ -806,6 +892,8 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   const DownPlan dp = down_plan(a.fmt, a.H);
   p.splits = dp.splits;
   p.n_blocks = dp.n_blocks;
+  p.tables = (uint32_t*)a.tables;
+  p.max_units = few_max_units(a.E, a.T, a.topk);
   p.arrived = (int*)a.arrived;
   p.part = (float*)a.part;
 
@@ -841,17 +929,17 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   d.ksteps = prepared_ksteps(wf, a.I);
   d.steps = nv4w(a.fmt) ? (d.ksteps + 1) / 2 : d.ksteps;
 
-  const int units = few_max_units(a.E, a.T, a.topk);
   auto up = [&](auto fmt, auto waves, auto ksp, auto depth) {
     constexpr Fmt F = decltype(fmt)::value;
     constexpr int W = decltype(waves)::value, KSP = decltype(ksp)::value, D = decltype(depth)::value;
     constexpr int per = W / KSP * (F == Fmt::MX ? 32 : 16);  // columns of h per workgroup
-    hipLaunchKernelGGL((few_gate_up_kernel<F, W, KSP, D>), dim3((unsigned)((a.I + per - 1) / per * units)), dim3(64 * W), 0, s, u);
+    hipLaunchKernelGGL((few_gate_up_kernel<F, W, KSP, D>), dim3((unsigned)((a.I + per - 1) / per * p.max_units + 1)), dim3(64 * W), 0, s, u);
   };
   auto down = [&](auto fmt, auto waves, auto rows, auto depth, auto lds_h) {
     constexpr Fmt F = decltype(fmt)::value;
     constexpr int W = decltype(waves)::value, R = decltype(rows)::value, D = decltype(depth)::value;
-    hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)(dp.n_blocks * dp.splits)), dim3(64 * W), (size_t)W * R * a.T * 64, s, d);
+    hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)(dp.n_blocks * dp.splits)), dim3(64 * W), (size_t)W * R * a.T * 64 + few_table_words(a.T * a.topk, p.max_units) * 4,
+                       s, d);
   };
 #define C_(v) std::integral_constant<int, v>{}
 #define F_(v) std::integral_constant<Fmt, v>{}

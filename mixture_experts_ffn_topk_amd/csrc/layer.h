@@ -59,6 +59,7 @@ struct FewArgs {
   const float* c_scales;
   void* h;        // the buffers of few_buffers
   void* h_sf;
+  void* tables;
   void* arrived;
   void* part;
   const void* shared;
@@ -70,7 +71,7 @@ struct FewArgs {
 // comes before it).
 bool few_routes_in_launch(int T);
 struct FewBuffers {
-  size_t h, h_sf, arrived, part;  // bytes
+  size_t h, h_sf, tables, arrived, part;  // bytes
 };
 FewBuffers few_buffers(Fmt f, int T, int topk, int E, int H, int I);
 hipError_t launch_few(const FewArgs& a, hipStream_t s);
