@@ -148,9 +148,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -235,31 +233,31 @@ def _byte_types():
     return _byte_kinds
 
 
-def _fit(*args) -> bool:
+def _fit(args) -> bool:
     """Whether every (tensor, bytes, dtypes) given is a contiguous GPU tensor of one of the
     dtypes (None: of any), on the current device, with at least so many bytes: the checks of _need and
     _on_current_gpu in one pass, without their messages (a call of a few microseconds
     should not spend more on them).  False says nothing about which check failed, nor
     that one did: raw addresses take the slow checks too."""
-    import torch
     cur = None
     for t, nbytes, dtypes in args:
-        if t is None or t.__class__ is int or (dtypes is not None and t.dtype not in dtypes) or t.nbytes < nbytes:
+        if t is None or t.__class__ is int or (dtypes is not None and t.dtype not in dtypes):
             return False
-        if not t.is_contiguous():
-            return False
-        d = t.get_device()
-        if d != cur:
-            if cur is not None or d < 0 or d != torch.cuda.current_device():
+        if t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != cur:
+            if cur is not None or t.nbytes < nbytes or not t.is_contiguous() or not t.is_cuda:
                 return False
-            cur = d
+            import torch
+            cur = torch.cuda.current_device()
+            if t.get_device() != cur:
+                return False
     return True
 
 
 def _current_stream() -> int:
     """The current stream's handle (_stream(None) without making a Stream object)."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    c = torch._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 class MoEFFN:
@@ -641,24 +639,24 @@ class MoEFFN:
         T, H = num_tokens, self.hidden
         n, bf16, f32 = T * H, torch.bfloat16, torch.float32
         xf, rf, wf = (getattr(t, "dtype", None) is f32 for t in (x, residual, weight))
-        kinds, res = (bf16, f32), n * (4 if rf else 2)
+        kinds, codes, res = (bf16, f32), _byte_types(), n * (4 if rf else 2)
         sf_bytes = T * self._x_sf_row()
-        sf_kinds = (f32,) if self.fmt == "fp8_block128" else _byte_types()
+        sf_kinds = kinds[1:] if self.fmt == "fp8_block128" else codes
         fast = [(x, n * (4 if xf else 2), kinds), (weight, H * (4 if wf else 2), kinds)]
-        if residual is not None and residual_out is not None:
-            fast += ((residual, res, kinds), (residual_out, res, (f32 if rf else bf16,)))
+        if residual is not None or residual_out is not None:
+            fast += ((residual, res, kinds), (residual_out, res, kinds[1:] if rf else kinds[:1]))
         if x_norm is not None:
-            fast.append((x_norm, n * 2, (bf16,)))
-        if x_q is not None and x_sf is not None:
-            fast += ((x_q, T * self._x_bytes(H), _byte_types()), (x_sf, sf_bytes, sf_kinds))
-        if len(fast) != 2 + sum(t is not None for t in (residual, residual_out, x_norm, x_q, x_sf)) or not _fit(*fast):
+            fast.append((x_norm, n * 2, kinds[:1]))
+        if x_q is not None or x_sf is not None:
+            fast += ((x_q, T * self._x_bytes(H), codes), (x_sf, sf_bytes, sf_kinds))
+        if not _fit(fast):
             _need(x, "x", n * (4 if xf else 2), kinds)
             _need(weight, "weight", H * (4 if wf else 2), kinds)
             _need(residual, "residual", res, kinds, required=False)
-            _need(residual_out, "residual_out", res, (f32 if rf else bf16,), required=residual is not None)
-            _need(x_norm, "x_norm", n * 2, (bf16,), required=x_q is None)
+            _need(residual_out, "residual_out", res, kinds[1:] if rf else kinds[:1], required=residual is not None)
+            _need(x_norm, "x_norm", n * 2, kinds[:1], required=x_q is None)
             if sf_bytes > 0:
-                _need(x_q, "x_q", T * self._x_bytes(H), _byte_types(), required=x_sf is not None)
+                _need(x_q, "x_q", T * self._x_bytes(H), codes, required=x_sf is not None)
                 _need(x_sf, "x_sf", sf_bytes, sf_kinds, required=x_q is not None)
             _on_current_gpu(x=x, residual=residual, weight=weight, residual_out=residual_out, x_norm=x_norm, x_q=x_q,
                             x_sf=x_sf)
@@ -683,7 +681,7 @@ class MoEFFN:
                 (logits, T * E * 4, (torch.float32,))]
         if ws is not None:
             fast.append((ws, 0, (torch.uint8,)))
-        if not _fit(*fast):
+        if not _fit(fast):
             _need(x, "x", T * H * 2, (torch.bfloat16,))
             _need(router_w, "router_w", E * H * (4 if w32 else 2), (torch.bfloat16, torch.float32))
             _need(logits, "logits", T * E * 4, (torch.float32,))
@@ -718,7 +716,7 @@ class MoEFFN:
             fast.append((routing_logits, T * self.experts * 4, f32))
         fast += [(t, n * 2, (torch.bfloat16,)) for t in (shared, residual) if t is not None]
         # (a routing bias and NVFP4's per-expert scales take the slow checks)
-        if routing_bias is not None or self.fmt in ("nvfp4_w4a16", "nvfp4") or not _fit(*fast):
+        if routing_bias is not None or self.fmt in ("nvfp4_w4a16", "nvfp4") or not _fit(fast):
             self._check_x(x, x_sf, T)
             self._check_weights(weights)
             self._check_routing_in(T, topk_idx, routing_logits, routing_bias)
