@@ -355,14 +355,14 @@ MOE_DEV int e4m3x4(f32x4 v) {
   return __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false), true);
 }
 
-// KSP: waves that share one slice of columns.  D: K-steps in flight per wave.
-// FP8: 8 waves hold (and quantise) a 128-column block, 4 leave h in fp32.
-template <Fmt F, int WAVES, int KSP, int D>
+// KSP: waves that share one slice of 16 CT columns.  D: K-steps in flight per wave.
+// FP8: waves with the whole K quantise the workgroup's 128 columns, the others leave h in fp32.
+template <Fmt F, int WAVES, int KSP, int CT, int D>
 __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
-  constexpr int CT = F == Fmt::MX ? 2 : 1;  // 16-column groups per wave
   constexpr int kSlices = WAVES / KSP;
-  constexpr bool kBlock = F == Fmt::FP8 && WAVES == 8;
-  static_assert(!kBlock || KSP == 1, "a wave of a block has its columns' whole sums");
+  constexpr bool kBlock = F == Fmt::FP8 && KSP == 1;
+  static_assert(!kBlock || WAVES * CT == 8, "the workgroup holds one block");
+  static_assert(F != Fmt::MX || CT % 2 == 0, "a wave holds whole blocks of 32 columns");
   __shared__ RouteLds route;
   __shared__ f32x4 red[KSP > 1 ? WAVES : 1][KSP > 1 ? CT * 2 : 1][KSP > 1 ? 64 : 1];
   __shared__ uint32_t amax[kBlock ? WAVES : 1][16];
@@ -382,7 +382,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   route_to_lds<WAVES>(p, route, nullptr);
 
   // this workgroup's unit
-  const int n_slices = p.I / (16 * CT), blocks = (n_slices + kSlices - 1) / kSlices;
+  const int n_slices = (p.I + 16 * CT - 1) / (16 * CT), blocks = (n_slices + kSlices - 1) / kSlices;
   const int a = (int)blockIdx.x / blocks, slice = ((int)blockIdx.x % blocks) * kSlices + wave / KSP;
   int e = -1, half = 0;
   for_units(route, p.E, [&](int before, int le, int n) {
@@ -421,7 +421,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   for (int c = 0; c < CT; ++c)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      wa[c][u] = w_addr<F>(slice, u, slice * CT + c + u * (p.I / 16), p.ksteps, g, r16, live);
+      wa[c][u] = w_addr<F>(slice * CT + c, u, slice * CT + c + u * (p.I / 16), p.ksteps, g, r16, (slice * CT + c) * 16 < p.I);
   // FP8: the 128-row blocks' scales
   const float* sbg = (const float*)(p.w_sf + (size_t)e * p.w_sf_expert) + (size_t)((live ? col0 : 0) / 128) * p.ksteps;
   const float* sbu = sbg + (size_t)(p.I / 128) * p.ksteps;
@@ -528,50 +528,61 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
     h[c] = swiglu4(gt, up, p.clamp, p.fast);
   }
   if constexpr (kBlock) {
-    const uint32_t mw = max_over_g(amax_bits4(h[0]));
-    if (g == 0) amax[wave][r16] = mw;
-    __syncthreads();
     uint32_t m = 0;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) m = max(m, amax_bits4(h[c]));
+    m = max_over_g(m);
+    if (g == 0) amax[wave][r16] = m;
+    __syncthreads();
+    m = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) m = max(m, amax[w][r16]);
     float inv;
     const float sc = fp8_scale(m, inv);
     if (t < 0) return;
-    *(int*)((uint8_t*)p.h + row * p.I + col0 + 4 * g) = e4m3x4(h[0] * inv);
+#pragma unroll
+    for (int c = 0; c < CT; ++c) *(int*)((uint8_t*)p.h + row * p.I + col0 + 16 * c + 4 * g) = e4m3x4(h[c] * inv);
     if (wave == 0 && g == 0) ((float*)p.h_sf)[row * (p.I / 128) + col0 / 128] = sc;
-  } else if constexpr (F == Fmt::FP8) {
-    if (t >= 0) *(f32x4*)((float*)p.h + row * p.I + col0 + 4 * g) = h[0];
   } else if constexpr (F == Fmt::MX) {
-    const uint32_t m = max_over_g(max(amax_bits4(h[0]), amax_bits4(h[1])));
-    const int ex = mx_exponent_for_amax(__uint_as_float(m));
-    const float inv = exp2i(-ex);
-    if (t < 0) return;
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-      *(uint32_t*)((uint8_t*)p.h + row * p.I + col0 + 16 * c + 4 * g) =
-          f32x2_to_e4m3_sat(h[c][0] * inv, h[c][1] * inv) | f32x2_to_e4m3_sat(h[c][2] * inv, h[c][3] * inv) << 16;
-    // (a NaN in the block: UE8M0's NaN)
-    if (g == 0) ((uint8_t*)p.h_sf)[row * (p.I / 32) + slice] = m > 0x7F800000u ? (uint8_t)255 : (uint8_t)(ex + 127);
-  } else {
-    f32x4 v = h[0];
-    if constexpr (F == Fmt::NVF4) {
-      // block scale E4M3(amax / (6 c)), codes E2M1(h / (scale c)); kept as code x scale, exact in bf16
-      const uint32_t m = max_over_g(amax_bits4(v));
-      const float c = p.c_gs[e], s6 = __uint_as_float(m) / (6.0f * c);
-      const float sc = e4m3_byte<0>(__builtin_amdgcn_cvt_pk_fp8_f32(s6 > 448.0f ? 448.0f : s6, 0.0f, 0, false));
-      const float den = sc * c, inv = den > 0.0f ? 1.0f / den : 0.0f;
+    for (int b = 0; b < CT; b += 2) {
+      const uint32_t m = max_over_g(max(amax_bits4(h[b]), amax_bits4(h[b + 1])));
+      const int ex = mx_exponent_for_amax(__uint_as_float(m));
+      const float inv = exp2i(-ex);
+      const int at = col0 + 16 * b;
+      if (t < 0 || at >= p.I) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = e2m1_rne_sat(v[i] * inv) * sc;  // (a NaN in the block: sc is NaN)
+      for (int c = b; c < b + 2; ++c)
+        *(uint32_t*)((uint8_t*)p.h + row * p.I + col0 + 16 * c + 4 * g) =
+            f32x2_to_e4m3_sat(h[c][0] * inv, h[c][1] * inv) | f32x2_to_e4m3_sat(h[c][2] * inv, h[c][3] * inv) << 16;
+      // (a NaN in the block: UE8M0's NaN)
+      if (g == 0) ((uint8_t*)p.h_sf)[row * (p.I / 32) + at / 32] = m > 0x7F800000u ? (uint8_t)255 : (uint8_t)(ex + 127);
     }
-    if (t >= 0)
-      *(uint2*)((uint16_t*)p.h + row * p.I + col0 + 4 * g) = uint2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+  } else {
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      f32x4 v = h[c];
+      const int at = col0 + 16 * c + 4 * g;
+      if constexpr (F == Fmt::NVF4) {
+        // block scale E4M3(amax / (6 c)), codes E2M1(h / (scale c)); kept as code x scale, exact in bf16
+        const uint32_t m = max_over_g(amax_bits4(v));
+        const float cs = p.c_gs[e], s6 = __uint_as_float(m) / (6.0f * cs);
+        const float sc = e4m3_byte<0>(__builtin_amdgcn_cvt_pk_fp8_f32(s6 > 448.0f ? 448.0f : s6, 0.0f, 0, false));
+        const float den = sc * cs, inv = den > 0.0f ? 1.0f / den : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = e2m1_rne_sat(v[i] * inv) * sc;  // (a NaN in the block: sc is NaN)
+      }
+      if (t < 0 || at >= p.I) continue;
+      if constexpr (F == Fmt::FP8) *(f32x4*)((float*)p.h + row * p.I + at) = v;
+      else *(uint2*)((uint16_t*)p.h + row * p.I + at) = uint2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+    }
   }
 }
 
-// ---------------------------------------------------------------- down
 // A workgroup barrier that waits for this wave's LDS accesses only.
 MOE_DEV void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// ---------------------------------------------------------------- down
 // R: 16-row weight tiles (output column groups) per workgroup.  HL (FP8): h is fp32 and
 // quantised into LDS here.
 template <Fmt F, int WAVES, int R, int D, bool HL>
@@ -929,11 +940,12 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   d.ksteps = prepared_ksteps(wf, a.I);
   d.steps = nv4w(a.fmt) ? (d.ksteps + 1) / 2 : d.ksteps;
 
-  auto up = [&](auto fmt, auto waves, auto ksp, auto depth) {
+  auto up = [&](auto fmt, auto waves, auto ksp, auto groups, auto depth) {
     constexpr Fmt F = decltype(fmt)::value;
-    constexpr int W = decltype(waves)::value, KSP = decltype(ksp)::value, D = decltype(depth)::value;
-    constexpr int per = W / KSP * (F == Fmt::MX ? 32 : 16);  // columns of h per workgroup
-    hipLaunchKernelGGL((few_gate_up_kernel<F, W, KSP, D>), dim3((unsigned)((a.I + per - 1) / per * p.max_units + 1)), dim3(64 * W), 0, s, u);
+    constexpr int W = decltype(waves)::value, KSP = decltype(ksp)::value, CT = decltype(groups)::value,
+                  D = decltype(depth)::value;
+    constexpr int per = W / KSP * 16 * CT;  // columns of h per workgroup
+    hipLaunchKernelGGL((few_gate_up_kernel<F, W, KSP, CT, D>), dim3((unsigned)((a.I + per - 1) / per * p.max_units + 1)), dim3(64 * W), 0, s, u);
   };
   auto down = [&](auto fmt, auto waves, auto rows, auto depth, auto lds_h) {
     constexpr Fmt F = decltype(fmt)::value;
@@ -946,27 +958,27 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   switch (a.fmt) {
     case Fmt::FP8:
       if (few_h_fp32(a.fmt, a.T, a.topk, a.E, a.I)) {
-        up(F_(Fmt::FP8), C_(4), C_(4), C_(2));
+        up(F_(Fmt::FP8), C_(4), C_(4), C_(1), C_(2));
         down(F_(Fmt::FP8), C_(8), C_(2), C_(2), std::true_type{});
       } else {
-        up(F_(Fmt::FP8), C_(8), C_(1), C_(2));
+        up(F_(Fmt::FP8), C_(8), C_(1), C_(1), C_(2));
         down(F_(Fmt::FP8), C_(8), C_(2), C_(2), std::false_type{});
       }
       break;
     case Fmt::BF16:
-      up(F_(Fmt::BF16), C_(4), C_(4), C_(2));
+      up(F_(Fmt::BF16), C_(4), C_(4), C_(1), C_(2));
       down(F_(Fmt::BF16), C_(8), C_(1), C_(2), std::false_type{});
       break;
     case Fmt::MX:
-      up(F_(Fmt::MX), C_(4), C_(4), C_(2));
+      up(F_(Fmt::MX), C_(4), C_(4), C_(2), C_(2));
       down(F_(Fmt::MX), C_(8), C_(4), C_(2), std::false_type{});
       break;
     case Fmt::NV4:
-      up(F_(Fmt::NV4), C_(4), C_(4), C_(2));
+      up(F_(Fmt::NV4), C_(4), C_(4), C_(1), C_(2));
       down(F_(Fmt::NV4), C_(8), C_(2), C_(2), std::false_type{});
       break;
     case Fmt::NVF4:
-      up(F_(Fmt::NVF4), C_(4), C_(4), C_(2));
+      up(F_(Fmt::NVF4), C_(4), C_(4), C_(2), C_(1));
       down(F_(Fmt::NVF4), C_(8), C_(2), C_(2), std::false_type{});
       break;
   }
