@@ -446,24 +446,27 @@ moe_status moe_add_rmsnorm(const moe_handle* h, int32_t num_tokens, const void* 
                            float eps, void* residual_out, void* x_norm, void* x_q, void* x_sf, float x_global_scale,
                            hipStream_t stream);
 
-/* Bytes of workspace moe_router_logits needs (0 for many sizes, and if num_tokens is
-   out of range or the call would not be supported). */
+/* Bytes of workspace moe_router_logits needs for num_tokens tokens (0 for small sizes, and if
+   num_tokens is out of range or the call would not be supported).  It never shrinks as num_tokens
+   grows: one of the largest step's serves them all. */
 size_t moe_router_workspace_size(const moe_handle* h, int32_t num_tokens);
 
 /* Router logits ([ActPack] routing_input_mode FromLogits: the routing_logits it takes):
    logits[t,e] = sum over hidden of x[t,:] * router_w[e,:], x [T,H] bf16 (x_norm of
    moe_add_rmsnorm), router_w [E,H] bf16 or fp32 (router_w_fp32), logits [T,E] fp32.  The sums
    are fp32, of exact products for bf16 weights and of products exact to 2^-24 for fp32
-   ones; their order depends on the sizes alone.  x, router_w and logits 16-byte aligned; ws as for
-   moe_plan.  hidden above 32768 or T x E above 2^31 is MOE_ERR_UNSUPPORTED. */
+   ones; their order depends on the sizes alone.  A NaN or infinity stays in its token's row or its
+   expert's column; an infinity of x with fp32 router_w makes the row NaN where the infinite product
+   would be, and may where it would not (an fp32 weight is a sum of three terms, some of them zero).
+   x, router_w and logits 16-byte aligned; ws as for moe_plan.  hidden above 32768 or T x E above 2^31 is MOE_ERR_UNSUPPORTED. */
 moe_status moe_router_logits(const moe_handle* h, int32_t num_tokens, const void* x, const void* router_w,
                              int32_t router_w_fp32, float* logits, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Largest num_tokens of moe_forward_few. */
 #define MOE_FEW_MAX_TOKENS 32
 
-/* Bytes of workspace moe_forward_few needs for num_tokens tokens; 0 if num_tokens is
-   out of range or above MOE_FEW_MAX_TOKENS. */
+/* Bytes of workspace moe_forward_few needs for num_tokens tokens (it never shrinks as
+   num_tokens grows); 0 if num_tokens is out of range or above MOE_FEW_MAX_TOKENS. */
 size_t moe_few_workspace_size(const moe_handle* h, int32_t num_tokens);
 
 /* The routed layer for few tokens: moe_forward_ex's operator, formats and arguments in two

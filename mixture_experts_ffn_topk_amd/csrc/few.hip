@@ -870,7 +870,8 @@ FewBuffers few_buffers(Fmt f, int T, int topk, int E, int H, int I) {
   FewBuffers b{};
   if (T == 0) return b;
   const size_t pairs = (size_t)T * topk;
-  b.h = pairs * I * (few_h_fp32(f, T, topk, E, I) ? 4 : bf16_mma(f) ? 2 : 1);
+  // (FP8: room for fp32 whether this T takes it or not, so that the size never shrinks as T grows)
+  b.h = pairs * I * (f == Fmt::FP8 ? 4 : bf16_mma(f) ? 2 : 1);
   b.h_sf = f == Fmt::FP8 ? pairs * (I / 128) * 4 : f == Fmt::MX ? pairs * (I / 32) : 0;
   const DownPlan d = down_plan(f, H);
   b.tables = few_table_words(T * topk, few_max_units(E, T, topk)) * 4;

@@ -33,7 +33,7 @@ struct RouterArgs {
   float* logits;  // [T, E]
   float* partial; // router_workspace_bytes(T, H, E)
 };
-size_t router_workspace_bytes(int T, int H, int E);
+size_t router_workspace_bytes(int T, int H, int E);  // never shrinks with T
 hipError_t launch_router_logits(const RouterArgs& a, hipStream_t s);
 
 // ---------------------------------------------------------------- the layer for few tokens

@@ -7,6 +7,7 @@
 // holds all 24 bits of the weight (w = w0 + w1 + w2 exactly, barring underflow),
 // each multiplied on the matrix cores: bf16 products are exact in fp32, so the
 // result has the error of an fp32 sum.
+#include <algorithm>
 #include <type_traits>
 
 #include "gemm_common.h"
@@ -122,7 +123,9 @@ __global__ __launch_bounds__(64 * WT * WK) void router_tile_kernel(RouterParams 
   using TL = RouterTile<BM, BN, WT, WK, STG, W32>;
   constexpr int F = TL::kF;
   constexpr bool k32 = BM >= 32;           // 32x32x16 MFMA, else 16x16x32
-  constexpr int WM = WT >= 4 ? 2 : 1, WN = WT / WM;  // waves over the tile
+  // Waves over the tile.  fp32 weights: every wave takes all BM tokens, so that each weight is
+  // split once (2 x 2 waves split it twice: T 2047 at H 7168, E 256 50.7 us, this 42.0).
+  constexpr int WM = WT >= 4 && !W32 ? 2 : 1, WN = WT / WM;
   constexpr int R = k32 ? 32 : 16;
   constexpr int MT = BM / WM / R, NT = BN / WN / R;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TL::kLds];
@@ -282,7 +285,7 @@ __global__ __launch_bounds__(256) void router_sum_kernel(const float* __restrict
 }
 
 struct RouterPlan {
-  int kind;  // 0: dot products, 16 and 32: square tiles of one wave per K group, 64: 64 x 128 tiles
+  int kind;  // 0: dot products, 16 and 32: square tiles of one wave per K group, 64 and 128: kind x 128 tiles
   int splits;
 };
 // The smallest tile that leaves no CU a second workgroup (small tiles have the most
@@ -291,27 +294,36 @@ struct RouterPlan {
 //   T 256 (256 / 64 / 8 workgroups): 16-tiles 7.7 us, 32-tiles 12.6, 64-tiles 38
 //   T 1024: 16-tiles 22 us, 32-tiles 12.8, 64-tiles in 4 splits 15.5
 //   T 2048: 32-tiles 24 us, 64-tiles in 4 splits 18.2; T 8192: 123 and (1 split) 51
+//   T 16384: 64-tiles 105 us, 128-tiles 79; T 8192 at H 4096, E 384: 48 and 37
 // With E <= 32 a 32-tile reads x once as it is: T 8192, E 32: 23.5 us against 27.
-RouterPlan router_plan(int T, int H, int E) {
+// fp32 weights are bound by their splitting, which a 128-tile does half as often: it is
+// taken wherever 8 splits of it fill the part (T 2047, 4096, 8192: 36.7, 59.5, 112 us;
+// 64-tiles 42.0, 71.6, 132; below that, T 1000, 33.9 and 26.2).
+RouterPlan router_plan(int T, int H, int E, bool w_f32) {
   if (T <= 4) return RouterPlan{0, 1};
   auto tiles = [&](int m, int n) { return (long long)((T + m - 1) / m) * ((E + n - 1) / n); };
   if (tiles(16, 16) <= 256) return RouterPlan{16, 1};
   if (tiles(32, 32) <= 256 || E <= 32) return RouterPlan{32, 1};
+  const int bm = (w_f32 ? tiles(128, 128) * 8 >= 256 : tiles(64, 128) > 256) ? 128 : 64;
   int splits = 1;
-  while (splits < 8 && tiles(64, 128) * splits * 2 <= 256 && splits * 16 * 64 <= H) splits *= 2;
-  return RouterPlan{64, splits};
+  while (splits < 8 && tiles(bm, 128) * splits * 2 <= 256 && splits * 16 * 64 <= H) splits *= 2;
+  return RouterPlan{bm, splits};
 }
 
 }  // namespace
 
 size_t router_workspace_bytes(int T, int H, int E) {
-  const RouterPlan r = router_plan(T, H, E);
-  return r.splits > 1 ? (size_t)r.splits * T * E * 4 : 0;
+  // Enough for the partial sums of every plan of up to T tokens and both types of weights: a split
+  // plan has more than 256 32-tiles, at most 8 splits of at least 512 elements, and at most 256
+  // workgroups of 128 rows.
+  const long long n_tiles = (E + 127) / 128;
+  if (E <= 32 || H < 1024 || (long long)((T + 31) / 32) * ((E + 31) / 32) <= 256) return 0;
+  return (size_t)std::min<long long>(8LL * T, 256 * 128 / n_tiles) * E * 4;
 }
 
 hipError_t launch_router_logits(const RouterArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  const RouterPlan r = router_plan(a.T, a.H, a.E);
+  const RouterPlan r = router_plan(a.T, a.H, a.E, a.w_f32);
   RouterParams p{(const uint8_t*)a.x, (const uint8_t*)a.w, r.splits > 1 ? a.partial : a.logits, a.T, a.H, a.E, 0,
                  (a.H + 63) / 64, r.splits};
   if (r.kind == 0) {
@@ -326,7 +338,7 @@ hipError_t launch_router_logits(const RouterArgs& a, hipStream_t s) {
     else go(std::integral_constant<int, 4>{});
     return hipGetLastError();
   }
-  const int bm = r.kind, bn = r.kind == 64 ? 128 : r.kind;
+  const int bm = r.kind, bn = r.kind >= 64 ? 128 : r.kind;
   p.n_tiles = (a.E + bn - 1) / bn;
   const dim3 grid((unsigned)((a.T + bm - 1) / bm * p.n_tiles * r.splits));
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, p); };
@@ -334,8 +346,10 @@ hipError_t launch_router_logits(const RouterArgs& a, hipStream_t s) {
     a.w_f32 ? go(router_tile_kernel<16, 16, 1, 4, 4, false, true>) : go(router_tile_kernel<16, 16, 1, 4, 4, false, false>);
   else if (r.kind == 32)
     a.w_f32 ? go(router_tile_kernel<32, 32, 1, 4, 3, true, true>) : go(router_tile_kernel<32, 32, 1, 4, 4, true, false>);
-  else
+  else if (r.kind == 64)
     a.w_f32 ? go(router_tile_kernel<64, 128, 4, 1, 3, true, true>) : go(router_tile_kernel<64, 128, 4, 1, 4, true, false>);
+  else
+    a.w_f32 ? go(router_tile_kernel<128, 128, 4, 1, 3, true, true>) : go(router_tile_kernel<128, 128, 4, 1, 4, true, false>);
   if (r.splits > 1) {
     const size_t n = (size_t)a.T * a.E;
     hipLaunchKernelGGL(router_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.partial, a.logits, n,

@@ -191,7 +191,8 @@ def router_tolerance(x, w, H):
 @pytest.mark.parametrize("T,H,E", [
     (1, 7168, 256), (1, 64, 1), (2, 96, 3), (3, 2880, 128), (5, 4096, 8), (8, 512, 40), (9, 512, 33), (16, 1056, 17),
     (31, 7168, 256), (64, 2880, 128), (100, 320, 512), (257, 7168, 64), (300, 32, 1000), (1000, 1024, 256),
-    (2047, 2880, 128), (4099, 256, 8), (8192, 128, 257)])
+    (2047, 2880, 128), (4099, 256, 8), (8192, 128, 257),
+    (1500, 1056, 257), (4100, 1024, 128), (8500, 192, 260)])
 @pytest.mark.parametrize("w32", [False, True])
 def test_router_logits(T, H, E, w32):
     print(f"[router] T={T} H={H} E={E} w32={w32}", flush=True)

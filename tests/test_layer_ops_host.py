@@ -96,6 +96,18 @@ def test_router_refusals():
     lib.moe_destroy(h)
 
 
+def test_a_workspace_of_the_largest_step_serves_every_smaller_one():
+    for fmt, kw in ((2, {}), (0, {}), (2, dict(num_experts=40, hidden=1024)), (2, dict(num_experts=1000, num_topk=1)),
+                    (2, dict(num_experts=129, hidden=2048, num_topk=1)), (2, dict(num_experts=32)),
+                    (2, dict(hidden=992, intermediate_hidden=96)), (0, dict(hidden=256, intermediate_hidden=128))):
+        lib, h = handle(format=fmt, max_num_tokens=40000, **kw)
+        router = [lib.moe_router_workspace_size(h, T) for T in range(0, 40001, 7)]
+        assert router == sorted(router)
+        few_sizes = [lib.moe_few_workspace_size(h, T) for T in range(33)]
+        assert few_sizes == sorted(few_sizes), few_sizes
+        lib.moe_destroy(h)
+
+
 def few(lib, h, **kw):
     a = dict(T=4, x=M, sf=2 * M, ids=3 * M, tw=4 * M, lg=None, b=None, sh=None, rs=None, out=5 * M, ws=6 * M, n=1 << 40,
              w=mx._Weights(7 * M, 8 * M, 9 * M, 10 * M))
