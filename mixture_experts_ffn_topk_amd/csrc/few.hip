@@ -846,6 +846,9 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
 
 }  // namespace
 
+// The top-k in the first launch saves a launch, but every workgroup repeats it.  Measured, us, in the
+// launch / before it: MX H 2880, I 2880, E 128, k 4: T 1 23.0 / 24.4, T 4 51.2 / 50.6, T 8 87.5 / 77.3,
+// T 32 442 / 195; FP8 H 7168, I 256, E 256, k 8: T 1 23.3 / 24.8, T 4 38.8 / 40.1, T 8 68.6 / 64.8.
 bool few_routes_in_launch(int T) { return T <= 4; }
 
 // FP8: h in fp32 between the launches (see above).  Whole 128-column blocks need about as many
@@ -946,13 +949,15 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
     constexpr int W = decltype(waves)::value, KSP = decltype(ksp)::value, CT = decltype(groups)::value,
                   D = decltype(depth)::value;
     constexpr int per = W / KSP * 16 * CT;  // columns of h per workgroup
-    hipLaunchKernelGGL((few_gate_up_kernel<F, W, KSP, CT, D>), dim3((unsigned)((a.I + per - 1) / per * p.max_units + 1)), dim3(64 * W), 0, s, u);
+    const dim3 grid((unsigned)((a.I + per - 1) / per * p.max_units + 1));
+    hipLaunchKernelGGL((few_gate_up_kernel<F, W, KSP, CT, D>), grid, dim3(64 * W), 0, s, u);
   };
   auto down = [&](auto fmt, auto waves, auto rows, auto depth, auto lds_h) {
     constexpr Fmt F = decltype(fmt)::value;
     constexpr int W = decltype(waves)::value, R = decltype(rows)::value, D = decltype(depth)::value;
-    hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)(dp.n_blocks * dp.splits)), dim3(64 * W), (size_t)W * R * a.T * 64 + few_table_words(a.T * a.topk, p.max_units) * 4,
-                       s, d);
+    const size_t lds = (size_t)W * R * a.T * 64 + few_table_words(a.T * a.topk, p.max_units) * 4;
+    hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)(dp.n_blocks * dp.splits)),
+                       dim3(64 * W), lds, s, d);
   };
 #define C_(v) std::integral_constant<int, v>{}
 #define F_(v) std::integral_constant<Fmt, v>{}

@@ -367,7 +367,8 @@ def test_few(fmt, T, routing):
     ("nvfp4_w4a16", 64, 64, 4, 2, 7), ("nvfp4_w4a16", 1216, 192, 9, 4, 1), ("nvfp4", 64, 64, 4, 2, 7),
     ("nvfp4", 192, 1088, 9, 4, 18),
     ("bf16", 64, 64, 1000, 32, 32),            # more experts and slots than any wave holds
-    ("w4a8_mx", 64, 64, 40, 32, 32)])
+    ("w4a8_mx", 64, 64, 40, 32, 32),
+    ("w4a8_mx", 512, 64, 1000, 32, 32)])       # the largest tables and sums in LDS
 def test_few_sizes(fmt, H, I, E, k, T):
     sh = shape(fmt, T, H, I, E, k, seed=H + I)
     print(f"[few] {sh}", flush=True)
@@ -438,6 +439,70 @@ def test_few_nan_stays_in_its_token(fmt, T):
     assert torch.isnan(got[1]).all()
     keep = [t for t in range(T) if t != 1]
     assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4_w4a16", "nvfp4"])
+def test_few_nan_stays_in_its_token_nvfp4(fmt):
+    H, I = SIZES[fmt]
+    sh = shape(fmt, 5, H, I, 4, 2, seed=32)
+    inp, d, kw, okw = few_inputs(sh)
+    moe = make_moe(sh)
+    clean = run_few(moe, d, 5, kw)
+    if fmt == "nvfp4":
+        d["x_sf"] = d["x_sf"].clone()
+        d["x_sf"].view(torch.uint8)[1, 3] = 0x7F
+    else:
+        d["x"] = d["x"].clone()
+        d["x"].view(torch.bfloat16)[1, H - 1] = float("nan")
+    got = run_few(moe, d, 5, kw)
+    assert torch.isnan(got[1]).all()
+    keep = [0, 2, 3, 4]
+    assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("fmt", list(SIZES))
+def test_few_masked_slots_weights_are_not_read(fmt):
+    """NaN and infinite router weights of masked slots change nothing; a valid slot's NaN stays in its token."""
+    H, I = SIZES[fmt]
+    T, E, k = 4, 5, 3
+    ids = np.array([[0, -1, 2], [-1, -1, -1], [4, 4, E], [1, 2, 3]])
+    tw = np.full((T, k), 0.25, np.float32)
+    sh = shape(fmt, T, H, I, E, k, seed=14)
+    inp, d, kw, _ = few_inputs(sh, ids, tw)
+    moe = make_moe(sh)
+    clean = run_few(moe, d, T, kw)
+    bad = tw.copy()
+    bad[0, 1] = bad[1, 0] = np.nan
+    bad[1, 2] = bad[2, 2] = np.inf
+    inp, d, kw, _ = few_inputs(sh, ids, bad)
+    assert torch.equal(run_few(moe, d, T, kw)[:T], clean[:T])
+    bad[3, 1] = np.nan
+    inp, d, kw, _ = few_inputs(sh, ids, bad)
+    got = run_few(moe, d, T, kw)
+    assert torch.equal(got[:3], clean[:3]) and torch.isnan(got[3]).all()
+
+
+@pytest.mark.parametrize("T", [4, 12])
+def test_few_routes_odd_logits_as_the_top_k_does(T):
+    """Rows of NaN, of infinities, of one value, of the type's lowest value: experts and weights as moe_forward has them,
+    in the launch (4 tokens) and before it (12)."""
+    sh = shape("w4a8_mx", T, 416, 288, 70, 3, "from_logits", seed=15)
+    inp, d, kw, _ = few_inputs(sh)
+    lg = d["logits"]
+    lg[0] = float("nan")
+    lg[1] = torch.finfo(torch.float32).min
+    lg[1, 69] = 1.0
+    lg[2] = float("-inf")
+    lg[2, 65] = 0.5
+    lg[3, 3] = float("nan")
+    lg[3, 66] = float("inf")
+    moe = make_moe(sh)
+    run_few(moe, d, T, kw)
+    ids, tw = torch.empty_like(d["topk_idx"]), torch.empty_like(d["topk_weights"])
+    moe.forward(T, d["x"], d["x_sf"], ids, tw, lg, prepared(moe, d), torch.empty((T, 416), dtype=torch.bfloat16, device="cuda"),
+                moe.alloc_workspace(T))
+    assert torch.equal(d["topk_idx"], ids)
+    assert torch.equal(d["topk_weights"].view(torch.int32), tw.view(torch.int32))
 
 
 def test_few_infinite_weight_reaches_only_its_tokens():
@@ -567,3 +632,15 @@ def test_few_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o[:8], want[:8])
+
+
+def test_a_workspace_for_32_tokens_serves_fewer():
+    sh = shape("fp8_block128", 32, 256, 256, 6, 2, seed=16)
+    inp, d, kw, _ = few_inputs(sh)
+    moe = make_moe(sh)
+    ws = moe.alloc_few_workspace(32)
+    whole = run_few(moe, d, 32, kw, ws=ws)
+    for T in (1, 2, 9, 31):
+        own = run_few(moe, d, T, kw)
+        assert torch.equal(run_few(moe, d, T, kw, ws=ws)[:T], own[:T])
+    assert torch.equal(run_few(moe, d, 32, kw, ws=ws)[:32], whole[:32])
