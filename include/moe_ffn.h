@@ -456,9 +456,8 @@ size_t moe_router_workspace_size(const moe_handle* h, int32_t num_tokens);
    moe_add_rmsnorm), router_w [E,H] bf16 or fp32 (router_w_fp32), logits [T,E] fp32.  The sums
    are fp32, of exact products for bf16 weights and of products exact to 2^-24 for fp32
    ones; their order depends on the sizes alone.  A NaN or infinity stays in its token's row or its
-   expert's column; an infinity of x with fp32 router_w makes the row NaN where the infinite product
-   would be, and may where it would not (an fp32 weight is a sum of three terms, some of them zero).
-   x, router_w and logits 16-byte aligned; ws as for moe_plan.  hidden above 32768 or T x E above 2^31 is MOE_ERR_UNSUPPORTED. */
+   expert's column.  x, router_w and logits 16-byte aligned; ws as for moe_plan.  hidden above 32768
+   or T x E above 2^31 is MOE_ERR_UNSUPPORTED. */
 moe_status moe_router_logits(const moe_handle* h, int32_t num_tokens, const void* x, const void* router_w,
                              int32_t router_w_fp32, float* logits, void* ws, size_t ws_bytes, hipStream_t stream);
 

@@ -245,6 +245,38 @@ def test_router_nan_and_inf_stay_in_their_row_and_column(T):
         assert torch.equal(got[: T - 1][:, keep], clean_w[: T - 1][:, keep])
 
 
+@pytest.mark.parametrize("T,H,E", [(2, 640, 48), (6, 640, 48), (40, 640, 48), (700, 640, 48), (1500, 2112, 257), (4100, 1024, 128)])
+@pytest.mark.parametrize("w32", [False, True])
+def test_router_infinities_keep_their_sign(T, H, E, w32):
+    """An infinite activation or weight gives infinities of the products' signs, NaN where both signs or 0 x inf meet."""
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, H, generator=g).bfloat16()
+    w = torch.randn(E, H, generator=g)
+    w[w == 0] = 1.0
+    w[:, 9] = torch.where(w[:, 9].bfloat16() == 0, 1.0, w[:, 9])
+    x[0, 9] = float("-inf")
+    w[3, 9] = 0.0
+    w[5, H - 1] = float("inf")
+    w[6, 1], w[6, 2] = float("inf"), float("-inf")
+    x[:, 1], x[:, 2] = 1.0, 2.0
+    x[1, H - 1] = 0.0
+    if not w32:
+        w = w.bfloat16()
+    moe = MoEFFN(H, 64, E, 1, T, fmt="w4a8_mx")
+    out = torch.empty(T, E, device="cuda")
+    moe.router_logits(T, x.cuda(), w.cuda(), out, moe.alloc_router_workspace(T))
+    got = out.cpu().double()
+    ref = torch.zeros(T, E, dtype=torch.float64)
+    ref[0] = -torch.sign(w[:, 9].double()) * float("inf")
+    ref[:, 5] = torch.sign(x[:, H - 1].double()) * float("inf")
+    ref[0, 5] = ref[0, 5] - torch.sign(w[5, 9].double()) * float("inf")
+    ref[:, 6] = float("nan")
+    odd = ~torch.isfinite(ref)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    inf = odd & ~torch.isnan(ref)
+    assert torch.equal(got[inf], ref[inf]) and torch.isfinite(got[~odd]).all()
+
+
 # ------------------------------------------------------------------ the layer for few tokens
 def shape(fmt, T, H, I, E, k, routing="precomputed", seed=1, **kw):
     return moe_synth.MoEShape(f"few_{fmt}", seed, T, H, I, E, k, fmt, routing, **kw)
