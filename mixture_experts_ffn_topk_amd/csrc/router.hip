@@ -142,7 +142,7 @@ __global__ __launch_bounds__(64 * WT * WK) void router_tile_kernel(RouterParams 
   constexpr int F = TL::kF;
   constexpr bool k32 = BM >= 32;           // 32x32x16 MFMA, else 16x16x32
   // Waves over the tile.  fp32 weights: every wave takes all BM tokens, so that each weight is
-  // split once (2 x 2 waves split it twice: T 2047 at H 7168, E 256 50.7 us, this 42.0).
+  // split once (128 x 128 tiles at T 8192, H 7168, E 256, 2 splits: 133 us with 2 x 2 waves, this 112).
   constexpr int WM = WT >= 4 && !W32 ? 2 : 1, WN = WT / WM;
   constexpr int R = k32 ? 32 : 16;
   constexpr int MT = BM / WM / R, NT = BN / WN / R;
@@ -297,52 +297,56 @@ __global__ __launch_bounds__(64 * WT * WK) void router_tile_kernel(RouterParams 
   }
 }
 
-// logits = the splits' partial sums, added in order
-template <bool W32>
+// logits = the splits' partial sums, added in order (fp32 weights; bf16 ones never split)
 __global__ __launch_bounds__(256) void router_sum_kernel(RouterParams p, float* __restrict__ out) {
   const size_t n = (size_t)p.T * p.E, i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float s = p.out[i];
   for (int k = 1; k < p.splits; ++k) s += p.out[(size_t)k * n + i];
-  if (W32 && s != s) s = plain_dot(p, (int)(i / p.E), (int)(i % p.E));
+  if (s != s) s = plain_dot(p, (int)(i / p.E), (int)(i % p.E));
   out[i] = s;
 }
 
 struct RouterPlan {
-  int kind;  // 0: dot products, 16 and 32: square tiles of one wave per K group, 64 and 128: kind x 128 tiles
+  int bm, bn;  // tile; bm 0: dot products
   int splits;
 };
-// The smallest tile that leaves no CU a second workgroup (small tiles have the most
-// bytes per flop and the shortest way through K).  Measured, bf16, H 7168, E 256:
-//   T 1: dot 2.6 us, 16-tiles 5.8; T 4: 3.2 / 5.8; T 8: 7.2 / 5.8
-//   T 256 (256 / 64 / 8 workgroups): 16-tiles 7.7 us, 32-tiles 12.6, 64-tiles 38
-//   T 1024: 16-tiles 22 us, 32-tiles 12.8, 64-tiles in 4 splits 15.5
-//   T 2048: 32-tiles 24 us, 64-tiles in 4 splits 18.2; T 8192: 123 and (1 split) 51
-//   T 16384: 64-tiles 105 us, 128-tiles 79; T 8192 at H 4096, E 384: 48 and 37
-// With E <= 32 a 32-tile reads x once as it is: T 8192, E 32: 23.5 us against 27.
-// fp32 weights are bound by their splitting, which a 128-tile does half as often: it is
-// taken wherever 8 splits of it fill the part (T 2047, 4096, 8192: 36.7, 59.5, 112 us;
-// 64-tiles 42.0, 71.6, 132; below that, T 1000, 33.9 and 26.2).
+// The smallest tile that leaves no CU a second workgroup: small tiles have the most bytes per flop
+// and the shortest way through K.  Measured, bf16, H 7168, E 256 unless said, us:
+//   T 1: dot 2.6, 16 x 16 5.8; T 4: 3.2, 5.8; T 8: 7.2, 5.8
+//   T 256: 16 x 16 7.7, 32 x 32 12.6; T 1024: 22, 12.8, 32 x 64 17.6
+//   T 2048: 32 x 32 24.0, 32 x 64 18.5, 64 x 64 22.5; T 4096: 46.2, 35.0, 23.8, 64 x 128 39.5
+//   T 8192: 64 x 64 65, 64 x 128 51, 128 x 128 71; T 16384: 134, 105, 79
+//   T 8192, H 2880, E 128: 64 x 64 14.4, 64 x 128 19.3 (2 splits of it 16.9)
+// With E <= 32 a 32 x 32 tile reads x once as it is: T 8192, E 32: 23.5 against 27 with 64 x 128.
+// fp32 weights, whose splitting a taller tile repeats less often:
+//   T 1024: 32 x 32 25.1, 64 x 32 32.3; T 2047: 46.6, 33.4
+//   T 4096: 64 x 32 62.4, 128 x 64 in 2 splits 55.4 (1: 92.8), 128 x 128 in 4 57.1
+//   T 8192: 126, 107 (1 split), 128 x 128 in 2 105; T 16384: 128 x 64 214, 128 x 128 181
 RouterPlan router_plan(int T, int H, int E, bool w_f32) {
-  if (T <= 4) return RouterPlan{0, 1};
+  if (T <= 4) return RouterPlan{0, 1, 1};
   auto tiles = [&](int m, int n) { return (long long)((T + m - 1) / m) * ((E + n - 1) / n); };
-  if (tiles(16, 16) <= 256) return RouterPlan{16, 1};
-  if (tiles(32, 32) <= 256 || E <= 32) return RouterPlan{32, 1};
-  const int bm = (w_f32 ? tiles(128, 128) * 8 >= 256 : tiles(64, 128) > 256) ? 128 : 64;
-  int splits = 1;
-  while (splits < 8 && tiles(bm, 128) * splits * 2 <= 256 && splits * 16 * 64 <= H) splits *= 2;
-  return RouterPlan{bm, splits};
+  if (tiles(16, 16) <= 256) return RouterPlan{16, 16, 1};
+  if (tiles(32, 32) <= 256 || E <= 32) return RouterPlan{32, 32, 1};
+  if (w_f32) {
+    if (tiles(64, 32) <= 256) return RouterPlan{64, 32, 1};
+    const long long n = tiles(128, 64);
+    if (n > 256) return RouterPlan{128, 128, 1};
+    return RouterPlan{128, 64, std::max(1, std::min((int)(256 / n), H / 1024))};
+  }
+  if (tiles(32, 64) <= 256) return RouterPlan{32, 64, 1};
+  if (tiles(64, 64) <= 256) return RouterPlan{64, 64, 1};
+  return tiles(64, 128) <= 256 ? RouterPlan{64, 128, 1} : RouterPlan{128, 128, 1};
 }
 
 }  // namespace
 
 size_t router_workspace_bytes(int T, int H, int E) {
-  // Enough for the partial sums of every plan of up to T tokens and both types of weights: a split
-  // plan has more than 256 32-tiles, at most 8 splits of at least 512 elements, and at most 256
-  // workgroups of 128 rows.
-  const long long n_tiles = (E + 127) / 128;
-  if (E <= 32 || H < 1024 || (long long)((T + 31) / 32) * ((E + 31) / 32) <= 256) return 0;
-  return (size_t)std::min<long long>(8LL * T, 256 * 128 / n_tiles) * E * 4;
+  // Enough for the partial sums of every plan of up to T tokens with fp32 weights (bf16 ones never
+  // split): a split plan has more than 256 tiles of 64 x 32, and 3 splits (more than 64 of its own
+  // tiles) and 256 workgroups at most.
+  if (E <= 32 || H < 2048 || (long long)((T + 63) / 64) * ((E + 31) / 32) <= 256) return 0;
+  return (size_t)std::min(3LL * T, 256LL * 128 / ((E + 63) / 64)) * E * 4;
 }
 
 hipError_t launch_router_logits(const RouterArgs& a, hipStream_t s) {
@@ -350,7 +354,7 @@ hipError_t launch_router_logits(const RouterArgs& a, hipStream_t s) {
   const RouterPlan r = router_plan(a.T, a.H, a.E, a.w_f32);
   RouterParams p{(const uint8_t*)a.x, (const uint8_t*)a.w, r.splits > 1 ? a.partial : a.logits, a.T, a.H, a.E, 0,
                  (a.H + 63) / 64, r.splits};
-  if (r.kind == 0) {
+  if (r.bm == 0) {
     auto go = [&](auto tt) {
       constexpr int TT = decltype(tt)::value;
       const dim3 grid((unsigned)a.E);
@@ -362,22 +366,26 @@ hipError_t launch_router_logits(const RouterArgs& a, hipStream_t s) {
     else go(std::integral_constant<int, 4>{});
     return hipGetLastError();
   }
-  const int bm = r.kind, bn = r.kind >= 64 ? 128 : r.kind;
-  p.n_tiles = (a.E + bn - 1) / bn;
-  const dim3 grid((unsigned)((a.T + bm - 1) / bm * p.n_tiles * r.splits));
+  p.n_tiles = (a.E + r.bn - 1) / r.bn;
+  const dim3 grid((unsigned)((a.T + r.bm - 1) / r.bm * p.n_tiles * r.splits));
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, p); };
-  if (r.kind == 16)
-    a.w_f32 ? go(router_tile_kernel<16, 16, 1, 4, 4, false, true>) : go(router_tile_kernel<16, 16, 1, 4, 4, false, false>);
-  else if (r.kind == 32)
-    a.w_f32 ? go(router_tile_kernel<32, 32, 1, 4, 3, true, true>) : go(router_tile_kernel<32, 32, 1, 4, 4, true, false>);
-  else if (r.kind == 64)
-    a.w_f32 ? go(router_tile_kernel<64, 128, 4, 1, 3, true, true>) : go(router_tile_kernel<64, 128, 4, 1, 4, true, false>);
-  else
-    a.w_f32 ? go(router_tile_kernel<128, 128, 4, 1, 3, true, true>) : go(router_tile_kernel<128, 128, 4, 1, 4, true, false>);
+  if (a.w_f32) {
+    if (r.bm == 16) go(router_tile_kernel<16, 16, 1, 4, 4, false, true>);
+    else if (r.bm == 32) go(router_tile_kernel<32, 32, 1, 4, 3, true, true>);
+    else if (r.bm == 64) go(router_tile_kernel<64, 32, 1, 4, 2, true, true>);
+    else if (r.bn == 64) go(router_tile_kernel<128, 64, 2, 2, 2, true, true>);
+    else go(router_tile_kernel<128, 128, 4, 1, 3, true, true>);
+  } else {
+    if (r.bm == 16) go(router_tile_kernel<16, 16, 1, 4, 4, false, false>);
+    else if (r.bm == 32 && r.bn == 32) go(router_tile_kernel<32, 32, 1, 4, 4, true, false>);
+    else if (r.bm == 32) go(router_tile_kernel<32, 64, 1, 4, 3, true, false>);
+    else if (r.bm == 64 && r.bn == 64) go(router_tile_kernel<64, 64, 1, 4, 2, true, false>);
+    else if (r.bm == 64) go(router_tile_kernel<64, 128, 4, 1, 4, true, false>);
+    else go(router_tile_kernel<128, 128, 4, 1, 4, true, false>);
+  }
   if (r.splits > 1) {
     const dim3 sum_grid((unsigned)(((size_t)a.T * a.E + 255) / 256));
-    if (a.w_f32) hipLaunchKernelGGL(router_sum_kernel<true>, sum_grid, dim3(256), 0, s, p, a.logits);
-    else hipLaunchKernelGGL(router_sum_kernel<false>, sum_grid, dim3(256), 0, s, p, a.logits);
+    hipLaunchKernelGGL(router_sum_kernel, sum_grid, dim3(256), 0, s, p, a.logits);
   }
   return hipGetLastError();
 }

@@ -183,16 +183,20 @@ def test_norm_leaves_rows_behind_the_last():
 
 # ------------------------------------------------------------------ router logits
 def router_tolerance(x, w, H):
-    """fp32 sums: at most 32 additions inside an MFMA, two MFMAs (six for fp32 weights) per K-step of 64 along a
-    chain, 8 waves and at most 64 splits, each within 2^-23 of the running sum's bound; fp32 weights lose 2^-24 each."""
-    return (32 + 6 * (-(-H // 512)) + 8 + 64) * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T) + 1e-37
+    """fp32 sums: at most 32 additions inside an MFMA; a chain of 12 MFMAs per K-step of 64 (three terms of four) over
+    a fourth of the K-steps, rounded up, where four groups share them, or over at most nine (the larger tiles: H up to
+    1024 in two groups, 2112 in four parts, 192 in one); 8 for the groups' and splits' sums: each within 2^-23 of the
+    running sum's bound.  The terms of an fp32 weight hold it exactly."""
+    steps = -(-H // 64)
+    return (40 + max(3 * (steps + 3), min(12 * steps, 108))) * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T) + 1e-37
 
 
 @pytest.mark.parametrize("T,H,E", [
     (1, 7168, 256), (1, 64, 1), (2, 96, 3), (3, 2880, 128), (5, 4096, 8), (8, 512, 40), (9, 512, 33), (16, 1056, 17),
     (31, 7168, 256), (64, 2880, 128), (100, 320, 512), (257, 7168, 64), (300, 32, 1000), (1000, 1024, 256),
     (2047, 2880, 128), (4099, 256, 8), (8192, 128, 257),
-    (1500, 1056, 257), (4100, 1024, 128), (8500, 192, 260)])
+    (1500, 1056, 257), (4100, 1024, 128), (8500, 192, 260),
+    (1111, 544, 256), (3000, 480, 200), (2500, 2080, 300), (5000, 2080, 129), (20000, 96, 40), (9000, 64, 64)])
 @pytest.mark.parametrize("w32", [False, True])
 def test_router_logits(T, H, E, w32):
     print(f"[router] T={T} H={H} E={E} w32={w32}", flush=True)
@@ -213,6 +217,22 @@ def test_router_logits(T, H, E, w32):
     again = torch.empty_like(out)
     moe.router_logits(T, x.cuda(), w.cuda(), again, ws)
     assert torch.equal(out[:T], again[:T])
+
+
+@pytest.mark.parametrize("T,H,E", [(1, 96, 5), (4, 96, 5), (64, 192, 40), (1000, 224, 256), (1500, 128, 256), (4096, 2080, 256),
+                                   (9000, 64, 300)])
+@pytest.mark.parametrize("w32", [False, True])
+def test_router_one_hot_rows_read_the_weights_exactly(T, H, E, w32):
+    g = torch.Generator().manual_seed(H)
+    w = torch.randn(E, H, generator=g) * torch.exp2(torch.randint(-60, 60, (E, H), generator=g).float())
+    w = w if w32 else w.bfloat16()
+    at = torch.randint(0, H, (T,), generator=g)
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    x[torch.arange(T), at] = -2.0
+    moe = MoEFFN(H, 64, E, 1, T, fmt="w4a8_mx")
+    out = torch.empty(T, E, device="cuda")
+    moe.router_logits(T, x.cuda(), w.cuda(), out, moe.alloc_router_workspace(T))
+    assert torch.equal(out.cpu(), -2.0 * w.float()[:, at].T)
 
 
 @pytest.mark.parametrize("T", [1, 6, 40, 700])
