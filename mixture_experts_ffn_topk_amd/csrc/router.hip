@@ -318,7 +318,8 @@ struct RouterPlan {
 //   T 2048: 32 x 32 24.0, 32 x 64 18.5, 64 x 64 22.5; T 4096: 46.2, 35.0, 23.8, 64 x 128 39.5
 //   T 8192: 64 x 64 65, 64 x 128 51, 128 x 128 71; T 16384: 134, 105, 79
 //   T 8192, H 2880, E 128: 64 x 64 14.4, 64 x 128 19.3 (2 splits of it 16.9)
-// With E <= 32 a 32 x 32 tile reads x once as it is: T 8192, E 32: 23.5 against 27 with 64 x 128.
+// With E <= 32 a tile 32 wide reads x once as it is: T 65536, H 1024, E 8 38.5 with 32 x 32, 41.6 with
+// 64 x 64 (fp32 weights: 57.9 with 32 x 32, 41.8 with 64 x 32).
 // fp32 weights, whose splitting a taller tile repeats less often:
 //   T 1024: 32 x 32 25.1, 64 x 32 32.3; T 2047: 46.6, 33.4
 //   T 4096: 64 x 32 62.4, 128 x 64 in 2 splits 55.4 (1: 92.8), 128 x 128 in 4 57.1
@@ -327,9 +328,9 @@ RouterPlan router_plan(int T, int H, int E, bool w_f32) {
   if (T <= 4) return RouterPlan{0, 1, 1};
   auto tiles = [&](int m, int n) { return (long long)((T + m - 1) / m) * ((E + n - 1) / n); };
   if (tiles(16, 16) <= 256) return RouterPlan{16, 16, 1};
-  if (tiles(32, 32) <= 256 || E <= 32) return RouterPlan{32, 32, 1};
+  if (tiles(32, 32) <= 256 || (E <= 32 && !w_f32)) return RouterPlan{32, 32, 1};
   if (w_f32) {
-    if (tiles(64, 32) <= 256) return RouterPlan{64, 32, 1};
+    if (tiles(64, 32) <= 256 || E <= 32) return RouterPlan{64, 32, 1};
     const long long n = tiles(128, 64);
     if (n > 256) return RouterPlan{128, 128, 1};
     return RouterPlan{128, 64, std::max(1, std::min((int)(256 / n), H / 1024))};

@@ -196,7 +196,7 @@ def router_tolerance(x, w, H):
     (31, 7168, 256), (64, 2880, 128), (100, 320, 512), (257, 7168, 64), (300, 32, 1000), (1000, 1024, 256),
     (2047, 2880, 128), (4099, 256, 8), (8192, 128, 257),
     (1500, 1056, 257), (4100, 1024, 128), (8500, 192, 260),
-    (1111, 544, 256), (3000, 480, 200), (2500, 2080, 300), (5000, 2080, 129), (20000, 96, 40), (9000, 64, 64)])
+    (1111, 544, 256), (3000, 480, 200), (2500, 2080, 300), (5000, 2080, 129), (20000, 96, 40), (9000, 64, 64), (17000, 64, 8)])
 @pytest.mark.parametrize("w32", [False, True])
 def test_router_logits(T, H, E, w32):
     print(f"[router] T={T} H={H} E={E} w32={w32}", flush=True)
