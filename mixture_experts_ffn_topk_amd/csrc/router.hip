@@ -311,42 +311,41 @@ struct RouterPlan {
   int bm, bn;  // tile; bm 0: dot products
   int splits;
 };
-// The smallest tile that leaves no CU a second workgroup: small tiles have the most bytes per flop
-// and the shortest way through K.  Measured, bf16, H 7168, E 256 unless said, us:
-//   T 1: dot 2.6, 16 x 16 5.8; T 4: 3.2, 5.8; T 8: 7.2, 5.8
-//   T 256: 16 x 16 7.7, 32 x 32 12.6; T 1024: 22, 12.8, 32 x 64 17.6
-//   T 2048: 32 x 32 24.0, 32 x 64 18.5, 64 x 64 22.5; T 4096: 46.2, 35.0, 23.8, 64 x 128 39.5
-//   T 8192: 64 x 64 65, 64 x 128 51, 128 x 128 71; T 16384: 134, 105, 79
-//   T 8192, H 2880, E 128: 64 x 64 14.4, 64 x 128 19.3 (2 splits of it 16.9)
-// With E <= 32 a tile 32 wide reads x once as it is: T 65536, H 1024, E 8 38.5 with 32 x 32, 41.6 with
-// 64 x 64 (fp32 weights: 57.9 with 32 x 32, 41.8 with 64 x 32).
-// fp32 weights, whose splitting a taller tile repeats less often:
-//   T 1024: 32 x 32 25.1, 64 x 32 32.3; T 2047: 46.6, 33.4
-//   T 4096: 64 x 32 62.4, 128 x 64 in 2 splits 55.4 (1: 92.8), 128 x 128 in 4 57.1
-//   T 8192: 126, 107 (1 split), 128 x 128 in 2 105; T 16384: 128 x 64 214, 128 x 128 181
+// The tile with the least rounds of 256 workgroups times what a round takes.  A small tile has the most
+// bytes per flop and the shortest way through K; a taller one splits fp32 weights less often.  A round's
+// time at H 7168, from runs at E 256, us (bf16, then fp32 weights):
+//   16 x 16: T 256 7.7, 13; 32 x 32: T 1024 12.7, T 2048 24.0; 25.1, 46.6
+//   32 x 64: T 2048 18.5, T 4096 35.0; 64 x 32: T 2048 33.4, T 4096 62.4
+//   64 x 64: T 4096 23.8, T 8192 65 (its rounds slow down as more of x streams), T 16384 134
+//   64 x 128: T 4096 39.5, T 8192 51, T 16384 105; 128 x 64: T 4096 92.8, T 8192 107, T 16384 214
+//   128 x 128: T 8192 71, T 16384 79; 177, 181
+// Splitting K costs a second launch of about 5 us.  It pays for fp32 weights between 64 x 32 and a full
+// round of 128 x 64 tiles (T 4096: 55.4 in 2 splits, 62.4 with 64 x 32), never for bf16 ones (T 2048:
+// 64 x 128 in 4 splits 18.2; T 4096 in 2: 26.9).  T 1 to 4: dot products 2.6 to 3.2, 16 x 16 5.8.
 RouterPlan router_plan(int T, int H, int E, bool w_f32) {
   if (T <= 4) return RouterPlan{0, 1, 1};
-  auto tiles = [&](int m, int n) { return (long long)((T + m - 1) / m) * ((E + n - 1) / n); };
-  if (tiles(16, 16) <= 256) return RouterPlan{16, 16, 1};
-  if (tiles(32, 32) <= 256 || (E <= 32 && !w_f32)) return RouterPlan{32, 32, 1};
-  if (w_f32) {
-    if (tiles(64, 32) <= 256 || E <= 32) return RouterPlan{64, 32, 1};
-    const long long n = tiles(128, 64);
-    if (n > 256) return RouterPlan{128, 128, 1};
-    return RouterPlan{128, 64, std::max(1, std::min((int)(256 / n), H / 1024))};
+  constexpr struct { int bm, bn; float us; } kTiles[2][6] = {
+      {{16, 16, 8}, {32, 32, 13}, {32, 64, 18}, {64, 64, 26}, {64, 128, 51}, {128, 128, 78}},
+      {{16, 16, 13}, {32, 32, 24}, {64, 32, 34}, {128, 64, 100}, {128, 128, 177}, {}}};
+  RouterPlan best{};
+  float least = INFINITY;
+  for (const auto& t : kTiles[w_f32]) {
+    if (t.bm == 0) break;
+    const long long n = (long long)((T + t.bm - 1) / t.bm) * ((E + t.bn - 1) / t.bn);
+    for (int splits = 1; splits == 1 || (w_f32 && t.bm == 128 && t.bn == 64 && splits <= 3 && n * splits <= 256); ++splits) {
+      const float us = (float)((n * splits + 255) / 256) * t.us * (float)H / (7168.0f * (float)splits) + (splits > 1 ? 5 : 0);
+      if (us < least) least = us, best = RouterPlan{t.bm, t.bn, splits};
+    }
   }
-  if (tiles(32, 64) <= 256) return RouterPlan{32, 64, 1};
-  if (tiles(64, 64) <= 256) return RouterPlan{64, 64, 1};
-  return tiles(64, 128) <= 256 ? RouterPlan{64, 128, 1} : RouterPlan{128, 128, 1};
+  return best;
 }
 
 }  // namespace
 
 size_t router_workspace_bytes(int T, int H, int E) {
   // Enough for the partial sums of every plan of up to T tokens with fp32 weights (bf16 ones never
-  // split): a split plan has more than 256 tiles of 64 x 32, and 3 splits (more than 64 of its own
-  // tiles) and 256 workgroups at most.
-  if (E <= 32 || H < 2048 || (long long)((T + 63) / 64) * ((E + 31) / 32) <= 256) return 0;
+  // split): a split plan has more than one round of 64 x 32 tiles, and at most 3 splits and 256 workgroups.
+  if (H < 1024 || (long long)((T + 63) / 64) * ((E + 31) / 32) <= 256) return 0;
   return (size_t)std::min(3LL * T, 256LL * 128 / ((E + 63) / 64)) * E * 4;
 }
 
