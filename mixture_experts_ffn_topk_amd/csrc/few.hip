@@ -437,7 +437,9 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   const int c = col[16 * half + r16];
   const int t = c == 0x7FFF ? -1 : c >> 5, slot = c & 31;
   // the lane's first byte of a K-step, as XFrag describes
-  const uint32_t at = F == Fmt::NV4 ? 128u * (g >> 1) + 16u * (g & 1) : F == Fmt::NVF4 ? 32u * (g >> 1) + 4u * (g & 1) : 16u * g;
+  const uint32_t at = F == Fmt::NV4    ? 128u * (g >> 1) + 16u * (g & 1)
+                      : F == Fmt::NVF4 ? 32u * (g >> 1) + 4u * (g & 1)
+                                       : 16u * g;
   const uint32_t sat = F == Fmt::MX ? (uint32_t)g : F == Fmt::NVF4 ? 4u * (g >> 1) : 0u;
   const uint32_t xo = t >= 0 ? (uint32_t)t * p.x_row + at : kOOB;
   const uint32_t xso = t >= 0 ? (uint32_t)t * p.x_sf_row + sat : kOOB;
@@ -452,7 +454,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   for (int c = 0; c < CT; ++c)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      wa[c][u] = w_addr<F>(slice * CT + c, u, slice * CT + c + u * (p.I / 16), p.ksteps, g, r16, (slice * CT + c) * 16 < p.I);
+      wa[c][u] = w_addr<F>(slice * CT + c, u, slice * CT + c + u * (p.I / 16), p.ksteps, g, r16,
+                           (slice * CT + c) * 16 < p.I);
   // FP8: the 128-row blocks' scales
   const float* sbg = (const float*)(p.w_sf + (size_t)e * p.w_sf_expert) + (size_t)((live ? col0 : 0) / 128) * p.ksteps;
   const float* sbu = sbg + (size_t)(p.I / 128) * p.ksteps;
@@ -482,7 +485,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
       // K tail: rows of any multiple of 32 elements
       s.x.v[0] = bload16(x_rs, o | oob_if(k * 128 + 16 * g >= p.H), (uint32_t)k * 128u);
       s.x.v[1] = bload16(x_rs, (o + 64u) | oob_if(k * 128 + 64 + 16 * g >= p.H), (uint32_t)k * 128u);
-      s.x.s = (int)__builtin_amdgcn_raw_buffer_load_b8(xs_rs, xso | dead | oob_if(k * 128 + 32 * g >= p.H), (uint32_t)k * 4u, 0);
+      s.x.s = (int)__builtin_amdgcn_raw_buffer_load_b8(xs_rs, xso | dead | oob_if(k * 128 + 32 * g >= p.H),
+                                                       (uint32_t)k * 4u, 0);
     } else if constexpr (F == Fmt::BF16) {
       s.x.v[0] = bload16(x_rs, o, (uint32_t)k * 128u);
       s.x.v[1] = bload16(x_rs, o + 64u, (uint32_t)k * 128u);
@@ -606,8 +610,9 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
       if (t < 0 || at >= p.I) continue;
       if constexpr (F == Fmt::FP8) *(f32x4*)((float*)p.h + row * p.I + at) = v;
       else if constexpr (F == Fmt::NVF4)
-        *(uint2*)((uint16_t*)p.h + row * p.I + at) = uint2{__builtin_bit_cast(uint32_t, f16x2{(_Float16)v[0], (_Float16)v[1]}),
-                                                           __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2], (_Float16)v[3]})};
+        *(uint2*)((uint16_t*)p.h + row * p.I + at) =
+            uint2{__builtin_bit_cast(uint32_t, f16x2{(_Float16)v[0], (_Float16)v[1]}),
+                  __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2], (_Float16)v[3]})};
       else *(uint2*)((uint16_t*)p.h + row * p.I + at) = uint2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
     }
   }
@@ -746,7 +751,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
     } else if constexpr (F == Fmt::MX) {
       s.x.v[0] = bload16(h_rs, o | oob_if(k * 128 + 16 * g >= p.I), (uint32_t)k * 128u);
       s.x.v[1] = bload16(h_rs, (o + 64u) | oob_if(k * 128 + 64 + 16 * g >= p.I), (uint32_t)k * 128u);
-      s.x.s = (int)__builtin_amdgcn_raw_buffer_load_b8(hs_rs, hso | dead | oob_if(k * 128 + 32 * g >= p.I), (uint32_t)k * 4u, 0);
+      s.x.s = (int)__builtin_amdgcn_raw_buffer_load_b8(hs_rs, hso | dead | oob_if(k * 128 + 32 * g >= p.I),
+                                                       (uint32_t)k * 4u, 0);
     } else if constexpr (F == Fmt::BF16) {
       s.x.v[0] = bload16(h_rs, o, (uint32_t)k * 128u);
       s.x.v[1] = bload16(h_rs, o + 64u, (uint32_t)k * 128u);
@@ -868,10 +874,10 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
   for (int i = tid; i < entries; i += 64 * WAVES) {
     f32x4 v[kFewMaxSplits];
 #pragma unroll
-    for (int q = 0; q < kFewMaxSplits; ++q)  // (all in flight at once; past the last split: zeros)
-      v[q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                           p_rs, q < p.splits ? (uint32_t)((q * p.n_blocks + blk) * entries + i) * 16u : kOOB,
-                                           0, kCpolDevice));
+    for (int q = 0; q < kFewMaxSplits; ++q) {  // (all in flight at once; past the last split: zeros)
+      const uint32_t o = q < p.splits ? (uint32_t)((q * p.n_blocks + blk) * entries + i) * 16u : kOOB;
+      v[q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(p_rs, o, 0, kCpolDevice));
+    }
 #pragma unroll
     for (int q = 1; q < kFewMaxSplits; ++q) v[0] += v[q];
     finish(i, v[0]);
@@ -996,6 +1002,12 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)(dp.n_blocks * dp.splits)),
                        dim3(64 * W), lds, s, d);
   };
+  // The waves of gate_up share a slice's K-steps by four: BF16, T 4, H 4096, I 14336 248 us, by two 254, whole
+  // 266 (T 1, H 2048, I 1024: 18.1, 21.1, 25.6; FP8, T 1, a 1/8 shard: 18.4 by four, 23.6 by two).  MX needs
+  // slices of 32 columns (64: T 32 186 against 188 us, T 1 24.1 against 22.8).  NVFP4's x operand serves two
+  // slices of 16 where they still make a round of workgroups: T 20, H 2880, I 2880 100 us against 110, T 16,
+  // H 7168, I 2048 151 against 162; not with fewer: T 1, H 7168, I 256 25.9 against 18.9.
+  const bool wide = (long long)min(a.E, a.T * a.topk) * ((a.I + 31) / 32) >= 256;
 #define C_(v) std::integral_constant<int, v>{}
 #define F_(v) std::integral_constant<Fmt, v>{}
   switch (a.fmt) {
@@ -1017,11 +1029,13 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
       down(F_(Fmt::MX), C_(8), C_(4), C_(2), std::false_type{});
       break;
     case Fmt::NV4:
-      up(F_(Fmt::NV4), C_(4), C_(4), C_(1), C_(2));
+      if (wide) up(F_(Fmt::NV4), C_(4), C_(4), C_(2), C_(1));
+      else up(F_(Fmt::NV4), C_(4), C_(4), C_(1), C_(2));
       down(F_(Fmt::NV4), C_(8), C_(2), C_(2), std::false_type{});
       break;
     case Fmt::NVF4:
-      up(F_(Fmt::NVF4), C_(4), C_(4), C_(2), C_(1));
+      if (wide) up(F_(Fmt::NVF4), C_(4), C_(4), C_(2), C_(1));
+      else up(F_(Fmt::NVF4), C_(4), C_(4), C_(1), C_(1));
       down(F_(Fmt::NVF4), C_(8), C_(2), C_(2), std::false_type{});
       break;
   }

@@ -333,7 +333,8 @@ RouterPlan router_plan(int T, int H, int E, bool w_f32) {
     if (t.bm == 0) break;
     const long long n = (long long)((T + t.bm - 1) / t.bm) * ((E + t.bn - 1) / t.bn);
     for (int splits = 1; splits == 1 || (w_f32 && t.bm == 128 && t.bn == 64 && splits <= 3 && n * splits <= 256); ++splits) {
-      const float us = (float)((n * splits + 255) / 256) * t.us * (float)H / (7168.0f * (float)splits) + (splits > 1 ? 5 : 0);
+      const float rounds = (float)((n * splits + 255) / 256);
+      const float us = rounds * t.us * (float)H / (7168.0f * (float)splits) + (splits > 1 ? 5.0f : 0.0f);
       if (us < least) least = us, best = RouterPlan{t.bm, t.bn, splits};
     }
   }

@@ -417,7 +417,7 @@ def test_few(fmt, T, routing):
     ("bf16", 64, 64, 7, 7, 4), ("bf16", 2048, 64, 2, 1, 3), ("bf16", 64, 4096, 3, 2, 20),
     ("w4a8_mx", 32, 32, 5, 2, 3), ("w4a8_mx", 2880, 96, 40, 4, 32), ("w4a8_mx", 96, 2880, 6, 3, 2),
     ("nvfp4_w4a16", 64, 64, 4, 2, 7), ("nvfp4_w4a16", 1216, 192, 9, 4, 1), ("nvfp4", 64, 64, 4, 2, 7),
-    ("nvfp4", 192, 1088, 9, 4, 18),
+    ("nvfp4", 192, 1088, 9, 4, 18), ("nvfp4_w4a16", 192, 1088, 9, 4, 18), ("nvfp4_w4a16", 2880, 64, 5, 2, 6),
     ("bf16", 64, 64, 1000, 32, 32),            # more experts and slots than any wave holds
     ("w4a8_mx", 64, 64, 40, 32, 32),
     ("w4a8_mx", 512, 64, 1000, 32, 32)])       # the largest tables and sums in LDS
