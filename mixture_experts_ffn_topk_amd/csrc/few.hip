@@ -16,7 +16,7 @@
 //     down launch, whose start is then one load away.
 //   * Weights go straight from HBM into registers, each byte read once, non-temporal,
 //     and nothing is staged in LDS: a wave is on its own until its sums are complete.
-//   * gate_up: a wave owns 16 columns of h (MX: 32, one scale block) of one expert,
+//   * gate_up: a wave owns 16 or 32 columns of h (MX: 32, one scale block) of one expert,
 //     or 1/KSP of their K-steps where that would leave the part underfilled.
 //   * down: a workgroup owns 16 R output columns and all units, or one of `splits`
 //     parts of them; its waves split its (unit, K-step) sequence evenly and add each
