@@ -233,24 +233,28 @@ def _byte_types():
     return _byte_kinds
 
 
-def _fit(args) -> bool:
-    """Whether every (tensor, bytes, dtypes) given is a contiguous GPU tensor of one of the
-    dtypes (None: of any), on the current device, with at least so many bytes: the checks of _need and
-    _on_current_gpu in one pass, without their messages (a call of a few microseconds
-    should not spend more on them).  False says nothing about which check failed, nor
-    that one did: raw addresses take the slow checks too."""
-    cur = None
+def _fit(args):
+    """The tensors' addresses if every (tensor, bytes, dtypes) given is None (its address too) or a
+    contiguous GPU tensor of one of the dtypes (None: of any), on the current device, with at least so many
+    bytes: the checks of _need and _on_current_gpu in one pass, without their messages (a call of a
+    few microseconds should not spend more on them).  None says nothing about which check failed,
+    nor that one did: raw addresses take the slow checks too."""
+    cur, ptrs = None, []
     for t, nbytes, dtypes in args:
-        if t is None or t.__class__ is int or (dtypes is not None and t.dtype not in dtypes):
-            return False
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.__class__ is int or (dtypes is not None and t.dtype not in dtypes):
+            return None
         if t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != cur:
             if cur is not None or t.nbytes < nbytes or not t.is_contiguous() or not t.is_cuda:
-                return False
+                return None
             import torch
-            cur = torch.cuda.current_device()
+            cur = torch._C._cuda_getDevice()
             if t.get_device() != cur:
-                return False
-    return True
+                return None
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
 def _current_stream() -> int:
@@ -638,30 +642,30 @@ class MoEFFN:
         import torch
         T, H = num_tokens, self.hidden
         n, bf16, f32 = T * H, torch.bfloat16, torch.float32
-        xf, rf, wf = (getattr(t, "dtype", None) is f32 for t in (x, residual, weight))
+        xf, rf, wf = (t is not None and t.__class__ is not int and t.dtype is f32 for t in (x, residual, weight))
         kinds, codes, res = (bf16, f32), _byte_types(), n * (4 if rf else 2)
-        sf_bytes = T * self._x_sf_row()
+        q_bytes, sf_bytes = T * self._x_bytes(H), T * self._x_sf_row()
         sf_kinds = kinds[1:] if self.fmt == "fp8_block128" else codes
-        fast = [(x, n * (4 if xf else 2), kinds), (weight, H * (4 if wf else 2), kinds)]
-        if residual is not None or residual_out is not None:
-            fast += ((residual, res, kinds), (residual_out, res, kinds[1:] if rf else kinds[:1]))
-        if x_norm is not None:
-            fast.append((x_norm, n * 2, kinds[:1]))
-        if x_q is not None or x_sf is not None:
-            fast += ((x_q, T * self._x_bytes(H), codes), (x_sf, sf_bytes, sf_kinds))
-        if not _fit(fast):
+        args = ((x, n * (4 if xf else 2), kinds), (residual, res, kinds), (weight, H * (4 if wf else 2), kinds),
+                (residual_out, res, kinds[1:] if rf else kinds[:1]), (x_norm, n * 2, kinds[:1]), (x_q, q_bytes, codes),
+                (x_sf, sf_bytes, sf_kinds))
+        whole = (x is not None and weight is not None and (residual is None) == (residual_out is None) and
+                 (x_q is None) == (x_sf is None) and (x_norm is not None or x_q is not None))
+        ptrs = _fit(args) if whole else None
+        if ptrs is None:
             _need(x, "x", n * (4 if xf else 2), kinds)
             _need(weight, "weight", H * (4 if wf else 2), kinds)
             _need(residual, "residual", res, kinds, required=False)
             _need(residual_out, "residual_out", res, kinds[1:] if rf else kinds[:1], required=residual is not None)
             _need(x_norm, "x_norm", n * 2, kinds[:1], required=x_q is None)
             if sf_bytes > 0:
-                _need(x_q, "x_q", T * self._x_bytes(H), codes, required=x_sf is not None)
+                _need(x_q, "x_q", q_bytes, codes, required=x_sf is not None)
                 _need(x_sf, "x_sf", sf_bytes, sf_kinds, required=x_q is not None)
             _on_current_gpu(x=x, residual=residual, weight=weight, residual_out=residual_out, x_norm=x_norm, x_q=x_q,
                             x_sf=x_sf)
-        _check(self.lib.moe_add_rmsnorm(self._h, T, _ptr(x), xf, _ptr(residual), rf, _ptr(weight), wf, eps,
-                                        _ptr(residual_out), _ptr(x_norm), _ptr(x_q), _ptr(x_sf), x_global_scale,
+            ptrs = [_ptr(t) for t, _, _ in args]
+        xp, rp, wp, rop, xnp, xqp, sfp = ptrs
+        _check(self.lib.moe_add_rmsnorm(self._h, T, xp, xf, rp, rf, wp, wf, eps, rop, xnp, xqp, sfp, x_global_scale,
                                         _current_stream() if stream is None else _stream(stream)), "moe_add_rmsnorm")
 
     def router_workspace_size(self, num_tokens: int) -> int:
@@ -677,18 +681,20 @@ class MoEFFN:
         import torch
         T, H, E = num_tokens, self.hidden, self.experts
         w32 = getattr(router_w, "dtype", None) is torch.float32
-        fast = [(x, T * H * 2, (torch.bfloat16,)), (router_w, E * H * (4 if w32 else 2), (torch.bfloat16, torch.float32)),
-                (logits, T * E * 4, (torch.float32,))]
-        if ws is not None:
-            fast.append((ws, 0, (torch.uint8,)))
-        if not _fit(fast):
-            _need(x, "x", T * H * 2, (torch.bfloat16,))
+        bf16 = (torch.bfloat16,)
+        args = ((x, T * H * 2, bf16), (router_w, E * H * (4 if w32 else 2), (torch.bfloat16, torch.float32)),
+                (logits, T * E * 4, (torch.float32,)), (ws, 0, (torch.uint8,)))
+        ptrs = None if x is None or router_w is None or logits is None else _fit(args)
+        if ptrs is None:
+            _need(x, "x", T * H * 2, bf16)
             _need(router_w, "router_w", E * H * (4 if w32 else 2), (torch.bfloat16, torch.float32))
             _need(logits, "logits", T * E * 4, (torch.float32,))
             _need(ws, "ws", 0, required=False)
             _on_current_gpu(x=x, router_w=router_w, logits=logits, ws=ws)
-        _check(self.lib.moe_router_logits(self._h, T, _ptr(x), _ptr(router_w), w32, _ptr(logits), _ptr(ws),
-                                          self._nbytes(ws), _current_stream() if stream is None else _stream(stream)),
+            ptrs = [_ptr(t) for t, _, _ in args]
+        xp, wp, lp, wsp = ptrs
+        _check(self.lib.moe_router_logits(self._h, T, xp, wp, w32, lp, wsp, 0 if ws is None else self._nbytes(ws),
+                                          _current_stream() if stream is None else _stream(stream)),
                "moe_router_logits")
 
     def few_workspace_size(self, num_tokens: int) -> int:
@@ -716,7 +722,8 @@ class MoEFFN:
             fast.append((routing_logits, T * self.experts * 4, f32))
         fast += [(t, n * 2, (torch.bfloat16,)) for t in (shared, residual) if t is not None]
         # (a routing bias and NVFP4's per-expert scales take the slow checks)
-        if routing_bias is not None or self.fmt in ("nvfp4_w4a16", "nvfp4") or not _fit(fast):
+        if (routing_bias is not None or self.fmt in ("nvfp4_w4a16", "nvfp4") or
+                any(t is None for t, _, _ in fast) or _fit(fast) is None):
             self._check_x(x, x_sf, T)
             self._check_weights(weights)
             self._check_routing_in(T, topk_idx, routing_logits, routing_bias)
