@@ -709,36 +709,47 @@ class MoEFFN:
         """moe_forward_few: forward() for at most FEW_MAX_TOKENS tokens in two launches; ws
         from alloc_few_workspace."""
         import torch
-        T, n, f32 = num_tokens, num_tokens * self.hidden, (torch.float32,)
-        if not hasattr(self, "_psizes"):
-            self._psizes = self.prepared_weights_size()
-        fast = [(x, T * self._x_bytes(self.hidden), None), (ws, 0, None),
-                (topk_idx, T * self.topk * self.topk_idx_bits // 8, self._idx_dtypes()), (topk_weights, T * self.topk * 4, f32),
-                (out, n * (4 if self.out_fp32 else 2), f32 if self.out_fp32 else (torch.bfloat16,))]
-        fast += [(weights.get(name), size, None) for name, size in self._psizes.items() if size]
-        if self._x_sf_row() > 0:
-            fast.append((x_sf, T * self._x_sf_row(), None))
-        if self.route_mode != "precomputed":
-            fast.append((routing_logits, T * self.experts * 4, f32))
-        fast += [(t, n * 2, (torch.bfloat16,)) for t in (shared, residual) if t is not None]
-        # (a routing bias and NVFP4's per-expert scales take the slow checks)
-        if (routing_bias is not None or self.fmt in ("nvfp4_w4a16", "nvfp4") or
-                any(t is None for t, _, _ in fast) or _fit(fast) is None):
+        T, n, f32, bf16 = num_tokens, num_tokens * self.hidden, (torch.float32,), (torch.bfloat16,)
+        logits = self.route_mode != "precomputed"
+        ids_bytes, w_bytes, out_types = T * self.topk * self.topk_idx_bits // 8, T * self.topk * 4, f32 if self.out_fp32 else bf16
+        wargs = [(weights.get(f), size, types) for f, size, types in self._weight_fields()]
+        needed = [(x, T * self._x_bytes(self.hidden), None), (topk_idx, ids_bytes, self._idx_dtypes()),
+                  (topk_weights, w_bytes, f32), (out, n * (4 if self.out_fp32 else 2), out_types), (ws, 0, None)]
+        others = [(x_sf, T * self._x_sf_row(), None), (routing_logits, T * self.experts * 4 if logits else 0, f32),
+                  (routing_bias, self.experts * 4, f32), (shared, n * 2, bf16), (residual, n * 2, bf16)]
+        args = needed + others + wargs
+        ptrs = None
+        if not any(t is None and (size > 0 or t is ws) for t, size, _ in needed + others[:2] + wargs) and (
+                logits or routing_bias is None):
+            ptrs = _fit(args)
+        if ptrs is None:
             self._check_x(x, x_sf, T)
             self._check_weights(weights)
             self._check_routing_in(T, topk_idx, routing_logits, routing_bias)
-            _need(topk_idx, "topk_idx", T * self.topk * self.topk_idx_bits // 8, self._idx_dtypes())
-            _need(topk_weights, "topk_weights", T * self.topk * 4, f32)
+            _need(topk_idx, "topk_idx", ids_bytes, self._idx_dtypes())
+            _need(topk_weights, "topk_weights", w_bytes, f32)
             self._check_out(T, out, shared, residual)
             _need(ws, "ws", 0, required=False)
             _on_current_gpu(x=x, x_sf=x_sf, weights=weights, topk_idx=topk_idx, topk_weights=topk_weights,
                             routing_logits=routing_logits, routing_bias=routing_bias, out=out, ws=ws, shared=shared,
                             residual=residual)
-        ws_ = self._weights_struct(weights)
-        _check(self.lib.moe_forward_few(self._h, T, _ptr(x), _ptr(x_sf), _ptr(topk_idx), _ptr(topk_weights),
-                                        _ptr(routing_logits), _ptr(routing_bias), ctypes.byref(ws_), _ptr(shared),
-                                        _ptr(residual), _ptr(out), _ptr(ws), self._nbytes(ws),
-                                        _current_stream() if stream is None else _stream(stream)), "moe_forward_few")
+            ptrs = [_ptr(t) for t, _, _ in args]
+        xp, ip, twp, op, wsp, sfp, lp, bp, shp, rp = ptrs[:10]
+        ws_ = _Weights(*ptrs[10:])
+        _check(self.lib.moe_forward_few(self._h, T, xp, sfp, ip, twp, lp, bp, ctypes.byref(ws_), shp, rp, op, wsp,
+                                        self._nbytes(ws), _current_stream() if stream is None else _stream(stream)),
+               "moe_forward_few")
+
+    def _weight_fields(self):
+        """(name, bytes, dtypes) of the prepared weights, in moe_weights' order; 0 bytes: not read."""
+        if not hasattr(self, "_wfields"):
+            import torch
+            sizes = self.prepared_weights_size()
+            nv = self.fmt in ("nvfp4_w4a16", "nvfp4")
+            gs = {"w13_gs": nv, "w2_gs": nv, "c_input_scales": self.fmt == "nvfp4"}
+            self._wfields = [(f, sizes[f], None) if f in sizes else (f, 4 * self.experts * gs[f], (torch.float32,))
+                             for f, _ in _Weights._fields_]
+        return self._wfields
 
 
 __all__ = ["MoEFFN", "MoEError", "load_library", "LIB_PATH", "EXPORTED", "FORMATS", "ROUTE_MODES", "TILE_REGIMES",
