@@ -239,21 +239,23 @@ def _fit(args):
     bytes: the checks of _need and _on_current_gpu in one pass, without their messages (a call of a
     few microseconds should not spend more on them).  None says nothing about which check failed,
     nor that one did: raw addresses take the slow checks too."""
+    import torch
     cur, ptrs = None, []
-    for t, nbytes, dtypes in args:
-        if t is None:
-            ptrs.append(None)
-            continue
-        if t.__class__ is int or (dtypes is not None and t.dtype not in dtypes):
-            return None
-        if t.nbytes < nbytes or not t.is_contiguous() or t.get_device() != cur:
-            if cur is not None or t.nbytes < nbytes or not t.is_contiguous() or not t.is_cuda:
+    try:
+        for t, nbytes, dtypes in args:
+            if t is None:
+                ptrs.append(None)
+            elif (dtypes is None or t.dtype in dtypes) and t.nbytes >= nbytes and t.is_contiguous():
+                device = t.get_device()
+                if device != cur:
+                    if cur is not None or not t.is_cuda or device != torch._C._cuda_getDevice():
+                        return None
+                    cur = device
+                ptrs.append(t.data_ptr())
+            else:
                 return None
-            import torch
-            cur = torch._C._cuda_getDevice()
-            if t.get_device() != cur:
-                return None
-        ptrs.append(t.data_ptr())
+    except AttributeError:  # (a raw address)
+        return None
     return ptrs
 
 
@@ -290,6 +292,7 @@ class MoEFFN:
         self.hidden, self.inter, self.experts, self.topk = hidden, intermediate_hidden, num_experts, num_topk
         self.max_num_tokens = max_num_tokens
         self.topk_idx_bits = topk_idx_bits
+        self._x_row_bytes, self._sf_row_bytes = self._x_bytes(hidden), self._x_sf_row()
         h = ctypes.c_void_p()
         _check(self.lib.moe_create(ctypes.byref(self.cfg), ctypes.byref(h)), "moe_create")
         self._h = h
@@ -642,9 +645,10 @@ class MoEFFN:
         import torch
         T, H = num_tokens, self.hidden
         n, bf16, f32 = T * H, torch.bfloat16, torch.float32
-        xf, rf, wf = (t is not None and t.__class__ is not int and t.dtype is f32 for t in (x, residual, weight))
+        xf, rf = getattr(x, "dtype", None) is f32, getattr(residual, "dtype", None) is f32
+        wf = getattr(weight, "dtype", None) is f32
         kinds, codes, res = (bf16, f32), _byte_types(), n * (4 if rf else 2)
-        q_bytes, sf_bytes = T * self._x_bytes(H), T * self._x_sf_row()
+        q_bytes, sf_bytes = T * self._x_row_bytes, T * self._sf_row_bytes
         sf_kinds = kinds[1:] if self.fmt == "fp8_block128" else codes
         args = ((x, n * (4 if xf else 2), kinds), (residual, res, kinds), (weight, H * (4 if wf else 2), kinds),
                 (residual_out, res, kinds[1:] if rf else kinds[:1]), (x_norm, n * 2, kinds[:1]), (x_q, q_bytes, codes),
@@ -713,9 +717,9 @@ class MoEFFN:
         logits = self.route_mode != "precomputed"
         ids_bytes, w_bytes, out_types = T * self.topk * self.topk_idx_bits // 8, T * self.topk * 4, f32 if self.out_fp32 else bf16
         wargs = [(weights.get(f), size, types) for f, size, types in self._weight_fields()]
-        needed = [(x, T * self._x_bytes(self.hidden), None), (topk_idx, ids_bytes, self._idx_dtypes()),
+        needed = [(x, T * self._x_row_bytes, None), (topk_idx, ids_bytes, self._idx_dtypes()),
                   (topk_weights, w_bytes, f32), (out, n * (4 if self.out_fp32 else 2), out_types), (ws, 0, None)]
-        others = [(x_sf, T * self._x_sf_row(), None), (routing_logits, T * self.experts * 4 if logits else 0, f32),
+        others = [(x_sf, T * self._sf_row_bytes, None), (routing_logits, T * self.experts * 4 if logits else 0, f32),
                   (routing_bias, self.experts * 4, f32), (shared, n * 2, bf16), (residual, n * 2, bf16)]
         args = needed + others + wargs
         ptrs = None
