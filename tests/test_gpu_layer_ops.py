@@ -297,6 +297,31 @@ def test_router_infinities_keep_their_sign(T, H, E, w32):
     assert torch.equal(got[inf], ref[inf]) and torch.isfinite(got[~odd]).all()
 
 
+def test_norm_and_router_offsets_past_32_bits():
+    """An fp32 stream of 8.3 GB and activations of 4.2 GB: the first, a middle and the last rows."""
+    T, H, E = 290000, 7168, 8
+    rows = [0, 1, T // 2, T - 2, T - 1]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty((T, H), device="cuda").normal_(generator=g)
+    r = torch.empty((T, H), device="cuda").normal_(generator=g)
+    w = torch.empty(H, device="cuda").normal_(generator=g)
+    xs, rs = x[rows].clone(), r[rows].clone()
+    moe = MoEFFN(H, 64, E, 1, T, fmt="w4a8_mx")
+    xn = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    q = torch.empty((T, H), dtype=torch.uint8, device="cuda")
+    sf = torch.empty((T, H // 32), dtype=torch.uint8, device="cuda")
+    moe.add_rmsnorm(T, x, r, w, 1e-6, residual_out=r, x_norm=xn, x_q=q, x_sf=sf)
+    z, n = ol.add_rmsnorm(bits(xs), bits(rs), bits(w), 1e-6)
+    check_norm("w4a8_mx", {"residual_out": r[rows], "x_norm": xn[rows], "x_q": q[rows], "x_sf": sf[rows]}, z, n)
+    for w32 in (False, True):
+        rw = torch.empty((E, H), device="cuda").normal_(generator=g)
+        rw = rw if w32 else rw.bfloat16()
+        out = torch.empty((T, E), device="cuda")
+        moe.router_logits(T, xn, rw, out, moe.alloc_router_workspace(T))
+        ref = ol.router_logits(bits(xn[rows]), bits(rw))
+        assert np.all(np.abs(bits(out[rows]) - ref) <= router_tolerance(bits(xn[rows]), bits(rw), H))
+
+
 # ------------------------------------------------------------------ the layer for few tokens
 def shape(fmt, T, H, I, E, k, routing="precomputed", seed=1, **kw):
     return moe_synth.MoEShape(f"few_{fmt}", seed, T, H, I, E, k, fmt, routing, **kw)
@@ -696,3 +721,25 @@ def test_a_workspace_for_32_tokens_serves_fewer():
         own = run_few(moe, d, T, kw)
         assert torch.equal(run_few(moe, d, T, kw, ws=ws)[:T], own[:T])
     assert torch.equal(run_few(moe, d, 32, kw, ws=ws)[:32], whole[:32])
+
+
+def test_few_weights_past_32_bits():
+    """The last expert of 14 GB of weights gives the bits of the same expert on its own."""
+    H, I, E, T = 4096, 14336, 40, 3
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w13 = torch.zeros((E, 2 * I, H), dtype=torch.bfloat16, device="cuda")
+    w2 = torch.zeros((E, H, I), dtype=torch.bfloat16, device="cuda")
+    w13[-1].normal_(0.0, H ** -0.5, generator=g)
+    w2[-1].normal_(0.0, I ** -0.5, generator=g)
+    x = torch.empty((T, H), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    tw = torch.rand((T, 1), generator=g, device="cuda")
+    outs = []
+    for first in (0, E - 1):
+        moe = MoEFFN(H, I, E - first, 1, T, fmt="bf16")
+        w = moe.prepare_weights({"w13": w13[first:], "w2": w2[first:]})
+        ids = torch.full((T, 1), E - 1 - first, dtype=torch.int64, device="cuda")
+        out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+        moe.forward_few(T, x, None, ids, tw, None, w, out, moe.alloc_few_workspace(T))
+        torch.cuda.synchronize()
+        outs.append(out)
+    assert outs[0].float().abs().max() > 0 and torch.equal(*outs)
