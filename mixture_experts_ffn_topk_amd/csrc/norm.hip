@@ -18,6 +18,9 @@
 // and the outputs: thread i holds the 8-column chunks i, i + threads, ....  Each
 // quantisation block then lies in 16, 4 or 2 neighbouring lanes, and its maximum
 // takes DPP moves only.
+//
+// Bound by the bytes: 8192 x 7168 with residual, bf16 norm and FP8 codes moves 530 MB in 91 us (5.8 TB/s; a plain
+// copy of 2 GiB reaches 4.9), 2048 x 2880 with an fp32 stream 89 MB in 15.7; one row by its latency, 3.2 us.
 #include <type_traits>
 
 #include "layer.h"

@@ -7,6 +7,11 @@
 // holds all 24 bits of the weight (w = w0 + w1 + w2 exactly, barring underflow),
 // each multiplied on the matrix cores: bf16 products are exact in fp32, so the
 // result has the error of an fp32 sum.
+//
+// Bound by what one CU can read: about 118 requests of 128 bytes are in flight in its vector cache, at 631 cycles
+// each with x from HBM (54 GB/s; T 8192, H 7168, E 256: 192 lines a K-step and workgroup, 53 us, 570 TFLOP/s), and
+// at 60 to 78 GB/s where the operands come from L2 (T 256: 458 KB per 16 x 16 tile, 7.5 us).  fp32 weights: by the
+// VALU work of their split.
 #include <algorithm>
 #include <type_traits>
 
