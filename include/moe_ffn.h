@@ -431,8 +431,8 @@ moe_status moe_forward_static(const moe_handle* h, int32_t num_tokens, const voi
                       codes E4M3_RNE_sat(n / s), x_sf the UE8M0 byte e + 127
        NVFP4 x NVFP4  per 16 columns s = E4M3_RNE_sat(amax / (6 x_global_scale)), codes
                       E2M1_RNE_sat(n / (s x_global_scale)), zero where s = 0
-     A block that holds a NaN gets a NaN scale.  The squares are summed in fp32: a row needs a sum of
-   z^2 below 2^128 (beyond: r is 0), and with eps = 0 one that does not underflow to 0.
+     A block that holds a NaN gets a NaN scale.  The squares are summed in fp64, so no finite z
+   overflows the mean.
    x [T,H] and weight [H] are bf16 or, with x_fp32 / weight_fp32 = 1, fp32; residual and
    residual_out [T,H] are both given or both NULL, bf16 or fp32 (residual_fp32).
    x_norm [T,H] bf16 and the pair x_q, x_sf may be NULL, not all three; BF16 and NVFP4 x

@@ -14,6 +14,8 @@
 // NaN gets a NaN scale (the codes of such a block mean nothing), so that a NaN
 // is never turned into a number on the way into the experts.
 //
+// The squares are summed in fp64 and r is a pair of floats, so that n is rounded once, for any finite z.
+//
 // A workgroup owns one row, which stays in registers between the sum of squares
 // and the outputs: thread i holds the 8-column chunks i, i + threads, ....  Each
 // quantisation block then lies in 16, 4 or 2 neighbouring lanes, and its maximum
@@ -81,15 +83,27 @@ MOE_DEV uint32_t amax_bits8(const float (&f)[8]) {
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
   return m;
 }
-// 1 / sqrt(m) to about half a float's step: the row's codes share this factor, and each one that lies
-// nearer to a rounding border than its error comes out as the other code.  One Newton step
-// on the float root, with m's lower half and the products' lost parts.
-MOE_DEV float inv_root(double m) {
-  const float hi = (float)m, lo = (float)(m - (double)hi);
-  const float r = 1.0f / sqrtf(hi);
-  const float t = hi * r;
-  const float e = fmaf(-t, r, 1.0f) - fmaf(hi, r, -t) * r - lo * r * r;
-  return hi < INFINITY && hi > 0.0f ? fmaf(0.5f * r, e, r) : r;
+// 1 / sqrt(m) as hi + lo: the row's codes share this factor, and each one that lies nearer to a
+// rounding border than its error comes out as the other code.  One Newton step in fp64 from the float
+// root, or the fp64 root where m is no normal float.
+MOE_DEV void inv_root(double m, float& hi, float& lo) {
+  const float f = (float)m;
+  double r;
+  if (f < INFINITY && f >= kMinNormal) {
+    r = (double)__builtin_amdgcn_rsqf(f);
+    r = fma(0.5 * r, fma(-m * r, r, 1.0), r);
+    r = fma(0.5 * r, fma(-m * r, r, 1.0), r);
+  } else {
+    r = 1.0 / sqrt(m);
+  }
+  hi = (float)r;
+  lo = hi < INFINITY ? (float)(r - (double)hi) : 0.0f;
+}
+// n + e, |e| at most half a step of n, to odd: the value cut to 24 bits with the last one set if anything was
+// cut.  Rounding that to fewer bits gives what rounding n + e itself would.
+MOE_DEV float to_odd(float n, float e) {
+  const uint32_t u = __float_as_uint(n), cut = __builtin_islessgreater(e, 0.0f) ? 1u : 0u;  // (an infinity's e is NaN)
+  return __uint_as_float((u - ((u ^ __float_as_uint(e)) >> 31 & cut)) | cut);
 }
 
 // What one row's chunk writes of the format's activations: n the 8 values, c the chunk.
@@ -151,11 +165,11 @@ MOE_DEV void quantise8(const NormParams& p, size_t t, int c, const float (&n)[8]
 // NV: chunks a thread holds.  RES: 0 no residual, 1 bf16, 2 fp32.
 template <Fmt F, int NV, bool XF32, int RES>
 __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
-  __shared__ float part[16];
+  __shared__ double part[16];
   const size_t t = blockIdx.x;
   const int tid = threadIdx.x, C = p.H >> 3, nthr = blockDim.x;
   float z[NV][8];
-  float ss = 0.0f;
+  double ss = 0.0;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = tid + v * nthr;
@@ -173,17 +187,18 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
       for (int i = 0; i < 8; ++i) z[v][i] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(z[v][i], z[v][i], ss);
+    for (int i = 0; i < 8; ++i) ss = fma((double)z[v][i], (double)z[v][i], ss);
   }
-  ss = wave_sum_f32(ss);
+  ss = wave_sum_f64(ss);
   double sum = ss;
   if (nthr > 64) {
     if ((tid & 63) == 0) part[tid >> 6] = ss;
     __syncthreads();
     sum = 0.0;
-    for (int w = 0; w < nthr >> 6; ++w) sum += (double)part[w];
+    for (int w = 0; w < nthr >> 6; ++w) sum += part[w];
   }
-  const float r = inv_root(sum * p.inv_h + (double)p.eps);
+  float r, r_lo;
+  inv_root(sum * p.inv_h + (double)p.eps, r, r_lo);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = tid + v * nthr;
@@ -199,14 +214,35 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
         store16((float*)p.residual_out + at + 4, __builtin_bit_cast(i32x4, f32x4{z[v][4], z[v][5], z[v][6], z[v][7]}));
       }
     }
+    // n = z r w, rounded once: what the products drop (r's lower half too) goes into the last one
+    float n[8];
+    auto product = [&](int i, float& a, float& lost) {
+      a = z[v][i] * r;
+      lost = fmaf(z[v][i], r_lo, fmaf(z[v][i], r, -a)) * w[i];
+      return fmaf(a, w[i], lost);
+    };
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // z r w with one rounding: what the first product drops is added to the second
-      const float a = z[v][i] * r, lost = fmaf(z[v][i], r, -a);
-      z[v][i] = fmaf(a, w[i], lost * w[i]);
+      float a, lost;
+      n[i] = product(i, a, lost);
     }
-    if (live && p.x_norm != nullptr) store16((uint16_t*)p.x_norm + at, pack8(z[v]));
-    if constexpr (F != Fmt::BF16) quantise8<F>(p, t, c, z[v], live);
+    if constexpr (F == Fmt::MX) {
+      // MX codes are n times a power of two: where its 24 bits end in a tie of E4M3's 4 (one in 2^20; a wave in
+      // 2000), what was rounded off decides.  (Always to odd: 8192 x 7168 95 -> 98 us.)
+      uint32_t tie = ~0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) tie = min(tie, (__float_as_uint(n[i]) << 12) ^ 0x80000000u);
+      if (tie == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float a, lost;
+          product(i, a, lost);
+          n[i] = to_odd(n[i], fmaf(a, w[i], -n[i]) + lost);
+        }
+      }
+    }
+    if (live && p.x_norm != nullptr) store16((uint16_t*)p.x_norm + at, pack8(n));
+    if constexpr (F != Fmt::BF16) quantise8<F>(p, t, c, n, live);
   }
 }
 

@@ -67,6 +67,30 @@ MOE_DEV float wave_sum_f32(float x) {
   return m;
 }
 
+// The wave's sum of a double, the same way.
+template <int CTRL>
+MOE_DEV double dpp_f64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+MOE_DEV double wave_sum_f64(double x) {
+  x += dpp_f64<0xB1>(x);
+  x += dpp_f64<0x4E>(x);
+  x += dpp_f64<0x141>(x);
+  x += dpp_f64<0x140>(x);
+  double m = 0.0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint64_t v = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 16 * r) << 32 |
+                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 16 * r);
+    m += __builtin_bit_cast(double, v);
+  }
+  return m;
+}
+
 // The larger of a lane's value and a DPP neighbour's.
 template <int CTRL>
 MOE_DEV uint32_t dpp_max_u32(uint32_t x) {

@@ -129,6 +129,40 @@ def test_norm_scale_floor():
     check_norm("fp8_block128", o, z, n)
 
 
+@pytest.mark.parametrize("fmt", ["fp8_block128", "w4a8_mx", "bf16"])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norm_rows_whose_squares_leave_fp32(fmt, eps):
+    """Rows of 2^100 and, without eps, of 2^-100: their norms are those of the same rows at 1."""
+    def make(x, r, w):
+        x[1] *= 2.0 ** 100
+        r[1] *= 2.0 ** 100
+        if eps == 0.0:
+            x[2] *= 2.0 ** -100
+            r[2] *= 2.0 ** -100
+    o, z, n = norm_case(fmt, 4, 512, torch.bfloat16, torch.bfloat16, torch.bfloat16, seed=6, make=make, eps=eps)
+    check_norm(fmt, o, z, n)
+
+
+def test_norm_mx_codes_are_those_of_the_unrounded_norm():
+    """Codes of the fp64 norm, rounded once (the stream's sums are exact in fp32: small integers times 2^-6)."""
+    T, H = 4096, 352
+    g = torch.Generator().manual_seed(8)
+    x = (torch.randint(-120, 121, (T, H), generator=g) * 2.0 ** -6).bfloat16()
+    r = (torch.randint(-120, 121, (T, H), generator=g) * 2.0 ** -6).bfloat16()
+    w = (1 + 0.3 * torch.randn(H, generator=g)).bfloat16()
+    moe = MoEFFN(H, 32, 2, 1, T, fmt="w4a8_mx")
+    q = torch.empty((T, H), dtype=torch.uint8, device="cuda")
+    sf = torch.empty((T, H // 32), dtype=torch.uint8, device="cuda")
+    ro = torch.empty_like(r, device="cuda")
+    moe.add_rmsnorm(T, x.cuda(), r.cuda(), w.cuda(), 1e-6, residual_out=ro, x_q=q, x_sf=sf)
+    _, n = ol.add_rmsnorm(bits(x), bits(r), bits(w), 1e-6)
+    codes = oracle.e4m3_decode(q.cpu().numpy()).reshape(T, H // 32, 32)
+    v = n.reshape(T, H // 32, 32) / oracle.ue8m0_decode(sf.cpu().numpy())[..., None]
+    step = np.exp2(np.maximum(np.floor(np.log2(np.abs(v) + 1e-300)), -6.0) - 3.0)
+    # half a step, and what two fp64 evaluations of the norm may differ by
+    assert np.all(np.abs(codes - v) <= 0.5 * step * (1 + 2.0 ** -30))
+
+
 @pytest.mark.parametrize("fmt", ["fp8_block128", "w4a8_mx", "nvfp4"])
 def test_norm_nan_and_inf(fmt):
     """A NaN makes its row NaN, an infinity its own element (the rest of the row is finite / inf = 0); other rows keep
