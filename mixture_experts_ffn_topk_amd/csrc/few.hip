@@ -406,7 +406,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   const int tid = threadIdx.x, lane = lane_id(), g = lane >> 4, r16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   __shared__ int col[32];  // the columns of this workgroup's expert
-  if (blockIdx.x == gridDim.x - 1) {  // the down launch's tables and counters
+  if (blockIdx.y == gridDim.y - 1) {  // the down launch's tables and counters: one workgroup of the last row
+    if (blockIdx.x != 0) return;
     __shared__ float tw[kFewMaxPairs];
     __shared__ short ustart[kFewMaxExperts];
     if (p.splits > 1)
@@ -419,8 +420,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_gate_up_kernel(FewParams p) {
   route_to_lds<WAVES>(p, route, nullptr);
 
   // this workgroup's unit
-  const int n_slices = (p.I + 16 * CT - 1) / (16 * CT), blocks = (n_slices + kSlices - 1) / kSlices;
-  const int a = (int)blockIdx.x / blocks, slice = ((int)blockIdx.x % blocks) * kSlices + wave / KSP;
+  const int n_slices = (p.I + 16 * CT - 1) / (16 * CT);
+  const int a = (int)blockIdx.y, slice = (int)blockIdx.x * kSlices + wave / KSP;
   int e = -1, half = 0;
   for_units(route, p.E, [&](int before, int le, int n) {
     const uint64_t hit = __ballot(a >= before && a < before + n);
@@ -689,10 +690,12 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
   __syncthreads();
 
   // this wave's part of the (unit, K-step) sequence
-  const int blk = (int)blockIdx.x % p.n_blocks, split = (int)blockIdx.x / p.n_blocks;
-  const long long total = (long long)n_units * p.steps;
-  const int at = split * WAVES + wave, parts = p.splits * WAVES;
-  const int lo = (int)(total * at / parts), hi = (int)(total * (at + 1) / parts);
+  const int blk = (int)blockIdx.x, split = (int)blockIdx.y;
+  const uint32_t total = (uint32_t)n_units * (uint32_t)p.steps;
+  const int at = split * WAVES + wave;
+  const int share = (int)(p.splits == 1 ? total / WAVES : total / (uint32_t)(p.splits * WAVES));
+  const int more = (int)total - share * p.splits * WAVES;  // parts of one step more
+  const int lo = at * share + min(at, more), hi = lo + share + (at < more ? 1 : 0);
   const int rb0 = blk * R;  // first 16-row block
   const int n_rb = p.H / 16;
   WAddr<F> wa[R];
@@ -706,7 +709,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_kernel(FewParams p) {
   const __amdgpu_buffer_rsrc_t hs_rs = make_rsrc(p.h_sf, rows * hs_row);
 
   // the load side's position: unit, its expert's resources, the lane's token, row and router weight
-  int lu = lo / p.steps, lk = lo % p.steps, lf = lo;
+  int lu = (int)((uint32_t)lo / (uint32_t)p.steps), lk = lo - lu * p.steps, lf = lo;
   __amdgpu_buffer_rsrc_t w_rs, ws_rs;
   const float* sb = nullptr;
   uint32_t ho, hso;
@@ -999,14 +1002,14 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
     constexpr int W = decltype(waves)::value, KSP = decltype(ksp)::value, CT = decltype(groups)::value,
                   D = decltype(depth)::value;
     constexpr int per = W / KSP * 16 * CT;  // columns of h per workgroup
-    const dim3 grid((unsigned)((a.I + per - 1) / per * p.max_units + 1));
+    const dim3 grid((unsigned)((a.I + per - 1) / per), (unsigned)(p.max_units + 1));
     hipLaunchKernelGGL((few_gate_up_kernel<F, W, KSP, CT, D>), grid, dim3(64 * W), 0, s, u);
   };
   auto down = [&](auto fmt, auto waves, auto rows, auto depth, auto lds_h) {
     constexpr Fmt F = decltype(fmt)::value;
     constexpr int W = decltype(waves)::value, R = decltype(rows)::value, D = decltype(depth)::value;
     const size_t lds = (size_t)W * R * a.T * 64 + few_table_words(a.T * a.topk, p.max_units) * 4;
-    hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)(dp.n_blocks * dp.splits)),
+    hipLaunchKernelGGL((few_down_kernel<F, W, R, D, decltype(lds_h)::value>), dim3((unsigned)dp.n_blocks, (unsigned)dp.splits),
                        dim3(64 * W), lds, s, d);
   };
   // The waves of gate_up share a slice's K-steps by four: BF16, T 4, H 4096, I 14336 248 us, by two 254, whole
