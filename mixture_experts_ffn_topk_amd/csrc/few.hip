@@ -1013,17 +1013,22 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
                        dim3(64 * W), lds, s, d);
   };
   // The waves of gate_up share a slice's K-steps by four: BF16, T 4, H 4096, I 14336 248 us, by two 254, whole
-  // 266 (T 1, H 2048, I 1024: 18.1, 21.1, 25.6; FP8, T 1, a 1/8 shard: 18.4 by four, 23.6 by two).  MX needs
-  // slices of 32 columns (64: T 32 186 against 188 us, T 1 24.1 against 22.8).  NVFP4's x operand serves two
-  // slices of 16 where they still make a round of workgroups: T 20, H 2880, I 2880 100 us against 110, T 16,
-  // H 7168, I 2048 151 against 162; not with fewer: T 1, H 7168, I 256 25.9 against 18.9.
-  const bool wide = (long long)min(a.E, a.T * a.topk) * ((a.I + 31) / 32) >= 256;
+  // 266 (T 1, H 2048, I 1024: 18.1, 21.1, 25.6; FP8, T 1, a 1/8 shard: 18.4 by four, 23.6 by two).  By eight, one
+  // K-step in flight each, in a single round of workgroups (FP8, T 1, H 7168, I 256: 17.6 against 18.5; MX, T 27,
+  // H 4608, I 224, 20 experts: 17.2 against 18.7), not beyond (MX, T 32, I 2880, 128 experts: 202 against 188).
+  // MX needs slices of 32 columns (64: T 32 186 against 188 us, T 1 24.1 against 22.8).  NVFP4's x operand serves
+  // two slices of 16 where they still make a round: T 20, H 2880, I 2880 100 us against 110, T 16, H 7168, I 2048
+  // 151 against 162; not with fewer: T 1, H 7168, I 256 25.9 against 18.9 (by eight 17.0).
+  const long long units = min(a.E, a.T * a.topk);
+  const bool wide = units * ((a.I + 31) / 32) >= 256;
+  const bool thin = units * ((a.I + 31) / 32) * (a.fmt == Fmt::MX ? 1 : 2) <= 256;
 #define C_(v) std::integral_constant<int, v>{}
 #define F_(v) std::integral_constant<Fmt, v>{}
   switch (a.fmt) {
     case Fmt::FP8:
       if (few_h_fp32(a.fmt, a.T, a.topk, a.E, a.I)) {
-        up(F_(Fmt::FP8), C_(4), C_(4), C_(1), C_(2));
+        if (thin) up(F_(Fmt::FP8), C_(8), C_(8), C_(1), C_(1));
+        else up(F_(Fmt::FP8), C_(4), C_(4), C_(1), C_(2));
         down(F_(Fmt::FP8), C_(8), C_(2), C_(2), std::true_type{});
       } else {
         up(F_(Fmt::FP8), C_(8), C_(1), C_(1), C_(2));
@@ -1031,21 +1036,23 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
       }
       break;
     case Fmt::BF16:
-      up(F_(Fmt::BF16), C_(4), C_(4), C_(1), C_(2));
+      if (thin) up(F_(Fmt::BF16), C_(8), C_(8), C_(1), C_(1));
+      else up(F_(Fmt::BF16), C_(4), C_(4), C_(1), C_(2));
       down(F_(Fmt::BF16), C_(8), C_(1), C_(2), std::false_type{});
       break;
     case Fmt::MX:
-      up(F_(Fmt::MX), C_(4), C_(4), C_(2), C_(2));
+      if (thin) up(F_(Fmt::MX), C_(8), C_(8), C_(2), C_(1));
+      else up(F_(Fmt::MX), C_(4), C_(4), C_(2), C_(2));
       down(F_(Fmt::MX), C_(8), C_(4), C_(2), std::false_type{});
       break;
     case Fmt::NV4:
       if (wide) up(F_(Fmt::NV4), C_(4), C_(4), C_(2), C_(1));
-      else up(F_(Fmt::NV4), C_(4), C_(4), C_(1), C_(2));
+      else up(F_(Fmt::NV4), C_(8), C_(8), C_(1), C_(1));
       down(F_(Fmt::NV4), C_(8), C_(2), C_(2), std::false_type{});
       break;
     case Fmt::NVF4:
       if (wide) up(F_(Fmt::NVF4), C_(4), C_(4), C_(2), C_(1));
-      else up(F_(Fmt::NVF4), C_(4), C_(4), C_(1), C_(1));
+      else up(F_(Fmt::NVF4), C_(8), C_(8), C_(1), C_(1));
       down(F_(Fmt::NVF4), C_(8), C_(2), C_(2), std::false_type{});
       break;
   }

@@ -472,6 +472,7 @@ def test_few(fmt, T, routing):
     ("fp8_block128", 256, 128, 1, 1, 32),      # every token to one expert
     ("fp8_block128", 7168, 256, 16, 8, 1),     # a thin shard of a wide layer (h in LDS)
     ("fp8_block128", 256, 4096, 64, 8, 3),     # whole 128-column blocks
+    ("fp8_block128", 384, 1024, 8, 2, 3), ("fp8_block128", 2944, 640, 9, 3, 5),  # h in LDS, more than a round of workgroups
     ("fp8_block128", 1024, 1024, 2, 2, 24),    # few experts, h too large for LDS
     ("bf16", 64, 64, 7, 7, 4), ("bf16", 2048, 64, 2, 1, 3), ("bf16", 64, 4096, 3, 2, 20),
     ("w4a8_mx", 32, 32, 5, 2, 3), ("w4a8_mx", 2880, 96, 40, 4, 32), ("w4a8_mx", 96, 2880, 6, 3, 2),
