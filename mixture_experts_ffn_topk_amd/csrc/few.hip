@@ -1022,6 +1022,10 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   const long long units = min(a.E, a.T * a.topk);
   const bool wide = units * ((a.I + 31) / 32) >= 256;
   const bool thin = units * ((a.I + 31) / 32) * (a.fmt == Fmt::MX ? 1 : 2) <= 256;
+  // down: K-steps in flight per wave.  One: FP8, T 16, H 7168, I 2048 216 us, two 220; MX, T 1, H 2880, I 2880
+  // 22.2 and 23.1.  Two: BF16, T 4, H 4096, I 14336 248, one 262; NVFP4, T 20, H 2880, I 2880 99 and 107, unless a
+  // wave has only a step or two (T 1, H 2048, I 1024 13.8, one 13.0).
+  const bool brief = units * d.steps <= 2LL * dp.splits * 8;
 #define C_(v) std::integral_constant<int, v>{}
 #define F_(v) std::integral_constant<Fmt, v>{}
   switch (a.fmt) {
@@ -1029,10 +1033,10 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
       if (few_h_fp32(a.fmt, a.T, a.topk, a.E, a.I)) {
         if (thin) up(F_(Fmt::FP8), C_(8), C_(8), C_(1), C_(1));
         else up(F_(Fmt::FP8), C_(4), C_(4), C_(1), C_(2));
-        down(F_(Fmt::FP8), C_(8), C_(2), C_(2), std::true_type{});
+        down(F_(Fmt::FP8), C_(8), C_(2), C_(1), std::true_type{});
       } else {
         up(F_(Fmt::FP8), C_(8), C_(1), C_(1), C_(2));
-        down(F_(Fmt::FP8), C_(8), C_(2), C_(2), std::false_type{});
+        down(F_(Fmt::FP8), C_(8), C_(2), C_(1), std::false_type{});
       }
       break;
     case Fmt::BF16:
@@ -1043,17 +1047,19 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
     case Fmt::MX:
       if (thin) up(F_(Fmt::MX), C_(8), C_(8), C_(2), C_(1));
       else up(F_(Fmt::MX), C_(4), C_(4), C_(2), C_(2));
-      down(F_(Fmt::MX), C_(8), C_(4), C_(2), std::false_type{});
+      down(F_(Fmt::MX), C_(8), C_(4), C_(1), std::false_type{});
       break;
     case Fmt::NV4:
       if (wide) up(F_(Fmt::NV4), C_(4), C_(4), C_(2), C_(1));
       else up(F_(Fmt::NV4), C_(8), C_(8), C_(1), C_(1));
-      down(F_(Fmt::NV4), C_(8), C_(2), C_(2), std::false_type{});
+      if (brief) down(F_(Fmt::NV4), C_(8), C_(2), C_(1), std::false_type{});
+      else down(F_(Fmt::NV4), C_(8), C_(2), C_(2), std::false_type{});
       break;
     case Fmt::NVF4:
       if (wide) up(F_(Fmt::NVF4), C_(4), C_(4), C_(2), C_(1));
       else up(F_(Fmt::NVF4), C_(8), C_(8), C_(1), C_(1));
-      down(F_(Fmt::NVF4), C_(8), C_(2), C_(2), std::false_type{});
+      if (brief) down(F_(Fmt::NVF4), C_(8), C_(2), C_(1), std::false_type{});
+      else down(F_(Fmt::NVF4), C_(8), C_(2), C_(2), std::false_type{});
       break;
   }
 #undef C_
