@@ -38,6 +38,7 @@
 // (5.3); BF16, T 4, H 4096, I 14336: 1096 MB in 167 (6.55), 548 MB in 85 (6.45); W4A8, T 32, H 2880, E 128:
 // 749 MB in 120 (6.25), 374 MB in 63 (5.9); NVFP4 x BF16, T 3: 242 MB in 45 (5.3), 121 MB in 26 (4.6).  A read
 // alone reaches 6.85 TB/s from 0.9 GB on, 6.4 at 0.24 GB.
+#include <algorithm>
 #include <type_traits>
 
 #include "gemm_common.h"
@@ -915,12 +916,19 @@ static bool few_h_fp32(Fmt f, int T, int topk, int E, int I) {
 struct DownPlan {
   int rows, n_blocks, splits;
 };
-static DownPlan down_plan(Fmt f, int H) {
-  DownPlan d;
-  d.rows = f == Fmt::BF16 ? 1 : f == Fmt::MX ? 4 : 2;
-  d.n_blocks = (H / 16 + d.rows - 1) / d.rows;
-  d.splits = max(1, min(256 / d.n_blocks, kFewMaxSplits));
-  return d;
+// Twice the tiles where that fills more of the part and a wave has more than four K-steps (BF16, T 10, H 5248,
+// I 768: 328 blocks of 1 tile 50.0, 164 of 2 46.2; FP8, T 16, H 4224, I 1024: 132 of 2 56.8, 66 of 4 in 3 splits
+// 53.2; NVFP4, T 20, H 2880, I 2880: 90 in 2 splits 99, 45 in 5 92.  At equal counts: BF16, H 4096 248 and 251;
+// with short parts: FP8, T 2, H 4224, I 512 16.8 and 18.0.)
+static DownPlan down_plan_rows(int H, int rows) {
+  const int n = (H / 16 + rows - 1) / rows;
+  return DownPlan{rows, n, max(1, min(256 / n, kFewMaxSplits))};
+}
+static DownPlan down_plan(Fmt f, int H, long long steps) {  // steps: K-steps of all units
+  auto used = [](const DownPlan& d) { return d.n_blocks > 256 ? 0 : d.n_blocks * d.splits; };  // of one round
+  const DownPlan few = down_plan_rows(H, f == Fmt::BF16 ? 1 : f == Fmt::MX ? 4 : 2);
+  const DownPlan many = down_plan_rows(H, 2 * few.rows);
+  return f != Fmt::MX && used(many) > used(few) && steps > 4LL * many.splits * 8 ? many : few;
 }
 FewBuffers few_buffers(Fmt f, int T, int topk, int E, int H, int I) {
   FewBuffers b{};
@@ -929,10 +937,13 @@ FewBuffers few_buffers(Fmt f, int T, int topk, int E, int H, int I) {
   // (FP8: room for fp32 whether this T takes it or not, so that the size never shrinks as T grows)
   b.h = pairs * I * (f == Fmt::FP8 ? 4 : mma16(f) ? 2 : 1);
   b.h_sf = f == Fmt::FP8 ? pairs * (I / 128) * 4 : f == Fmt::MX ? pairs * (I / 32) : 0;
-  const DownPlan d = down_plan(f, H);
   b.tables = few_table_words(T * topk, few_max_units(E, T, topk)) * 4;
-  b.arrived = d.splits > 1 ? (size_t)d.n_blocks * 4 : 0;
-  b.part = d.splits > 1 ? (size_t)d.splits * d.n_blocks * d.rows * T * 64 : 0;
+  for (const long long steps : {0LL, 1LL << 40}) {  // either plan
+    const DownPlan d = down_plan(f, H, steps);
+    if (d.splits == 1) continue;
+    b.arrived = std::max(b.arrived, (size_t)d.n_blocks * 4);
+    b.part = std::max(b.part, (size_t)d.splits * d.n_blocks * d.rows * T * 64);
+  }
   return b;
 }
 
@@ -957,7 +968,9 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   p.out = a.out;
   p.out_f32 = a.out_f32 ? 1 : 0;
 
-  const DownPlan dp = down_plan(a.fmt, a.H);
+  const long long units = min(a.E, a.T * a.topk);
+  const int ksteps = prepared_ksteps(wf, a.I), steps = nv4w(a.fmt) ? (ksteps + 1) / 2 : ksteps;  // the down leg's
+  const DownPlan dp = down_plan(a.fmt, a.H, units * steps);
   p.splits = dp.splits;
   p.n_blocks = dp.n_blocks;
   p.tables = (uint32_t*)a.tables;
@@ -994,8 +1007,8 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   d.w_sf_expert = a.fmt == Fmt::FP8 ? (uint32_t)(a.H / 128 * (a.I / 128) * 4)
                                     : (uint32_t)prepared_scale_expert_bytes(wf, a.H, a.I);
   d.w_gs = a.w2_gs;
-  d.ksteps = prepared_ksteps(wf, a.I);
-  d.steps = nv4w(a.fmt) ? (d.ksteps + 1) / 2 : d.ksteps;
+  d.ksteps = ksteps;
+  d.steps = steps;
 
   auto up = [&](auto fmt, auto waves, auto ksp, auto groups, auto depth) {
     constexpr Fmt F = decltype(fmt)::value;
@@ -1016,16 +1029,16 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   // 266 (T 1, H 2048, I 1024: 18.1, 21.1, 25.6; FP8, T 1, a 1/8 shard: 18.4 by four, 23.6 by two).  By eight, one
   // K-step in flight each, in a single round of workgroups (FP8, T 1, H 7168, I 256: 17.6 against 18.5; MX, T 27,
   // H 4608, I 224, 20 experts: 17.2 against 18.7), not beyond (MX, T 32, I 2880, 128 experts: 202 against 188).
-  // MX needs slices of 32 columns (64: T 32 186 against 188 us, T 1 24.1 against 22.8).  NVFP4's x operand serves
+  // MX needs slices of 32 columns (64: T 32 186 against 188 us, T 1 24.1 against 22.8) and keeps one K-step in
+  // flight per wave (T 32 182, two 187); FP8 and BF16 two (T 16 216, one 225; T 4 248 and 249).  NVFP4's x operand serves
   // two slices of 16 where they still make a round: T 20, H 2880, I 2880 100 us against 110, T 16, H 7168, I 2048
   // 151 against 162; not with fewer: T 1, H 7168, I 256 25.9 against 18.9 (by eight 17.0).
-  const long long units = min(a.E, a.T * a.topk);
   const bool wide = units * ((a.I + 31) / 32) >= 256;
   const bool thin = units * ((a.I + 31) / 32) * (a.fmt == Fmt::MX ? 1 : 2) <= 256;
   // down: K-steps in flight per wave.  One: FP8, T 16, H 7168, I 2048 216 us, two 220; MX, T 1, H 2880, I 2880
   // 22.2 and 23.1.  Two: BF16, T 4, H 4096, I 14336 248, one 262; NVFP4, T 20, H 2880, I 2880 99 and 107, unless a
   // wave has only a step or two (T 1, H 2048, I 1024 13.8, one 13.0).
-  const bool brief = units * d.steps <= 2LL * dp.splits * 8;
+  const bool brief = units * steps <= 2LL * dp.splits * 8;
 #define C_(v) std::integral_constant<int, v>{}
 #define F_(v) std::integral_constant<Fmt, v>{}
   switch (a.fmt) {
@@ -1033,32 +1046,37 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
       if (few_h_fp32(a.fmt, a.T, a.topk, a.E, a.I)) {
         if (thin) up(F_(Fmt::FP8), C_(8), C_(8), C_(1), C_(1));
         else up(F_(Fmt::FP8), C_(4), C_(4), C_(1), C_(2));
-        down(F_(Fmt::FP8), C_(8), C_(2), C_(1), std::true_type{});
+        if (dp.rows == 2) down(F_(Fmt::FP8), C_(8), C_(2), C_(1), std::true_type{});
+        else down(F_(Fmt::FP8), C_(8), C_(4), C_(1), std::true_type{});
       } else {
         up(F_(Fmt::FP8), C_(8), C_(1), C_(1), C_(2));
-        down(F_(Fmt::FP8), C_(8), C_(2), C_(1), std::false_type{});
+        if (dp.rows == 2) down(F_(Fmt::FP8), C_(8), C_(2), C_(1), std::false_type{});
+        else down(F_(Fmt::FP8), C_(8), C_(4), C_(1), std::false_type{});
       }
       break;
     case Fmt::BF16:
       if (thin) up(F_(Fmt::BF16), C_(8), C_(8), C_(1), C_(1));
       else up(F_(Fmt::BF16), C_(4), C_(4), C_(1), C_(2));
-      down(F_(Fmt::BF16), C_(8), C_(1), C_(2), std::false_type{});
+      if (dp.rows == 1) down(F_(Fmt::BF16), C_(8), C_(1), C_(2), std::false_type{});
+      else down(F_(Fmt::BF16), C_(8), C_(2), C_(1), std::false_type{});
       break;
     case Fmt::MX:
       if (thin) up(F_(Fmt::MX), C_(8), C_(8), C_(2), C_(1));
-      else up(F_(Fmt::MX), C_(4), C_(4), C_(2), C_(2));
+      else up(F_(Fmt::MX), C_(4), C_(4), C_(2), C_(1));
       down(F_(Fmt::MX), C_(8), C_(4), C_(1), std::false_type{});
       break;
     case Fmt::NV4:
       if (wide) up(F_(Fmt::NV4), C_(4), C_(4), C_(2), C_(1));
       else up(F_(Fmt::NV4), C_(8), C_(8), C_(1), C_(1));
-      if (brief) down(F_(Fmt::NV4), C_(8), C_(2), C_(1), std::false_type{});
+      if (dp.rows == 4) down(F_(Fmt::NV4), C_(8), C_(4), C_(2), std::false_type{});
+      else if (brief) down(F_(Fmt::NV4), C_(8), C_(2), C_(1), std::false_type{});
       else down(F_(Fmt::NV4), C_(8), C_(2), C_(2), std::false_type{});
       break;
     case Fmt::NVF4:
       if (wide) up(F_(Fmt::NVF4), C_(4), C_(4), C_(2), C_(1));
       else up(F_(Fmt::NVF4), C_(8), C_(8), C_(1), C_(1));
-      if (brief) down(F_(Fmt::NVF4), C_(8), C_(2), C_(1), std::false_type{});
+      if (dp.rows == 4) down(F_(Fmt::NVF4), C_(8), C_(4), C_(2), std::false_type{});
+      else if (brief) down(F_(Fmt::NVF4), C_(8), C_(2), C_(1), std::false_type{});
       else down(F_(Fmt::NVF4), C_(8), C_(2), C_(2), std::false_type{});
       break;
   }

@@ -478,6 +478,10 @@ def test_few(fmt, T, routing):
     ("w4a8_mx", 32, 32, 5, 2, 3), ("w4a8_mx", 2880, 96, 40, 4, 32), ("w4a8_mx", 96, 2880, 6, 3, 2),
     ("nvfp4_w4a16", 64, 64, 4, 2, 7), ("nvfp4_w4a16", 1216, 192, 9, 4, 1), ("nvfp4", 64, 64, 4, 2, 7),
     ("nvfp4", 192, 1088, 9, 4, 18), ("nvfp4_w4a16", 192, 1088, 9, 4, 18), ("nvfp4_w4a16", 2880, 64, 5, 2, 6),
+    # twice the tiles per down workgroup, and the same H with short parts
+    ("bf16", 2432, 1344, 7, 3, 4), ("bf16", 5248, 192, 9, 3, 20), ("fp8_block128", 4224, 640, 12, 3, 9),
+    ("fp8_block128", 4224, 128, 3, 1, 3), ("fp8_block128", 2944, 1152, 5, 2, 3), ("nvfp4_w4a16", 2880, 1024, 20, 4, 8),
+    ("nvfp4", 2880, 1024, 20, 4, 8), ("nvfp4", 2880, 64, 4, 2, 2),
     ("bf16", 64, 64, 1000, 32, 32),            # more experts and slots than any wave holds
     ("w4a8_mx", 64, 64, 40, 32, 32),
     ("w4a8_mx", 512, 64, 1000, 32, 32)])       # the largest tables and sums in LDS
