@@ -34,9 +34,9 @@
 // order of the sum is fixed by the sizes and the routing alone.
 //
 // Bound by the weights' bytes, except NVFP4's decode (VALU).  Kernel times and rates: FP8, T 16, H 7168, I 2048,
-// E 32, k 8: gate_up 920 MB in 138 us (6.65 TB/s), down 460 MB in 74 (6.2); T 1: 235 MB in 37 (6.35), 117 MB in 22
-// (5.3); BF16, T 4, H 4096, I 14336: 1096 MB in 167 (6.55), 548 MB in 85 (6.45); W4A8, T 32, H 2880, E 128:
-// 749 MB in 120 (6.25), 374 MB in 63 (5.9); NVFP4 x BF16, T 3: 242 MB in 45 (5.3), 121 MB in 26 (4.6).  A read
+// E 32, k 8: gate_up 920 MB in 139 us (6.6 TB/s), down 460 MB in 69 (6.6); T 1: 235 MB in 37 (6.4), 117 MB in 22.5
+// (5.2); BF16, T 4, H 4096, I 14336: 1096 MB in 167 (6.55), 548 MB in 85 (6.45); W4A8, T 32, H 2880, E 128:
+// 749 MB in 113 (6.6), 374 MB in 63 (5.95); NVFP4 x BF16, T 3: 242 MB in 46 (5.3), 121 MB in 26.5 (4.55).  A read
 // alone reaches 6.85 TB/s from 0.9 GB on, 6.4 at 0.24 GB.
 #include <algorithm>
 #include <type_traits>
