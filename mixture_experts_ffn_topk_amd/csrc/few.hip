@@ -17,7 +17,7 @@
 //   * Weights go straight from HBM into registers, each byte read once, non-temporal,
 //     and nothing is staged in LDS: a wave is on its own until its sums are complete.
 //   * gate_up: a wave owns 16 or 32 columns of h (MX: 32, one scale block) of one expert,
-//     or 1/KSP of their K-steps where that would leave the part underfilled.
+//     or (all but FP8's whole blocks) 1/KSP of their K-steps.
 //   * down: a workgroup owns 16 R output columns and all units, or one of `splits`
 //     parts of them; its waves split its (unit, K-step) sequence evenly and add each
 //     unit's result to their own sums per token in LDS: no y rows, no combine launch.
