@@ -14,7 +14,8 @@
 // NaN gets a NaN scale (the codes of such a block mean nothing), so that a NaN
 // is never turned into a number on the way into the experts.
 //
-// The squares are summed in fp64 and r is a pair of floats, so that n is rounded once, for any finite z.
+// The sum of squares and the root are fp64 and the products keep what they drop, so that n is rounded once, for any
+// finite z that is not below 2^-100 of its row's rms.
 //
 // A workgroup owns one row, which stays in registers between the sum of squares
 // and the outputs: thread i holds the 8-column chunks i, i + threads, ....  Each
@@ -83,27 +84,23 @@ MOE_DEV uint32_t amax_bits8(const float (&f)[8]) {
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
   return m;
 }
-// 1 / sqrt(m) as hi + lo: the row's codes share this factor, and each one that lies nearer to a
-// rounding border than its error comes out as the other code.  One Newton step in fp64 from the float
-// root, or the fp64 root where m is no normal float.
-MOE_DEV void inv_root(double m, float& hi, float& lo) {
+// 1 / sqrt(m) in fp64: the row's codes share this factor, and each one that lies nearer to a rounding border
+// than its error comes out as the other code.  Two Newton steps from the float root, or the fp64 root where m is
+// no normal float.
+MOE_DEV double inv_root(double m) {
   const float f = (float)m;
-  double r;
-  if (f < INFINITY && f >= kMinNormal) {
-    r = (double)__builtin_amdgcn_rsqf(f);
-    r = fma(0.5 * r, fma(-m * r, r, 1.0), r);
-    r = fma(0.5 * r, fma(-m * r, r, 1.0), r);
-  } else {
-    r = 1.0 / sqrt(m);
-  }
-  hi = (float)r;
-  lo = hi < INFINITY ? (float)(r - (double)hi) : 0.0f;
+  if (!(f < INFINITY && f >= kMinNormal)) return 1.0 / sqrt(m);
+  double r = (double)__builtin_amdgcn_rsqf(f);
+  r = fma(0.5 * r, fma(-m * r, r, 1.0), r);
+  return fma(0.5 * r, fma(-m * r, r, 1.0), r);
 }
-// n + e, |e| at most half a step of n, to odd: the value cut to 24 bits with the last one set if anything was
-// cut.  Rounding that to fewer bits gives what rounding n + e itself would.
-MOE_DEV float to_odd(float n, float e) {
-  const uint32_t u = __float_as_uint(n), cut = __builtin_islessgreater(e, 0.0f) ? 1u : 0u;  // (an infinity's e is NaN)
-  return __uint_as_float((u - ((u ^ __float_as_uint(e)) >> 31 & cut)) | cut);
+// v to odd: cut to 24 bits with the last one set if anything was cut.  Rounding that to fewer bits gives what
+// rounding v itself would.
+MOE_DEV float to_odd(double v) {
+  const float f = (float)v;
+  const double e = v - (double)f;
+  const uint32_t u = __float_as_uint(f), cut = __builtin_islessgreater(e, 0.0) ? 1u : 0u;  // (an infinity's e is NaN)
+  return __uint_as_float((u - ((u ^ (uint32_t)(__builtin_bit_cast(uint64_t, e) >> 32)) >> 31 & cut)) | cut);
 }
 
 // What one row's chunk writes of the format's activations: n the 8 values, c the chunk.
@@ -189,6 +186,11 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fma((double)z[v][i], (double)z[v][i], ss);
   }
+  // (the row stays as floats: kept alive past the sum, its fp64 copies double the registers, 92 -> 105 us)
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("" : "+v"(z[v][i]));
   ss = wave_sum_f64(ss);
   double sum = ss;
   if (nthr > 64) {
@@ -197,8 +199,10 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
     sum = 0.0;
     for (int w = 0; w < nthr >> 6; ++w) sum += part[w];
   }
-  float r, r_lo;
-  inv_root(sum * p.inv_h + (double)p.eps, r, r_lo);
+  const double r = inv_root(sum * p.inv_h + (double)p.eps);
+  const float r_hi = (float)r, r_lo = (float)(r - (double)r_hi);
+  // a row whose 1 / rms has no two full halves in fp32, or is 0, infinite or NaN
+  const bool far = !(r_hi >= 0x1p-100f && r_hi <= 0x1p100f);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = tid + v * nthr;
@@ -216,29 +220,25 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
     }
     // n = z r w, rounded once: what the products drop (r's lower half too) goes into the last one
     float n[8];
-    auto product = [&](int i, float& a, float& lost) {
-      a = z[v][i] * r;
-      lost = fmaf(z[v][i], r_lo, fmaf(z[v][i], r, -a)) * w[i];
-      return fmaf(a, w[i], lost);
-    };
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float a, lost;
-      n[i] = product(i, a, lost);
+      const float a = z[v][i] * r_hi, lost = fmaf(z[v][i], r_lo, fmaf(z[v][i], r_hi, -a));
+      n[i] = fmaf(a, w[i], lost * w[i]);
     }
+    bool again = far;
     if constexpr (F == Fmt::MX) {
       // MX codes are n times a power of two: where its 24 bits end in a tie of E4M3's 4 (one in 2^20; a wave in
       // 2000), what was rounded off decides.  (Always to odd: 8192 x 7168 95 -> 98 us.)
       uint32_t tie = ~0u;
 #pragma unroll
       for (int i = 0; i < 8; ++i) tie = min(tie, (__float_as_uint(n[i]) << 12) ^ 0x80000000u);
-      if (tie == 0) {
+      again = again || tie == 0;
+    }
+    if (again) {  // (fp64 for every row: 8192 x 7168 92.2 -> 94.7 us)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float a, lost;
-          product(i, a, lost);
-          n[i] = to_odd(n[i], fmaf(a, w[i], -n[i]) + lost);
-        }
+      for (int i = 0; i < 8; ++i) {
+        const double d = (double)z[v][i] * r * (double)w[i];
+        n[i] = F == Fmt::MX ? to_odd(d) : (float)d;
       }
     }
     if (live && p.x_norm != nullptr) store16((uint16_t*)p.x_norm + at, pack8(n));

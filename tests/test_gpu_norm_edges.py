@@ -1,0 +1,78 @@
+"""GPU tests of moe_add_rmsnorm at the ends of its range: rows whose root leaves fp32."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from mixture_experts_ffn_topk_amd import MoEFFN
+from oracle import layer as ol
+from test_gpu_layer_ops import bits
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+BLOCK = {"fp8_block128": 128, "w4a8_mx": 32, "nvfp4": 16}
+
+
+def norm(fmt, x, w, eps, x_gs=1.0):
+    """(x_norm, codes' values, scales' values) of rows x without a residual."""
+    T, H = x.shape
+    moe = MoEFFN(H, 128, 4, 2, T, fmt=fmt)
+    xn = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    q = sf = None
+    if fmt in BLOCK:
+        q = torch.empty((T, H // 2 if fmt == "nvfp4" else H), dtype=torch.uint8, device="cuda")
+        sf = torch.empty((T, H // BLOCK[fmt]), dtype=torch.float32 if fmt == "fp8_block128" else torch.uint8, device="cuda")
+    moe.add_rmsnorm(T, x.cuda(), None, w.cuda(), eps, x_norm=xn, x_q=q, x_sf=sf, x_global_scale=x_gs)
+    torch.cuda.synchronize()
+    if q is None:
+        return bits(xn), None, None
+    q, sf = q.cpu().numpy(), sf.cpu().numpy()
+    if fmt == "fp8_block128":
+        return bits(xn), oracle.e4m3_decode(q), sf.astype(np.float64)
+    if fmt == "w4a8_mx":
+        return bits(xn), oracle.e4m3_decode(q), oracle.ue8m0_decode(sf)
+    return bits(xn), oracle.e2m1_decode_nibbles(oracle.e2m1_unpack(q)), oracle.e4m3_decode(sf)
+
+
+def half_step(v, mantissa, emin):
+    """Half the step of a format with so many mantissa bits at |v| (emin: the smallest normal exponent)."""
+    return 0.5 * np.exp2(np.maximum(np.floor(np.log2(np.abs(v) + 1e-300)), emin) - mantissa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8_block128", "w4a8_mx"])
+def test_norm_rows_at_the_ends_of_fp32(fmt):
+    """Without eps a row's norm does not depend on its magnitude: subnormal rows (their 1 / rms is no fp32 number),
+    rows of the smallest number, rows whose 1 / rms is subnormal."""
+    T, H = 12, 512
+    g = torch.Generator().manual_seed(41)
+    x = torch.randn(T, H, generator=g)
+    for t, e in enumerate((-126, -130, -135, -140, -145, 100, 110, 120, 124, 125, 126)):
+        x[t] = (x[t].double().clamp(-3.0, 3.0) * 2.0 ** (e - (e > 0))).float()
+    x[11] = 2.0 ** -149
+    w = 1 + 0.3 * torch.randn(H, generator=g)
+    xn, codes, sf = norm(fmt, x, w, 0.0)
+    _, n = ol.add_rmsnorm(bits(x), None, bits(w), 0.0)
+    assert np.isfinite(n).all()
+    # rounded to fp32 (half a step: 2^-24), then to bf16
+    assert np.all(np.abs(xn - n) <= half_step(n, 7, -126) + 2.0 ** -24 * np.abs(n))
+    if codes is None:
+        return
+    v = n / np.repeat(sf, BLOCK[fmt], axis=1)
+    # FP8: the norm and the quotient are rounded to fp32 before the code (2^-24 each)
+    slack = 2.0 ** -30 * half_step(v, 3, -6) if fmt == "w4a8_mx" else 2.0 ** -23 * np.abs(v)
+    assert np.all(np.abs(codes - v) <= half_step(v, 3, -6) + slack)
+
+
+def test_norm_mx_codes_of_large_rows_are_those_of_the_unrounded_norm():
+    """Rows of 2^127, whose 1 / rms has few bits in fp32: as at 1, each code is the fp64 norm's, rounded once."""
+    T, H = 4096, 352
+    g = torch.Generator().manual_seed(8)
+    x = torch.randint(-240, 241, (T, H), generator=g).float() * 2.0 ** 120
+    w = (1 + 0.3 * torch.randn(H, generator=g)).bfloat16()
+    _, codes, sf = norm("w4a8_mx", x, w, 1e-6)
+    _, n = ol.add_rmsnorm(bits(x), None, bits(w), 1e-6)
+    v = n / np.repeat(sf, 32, axis=1)
+    assert np.all(np.abs(codes - v) <= half_step(v, 3, -6) * (1 + 2.0 ** -30))
