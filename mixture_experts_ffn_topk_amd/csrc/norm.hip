@@ -24,6 +24,7 @@
 //
 // Bound by the bytes: 8192 x 7168 with residual, bf16 norm and FP8 codes moves 530 MB in 91 us (5.8 TB/s; a plain
 // copy of 2 GiB reaches 4.9), 2048 x 2880 with an fp32 stream 89 MB in 15.7; one row by its latency, 3.2 us.
+#include <cfloat>
 #include <type_traits>
 
 #include "layer.h"
@@ -218,12 +219,13 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
         store16((float*)p.residual_out + at + 4, __builtin_bit_cast(i32x4, f32x4{z[v][4], z[v][5], z[v][6], z[v][7]}));
       }
     }
-    // n = z r w, rounded once: what the products drop (r's lower half too) goes into the last one
+    // n = z r w, rounded once: what the products drop (r's lower half too) goes into the last one, an infinite w
+    // does not
     float n[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float a = z[v][i] * r_hi, lost = fmaf(z[v][i], r_lo, fmaf(z[v][i], r_hi, -a));
-      n[i] = fmaf(a, w[i], lost * w[i]);
+      n[i] = fmaf(a, w[i], lost * __builtin_amdgcn_fmed3f(w[i], FLT_MAX, -FLT_MAX));
     }
     bool again = far;
     if constexpr (F == Fmt::MX) {

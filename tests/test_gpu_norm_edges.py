@@ -1,4 +1,4 @@
-"""GPU tests of moe_add_rmsnorm at the ends of its range: rows whose root leaves fp32."""
+"""GPU tests of moe_add_rmsnorm at the ends of its range: rows whose root leaves fp32, infinite weights."""
 import numpy as np
 import pytest
 import torch
@@ -76,3 +76,21 @@ def test_norm_mx_codes_of_large_rows_are_those_of_the_unrounded_norm():
     _, n = ol.add_rmsnorm(bits(x), None, bits(w), 1e-6)
     v = n / np.repeat(sf, 32, axis=1)
     assert np.all(np.abs(codes - v) <= half_step(v, 3, -6) * (1 + 2.0 ** -30))
+
+
+def test_norm_infinite_weights_give_infinities():
+    """inf x n is the infinity of the product's sign, NaN only against a zero; other columns keep their values."""
+    T, H = 64, 512
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(T, H, generator=g).bfloat16()
+    x[3, 7] = 0.0
+    w = (1 + 0.3 * torch.randn(H, generator=g)).bfloat16()
+    clean, _, _ = norm("bf16", x, w, 1e-6)
+    w[7], w[300] = float("inf"), float("-inf")
+    xn, _, _ = norm("bf16", x, w, 1e-6)
+    want = np.sign(bits(x))
+    with np.errstate(invalid="ignore"):
+        assert np.array_equal(xn[:, 7], want[:, 7] * np.inf, equal_nan=True)
+        assert np.array_equal(xn[:, 300], want[:, 300] * -np.inf, equal_nan=True)
+    keep = [c for c in range(H) if c not in (7, 300)]
+    assert np.array_equal(xn[:, keep], clean[:, keep])
