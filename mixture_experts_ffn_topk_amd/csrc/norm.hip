@@ -229,12 +229,17 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
     }
     bool again = far;
     if constexpr (F == Fmt::MX) {
-      // MX codes are n times a power of two: where its 24 bits end in a tie of E4M3's 4 (one in 2^20; a wave in
-      // 2000), what was rounded off decides.  (Always to odd: 8192 x 7168 95 -> 98 us.)
-      uint32_t tie = ~0u;
+      // MX codes are n times a power of two.  Where n's 24 bits end in a border of E4M3's codes (bit 19 alone of the
+      // last 20: a tie of the normal ones; none of them: a tie of the subnormal ones, or 448, where the scale
+      // changes; one in 2^19, a wave in 1000), what was rounded off decides.  (A subnormal n is left as it is;
+      // always to odd: 8192 x 7168 95 -> 98 us.)
+      uint32_t low = ~0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) tie = min(tie, (__float_as_uint(n[i]) << 12) ^ 0x80000000u);
-      again = again || tie == 0;
+      for (int i = 0; i < 8; ++i) low = min(low, __float_as_uint(n[i]) << 13);
+      if (low == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) again |= (__float_as_uint(n[i]) << 13) == 0 && n[i] != 0.0f;
+      }
     }
     if (again) {  // (fp64 for every row: 8192 x 7168 92.2 -> 94.7 us)
 #pragma unroll

@@ -1,4 +1,7 @@
-"""GPU tests of moe_add_rmsnorm at the ends of its range: rows whose root leaves fp32, infinite weights."""
+"""GPU tests of moe_add_rmsnorm at the ends of its range: rows whose root leaves fp32, infinite weights, ties."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -94,3 +97,30 @@ def test_norm_infinite_weights_give_infinities():
         assert np.array_equal(xn[:, 300], want[:, 300] * -np.inf, equal_nan=True)
     keep = [c for c in range(H) if c not in (7, 300)]
     assert np.array_equal(xn[:, keep], clean[:, keep])
+
+
+@pytest.mark.parametrize("a,b", [(1, 7), (7, 17), (7, 23)])
+def test_norm_mx_ties_of_subnormal_codes(a, b):
+    """Norms next to the ties of E4M3's subnormal and normal codes, nearer than fp32 can tell: half of the row's columns
+    are a, half b, whose rms is a whole number, and the weights put n at a tie times 1 + at most 2^-24."""
+    r = math.isqrt((a * a + b * b) // 2)
+    assert 2 * r * r == a * a + b * b
+    H = 1024
+    x = torch.tensor([a, b] * (H // 2), dtype=torch.float32).reshape(1, H)
+    ties = [Fraction(2 * k + 1, 1024) for k in range(8)] + [Fraction(2 * k + 1, 16) for k in range(8, 16)]
+    w = np.zeros(H)
+    for block in range(H // 32):
+        scale = Fraction(2) ** (block - 16)
+        for i in range(32):  # the largest, of the scale's binade; then each tie twice, for columns of a and of b
+            c = block * 32 + i
+            want = (440 if i == 0 else ties[i // 2] * (-1) ** (i // 4)) * scale
+            w[c] = np.float32(float(want * r / (a, b)[c % 2]))
+    _, codes, sf = norm("w4a8_mx", x, torch.from_numpy(w).float(), 0.0)
+    assert np.array_equal(sf[0], 2.0 ** np.arange(-16, 16))
+    wrong = []
+    for c in range(H):
+        v = Fraction(float(w[c])) * (a, b)[c % 2] / r / Fraction(float(sf[0, c // 32]))
+        half = Fraction(2) ** (max(math.floor(math.log2(abs(v))), -6) - 4)
+        if abs(Fraction(float(codes[0, c])) - v) > half * (1 + Fraction(1, 2 ** 30)):
+            wrong.append((c, float(v), codes[0, c]))
+    assert not wrong
