@@ -108,10 +108,8 @@ MOE_DEV float to_odd(double v) {
 template <Fmt F>
 MOE_DEV void quantise8(const NormParams& p, size_t t, int c, const float (&n)[8], bool live) {
   const int lane = lane_id(), C = p.H >> 3;
-  uint32_t m = amax_bits8(n);
-  m = dpp_max_u32<0xB1>(m);  // lanes l, l ^ 1
   if constexpr (F == Fmt::NVF4) {
-    const float a = __uint_as_float(m);
+    const float a = __uint_as_float(dpp_max_u32<0xB1>(amax_bits8(n)));  // lanes l, l ^ 1
     // v_cvt_pk_fp8_f32 past the E4M3 maximum would give NaN: the scale saturates; a NaN maximum stays one
     const float s6 = a / (6.0f * p.x_gs);
     const uint32_t code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s6 > 448.0f ? 448.0f : s6, 0.0f, 0, false) & 0xFFu;
@@ -120,10 +118,14 @@ MOE_DEV void quantise8(const NormParams& p, size_t t, int c, const float (&n)[8]
     uint32_t v = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float r = e2m1_rne_sat(n[i] * inv), b = fabsf(r);
-      // magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 -> codes 0 .. 7
-      const uint32_t k = b < 2.0f ? (uint32_t)(b * 2.0f) : (b < 4.0f ? (uint32_t)b + 2u : (b < 6.0f ? 6u : 7u));
-      v |= (k | (k != 0 && r < 0.0f ? 8u : 0u)) << (4 * i);
+      // the quotient n / den, rounded once, so that ties go to the even code (bounded, so that an infinite n keeps
+      // its sign)
+      float q = __builtin_amdgcn_fmed3f(n[i] * inv, 16.0f, -16.0f);
+      q = fmaf(fmaf(-q, den, n[i]), inv, q);
+      // magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 -> codes 0 .. 7, in steps of 0.5, 1 and 2; ties to even
+      const float b = fminf(fabsf(q), 6.0f);
+      const float k = __builtin_rintf(b * (b < 2.0f ? 2.0f : b < 4.0f ? 1.0f : 0.5f)) + (b < 2.0f ? 0.0f : b < 4.0f ? 2.0f : 4.0f);
+      v |= ((uint32_t)k | (k != 0.0f && q < 0.0f ? 8u : 0u)) << (4 * i);
     }
     if (live) {
       ((uint32_t*)p.x_q)[t * C + c] = v;
@@ -131,6 +133,8 @@ MOE_DEV void quantise8(const NormParams& p, size_t t, int c, const float (&n)[8]
     }
     return;
   }
+  uint32_t m = amax_bits8(n);
+  m = dpp_max_u32<0xB1>(m);  // lanes l, l ^ 1
   m = dpp_max_u32<0x4E>(m);  // 4 lanes: 32 columns
   float inv, sc = 1.0f;
   if constexpr (F == Fmt::FP8) {

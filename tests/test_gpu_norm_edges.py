@@ -124,3 +124,19 @@ def test_norm_mx_ties_of_subnormal_codes(a, b):
         if abs(Fraction(float(codes[0, c])) - v) > half * (1 + Fraction(1, 2 ** 30)):
             wrong.append((c, float(v), codes[0, c]))
     assert not wrong
+
+
+@pytest.mark.parametrize("x_gs", [0.01, 1 / 3, 0.7, 3.1, 0.001, 11 / 2688])
+def test_norm_nvfp4_ties_go_to_the_even_code(x_gs):
+    """n / (s x_global_scale) exactly at E2M1's ties (rows of 1, so n is the weight; a global scale of 17 bits, so
+    that the tie's n is an fp32 number)."""
+    gs = float((np.float32([x_gs]).view(np.uint32) & np.uint32(0xFFFFFF80)).view(np.float32)[0])
+    ties = [0.25, -0.75, 1.25, -1.75, 2.5, -3.5, 5.0, -0.25, 0.75, -1.25, 1.75, -2.5, 3.5, -5.0, 0.0]
+    even = [0.0, -1.0, 1.0, -2.0, 2.0, -4.0, 4.0, 0.0, 1.0, -1.0, 2.0, -2.0, 4.0, -4.0, 0.0]
+    scales = [1.0, 2.0, 0.5, 416.0, 0.875, 1.125, 13.0, 0.0625]
+    w = np.array([[6.0, *ties]]) * (np.array(scales) * gs)[:, None]
+    assert np.array_equal(w[:, 1:], w[:, 1:].astype(np.float32))
+    x = torch.ones(2, w.size)
+    _, codes, sf = norm("nvfp4", x, torch.from_numpy(w.reshape(-1)).float(), 0.0, gs)
+    assert np.array_equal(sf, np.tile(scales, (2, 1)))
+    assert np.array_equal(codes, np.tile(np.array([6.0, *even]), (2, len(scales))))
