@@ -25,6 +25,7 @@
 // Bound by the bytes: 8192 x 7168 with residual, bf16 norm and FP8 codes moves 530 MB in 91 us (5.8 TB/s; a plain
 // copy of 2 GiB reaches 4.9), 2048 x 2880 with an fp32 stream 89 MB in 15.7; one row by its latency, 3.2 us.
 #include <cfloat>
+#include <cmath>
 #include <type_traits>
 
 #include "layer.h"
@@ -46,7 +47,8 @@ struct NormParams {
   void* x_sf;
   int H;
   int weight_f32;
-  float eps, x_gs;
+  float eps, x_gs;  // x_gs: NVFP4's global scale, times 2^x_exp
+  int x_exp;
   double inv_h;
 };
 
@@ -109,7 +111,16 @@ template <Fmt F>
 MOE_DEV void quantise8(const NormParams& p, size_t t, int c, const float (&n)[8], bool live) {
   const int lane = lane_id(), C = p.H >> 3;
   if constexpr (F == Fmt::NVF4) {
-    const float a = __uint_as_float(dpp_max_u32<0xB1>(amax_bits8(n)));  // lanes l, l ^ 1
+    // an x_gs far from 1: n and x_gs both over its power of two, so that the scales' products and quotients are
+    // normal numbers
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = n[i];
+    if (p.x_exp != 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = __builtin_ldexpf(n[i], p.x_exp);
+    }
+    const float a = __uint_as_float(dpp_max_u32<0xB1>(amax_bits8(u)));  // lanes l, l ^ 1
     // v_cvt_pk_fp8_f32 past the E4M3 maximum would give NaN: the scale saturates; a NaN maximum stays one
     const float s6 = a / (6.0f * p.x_gs);
     const uint32_t code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s6 > 448.0f ? 448.0f : s6, 0.0f, 0, false) & 0xFFu;
@@ -118,10 +129,10 @@ MOE_DEV void quantise8(const NormParams& p, size_t t, int c, const float (&n)[8]
     uint32_t v = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // the quotient n / den, rounded once, so that ties go to the even code (bounded, so that an infinite n keeps
+      // the quotient u / den, rounded once, so that ties go to the even code (bounded, so that an infinite u keeps
       // its sign)
-      float q = __builtin_amdgcn_fmed3f(n[i] * inv, 16.0f, -16.0f);
-      q = fmaf(fmaf(-q, den, n[i]), inv, q);
+      float q = __builtin_amdgcn_fmed3f(u[i] * inv, 16.0f, -16.0f);
+      q = fmaf(fmaf(-q, den, u[i]), inv, q);
       // magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 -> codes 0 .. 7, in steps of 0.5, 1 and 2; ties to even
       const float b = fminf(fabsf(q), 6.0f);
       const float k = __builtin_rintf(b * (b < 2.0f ? 2.0f : b < 4.0f ? 1.0f : 0.5f)) + (b < 2.0f ? 0.0f : b < 4.0f ? 2.0f : 4.0f);
@@ -262,7 +273,11 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
   NormParams p{a.x, a.residual, a.weight, a.residual_out, a.x_norm, a.x_q, a.x_sf, a.H, a.weight_f32 ? 1 : 0,
-               a.eps, a.x_gs, 1.0 / a.H};
+               a.eps, a.x_gs, 0, 1.0 / a.H};
+  if (a.fmt == Fmt::NVF4 && !(a.x_gs > 0x1p-100f && a.x_gs < 0x1p100f)) {  // (finite and > 0)
+    p.x_exp = -std::ilogb(a.x_gs);
+    p.x_gs = std::ldexp(a.x_gs, p.x_exp);
+  }
   const int chunks = a.H / 8;
   // Chunks per thread: one where the row fits 1024 threads (one row's latency: 4.0 us against 4.2 with two
   // at H 7168), two for wide rows by the thousand (8192 x 7168: 93.6 us against 97; four: 108).

@@ -140,3 +140,27 @@ def test_norm_nvfp4_ties_go_to_the_even_code(x_gs):
     _, codes, sf = norm("nvfp4", x, torch.from_numpy(w.reshape(-1)).float(), 0.0, gs)
     assert np.array_equal(sf, np.tile(scales, (2, 1)))
     assert np.array_equal(codes, np.tile(np.array([6.0, *even]), (2, len(scales))))
+
+
+@pytest.mark.parametrize("x_gs", [2.0 ** -149, 3 * 2.0 ** -140, 2.0 ** -126, 1.7e-38, 1.0, 1.1e38, 3.4e38])
+@pytest.mark.parametrize("spread", [0.0, 1.0, 40.0, 3000.0, 1e9])
+def test_norm_nvfp4_takes_every_global_scale(x_gs, spread):
+    """Global scales at both ends of fp32, with norms from below the smallest code to beyond the largest; zeros are
+    zeros."""
+    H, top = 512, float(np.finfo(np.float32).max)
+    x_gs = float(np.float32(x_gs))
+    g = torch.Generator().manual_seed(3)
+    w = (torch.randn(H, generator=g).double() * x_gs * spread).clamp(-top, top).float()
+    w[5::7] = 0.0
+    w[64:96] = 0.0
+    xn, codes, sf = norm("nvfp4", torch.ones(1, H), w, 0.0, x_gs)
+    n = bits(w).reshape(-1, 16)
+    s6 = np.minimum(np.abs(n).max(axis=1) / (6.0 * x_gs), 448.0)
+    # 6 x_global_scale, the quotient: 2^-24 each
+    assert np.all(np.abs(sf[0] - s6) <= half_step(s6, 3, -6) + 2.0 ** -23 * s6)
+    den = sf[0][:, None] * x_gs
+    v = np.clip(np.where(den > 0, n / np.where(den > 0, den, 1.0), 0.0), -6.0, 6.0)
+    codes = codes.reshape(-1, 16)
+    # s x_global_scale, the quotient: 2^-24 each
+    assert np.all(np.abs(codes - v) <= half_step(v, 1, 0) + 2.0 ** -23 * np.abs(v))
+    assert not codes[n == 0].any()
