@@ -447,9 +447,9 @@ moe_status moe_add_rmsnorm(const moe_handle* h, int32_t num_tokens, const void* 
                            float eps, void* residual_out, void* x_norm, void* x_q, void* x_sf, float x_global_scale,
                            hipStream_t stream);
 
-/* Bytes of workspace moe_router_logits needs for num_tokens tokens (0 for small sizes, and if
-   num_tokens is out of range or the call would not be supported).  It never shrinks as num_tokens
-   grows: one of the largest step's serves them all. */
+/* Bytes of workspace moe_router_logits needs for num_tokens tokens with fp32 weights (0 for small
+   sizes, and if num_tokens is out of range or the call would not be supported; bf16 weights need none).
+   It never shrinks as num_tokens grows: one of the largest step's serves them all. */
 size_t moe_router_workspace_size(const moe_handle* h, int32_t num_tokens);
 
 /* Router logits ([ActPack] routing_input_mode FromLogits: the routing_logits it takes):
@@ -457,8 +457,8 @@ size_t moe_router_workspace_size(const moe_handle* h, int32_t num_tokens);
    moe_add_rmsnorm), router_w [E,H] bf16 or fp32 (router_w_fp32), logits [T,E] fp32.  The sums
    are fp32, of exact products for bf16 weights and of products exact to 2^-24 for fp32
    ones; their order depends on the sizes alone.  A NaN or infinity stays in its token's row or its
-   expert's column.  x, router_w and logits 16-byte aligned; ws as for moe_plan.  hidden above 32768
-   or T x E above 2^31 is MOE_ERR_UNSUPPORTED. */
+   expert's column.  x, router_w and logits 16-byte aligned; ws as for moe_plan (bf16 weights: may be
+   NULL).  hidden above 32768 or T x E above 2^31 is MOE_ERR_UNSUPPORTED. */
 moe_status moe_router_logits(const moe_handle* h, int32_t num_tokens, const void* x, const void* router_w,
                              int32_t router_w_fp32, float* logits, void* ws, size_t ws_bytes, hipStream_t stream);
 

@@ -681,7 +681,7 @@ class MoEFFN:
 
     def router_logits(self, num_tokens, x, router_w, logits, ws=None, stream=None):
         """moe_router_logits: logits [T,E] fp32 of x [T,H] bf16 and router_w [E,H] bf16 or
-        fp32 (a raw address: bf16); ws from alloc_router_workspace."""
+        fp32 (a raw address: bf16); ws from alloc_router_workspace (bf16 weights need none)."""
         import torch
         T, H, E = num_tokens, self.hidden, self.experts
         w32 = getattr(router_w, "dtype", None) is torch.float32

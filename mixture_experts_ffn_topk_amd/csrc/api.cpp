@@ -639,7 +639,7 @@ moe_status moe_router_logits(const moe_handle* h, int32_t T, const void* x, cons
   if (T > 0 && (!x || !router_w || !logits)) return MOE_ERR_INVALID_ARGUMENT;
   if (!al(x, 16) || !al(router_w, 16) || !al(logits, 16) || !al(ws, 256)) return MOE_ERR_INVALID_ARGUMENT;
   if (!router_supported(h->cfg, T)) return MOE_ERR_UNSUPPORTED;
-  const size_t need = moe_router_workspace_size(h, T);
+  const size_t need = router_w_fp32 ? moe_router_workspace_size(h, T) : 0;  // (bf16 weights never split K)
   if (ws_bytes < need || (need > 0 && !ws)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const moe::RouterArgs a{T, h->cfg.hidden, h->cfg.num_experts, x, router_w, router_w_fp32 != 0, logits, (float*)ws};
   return hip_status(moe::launch_router_logits(a, stream));
