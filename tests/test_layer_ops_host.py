@@ -202,3 +202,16 @@ def test_activation_codes():
     s = ol.act_scales("nvfp4", n / 448.0 * 6.0, 0.5)
     assert s[0].tolist() == [2.0] + [0.0] * 7
     assert ol.act_codes("nvfp4", n / 448.0 * 6.0, s, 0.5)[0, :4].tolist() == [6.0, -3.0, 0.0, 0.0]
+
+
+def test_router_workspace_refusals_where_one_is_needed():
+    """Sizes whose fp32 weights split K: a workspace too small by a byte, none, and a misaligned one are refused."""
+    lib, h = handle(num_experts=256, max_num_tokens=8192)
+    for T in (2100, 4100, 8192):
+        need = lib.moe_router_workspace_size(h, T)
+        assert need > 0 and need % 256 == 0
+        assert lib.moe_router_logits(h, T, M, 2 * M, 1, 3 * M, 4 * M, need - 1, None) == WS_SMALL
+        assert lib.moe_router_logits(h, T, M, 2 * M, 1, 3 * M, 4 * M, 0, None) == WS_SMALL
+        assert lib.moe_router_logits(h, T, M, 2 * M, 1, 3 * M, None, need, None) == WS_SMALL
+        assert lib.moe_router_logits(h, T, M, 2 * M, 1, 3 * M, 4 * M + 128, need, None) == INVALID
+    lib.moe_destroy(h)
