@@ -164,3 +164,23 @@ def test_norm_nvfp4_takes_every_global_scale(x_gs, spread):
     # s x_global_scale, the quotient: 2^-24 each
     assert np.all(np.abs(codes - v) <= half_step(v, 1, 0) + 2.0 ** -23 * np.abs(v))
     assert not codes[n == 0].any()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8_block128", "w4a8_mx", "nvfp4"])
+def test_norm_outputs_are_one_rounding_from_the_definition(fmt):
+    """x_norm and the codes within half of the step at each value, and what rounding n (MX: not), the quotient and
+    NVFP4's product of the scales to fp32 adds, 2^-24 of the value each (the stream is exact in fp32: small integers)."""
+    T, H, x_gs = 2048, 1920, 0.0019
+    g = torch.Generator().manual_seed(17)
+    x = torch.randint(-240, 241, (T, H), generator=g).float() * 2.0 ** -6
+    w = (1 + 0.3 * torch.randn(H, generator=g)).bfloat16()
+    xn, codes, sf = norm(fmt, x, w, 1e-6, x_gs)
+    _, n = ol.add_rmsnorm(bits(x), None, bits(w), float(np.float32(1e-6)))
+    assert np.all(np.abs(xn - n) <= half_step(n, 7, -126) + 2.0 ** -24 * np.abs(n))
+    if codes is None:
+        return
+    den = np.repeat(sf, BLOCK[fmt], axis=1) * (float(np.float32(x_gs)) if fmt == "nvfp4" else 1.0)
+    top, mantissa, emin = (6.0, 1, 0) if fmt == "nvfp4" else (448.0, 3, -6)
+    v = np.clip(n / den, -top, top)
+    slack = {"fp8_block128": 2 * 2.0 ** -24, "w4a8_mx": 2.0 ** -40, "nvfp4": 3 * 2.0 ** -24}[fmt]
+    assert np.all(np.abs(codes - v) <= half_step(v, mantissa, emin) + slack * np.abs(v))
