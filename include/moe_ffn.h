@@ -478,7 +478,8 @@ size_t moe_few_workspace_size(const moe_handle* h, int32_t num_tokens);
    sums are in another order, fixed by the sizes and the routing.  A token that lists an expert twice
    gets it by the sum of both weights.  Masked slots and ids outside [0,E) contribute
    nothing; a token with no valid slot gets the addends (or zeros).  A NaN or infinity in one token's activations
-   stays in that token's output.  out may be shared or residual itself when it is bf16.
+   stays in that token's output.  out may be shared or residual itself when it is bf16; any
+   other overlap with them is MOE_ERR_INVALID_ARGUMENT.
    Handles of any tile_regime, fuse_combine and fuse_plan (which do not apply).  num_tokens
    above MOE_FEW_MAX_TOKENS is MOE_ERR_UNSUPPORTED; ws as for moe_forward, of
    moe_few_workspace_size bytes, its contents neither read nor kept. */

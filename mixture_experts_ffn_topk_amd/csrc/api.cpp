@@ -241,7 +241,7 @@ bool sizes_supported(const moe_config& c) {
   return true;
 }
 
-// Host ranges of device buffers, for the overlap rules of moe_add_rmsnorm.
+// Host ranges of device buffers, for the overlap rules of moe_add_rmsnorm and moe_forward_few.
 struct Span {
   const void* p;
   size_t bytes;
@@ -666,6 +666,10 @@ moe_status moe_forward_few(const moe_handle* h, int32_t T, const void* x, const 
   if (!al(x, 16) || !al(x_sf, 4) || !al(out, 16) || !al(shared, 16) || !al(residual, 16) || !al(ws, 256) ||
       !al(w->w13, 16) || !al(w->w2, 16) || !al(w->w13_sf, 4) || !al(w->w2_sf, 4))
     return MOE_ERR_INVALID_ARGUMENT;
+  // (a thread reads the addends of the elements that it writes, no others)
+  const size_t n = (size_t)T * c.hidden, oe = c.out_fp32 ? 4 : 2;
+  for (const void* add : {shared, residual})
+    if (!apart_or_same(Span{out, n * oe, oe}, Span{add, n * 2, 2})) return MOE_ERR_INVALID_ARGUMENT;
   if (T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
   const FewLayout L = few_layout(c, T);
   if (ws_bytes < L.total || (L.total > 0 && !ws)) return MOE_ERR_WORKSPACE_TOO_SMALL;

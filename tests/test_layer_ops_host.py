@@ -215,3 +215,18 @@ def test_router_workspace_refusals_where_one_is_needed():
         assert lib.moe_router_logits(h, T, M, 2 * M, 1, 3 * M, None, need, None) == WS_SMALL
         assert lib.moe_router_logits(h, T, M, 2 * M, 1, 3 * M, 4 * M + 128, need, None) == INVALID
     lib.moe_destroy(h)
+
+
+def test_few_refuses_an_output_that_overlaps_an_addend():
+    """bf16: anything but the addend's own buffer; fp32 elements are never an addend's."""
+    for fp32 in (0, 1):
+        lib, h = handle(out_fp32=fp32)
+        out = 5 * M
+        for name in ("sh", "rs"):
+            for at in (out + 16, out - 16, out + ROW - 16) + ((out, out + 2 * ROW - 16) if fp32 else ()):
+                assert few(lib, h, **{name: at}) == INVALID, (fp32, name, at - out)
+        # past the end: whatever else is wrong is found (here the workspace)
+        assert few(lib, h, rs=out + ROW * (1 + fp32), n=0) == WS_SMALL
+        if not fp32:
+            assert few(lib, h, rs=out, sh=out, n=0) == WS_SMALL
+        lib.moe_destroy(h)
