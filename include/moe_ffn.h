@@ -432,7 +432,8 @@ moe_status moe_forward_static(const moe_handle* h, int32_t num_tokens, const voi
        NVFP4 x NVFP4  per 16 columns s = E4M3_RNE_sat(amax / (6 x_global_scale)), codes
                       E2M1_RNE_sat(n / (s x_global_scale)), zero where s = 0
      A block that holds a NaN gets a NaN scale.  The squares are summed in fp64, so no finite z
-   overflows the mean.
+   overflows the mean, and n is rounded to fp32 once.  MX codes are those of n before that; FP8 and
+   NVFP4 take the amax, the quotients and s x_global_scale as fp32 numbers of the rounded n.
    x [T,H] and weight [H] are bf16 or, with x_fp32 / weight_fp32 = 1, fp32; residual and
    residual_out [T,H] are both given or both NULL, bf16 or fp32 (residual_fp32).
    x_norm [T,H] bf16 and the pair x_q, x_sf may be NULL, not all three; BF16 and NVFP4 x
@@ -471,11 +472,13 @@ size_t moe_few_workspace_size(const moe_handle* h, int32_t num_tokens);
 
 /* The routed layer for few tokens: moe_forward_ex's operator, formats and arguments in two
    launches ([EPConfig] fused_moe_ready: as few launches as there are steps) -- routing,
-   gate_up, SwiGLU; then down, combine, addends -- that read each active expert's weights once
-   and build no plan.  (FROM_LOGITS with more than 4 tokens: the top-k is a launch of its own
-   before them.)  The intermediate is requantised exactly as in moe_forward; the expert outputs are
+   gate_up, SwiGLU; then down, combine, addends -- that read each active expert's weights once for up
+   to 16 of its tokens, twice for more, and build no plan.  (FROM_LOGITS with more than 4 tokens: the
+   top-k is a launch of its own before them.)  It is the faster call while most experts have at most
+   16 tokens; where T k / E is above about 12 and the weights are large, moe_forward_ex is.  The intermediate is requantised exactly as in moe_forward; the expert outputs are
    not rounded to bf16 before the router weights (moe_forward stores them as y), and the fp32
-   sums are in another order, fixed by the sizes and the routing.  A token that lists an expert twice
+   sums are in another order, fixed by the sizes and the routing.  shared and residual are bf16: an
+   fp32 residual stream takes the layer's out as x of the next moe_add_rmsnorm instead.  A token that lists an expert twice
    gets it by the sum of both weights.  Masked slots and ids outside [0,E) contribute
    nothing; a token with no valid slot gets the addends (or zeros).  A NaN or infinity in one token's activations
    stays in that token's output.  out may be shared or residual itself when it is bf16; any

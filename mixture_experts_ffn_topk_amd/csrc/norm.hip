@@ -22,8 +22,12 @@
 // quantisation block then lies in 16, 4 or 2 neighbouring lanes, and its maximum
 // takes DPP moves only.
 //
-// Bound by the bytes: 8192 x 7168 with residual, bf16 norm and FP8 codes moves 530 MB in 91 us (5.8 TB/s; a plain
-// copy of 2 GiB reaches 4.9), 2048 x 2880 with an fp32 stream 89 MB in 15.7; one row by its latency, 3.2 us.
+// FP8 and NVFP4 codes are those of the quotient of n and the scale, each an fp32 number, rounded to fp32 and then to
+// the code; MX codes those of n before any rounding.
+//
+// Bound by the bytes: 8192 x 7168 with residual, bf16 norm and FP8 codes moves 530 MB in 93 us (5.7 TB/s; a plain
+// copy of 2 GiB reaches 4.9), NVFP4 codes 504 MB in 94 (5.4), 2048 x 2880 with an fp32 stream 89 MB in 16.2; one row
+// by its latency, 3.4 us.
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -77,7 +81,7 @@ MOE_DEV i32x4 pack8(const float (&f)[8]) {
 }
 
 // The rows' stores are non-temporal: the lines of the inputs, which other rows' loads share, stay
-// (8192 x 7168: 101 -> 96 us, 512 x 7168: 9.0 -> 7.6; non-temporal loads were 8 to 30 % slower).
+// (8192 x 7168: 97 -> 93 us, 512 x 7168: 9.1 -> 7.4; non-temporal loads were 8 to 30 % slower).
 MOE_DEV void store16(void* p, i32x4 v) { __builtin_nontemporal_store(v, (i32x4*)p); }
 
 // The largest |f| of 8 values, as bits: unsigned order puts NaN above infinity, so a NaN survives.
@@ -246,8 +250,7 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(NormParams p) {
     if constexpr (F == Fmt::MX) {
       // MX codes are n times a power of two.  Where n's 24 bits end in a border of E4M3's codes (bit 19 alone of the
       // last 20: a tie of the normal ones; none of them: a tie of the subnormal ones, or 448, where the scale
-      // changes; one in 2^19, a wave in 1000), what was rounded off decides.  (A subnormal n is left as it is;
-      // always to odd: 8192 x 7168 95 -> 98 us.)
+      // changes; one in 2^19, a wave in 1000), what was rounded off decides.  (A subnormal n is left as it is.)
       uint32_t low = ~0u;
 #pragma unroll
       for (int i = 0; i < 8; ++i) low = min(low, __float_as_uint(n[i]) << 13);
@@ -279,8 +282,8 @@ hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
     p.x_gs = std::ldexp(a.x_gs, p.x_exp);
   }
   const int chunks = a.H / 8;
-  // Chunks per thread: one where the row fits 1024 threads (one row's latency: 4.0 us against 4.2 with two
-  // at H 7168), two for wide rows by the thousand (8192 x 7168: 93.6 us against 97; four: 108).
+  // Chunks per thread: one where the row fits 1024 threads (one row, H 7168, in a graph: 3.75 us, with two 4.3, with
+  // four 5.4), two for wide rows by the thousand (8192 x 7168: 92.7 us, with one 95.2, with four 99.7).
   const int nv = chunks <= 512 || (chunks <= 1024 && a.T < 1024) ? 1 : chunks <= 2048 ? 2 : 4;
   const int threads = ((chunks + nv - 1) / nv + 63) / 64 * 64;
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)a.T), dim3((unsigned)threads), 0, s, p); };

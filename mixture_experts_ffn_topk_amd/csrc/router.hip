@@ -8,9 +8,9 @@
 // each multiplied on the matrix cores: bf16 products are exact in fp32, so the
 // result has the error of an fp32 sum.
 //
-// Bound by what one CU can read: about 118 requests of 128 bytes are in flight in its vector cache, at 631 cycles
-// each with x from HBM (54 GB/s; T 8192, H 7168, E 256: 192 lines a K-step and workgroup, 53 us, 570 TFLOP/s), and
-// at 60 to 78 GB/s where the operands come from L2 (T 256: 458 KB per 16 x 16 tile, 7.5 us).  fp32 weights: by the
+// Bound by what one CU can read: on average 87 requests of 128 bytes are in flight in its vector cache, at 550 cycles
+// each with x from HBM (49 GB/s; T 8192, H 7168, E 256: 192 lines a K-step and workgroup, 56 us, 540 TFLOP/s), and
+// at 58 to 78 GB/s where the operands come from L2 (T 256: 458 KB per 16 x 16 tile, 8.0 us).  fp32 weights: by the
 // VALU work of their split.
 #include <algorithm>
 #include <type_traits>
@@ -58,7 +58,8 @@ MOE_DEV void split3(const f32x4 a, const f32x4 b, i32x4 (&o)[3]) {
   }
 }
 
-// logits[t, e] of fp32 weights without the split (rare: its result was NaN).  A NaN sum is final.
+// logits[t, e] of fp32 weights without the split (rare: its result was NaN).  A NaN sum is final.  One lane an
+// output, so slow: T 8192, H 7168, E 256, one token with a NaN in its last column 125 -> 1920 us, in its first 116.
 MOE_DEV float plain_dot(const RouterParams& p, int t, int e) {
   const uint16_t* x = (const uint16_t*)p.x + (size_t)t * p.H;
   const float* w = (const float*)p.w + (size_t)e * p.H;
