@@ -171,7 +171,8 @@ MOE_DEV void quantise8(const NormParams& p, size_t t, int c, const float (&n)[8]
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     q[i] = n[i] * inv;  // MX: exact
-    if constexpr (F == Fmt::FP8) q[i] = fmaf(fmaf(-q[i], sc, n[i]), inv, q[i]);  // the quotient n / sc, rounded once
+    // the quotient n / sc, rounded once (0 over an infinite scale)
+    if constexpr (F == Fmt::FP8) q[i] = fmaf(fmaf(-q[i], fminf(sc, FLT_MAX), n[i]), inv, q[i]);
   }
   uint2 v;
   v.x = f32x2_to_e4m3_sat(q[0], q[1]) | f32x2_to_e4m3_sat(q[2], q[3]) << 16;

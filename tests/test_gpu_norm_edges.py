@@ -184,3 +184,18 @@ def test_norm_outputs_are_one_rounding_from_the_definition(fmt):
     v = np.clip(n / den, -top, top)
     slack = {"fp8_block128": 2 * 2.0 ** -24, "w4a8_mx": 2.0 ** -40, "nvfp4": 3 * 2.0 ** -24}[fmt]
     assert np.all(np.abs(codes - v) <= half_step(v, mantissa, emin) + slack * np.abs(v))
+
+
+def test_norm_fp8_codes_beside_an_infinity_are_zero():
+    """A block with an infinite weight has an infinite scale: the codes of its finite elements are those of n / inf."""
+    H = 512
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(8, H, generator=g)
+    w = 1 + 0.3 * torch.randn(H, generator=g)
+    _, clean, clean_sf = norm("fp8_block128", x, w, 1e-6)
+    w[130] = float("inf")
+    _, codes, sf = norm("fp8_block128", x, w, 1e-6)
+    assert np.isposinf(sf[:, 1]).all()
+    assert not codes[:, [c for c in range(128, 256) if c != 130]].any()
+    other = [c for c in range(H) if not 128 <= c < 256]
+    assert np.array_equal(codes[:, other], clean[:, other]) and np.array_equal(sf[:, [0, 2, 3]], clean_sf[:, [0, 2, 3]])
