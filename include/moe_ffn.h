@@ -491,6 +491,79 @@ moe_status moe_forward_few(const moe_handle* h, int32_t num_tokens, const void* 
                            const float* routing_bias, const moe_weights* w /* host struct */, const void* shared,
                            const void* residual, void* out, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+   The experts' products outside the fused layer, on a plan's rows: bf16 with their gradients (training), MXFP4 x
+   MXFP4 (serving), and the SwiGLU between them.  Weights are canonical; nothing is laid out ahead.  Row r of the
+   plan belongs to expert e where expert_start_indices[e] <= r < expert_start_indices[e+1]; of *plan only
+   expert_start_indices and (in all calls but moe_swiglu*) src_info are read.  Rows behind the last expert's
+   are left as they are.  Handles of any format; sizes n and k are the call's own (a layer's gate_up: n = 2I, k =
+   H; down: n = H, k = I).  A plan that is none is never followed out of a buffer.
+   num_tokens x num_topk above 2^26, n or k above 2^20 or more than 2^31 tiles are MOE_ERR_UNSUPPORTED. */
+
+/* Where a plan row r lies in a tensor of rows. */
+typedef enum {
+  MOE_ROWS_PLAN = 0,   /* at r: [T*k, ..] in the plan's order */
+  MOE_ROWS_TOKEN = 1,  /* at token src_info[r] / k: [T, ..] (inputs only) */
+  MOE_ROWS_PAIR = 2    /* at pair src_info[r]: [T*k, ..] = [T, k, ..], as moe_combine reads y */
+} moe_row_order;
+
+/* Product by expert ([MegaFFN]: the two legs' GEMMs over expert_start_indices), bf16 with fp32 sums:
+     out[o(r), j] = sum over i < k of a[s(r), i] * w[e, j, i]     w [E,n,k]
+     with w_kn:                       a[s(r), i] * w[e, i, j]     w [E,k,n]: the gradient of a forward product's rows
+   a bf16 (rows of k; a_rows: any order), out (rows of n) bf16, one rounding of the sum, or fp32 (out_fp32);
+   out_rows PLAN or PAIR (TOKEN, where rows would meet, is MOE_ERR_UNSUPPORTED: moe_combine adds a token's pairs).
+   n and k multiples of 8; a, w and out 16-byte aligned; out overlaps no input.  The order of a sum depends on the
+   sizes alone. */
+moe_status moe_grouped_gemm(const moe_handle* h, int32_t num_tokens, int32_t n, int32_t k, const void* a,
+                            int32_t a_rows, const void* w, int32_t w_kn, const moe_plan_buffers* plan /* host struct */,
+                            void* out, int32_t out_fp32, int32_t out_rows, hipStream_t stream);
+
+/* The gradient of the weights of moe_grouped_gemm:
+     dw[e, j, i] = sum over expert e's rows r of dout[s(r), j] * a[s'(r), i]      (+= with accumulate)
+   dout (rows of n) and a (rows of k) bf16, each in any order; dw [E,n,k] bf16, one rounding of the fp32 sum, or fp32
+   (dw_fp32).  accumulate needs dw_fp32 (else MOE_ERR_UNSUPPORTED).  An expert without rows, and num_tokens = 0, get
+   zeros (with accumulate: what was there).  Sizes, alignment and overlaps as moe_grouped_gemm. */
+moe_status moe_grouped_gemm_wgrad(const moe_handle* h, int32_t num_tokens, int32_t n, int32_t k, const void* dout,
+                                  int32_t dout_rows, const void* a, int32_t a_rows,
+                                  const moe_plan_buffers* plan /* host struct */, void* dw, int32_t dw_fp32,
+                                  int32_t accumulate, hipStream_t stream);
+
+/* Rows to MXFP4, weights or activations ([ActPack] encodings; the MX encoding with 4-bit elements):
+     per 32 columns the smallest e in [-127, 127] with 6 * 2^e >= amax; sf = e + 127 (UE8M0), q = E2M1_RNE_sat(x / 2^e)
+   x [num_rows, cols] bf16 or fp32 (x_fp32), x_row_stride elements between rows; q packed E2M1 [num_rows, cols/2] (element
+   2i the low nibble of byte i), sf [num_rows, cols/32]; values [num_rows, cols] bf16, or NULL: what the codes stand for
+   (6 * 2^126 is an infinity there).  Infinities saturate; zeros keep their sign; a block that holds a NaN gets sf = 255,
+   values of NaN and codes of no meaning.  cols a multiple of 32; x, q and values 16-byte aligned (x_row_stride with them),
+   sf 4.  values may be x itself (bf16, rows without gaps); any other overlap is MOE_ERR_INVALID_ARGUMENT. */
+moe_status moe_quantize_mxfp4(const moe_handle* h, int64_t num_rows, int32_t cols, const void* x, int32_t x_fp32,
+                              int64_t x_row_stride, void* q, void* sf, void* values, hipStream_t stream);
+
+/* moe_grouped_gemm of MXFP4 rows and weights (moe_quantize_mxfp4's q and sf, or any in that encoding): a packed E2M1
+   rows of k/2 bytes with a_sf rows of k/32, w [E,n,k/2] with w_sf [E,n,k/32].  Products of the values, fp32 sums; a
+   scale of 255 makes its row's (its column's) results NaN.  k a multiple of 32, n of 8; a, w and out 16-byte aligned,
+   a_sf and w_sf 4. */
+moe_status moe_grouped_gemm_mxfp4(const moe_handle* h, int32_t num_tokens, int32_t n, int32_t k, const void* a,
+                                  const void* a_sf, int32_t a_rows, const void* w, const void* w_sf,
+                                  const moe_plan_buffers* plan /* host struct */, void* out, int32_t out_fp32,
+                                  int32_t out_rows, hipStream_t stream);
+
+/* The clamped SwiGLU of the plan's rows ([MegaFFN] clamp_activation; the handle's I, activation_clamp c and fast_math):
+     h = g' / (1 + e^-g') * u',  g' = min(g, c), u' = clamp(u, -c, c)
+   gu [T*k, 2I] bf16, gate columns first (a product with w13), h_out [T*k, I] bf16, and q, sf: MXFP4 of the unrounded
+   h (as moe_quantize_mxfp4).  h_out, or the pair q and sf, may be NULL, not all three.  A NaN stays one.  gu, h_out and
+   q 16-byte aligned, sf 4; no overlaps. */
+moe_status moe_swiglu(const moe_handle* h, int32_t num_tokens, const void* gu,
+                      const moe_plan_buffers* plan /* host struct */, void* h_out, void* q, void* sf,
+                      hipStream_t stream);
+
+/* Its backward pass, with s = 1 / (1 + e^-g'):
+     dgu = (dh u' s (1 + g' (1 - s)) where g <= c, dh g' s where |u| <= c, else 0)
+   dh [T*k, I], dgu [T*k, 2I] bf16; h_out [T*k, I] bf16 or NULL: the forward value, for the down weights' gradient.  dgu
+   may be gu itself and h_out dh itself; no other overlaps.  16-byte aligned. */
+moe_status moe_swiglu_backward(const moe_handle* h, int32_t num_tokens, const void* gu, const void* dh,
+                               const moe_plan_buffers* plan /* host struct */, void* dgu, void* h_out,
+                               hipStream_t stream);
+
 const char* moe_status_string(moe_status s);
 int32_t moe_abi_version(void);
 

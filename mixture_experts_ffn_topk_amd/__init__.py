@@ -24,6 +24,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPOR
 FORMATS = {"fp8_block128": 0, "bf16": 1, "w4a8_mx": 2, "nvfp4_w4a16": 3, "nvfp4": 4}
 ROUTE_MODES = {"precomputed": 0, "from_logits": 1}
 TILE_REGIMES = {"auto": 0, "decode": 1, "prefill": 2}
+ROW_ORDERS = {"plan": 0, "token": 1, "pair": 2}
 
 
 class MoEError(RuntimeError):
@@ -64,7 +65,9 @@ EXPORTED = ["moe_create", "moe_destroy", "moe_workspace_size", "moe_down_split_s
             "moe_plan_ex", "moe_combine_ex", "moe_forward_ex", "moe_ffn_gate_up_timed", "moe_ffn_down_timed",
             "moe_ffn_down_combine", "moe_ffn_down_combine_timed", "moe_plan_ffn_gate_up", "moe_plan_ffn_gate_up_timed",
             "moe_forward_static", "moe_add_rmsnorm", "moe_router_workspace_size", "moe_router_logits",
-            "moe_few_workspace_size", "moe_forward_few", "moe_status_string", "moe_abi_version"]
+            "moe_few_workspace_size", "moe_forward_few", "moe_grouped_gemm", "moe_grouped_gemm_wgrad",
+            "moe_quantize_mxfp4", "moe_grouped_gemm_mxfp4", "moe_swiglu", "moe_swiglu_backward", "moe_status_string",
+            "moe_abi_version"]
 FEW_MAX_TOKENS = 32  # MOE_FEW_MAX_TOKENS
 STATIC_SCRATCH_BYTES = 64 << 20  # MOE_STATIC_SCRATCH_BYTES
 
@@ -139,6 +142,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_few_workspace_size.restype = sz
     lib.moe_forward_few.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, ctypes.POINTER(_Weights), vp, vp, vp, vp, sz, vp]
     lib.moe_forward_few.restype = i32
+    i64, plan = ctypes.c_int64, ctypes.POINTER(_Plan)
+    lib.moe_grouped_gemm.argtypes = [vp, i32, i32, i32, vp, i32, vp, i32, plan, vp, i32, i32, vp]
+    lib.moe_grouped_gemm.restype = i32
+    lib.moe_grouped_gemm_wgrad.argtypes = [vp, i32, i32, i32, vp, i32, vp, i32, plan, vp, i32, i32, vp]
+    lib.moe_grouped_gemm_wgrad.restype = i32
+    lib.moe_quantize_mxfp4.argtypes = [vp, i64, i32, vp, i32, i64, vp, vp, vp, vp]
+    lib.moe_quantize_mxfp4.restype = i32
+    lib.moe_grouped_gemm_mxfp4.argtypes = [vp, i32, i32, i32, vp, vp, i32, vp, vp, plan, vp, i32, i32, vp]
+    lib.moe_grouped_gemm_mxfp4.restype = i32
+    lib.moe_swiglu.argtypes = [vp, i32, vp, plan, vp, vp, vp, vp]
+    lib.moe_swiglu.restype = i32
+    lib.moe_swiglu_backward.argtypes = [vp, i32, vp, vp, plan, vp, vp, vp]
+    lib.moe_swiglu_backward.restype = i32
     lib.moe_status_string.argtypes = [i32]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_abi_version.argtypes = []
@@ -744,6 +760,153 @@ class MoEFFN:
                                         self._nbytes(ws), _current_stream() if stream is None else _stream(stream)),
                "moe_forward_few")
 
+    # ---------------------------------------------------------------- products by expert outside the fused layer
+    def _tensors(self, given):
+        """The addresses of (name, tensor, bytes, dtypes, required) arguments, checked as every call's are."""
+        ptrs = None
+        if not any(t is None and required for _, t, _, _, required in given):
+            ptrs = _fit([(t, size, kinds) for _, t, size, kinds, _ in given])
+        if ptrs is None:
+            for name, t, size, kinds, required in given:
+                if t is None and required:
+                    raise ValueError(f"{name} is required")
+                _need(t, name, size, kinds, required=required)
+            _on_current_gpu(**{name: t for name, t, *_ in given})
+            ptrs = [_ptr(t) for _, t, *_ in given]
+        return ptrs
+
+    @staticmethod
+    def _order(name, value):
+        if value not in ROW_ORDERS:
+            raise ValueError(f"{name} must be one of {', '.join(ROW_ORDERS)} (got {value!r})")
+        return ROW_ORDERS[value]
+
+    def _rows_of(self, order: int, T: int) -> int:
+        return T if order == 1 else T * self.topk
+
+    def _sides(self, t, what, n, k, swapped=False):
+        """(n, k) of an [E, n, k] tensor ([E, k, n] swapped), or as given beside a raw address."""
+        if t is None or isinstance(t, int):
+            if n is None or k is None:
+                raise ValueError(f"n and k are required where {what} is a raw address")
+            return n, k
+        if t.dim() != 3 or t.shape[0] != self.experts:
+            raise ValueError(f"{what} must be [{self.experts}, .., ..] (got {list(t.shape)})")
+        have = (t.shape[2], t.shape[1]) if swapped else (t.shape[1], t.shape[2])
+        if (n is not None and n != have[0]) or (k is not None and k != have[1]):
+            raise ValueError(f"{what} gives n, k = {have}, the call {(n, k)}")
+        return have
+
+    def _rows_args(self, plan, T):
+        import torch
+        i32 = (torch.int32,)
+        return [("plan['expert_start_indices']", plan.get("expert_start_indices"), 4 * (self.experts + 1), i32, True),
+                ("plan['src_info']", plan.get("src_info"), 4 * T * self.topk, i32, True)]
+
+    @staticmethod
+    def _rows_plan(start, src=None) -> _Plan:
+        return _Plan(None, start, None, None, src)
+
+    def grouped_gemm(self, num_tokens, a, w, plan: dict, out, a_rows="plan", out_rows="plan", w_kn=False, n=None,
+                     k=None, stream=None):
+        """moe_grouped_gemm: every plan row's product with its expert's weight, a bf16 and w [E, n, k] bf16 (w_kn:
+        [E, k, n], the gradient of a forward product's rows), out bf16 or fp32.  Row orders: "plan", "token" (inputs
+        only), "pair".  n and k come from w (a raw address: from the call; a raw out is bf16)."""
+        import torch
+        T, ao, oo = num_tokens, self._order("a_rows", a_rows), self._order("out_rows", out_rows)
+        n, k = self._sides(w, "w", n, k, w_kn)
+        bf16, f32 = (torch.bfloat16,), getattr(out, "dtype", None) is torch.float32
+        ap, wp, op, sp, ip = self._tensors(
+            [("a", a, self._rows_of(ao, T) * k * 2, bf16, True), ("w", w, self.experts * n * k * 2, bf16, True),
+             ("out", out, T * self.topk * n * (4 if f32 else 2), (torch.bfloat16, torch.float32), True)] +
+            self._rows_args(plan, T))
+        ps = self._rows_plan(sp, ip)
+        _check(self.lib.moe_grouped_gemm(self._h, T, n, k, ap, ao, wp, bool(w_kn), ctypes.byref(ps), op, f32, oo,
+                                         _current_stream() if stream is None else _stream(stream)), "moe_grouped_gemm")
+
+    def grouped_gemm_wgrad(self, num_tokens, dout, a, plan: dict, dw, dout_rows="plan", a_rows="plan",
+                           accumulate=False, n=None, k=None, stream=None):
+        """moe_grouped_gemm_wgrad: dw [E, n, k] (bf16 or fp32; accumulate: fp32 only) of dout's rows of n and a's rows
+        of k, both bf16.  n and k come from dw (a raw address: from the call, and dw is bf16)."""
+        import torch
+        T, do, ao = num_tokens, self._order("dout_rows", dout_rows), self._order("a_rows", a_rows)
+        n, k = self._sides(dw, "dw", n, k)
+        bf16, f32 = (torch.bfloat16,), getattr(dw, "dtype", None) is torch.float32
+        dp, ap, wp, sp, ip = self._tensors(
+            [("dout", dout, self._rows_of(do, T) * n * 2, bf16, T > 0), ("a", a, self._rows_of(ao, T) * k * 2, bf16, T > 0),
+             ("dw", dw, self.experts * n * k * (4 if f32 else 2), (torch.bfloat16, torch.float32), True)] +
+            self._rows_args(plan, T))
+        ps = self._rows_plan(sp, ip)
+        _check(self.lib.moe_grouped_gemm_wgrad(self._h, T, n, k, dp, do, ap, ao, ctypes.byref(ps), wp, f32,
+                                               bool(accumulate), _current_stream() if stream is None else
+                                               _stream(stream)), "moe_grouped_gemm_wgrad")
+
+    def quantize_mxfp4(self, x, q, sf, values=None, stream=None):
+        """moe_quantize_mxfp4: the rows of x [..., cols] (a bf16 or fp32 tensor; two dimensions with any row stride, or
+        contiguous) to packed codes q and scales sf, and values (bf16): what the codes stand for."""
+        import torch
+        f32 = (cols := x.shape[-1]) and x.dtype is torch.float32
+        rows = x.numel() // max(1, cols)
+        stride = x.stride(0) if x.dim() == 2 and rows > 1 else cols
+        if x.dim() == 2 and rows > 0 and x.stride(1) == 1 and stride >= cols:
+            flat = x.as_strided((1, (rows - 1) * stride + cols), ((rows - 1) * stride + cols, 1)) if stride != cols else x
+        else:
+            flat, stride = x, cols  # (_need refuses other strides)
+        codes = _byte_types()
+        xp, qp, sp, vp = self._tensors(
+            [("x", flat, 0, (torch.bfloat16, torch.float32), True), ("q", q, rows * cols // 2, codes, True),
+             ("sf", sf, rows * (cols // 32), codes, True), ("values", values, rows * cols * 2, (torch.bfloat16,), False)])
+        _check(self.lib.moe_quantize_mxfp4(self._h, rows, cols, xp, bool(f32), stride, qp, sp, vp,
+                                           _current_stream() if stream is None else _stream(stream)),
+               "moe_quantize_mxfp4")
+
+    def grouped_gemm_mxfp4(self, num_tokens, a, a_sf, w, w_sf, plan: dict, out, a_rows="plan", out_rows="plan", n=None,
+                           k=None, stream=None):
+        """moe_grouped_gemm_mxfp4: grouped_gemm of MXFP4 codes a (rows of k / 2 bytes) and w [E, n, k / 2] with scales
+        a_sf and w_sf.  n and k come from w (a raw address: from the call; a raw out is bf16)."""
+        import torch
+        T, ao, oo = num_tokens, self._order("a_rows", a_rows), self._order("out_rows", out_rows)
+        if w is None or isinstance(w, int):
+            n, k = self._sides(w, "w", n, k)
+        else:
+            n, half = self._sides(w, "w", n, None if k is None else k // 2)
+            k = 2 * half
+        codes, f32, E = _byte_types(), getattr(out, "dtype", None) is torch.float32, self.experts
+        rows = self._rows_of(ao, T)
+        ap, fp, wp, gp, op, sp, ip = self._tensors(
+            [("a", a, rows * (k // 2), codes, True), ("a_sf", a_sf, rows * (k // 32), codes, True),
+             ("w", w, E * n * (k // 2), codes, True), ("w_sf", w_sf, E * n * (k // 32), codes, True),
+             ("out", out, T * self.topk * n * (4 if f32 else 2), (torch.bfloat16, torch.float32), True)] +
+            self._rows_args(plan, T))
+        ps = self._rows_plan(sp, ip)
+        _check(self.lib.moe_grouped_gemm_mxfp4(self._h, T, n, k, ap, fp, ao, wp, gp, ctypes.byref(ps), op, f32, oo,
+                                               _current_stream() if stream is None else _stream(stream)),
+               "moe_grouped_gemm_mxfp4")
+
+    def swiglu(self, num_tokens, gu, plan: dict, h=None, q=None, sf=None, stream=None):
+        """moe_swiglu: the clamped SwiGLU of gu [T*k, 2I] bf16 as h [T*k, I] bf16, as MXFP4 (q, sf), or both."""
+        import torch
+        n, bf16, codes = num_tokens * self.topk * self.inter, (torch.bfloat16,), _byte_types()
+        gp, hp, qp, fp, sp = self._tensors(
+            [("gu", gu, n * 4, bf16, True), ("h", h, n * 2, bf16, q is None), ("q", q, n // 2, codes, sf is not None),
+             ("sf", sf, n // 32, codes, q is not None), self._rows_args(plan, num_tokens)[0]])
+        ps = self._rows_plan(sp)
+        _check(self.lib.moe_swiglu(self._h, num_tokens, gp, ctypes.byref(ps), hp, qp, fp,
+                                   _current_stream() if stream is None else _stream(stream)), "moe_swiglu")
+
+    def swiglu_backward(self, num_tokens, gu, dh, plan: dict, dgu, h=None, stream=None):
+        """moe_swiglu_backward: dgu [T*k, 2I] of dh [T*k, I], and the forward value h where it is given (all bf16; dgu
+        may be gu itself, h may be dh)."""
+        import torch
+        n, bf16 = num_tokens * self.topk * self.inter, (torch.bfloat16,)
+        gp, dp, op, hp, sp = self._tensors(
+            [("gu", gu, n * 4, bf16, True), ("dh", dh, n * 2, bf16, True), ("dgu", dgu, n * 4, bf16, True),
+             ("h", h, n * 2, bf16, False), self._rows_args(plan, num_tokens)[0]])
+        ps = self._rows_plan(sp)
+        _check(self.lib.moe_swiglu_backward(self._h, num_tokens, gp, dp, ctypes.byref(ps), op, hp,
+                                            _current_stream() if stream is None else _stream(stream)),
+               "moe_swiglu_backward")
+
     def _weight_fields(self):
         """(name, bytes, dtypes) of the prepared weights, in moe_weights' order; 0 bytes: not read."""
         if not hasattr(self, "_wfields"):
@@ -756,5 +919,5 @@ class MoEFFN:
         return self._wfields
 
 
-__all__ = ["MoEFFN", "MoEError", "load_library", "LIB_PATH", "EXPORTED", "FORMATS", "ROUTE_MODES", "TILE_REGIMES",
+__all__ = ["MoEFFN", "MoEError", "load_library", "LIB_PATH", "EXPORTED", "FORMATS", "ROUTE_MODES", "TILE_REGIMES", "ROW_ORDERS",
            "FEW_MAX_TOKENS"]

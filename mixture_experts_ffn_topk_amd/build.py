@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_ffn.so")
 SOURCES = ["api.cpp", "route.hip", "gemm.hip", "combine.hip", "prepare.hip", "static_ws.hip", "norm.hip", "router.hip",
-           "few.hip"]
+           "few.hip", "grouped.hip", "mxfp4.hip"]
 ARCH = os.environ.get("MOE_FFN_ARCH", "gfx950")
 
 

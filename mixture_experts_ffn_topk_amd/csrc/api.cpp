@@ -5,8 +5,10 @@
 
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
+#include "grouped.h"
 #include "launch.h"
 #include "layer.h"
 
@@ -272,6 +274,44 @@ FewLayout few_layout(const moe_config& c, int T) {
 
 bool router_supported(const moe_config& c, int T) {
   return c.hidden <= moe::kNormMaxHidden && (long long)T * c.num_experts <= (1LL << 31);
+}
+
+// ---------------------------------------------------------------- products by expert
+constexpr int kGroupedMaxPairs = 1 << 26, kGroupedMaxSide = 1 << 20;
+
+bool flag(int32_t v) { return v == 0 || v == 1; }
+bool row_order(int32_t v) { return v >= MOE_ROWS_PLAN && v <= MOE_ROWS_PAIR; }
+size_t rows_of(const moe_config& c, int T, int32_t order) {
+  return (size_t)T * (order == MOE_ROWS_TOKEN ? 1 : c.num_topk);
+}
+bool any_overlap(const Span& a, std::initializer_list<Span> others) {
+  for (const Span& b : others)
+    if (a.p && b.p && (uintptr_t)a.p < (uintptr_t)b.p + b.bytes && (uintptr_t)b.p < (uintptr_t)a.p + a.bytes) return true;
+  return false;
+}
+
+// What moe_grouped_gemm and moe_grouped_gemm_mxfp4 share; bits: of an operand's element.
+moe_status grouped_gemm(const moe_handle* h, int32_t T, int32_t n, int32_t k, const void* a, const void* a_sf,
+                        int32_t a_rows, const void* w, const void* w_sf, int32_t w_kn, const moe_plan_buffers* plan,
+                        void* out, int32_t out_fp32, int32_t out_rows, bool mx, hipStream_t stream) {
+  if (!valid_T(h, T) || n <= 0 || k <= 0 || n % 8 || k % (mx ? 32 : 8)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!flag(w_kn) || !flag(out_fp32) || !row_order(a_rows) || !row_order(out_rows)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!plan || !plan->expert_start_indices || !plan->src_info) return MOE_ERR_INVALID_ARGUMENT;
+  if (T > 0 && (!a || !w || !out || (mx && (!a_sf || !w_sf)))) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al(a, 16) || !al(w, 16) || !al(out, 16) || !al(a_sf, 4) || !al(w_sf, 4)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_config& c = h->cfg;
+  const size_t bits = mx ? 4 : 16, ar = rows_of(c, T, a_rows), wr = (size_t)c.num_experts * n;
+  if (any_overlap(Span{out, rows_of(c, T, MOE_ROWS_PAIR) * n * (out_fp32 ? 4 : 2), 0},
+                  {Span{a, ar * k / 8 * bits, 0}, Span{w, wr * k / 8 * bits, 0}, Span{a_sf, ar * k / 32, 0},
+                   Span{w_sf, wr * k / 32, 0}}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (out_rows == MOE_ROWS_TOKEN || (long long)T * c.num_topk > kGroupedMaxPairs || n > kGroupedMaxSide ||
+      k > kGroupedMaxSide || !moe::grouped_gemm_fits(T * c.num_topk, c.num_experts, n))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const moe::GroupedArgs g{c.num_experts, c.num_topk, T, plan->expert_start_indices, plan->src_info, n, k, a, a_sf,
+                           (moe::Rows)a_rows, w, w_sf, w_kn != 0, out, out_fp32 != 0, (moe::Rows)out_rows};
+  return hip_status(mx ? moe::launch_grouped_gemm_mxfp4(g, stream) : moe::launch_grouped_gemm(g, stream));
 }
 
 }  // namespace
@@ -713,6 +753,91 @@ moe_status moe_forward_few(const moe_handle* h, int32_t T, const void* x, const 
   a.out = out;
   a.out_f32 = c.out_fp32 != 0;
   return hip_status(moe::launch_few(a, stream));
+}
+
+moe_status moe_grouped_gemm(const moe_handle* h, int32_t T, int32_t n, int32_t k, const void* a, int32_t a_rows,
+                            const void* w, int32_t w_kn, const moe_plan_buffers* plan, void* out, int32_t out_fp32,
+                            int32_t out_rows, hipStream_t stream) {
+  return grouped_gemm(h, T, n, k, a, nullptr, a_rows, w, nullptr, w_kn, plan, out, out_fp32, out_rows, false, stream);
+}
+
+moe_status moe_grouped_gemm_mxfp4(const moe_handle* h, int32_t T, int32_t n, int32_t k, const void* a,
+                                  const void* a_sf, int32_t a_rows, const void* w, const void* w_sf,
+                                  const moe_plan_buffers* plan, void* out, int32_t out_fp32, int32_t out_rows,
+                                  hipStream_t stream) {
+  return grouped_gemm(h, T, n, k, a, a_sf, a_rows, w, w_sf, 0, plan, out, out_fp32, out_rows, true, stream);
+}
+
+moe_status moe_grouped_gemm_wgrad(const moe_handle* h, int32_t T, int32_t n, int32_t k, const void* dout,
+                                  int32_t dout_rows, const void* a, int32_t a_rows, const moe_plan_buffers* plan,
+                                  void* dw, int32_t dw_fp32, int32_t accumulate, hipStream_t stream) {
+  if (!valid_T(h, T) || n <= 0 || k <= 0 || n % 8 || k % 8) return MOE_ERR_INVALID_ARGUMENT;
+  if (!flag(dw_fp32) || !flag(accumulate) || !row_order(dout_rows) || !row_order(a_rows)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!plan || !plan->expert_start_indices || !plan->src_info || !dw) return MOE_ERR_INVALID_ARGUMENT;
+  if (T > 0 && (!dout || !a)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al(dout, 16) || !al(a, 16) || !al(dw, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_config& c = h->cfg;
+  if (any_overlap(Span{dw, (size_t)c.num_experts * n * k * (dw_fp32 ? 4 : 2), 0},
+                  {Span{dout, rows_of(c, T, dout_rows) * n * 2, 0}, Span{a, rows_of(c, T, a_rows) * k * 2, 0}}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if ((accumulate && !dw_fp32) || (long long)T * c.num_topk > kGroupedMaxPairs || n > kGroupedMaxSide ||
+      k > kGroupedMaxSide || !moe::grouped_wgrad_fits(c.num_experts, n, k))
+    return MOE_ERR_UNSUPPORTED;
+  const moe::WgradArgs g{c.num_experts, c.num_topk, T, plan->expert_start_indices, plan->src_info, n, k, dout,
+                         (moe::Rows)dout_rows, a, (moe::Rows)a_rows, dw, dw_fp32 != 0, accumulate != 0};
+  return hip_status(moe::launch_grouped_wgrad(g, stream));
+}
+
+moe_status moe_quantize_mxfp4(const moe_handle* h, int64_t rows, int32_t cols, const void* x, int32_t x_fp32,
+                              int64_t stride, void* q, void* sf, void* values, hipStream_t stream) {
+  if (!h || rows < 0 || cols <= 0 || cols % 32 || !flag(x_fp32)) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t e = x_fp32 ? 4 : 2;
+  if (stride < cols || stride > (1LL << 40) || stride * e % 16 || rows > (1LL << 40)) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows > 0 && (!x || !q || !sf)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al(x, 16) || !al(q, 16) || !al(sf, 4) || !al(values, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  // (an address range of 2^63 bytes and more is none)
+  if ((double)rows * (double)stride * (double)e > 9.0e18) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MOE_OK;
+  const size_t n = (size_t)rows * cols;
+  const Span in{x, ((size_t)(rows - 1) * stride + cols) * e, x_fp32 || stride != cols ? 0u : 2u}, oq{q, n / 2, 0},
+      os{sf, n / 32, 0}, ov{values, n * 2, 2};
+  if (any_overlap(oq, {in, os, ov}) || any_overlap(os, {in, ov}) || !apart_or_same(ov, in))
+    return MOE_ERR_INVALID_ARGUMENT;
+  return hip_status(moe::launch_quantize_mxfp4(x, x_fp32 != 0, rows, cols, stride, q, sf, values, stream));
+}
+
+moe_status moe_swiglu(const moe_handle* h, int32_t T, const void* gu, const moe_plan_buffers* plan, void* h_out,
+                      void* q, void* sf, hipStream_t stream) {
+  if (!valid_T(h, T) || !plan || !plan->expert_start_indices || !q != !sf) return MOE_ERR_INVALID_ARGUMENT;
+  if (T > 0 && (!gu || (!h_out && !q))) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al(gu, 16) || !al(h_out, 16) || !al(q, 16) || !al(sf, 4)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_config& c = h->cfg;
+  const size_t n = (size_t)T * c.num_topk * c.intermediate_hidden;
+  const Span in{gu, n * 4, 0}, oh{h_out, n * 2, 0}, oq{q, n / 2, 0}, os{sf, n / 32, 0};
+  if (any_overlap(oh, {in, oq, os}) || any_overlap(oq, {in, os}) || any_overlap(os, {in})) return MOE_ERR_INVALID_ARGUMENT;
+  if ((long long)T * c.num_topk > kGroupedMaxPairs) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const moe::SwigluArgs a{c.num_experts, T * c.num_topk, c.intermediate_hidden, plan->expert_start_indices,
+                          c.activation_clamp, c.fast_math != 0, gu, nullptr, h_out, q, sf, nullptr};
+  return hip_status(moe::launch_swiglu(a, stream));
+}
+
+moe_status moe_swiglu_backward(const moe_handle* h, int32_t T, const void* gu, const void* dh,
+                               const moe_plan_buffers* plan, void* dgu, void* h_out, hipStream_t stream) {
+  if (!valid_T(h, T) || !plan || !plan->expert_start_indices) return MOE_ERR_INVALID_ARGUMENT;
+  if (T > 0 && (!gu || !dh || !dgu)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al(gu, 16) || !al(dh, 16) || !al(dgu, 16) || !al(h_out, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_config& c = h->cfg;
+  const size_t n = (size_t)T * c.num_topk * c.intermediate_hidden;
+  // (a thread reads the gate, up and dh elements whose gradients and value it writes, no others)
+  const Span ig{gu, n * 4, 4}, id{dh, n * 2, 2}, od{dgu, n * 4, 4}, oh{h_out, n * 2, 2};
+  if (!apart_or_same(od, ig) || !apart_or_same(oh, id) || any_overlap(od, {id, oh}) || any_overlap(oh, {ig}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if ((long long)T * c.num_topk > kGroupedMaxPairs) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const moe::SwigluArgs a{c.num_experts, T * c.num_topk, c.intermediate_hidden, plan->expert_start_indices,
+                          c.activation_clamp, c.fast_math != 0, gu, dh, h_out, nullptr, nullptr, dgu};
+  return hip_status(moe::launch_swiglu(a, stream));
 }
 
 }  // extern "C"
