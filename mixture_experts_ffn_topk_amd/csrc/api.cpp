@@ -284,6 +284,10 @@ bool row_order(int32_t v) { return v >= MOE_ROWS_PLAN && v <= MOE_ROWS_PAIR; }
 size_t rows_of(const moe_config& c, int T, int32_t order) {
   return (size_t)T * (order == MOE_ROWS_TOKEN ? 1 : c.num_topk);
 }
+// Tensors whose rows are found through src_info are addressed by 32-bit offsets.
+bool placed(const moe_config& c, int T, int32_t order, size_t row_bytes) {
+  return order == MOE_ROWS_PLAN || rows_of(c, T, order) * row_bytes < 0xFFFFFFF0u;
+}
 bool any_overlap(const Span& a, std::initializer_list<Span> others) {
   for (const Span& b : others)
     if (a.p && b.p && (uintptr_t)a.p < (uintptr_t)b.p + b.bytes && (uintptr_t)b.p < (uintptr_t)a.p + a.bytes) return true;
@@ -306,7 +310,8 @@ moe_status grouped_gemm(const moe_handle* h, int32_t T, int32_t n, int32_t k, co
                    Span{w_sf, wr * k / 32, 0}}))
     return MOE_ERR_INVALID_ARGUMENT;
   if (out_rows == MOE_ROWS_TOKEN || (long long)T * c.num_topk > kGroupedMaxPairs || n > kGroupedMaxSide ||
-      k > kGroupedMaxSide || !moe::grouped_gemm_fits(T * c.num_topk, c.num_experts, n))
+      k > kGroupedMaxSide || !moe::grouped_gemm_fits(T * c.num_topk, c.num_experts, n) ||
+      !placed(c, T, a_rows, k / 8 * bits) || !placed(c, T, out_rows, (size_t)n * (out_fp32 ? 4 : 2)))
     return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   const moe::GroupedArgs g{c.num_experts, c.num_topk, T, plan->expert_start_indices, plan->src_info, n, k, a, a_sf,
@@ -781,7 +786,8 @@ moe_status moe_grouped_gemm_wgrad(const moe_handle* h, int32_t T, int32_t n, int
                   {Span{dout, rows_of(c, T, dout_rows) * n * 2, 0}, Span{a, rows_of(c, T, a_rows) * k * 2, 0}}))
     return MOE_ERR_INVALID_ARGUMENT;
   if ((accumulate && !dw_fp32) || (long long)T * c.num_topk > kGroupedMaxPairs || n > kGroupedMaxSide ||
-      k > kGroupedMaxSide || !moe::grouped_wgrad_fits(c.num_experts, n, k))
+      k > kGroupedMaxSide || !moe::grouped_wgrad_fits(c.num_experts, n, k) || !placed(c, T, dout_rows, (size_t)n * 2) ||
+      !placed(c, T, a_rows, (size_t)k * 2))
     return MOE_ERR_UNSUPPORTED;
   const moe::WgradArgs g{c.num_experts, c.num_topk, T, plan->expert_start_indices, plan->src_info, n, k, dout,
                          (moe::Rows)dout_rows, a, (moe::Rows)a_rows, dw, dw_fp32 != 0, accumulate != 0};

@@ -13,6 +13,7 @@
 // is staged as rows of 128 bytes and read with ds_read_b128; the others (T: transposed) as 64 summed rows of all the
 // tile's columns, read with ds_read_b64_tr_b16, which hands a lane 4 summed rows of its column.
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_common.h"
 #include "grouped.h"
@@ -22,7 +23,6 @@ namespace moe {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 enum class Op { FWD, GRAD, WGRAD, MX };
 
@@ -31,11 +31,10 @@ enum class Op { FWD, GRAD, WGRAD, MX };
 struct Place {
   uint32_t inverse;  // ceil(2^32 / k); 0: the pair itself
   int whole;         // -1: the pair itself, else 0
-  int gathered;      // -1: by src, 0: r
+  int gathered;
   int places;        // the tensor's rows: a plan that is none reads nothing past them
-  MOE_DEV int of(int r, int src) const {
-    const int at = min(max((int)__umulhi((uint32_t)src, inverse) + (src & whole), 0), places - 1);
-    return (at & gathered) | (r & ~gathered);
+  MOE_DEV int of(int src) const {
+    return min(max((int)__umulhi((uint32_t)src, inverse) + (src & whole), 0), places - 1);
   }
 };
 
@@ -49,24 +48,52 @@ struct GroupedParams {
   const uint8_t* Q_sf;
   long long p_expert;    // bytes of one expert's weights
   long long p_sf_expert;
-  long long p_ld, q_ld;  // bytes between rows as they lie in memory
+  uint32_t p_ld, q_ld;   // bytes between rows as they lie in memory
   int p_cols, q_cols;    // extents of the output (q_cols: WGRAD only, else the expert's rows)
   int K;                 // summed length (WGRAD: the expert's rows)
   int sf_row;            // MXFP4: K / 32
   Place q_place, p_place;
-  void* out;
-  long long out_ld;      // elements
-  long long out_expert;  // WGRAD: elements of one expert's dw
+  uint8_t* out;
+  uint32_t out_ld;       // bytes
+  long long out_expert;  // WGRAD: bytes of one expert's dw
   int out_pair;          // rows go to src_info[r]
   int accumulate;
-  int p_tiles, q_tiles;  // q_tiles: WGRAD; else the worst case over all experts
+  int p_tiles, q_tiles;  // q_tiles: WGRAD only
 };
 
-// 16 bytes that masked lanes load.
-__device__ __attribute__((aligned(16))) const uint32_t zero16[4] = {0, 0, 0, 0};
+// Lane l's 16 bytes land at l + 16 l; a lane whose offset is out of the resource's bounds writes zeros.  HIDDEN: written so
+// that the compiler does not see a store to LDS -- it lets no ds_read_b64_tr pass one in flight; the kernel's own waits
+// order the two.
+constexpr uint32_t kNone = 0xFFFFFFFFu, kAll = 0xFFFFFFF0u;  // an offset, and an extent, for the two
+template <bool HIDDEN>
+MOE_DEV void lds_copy16(i32x4 rsrc, uint32_t voff, void* l) {
+  if constexpr (HIDDEN)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
+                     (uint32_t)(uintptr_t)(LDS3 void*)l),
+                 "v"(voff), "s"(rsrc)
+                 : "memory");
+  else
+    lds_load16(make_rsrc((const void*)((uint64_t)(uint32_t)rsrc[0] | (uint64_t)(uint32_t)rsrc[1] << 32), (uint32_t)rsrc[2]),
+               l, voff, 0);
+}
+// A value that is the same in every lane, in a scalar register.
+MOE_DEV int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+MOE_DEV const uint8_t* scalar(const uint8_t* v) {
+  const uint64_t b = (uint64_t)v;
+  return (const uint8_t*)((uint64_t)(uint32_t)scalar((int)(uint32_t)b) | (uint64_t)(uint32_t)scalar((int)(uint32_t)(b >> 32)) << 32);
+}
+MOE_DEV i32x4 resource(const void* base, uint32_t bytes) {
+  const uint64_t b = (uint64_t)base;
+  return i32x4{scalar((int)(uint32_t)b), scalar((int)(uint32_t)(b >> 32)), scalar((int)bytes), 0x00020000};
+}
 
-MOE_DEV void lds_copy16(const void* g, void* l) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g, (LDS3 void*)l, 16, 0, 0);
+// A word of zeros, for masked lanes.
+__device__ __attribute__((aligned(16))) const uint32_t zero_words[4] = {0, 0, 0, 0};
+MOE_DEV const uint32_t* zero16_words() { return zero_words; }
+
+// (A plain store would wait for every load into LDS that is in flight.  The caller waits for this one.)
+MOE_DEV void lds_store8(void* l, uint64_t v) {
+  asm volatile("ds_write_b64 %0, %1" ::"v"((uint32_t)(uintptr_t)(LDS3 void*)l), "v"(v) : "memory");
 }
 
 MOE_DEV int wave_scan(int v) {  // inclusive
@@ -79,69 +106,88 @@ MOE_DEV int wave_scan(int v) {  // inclusive
   return v;
 }
 
+// start[e], made safe against a plan that is none.
+MOE_DEV int row_at(const GroupedParams& p, int e) { return min(max(p.start[e], 0), p.npairs); }
+
 struct TileAt {
+  bool ok;
   int expert, lo, hi;  // the expert's rows
   int q, p;            // tile indices within the expert
 };
 
-// start[e], made safe against a plan that is none.
-MOE_DEV int row_at(const GroupedParams& p, int e) { return min(max(p.start[e], 0), p.npairs); }
-
-// The tile of this workgroup; false: there is none.  Tiles lie expert by expert, in groups of GQ q-tiles, within a group
-// p-tile by p-tile: the workgroups that an XCD runs at once then share few operand panels in its L2.
+// The tiles of a workgroup, one after the other.  Tiles lie expert by expert, in groups of GQ q-tiles, within a group
+// p-tile by p-tile, and each XCD takes a contiguous eighth (WGRAD, whose tiles cost what their expert has rows: an eighth of
+// every expert's), its workgroups in turn: what an XCD runs at once then shares few operand panels in its L2.
 template <bool WGRAD, int BQ, int GQ>
-MOE_DEV bool find_tile(const GroupedParams& p, TileAt* t) {
-  const int lane = lane_id();
-  int L, within = 0;
-  if (WGRAD) {
-    const int per = p.q_tiles * p.p_tiles;
-    L = xcd_remap(blockIdx.x, gridDim.x);
-    t->expert = L / per;
-    within = L - t->expert * per;
-    t->lo = row_at(p, t->expert);
-    t->hi = max(t->lo, row_at(p, t->expert + 1));
-  } else {
-    int total = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-      const int e = e0 + lane;
-      int c = 0;
-      if (e < p.E) c = (max(0, row_at(p, e + 1) - row_at(p, e)) + BQ - 1) / BQ;
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d);
-      total += c;
-    }
-    const int G = min(total * p.p_tiles, (int)gridDim.x);
-    if ((int)blockIdx.x >= G) return false;
-    L = xcd_remap(blockIdx.x, G);
-    int before = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-      const int e = e0 + lane;
-      int lo = 0, hi = 0;
-      if (e < p.E) lo = row_at(p, e), hi = max(lo, row_at(p, e + 1));
-      const int mine = (hi - lo + BQ - 1) / BQ * p.p_tiles, upto = before + wave_scan(mine);
-      const unsigned long long found = __ballot(upto > L);
-      if (found) {
-        const int at = __ffsll(found) - 1;
-        t->expert = e0 + at;
-        t->lo = __shfl(lo, at);
-        t->hi = __shfl(hi, at);
-        within = L - __shfl(upto - mine, at);
-        break;
+struct Walk {
+  int e0, before, lo, hi, upto;  // lane l: rows of expert e0 + l, and the tiles up to its last
+  int at, end, step;
+
+  MOE_DEV void chunk(const GroupedParams& p, int first) {
+    e0 = first;
+    const int e = e0 + lane_id();
+    lo = hi = 0;
+    if (e < p.E) lo = row_at(p, e), hi = max(lo, row_at(p, e + 1));
+    upto = before + wave_scan((hi - lo + BQ - 1) / BQ * p.p_tiles);
+  }
+  MOE_DEV void begin(const GroupedParams& p) {
+    const int xcd = blockIdx.x & 7, in = blockIdx.x >> 3;
+    step = gridDim.x >> 3;
+    before = 0;
+    if constexpr (WGRAD) {
+      at = in;
+      if (p.q_tiles * p.p_tiles < 64) at = blockIdx.x, step = gridDim.x;
+    } else {
+      for (int e = 0;;) {
+        chunk(p, e);
+        e += 64;
+        if (e >= p.E) break;
+        before = __builtin_amdgcn_readlane(upto, 63);
       }
-      before = __shfl(upto, 63);
+      const int G = __builtin_amdgcn_readlane(upto, 63), q = G >> 3, r = G & 7;
+      at = xcd * q + min(xcd, r);
+      end = at + q + (xcd < r ? 1 : 0);
+      at += in;
+      before = 0;
+      if (p.E > 64) chunk(p, 0);
     }
   }
-  t->expert = __builtin_amdgcn_readfirstlane(t->expert);
-  t->lo = __builtin_amdgcn_readfirstlane(t->lo);
-  t->hi = __builtin_amdgcn_readfirstlane(t->hi);
-  within = __builtin_amdgcn_readfirstlane(within);
-  const int qt = WGRAD ? p.q_tiles : (t->hi - t->lo + BQ - 1) / BQ;
-  const int group = within / (GQ * p.p_tiles), q0 = group * GQ, size = min(GQ, qt - q0);
-  const int in = within - group * GQ * p.p_tiles;
-  t->p = in / size;
-  t->q = q0 + in - t->p * size;
-  return true;
-}
+  MOE_DEV TileAt next(const GroupedParams& p) {
+    TileAt t{};
+    int within, q_tiles = p.q_tiles;
+    if constexpr (WGRAD) {
+      const int n = q_tiles * p.p_tiles, xcd = blockIdx.x & 7;
+      const int first = n < 64 ? 0 : (int)((long long)n * xcd >> 3), each = n < 64 ? n : (int)((long long)n * (xcd + 1) >> 3) - first;
+      t.expert = at / each;
+      t.ok = t.expert < p.E;
+      if (!t.ok) return t;
+      within = first + at - t.expert * each;
+      t.lo = row_at(p, t.expert);
+      t.hi = max(t.lo, row_at(p, t.expert + 1));
+    } else {
+      t.ok = at < end;
+      if (!t.ok) return t;
+      while (at >= __builtin_amdgcn_readlane(upto, 63)) before = __builtin_amdgcn_readlane(upto, 63), chunk(p, e0 + 64);
+      const int l = __ffsll((unsigned long long)__ballot(upto > at)) - 1;
+      t.expert = e0 + l;
+      t.lo = __builtin_amdgcn_readlane(lo, l);
+      t.hi = __builtin_amdgcn_readlane(hi, l);
+      q_tiles = (t.hi - t.lo + BQ - 1) / BQ;
+      within = at - (__builtin_amdgcn_readlane(upto, l) - q_tiles * p.p_tiles);
+    }
+    at += step;
+    const int group = within / (GQ * p.p_tiles), q0 = group * GQ, size = min(GQ, q_tiles - q0);
+    const int in = within - group * GQ * p.p_tiles;
+    t.p = in / size;
+    t.q = q0 + in - t.p * size;
+    t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+    t.lo = __builtin_amdgcn_readfirstlane(t.lo);
+    t.hi = __builtin_amdgcn_readfirstlane(t.hi);
+    t.p = __builtin_amdgcn_readfirstlane(t.p);
+    t.q = __builtin_amdgcn_readfirstlane(t.q);
+    return t;
+  }
+};
 
 // Where 16-byte chunk c of row r lies among its row's eight (rows of 128 bytes): a 32-row operand's lanes r and r + 16
 // are read together, so both row bits take part.
@@ -149,344 +195,444 @@ MOE_DEV int swz(int r) { return (r & 7) ^ ((r >> 4) & 1); }
 
 // Transposed operands: the 32-byte unit u of summed row r lies at u ^ trx(r), so that the 4 rows x 2 units that 32 lanes
 // read lie in different banks.
-template <int B>
-MOE_DEV int trx(int r) {
-  return B >= 256 ? (2 * (r & 3)) | (r & 8) : 2 * (r & 3);
-}
+MOE_DEV int trx(int r) { return 2 * (r & 3); }
 
 // ---------------------------------------------------------------- tiles
-// BP x BQ outputs per workgroup, WP x WQ waves, each TP x TQ MFMA tiles of 32 x 32.
-template <Op O, int BP, int BQ, int WP, int WQ>
+// BP x BQ outputs, WP x WQ waves, each TP x TQ MFMA tiles of 32 x 32.  A K-step (128 bytes of an operand's row) is staged in
+// parts of 16 KB -- 128 rows, or columns, of P or Q -- in a ring of SLOTS of them.
+template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS>
 struct GTile {
   static constexpr int kWaves = WP * WQ, kThreads = 64 * kWaves;
   static constexpr int TP = BP / 32 / WP, TQ = BQ / 32 / WQ;
   static constexpr bool kTP = O == Op::GRAD || O == Op::WGRAD, kTQ = O == Op::WGRAD;
-  static constexpr int kPBytes = BP * 128, kQBytes = BQ * 128, kStage = kPBytes + kQBytes;
+  static constexpr int kPart = 16384, kPP = BP / 128, kPQ = BQ / 128, kParts = kPP + kPQ, kHalf = kParts / 2;
+  static constexpr int kL = 16 / kWaves;  // a wave's loads of a part
   static constexpr int kSf = O == Op::MX ? (BP + BQ) * 8 : 0;  // a K-step's scales: 8 bytes a row
-  static constexpr int kLp = kPBytes / (16 * kThreads), kLq = kQBytes / (16 * kThreads);  // loads per lane and stage
-  static constexpr int kStages = 2 * kStage + 2 * kSf;
-  // the output on its way to memory: rows of BP fp32 or bf16, as many at once as fit
-  static constexpr int kLds = kStages;
+  static constexpr int kLds = SLOTS * kPart + 2 * kSf;
   static constexpr int kBK = O == Op::MX ? 256 : 64;  // elements of a K-step
+  static constexpr int kAhead = SLOTS - 2 * kParts;   // parts in flight past the next K-step's
+  static_assert(BP % 128 == 0 && BQ % 128 == 0 && 128 % (TP * 32) == 0 && 128 % (TQ * 32) == 0, "a wave reads one part");
+  static_assert(16 % kWaves == 0 && kPP == kPQ && kAhead > 0 && kAhead <= kHalf, "ring");
+  static_assert(O == Op::MX || kAhead == kHalf, "P and Q change tiles together");
 };
 
-template <Op O, int BP, int BQ, int WP, int WQ, bool F32, int GQ>
+// WHERE: bit 0: P's rows, bit 1: Q's rows are found through src_info (WGRAD; elsewhere Q's are looked up once a tile).
+// Registers: one workgroup a CU for the large tile.
+template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS, bool F32, int WHERE>
 __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams p) {
-  using TL = GTile<O, BP, BQ, WP, WQ>;
+  using TL = GTile<O, BP, BQ, WP, WQ, SLOTS>;
   constexpr bool MX = O == Op::MX, WG = O == Op::WGRAD, kTP = TL::kTP, kTQ = TL::kTQ;
-  constexpr int TP = TL::TP, TQ = TL::TQ, BK = TL::kBK, kThreads = TL::kThreads;
+  constexpr int TP = TL::TP, TQ = TL::TQ, BK = TL::kBK, kThreads = TL::kThreads, PT = TL::kParts, HALF = TL::kHalf;
+  constexpr int L = TL::kL;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TL::kLds];
-  TileAt t;
-  if (!find_tile<WG, BQ, GQ>(p, &t)) return;
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wp = wave % WP, wq = wave / WP, h = lane >> 5, r32 = lane & 31;
-  const int p0 = t.p * BP;
-  const int rows = t.hi - t.lo;
-  const int q0 = t.q * BQ;                        // of the expert's rows (WGRAD: of dout's columns)
-  const int q_last = (WG ? p.q_cols : rows) - 1;  // the last row (column) of the output there is
-  const int K = WG ? rows : p.K, steps = (K + BK - 1) / BK;
-  const uint8_t* P = p.P + (long long)t.expert * p.p_expert;
+  Walk<WG, BQ, 8> walk;
+  walk.begin(p);
+  TileAt now = walk.next(p);  // the tile of the MFMAs; the loads run up to two K-steps ahead, into `then`
+  if (!now.ok) return;
+  auto steps_of = [&](const TileAt& t) { return max(2, ((WG ? t.hi - t.lo : p.K) + BK - 1) / BK); };
 
   // ---------------------------------------------------------------- what each lane loads
-  const uint8_t* pp[TL::kLp];
-  const uint8_t* qq[TL::kLq];
-  int p_chunk = 0, q_chunk = 0;  // 16-byte chunk of the row
-  constexpr int kPC = BP / 8, kQC = BQ / 8;  // T operands: chunks per summed row
-  if constexpr (!kTP) {
-    p_chunk = (lane & 7) ^ swz((wave * 8 + (lane >> 3)));
-#pragma unroll
-    for (int i = 0; i < TL::kLp; ++i) {
-      const int r = min(p0 + (i * TL::kWaves + wave) * 8 + (lane >> 3), p.p_cols - 1);
-      pp[i] = P + r * p.p_ld + p_chunk * 16;
-    }
-  } else {
-    const int kr = wave * (64 / kPC) + lane / kPC, slot = lane % kPC;
-    p_chunk = (((slot >> 1) ^ trx<BP>(kr)) << 1) | (slot & 1);
-    p_chunk = min(p0 / 8 + p_chunk, p.p_cols / 8 - 1);
-#pragma unroll
-    for (int i = 0; i < TL::kLp; ++i)
-      pp[i] = P + (long long)(i * TL::kWaves * (64 / kPC) + kr) * p.p_ld + p_chunk * 16;
-  }
-  if constexpr (!kTQ) {
-    q_chunk = (lane & 7) ^ swz((wave * 8 + (lane >> 3)));
-#pragma unroll
-    for (int i = 0; i < TL::kLq; ++i) {
-      long long r = t.lo + min(q0 + (i * TL::kWaves + wave) * 8 + (lane >> 3), q_last);
-      if (p.q_place.gathered) r = p.q_place.of(0, p.src_info[r]);
-      qq[i] = p.Q + r * p.q_ld + q_chunk * 16;
-    }
-  } else {
-    const int kr = wave * (64 / kQC) + lane / kQC, slot = lane % kQC;
-    q_chunk = (((slot >> 1) ^ trx<BQ>(kr)) << 1) | (slot & 1);
-    q_chunk = min(q0 / 8 + q_chunk, p.q_cols / 8 - 1);
-  }
-  // WGRAD: src_info of the summed rows, one K-step ahead of their loads (read also where the rows are the plan's own: a
-  // test would split the loop into blocks)
-  int p_src[WG ? TL::kLp : 1], q_src[WG ? TL::kLq : 1];
-  const int p_kr = wave * (64 / kPC) + lane / kPC, q_kr = wave * (64 / kQC) + lane / kQC;
-  auto places = [&](int ks) {
+  // Load i of a part: rows (i * waves + wave) * 8 + lane / 8 of 128 bytes, or (T) summed rows (i * waves + wave) * 4 + lane
+  // / 16 of 256 bytes.  Bases are scalar and move by a K-step; offsets stay.  Summed rows past the last lie past the
+  // resource's end, chunks past K get an offset that does: both load zeros.
+  const int row8 = wave * 8 + (lane >> 3), row4 = wave * 4 + (lane >> 4);
+  const int chunk8 = (lane & 7) ^ swz(row8), chunk4 = ((((lane & 15) >> 1) ^ trx(row4)) << 1) | (lane & 1);
+  constexpr int kStep8 = TL::kWaves * 8, kStep4 = TL::kWaves * 4;
+  uint32_t voff[PT][L];  // (WGRAD through src_info: the column alone)
+  const uint8_t *p_base = nullptr, *q_base = nullptr;
+  int p_k = 0, q_k = 0;          // summed elements up to the next load's K-step
+  int load_lo = 0, load_hi = 0;  // WGRAD: the rows of the loads' tile
+  auto column = [&](int first, int cols) { return (uint32_t)min(first / 8 + chunk4, cols / 8 - 1) * 16; };
+  auto aim_p = [&](const TileAt& t) {
+    p_k = 0;
     if constexpr (WG) {
-#pragma unroll
-      for (int i = 0; i < TL::kLp; ++i)
-        p_src[i] = p.src_info[min(t.lo + ks * BK + i * TL::kWaves * (64 / kPC) + p_kr, t.hi - 1)];
-#pragma unroll
-      for (int i = 0; i < TL::kLq; ++i)
-        q_src[i] = p.src_info[min(t.lo + ks * BK + i * TL::kWaves * (64 / kQC) + q_kr, t.hi - 1)];
-    }
-  };
-  // MXFP4: thread -> a row's scales of a K-step, 8 bytes from an address that may be odd
-  typedef const __attribute__((address_space(1))) uint32_t* GlobalWord;
-  const uint8_t* sf_base = nullptr;
-  uint32_t sf_shift = 0;
-  uint32_t sf[3] = {0, 0, 0};
-  static_assert(!MX || BP + BQ == kThreads, "one thread per row of scales");
-  if constexpr (MX) {
-    const bool isp = tid < BP;
-    long long at;
-    if (isp) {
-      at = (long long)t.expert * p.p_sf_expert + (long long)min(p0 + tid, p.p_cols - 1) * p.sf_row;
+      load_lo = t.lo, load_hi = t.ok ? t.hi : t.lo;
+      p_base = p.P + ((WHERE & 1) ? 0 : (long long)t.lo * p.p_ld);
     } else {
-      long long r = t.lo + min(q0 + min(tid - BP, BQ - 1), q_last);
-      if (p.q_place.gathered) r = p.q_place.of(0, p.src_info[r]);
-      at = r * p.sf_row;
+      p_base = p.P + t.expert * p.p_expert + (kTP ? 0 : (long long)t.p * BP * p.p_ld);
     }
-    const uint8_t* s = (isp ? p.P_sf : p.Q_sf) + at;
-    sf_shift = (uint32_t)((uintptr_t)s & 3);
-    sf_base = s - sf_shift;
-  }
-  // the aligned words that hold a row's scales [8 ks, 8 ks + 8) (those past its end are not read)
-  auto load_sf = [&](int ks) {
-    if constexpr (MX) {
-      const int left = (int)sf_shift + p.sf_row - 8 * ks;  // bytes from the first word to the row's end
-      const GlobalWord w = (GlobalWord)(sf_base + 8 * ks), none = (GlobalWord)zero16;
+    p_base = scalar(p_base);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) sf[i] = *(4 * i < left ? w + i : none);
+    for (int j = 0; j < TL::kPP; ++j)
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        if constexpr (kTP)
+          voff[j][i] = column(t.p * BP + j * 128, p.p_cols) + ((WHERE & 1) ? 0 : (i * kStep4 + row4) * p.p_ld);
+        else
+          voff[j][i] = (uint32_t)min(j * 128 + i * kStep8 + row8, p.p_cols - 1 - t.p * BP) * p.p_ld + chunk8 * 16;
+      }
+  };
+  auto aim_q = [&](const TileAt& t) {
+    q_k = 0;
+    q_base = p.Q;
+    if constexpr (WG) {
+      if (!(WHERE & 2)) q_base += (long long)t.lo * p.q_ld;
+    } else if (!p.q_place.gathered) {
+      q_base += ((long long)t.lo + t.q * BQ) * p.q_ld;
+    }
+    q_base = scalar(q_base);
+#pragma unroll
+    for (int j = 0; j < TL::kPQ; ++j)
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        if constexpr (kTQ) {
+          voff[TL::kPP + j][i] = column(t.q * BQ + j * 128, p.q_cols) + ((WHERE & 2) ? 0 : (i * kStep4 + row4) * p.q_ld);
+        } else {
+          int r = max(min(j * 128 + i * kStep8 + row8, t.hi - t.lo - 1 - t.q * BQ), 0);
+          if (p.q_place.gathered && t.ok) r = p.q_place.of(p.src_info[t.lo + t.q * BQ + r]);
+          voff[TL::kPP + j][i] = (uint32_t)r * p.q_ld + chunk8 * 16;
+        }
+      }
+  };
+  // WGRAD: src_info of this lane's summed rows, by scalar loads (a vector load would have to wait for the loads into LDS
+  // behind it)
+  int src[L] = {};
+  auto sources = [&](int k0) {
+    if constexpr (WG && WHERE != 0) {
+      typedef const __attribute__((address_space(4))) int* Uniform;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        int v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[j] = ((Uniform)(uintptr_t)p.src_info)[max(min(load_lo + k0 + i * kStep4 + wave * 4 + j, load_hi - 1), 0)];
+        src[i] = lane < 32 ? (lane < 16 ? v[0] : v[1]) : lane < 48 ? v[2] : v[3];
+      }
     }
   };
-  auto store_sf = [&](int ks, int buf) {
-    if constexpr (MX) {
-      const int left = p.sf_row - 8 * ks;
-      uint32_t lo = __builtin_amdgcn_alignbyte(sf[1], sf[0], sf_shift), hi = __builtin_amdgcn_alignbyte(sf[2], sf[1], sf_shift);
-      // blocks past K: scale 2^-127 on codes of zero
-      const uint64_t keep = left >= 8 ? ~0ull : left <= 0 ? 0ull : (1ull << (8 * left)) - 1;
-      *(uint2*)(lds + 2 * TL::kStage + buf * TL::kSf + tid * 8) = uint2{lo & (uint32_t)keep, hi & (uint32_t)(keep >> 32)};
+  // load i of part J (P's first) of the K-step that its operand has come to, into a slot
+  bool p_live = true, q_live = true;  // there is a tile to load
+  auto issue = [&](int J, int i, int slot) {
+    const bool isP = J < TL::kPP, tr = isP ? kTP : kTQ, look = WG && (WHERE & (isP ? 1 : 2));
+    const int k0 = isP ? p_k : q_k, K = WG ? load_hi - load_lo : p.K;
+    uint32_t v = voff[J][i], extent = kAll;
+    if (look) {
+      v += (uint32_t)(isP ? p.p_place : p.q_place).of(src[i]) * (isP ? p.p_ld : p.q_ld);
+      v |= i * kStep4 + row4 < K - k0 ? 0u : kNone;
+    } else if (tr) {
+      extent = (uint32_t)max(min(K - k0, 64), 0) * (isP ? p.p_ld : p.q_ld);
+    } else {
+      v |= k0 + chunk8 * (MX ? 32 : 8) < K ? 0u : kNone;
     }
+    if (!(isP ? p_live : q_live)) extent = 0;
+    lds_copy16<kTP>(resource(isP ? p_base : q_base, extent), v, lds + slot * TL::kPart + (i * TL::kWaves + wave) * 1024);
+  };
+  // an operand's next K-step
+  auto advance_p = [&] {
+    p_k += BK;
+    if (!(WG && (WHERE & 1))) p_base += kTP ? 64 * (long long)p.p_ld : 128;
+  };
+  auto advance_q = [&] {
+    q_k += BK;
+    if (!(WG && (WHERE & 2))) q_base += kTQ ? 64 * (long long)p.q_ld : 128;
   };
 
-  auto issue = [&](int ks, int buf) {
-    uint8_t* lp = lds + buf * TL::kStage + wave * 1024;
-    uint8_t* lq = lp + TL::kPBytes;
-    if constexpr (WG) {
-#pragma unroll
-      for (int i = 0; i < TL::kLp; ++i) {
-        const int r = t.lo + ks * BK + i * TL::kWaves * (64 / kPC) + p_kr;
-        const uint8_t* g = p.P + (long long)p.p_place.of(r, p_src[i]) * p.p_ld + p_chunk * 16;
-        lds_copy16(r < t.hi ? g : (const uint8_t*)zero16, lp + i * TL::kWaves * 1024);
+  // MXFP4: thread -> a row's scales of a K-step, 8 bytes from an address that may be odd
+  typedef const __attribute__((address_space(1))) uint32_t* GlobalWord;
+  static_assert(!MX || BP + BQ == kThreads, "a thread for each row of scales");
+  const uint8_t* sf_base = (const uint8_t*)zero16_words();
+  uint32_t sf_shift = 0, sf[3] = {};
+  int sf_left = 0, sf_k = 0;
+  auto aim_sf = [&](const TileAt& t) {
+    if constexpr (MX) {
+      long long at;
+      if (tid < BP) {
+        at = (long long)t.expert * p.p_sf_expert + (long long)min(t.p * BP + tid, p.p_cols - 1) * p.sf_row;
+      } else {
+        int r = max(min(t.lo + t.q * BQ + tid - BP, t.hi - 1), t.lo);
+        if (p.q_place.gathered && t.ok) r = p.q_place.of(p.src_info[r]);
+        at = (long long)r * p.sf_row;
       }
-#pragma unroll
-      for (int i = 0; i < TL::kLq; ++i) {
-        const int r = t.lo + ks * BK + i * TL::kWaves * (64 / kQC) + q_kr;
-        const uint8_t* g = p.Q + (long long)p.q_place.of(r, q_src[i]) * p.q_ld + q_chunk * 16;
-        lds_copy16(r < t.hi ? g : (const uint8_t*)zero16, lq + i * TL::kWaves * 1024);
-      }
-      return;
+      const uint8_t* s = (tid < BP ? p.P_sf : p.Q_sf) + at;
+      sf_shift = (uint32_t)((uintptr_t)s & 3);
+      sf_base = s - sf_shift;
+      sf_left = t.ok ? p.sf_row : 0;
     }
-    constexpr int kPer = MX ? 32 : 8;  // elements of a chunk
+  };
+  // the aligned words that hold a row's next 8 scales (those past its end are not read)
+  auto load_sf = [&] {
+    if constexpr (MX) {
+      const int left = sf_left > 0 ? (int)sf_shift + sf_left : 0;  // bytes from the first word to the row's end
+      const GlobalWord w = (GlobalWord)sf_base, none = (GlobalWord)zero16_words();
 #pragma unroll
-    for (int i = 0; i < TL::kLp; ++i) {
-      const int at = kTP ? ks * BK + i * TL::kWaves * (64 / kPC) + p_kr : ks * BK + p_chunk * kPer;
-      lds_copy16(at < K ? pp[i] : (const uint8_t*)zero16, lp + i * TL::kWaves * 1024);
-      pp[i] += kTP ? 64 * p.p_ld : 128;
+      for (int i = 0; i < 3; ++i) sf[i] = *(4 * i < left ? w + i : none);
+      sf_k = sf_left;
+      sf_base += 8;
+      sf_left -= 8;
     }
-#pragma unroll
-    for (int i = 0; i < TL::kLq; ++i) {
-      lds_copy16(ks * BK + q_chunk * kPer < K ? qq[i] : (const uint8_t*)zero16, lq + i * TL::kWaves * 1024);
-      qq[i] += 128;
+  };
+  auto store_sf = [&](int buf) {
+    if constexpr (MX) {
+      // blocks past K: scale 2^-127 on codes of zero
+      const uint64_t keep = sf_k >= 8 ? ~0ull : sf_k <= 0 ? 0ull : (1ull << (8 * sf_k)) - 1;
+      const uint32_t lo = __builtin_amdgcn_alignbyte(sf[1], sf[0], sf_shift),
+                     hi = __builtin_amdgcn_alignbyte(sf[2], sf[1], sf_shift);
+      lds_store8(lds + SLOTS * TL::kPart + buf * TL::kSf + tid * 8, ((uint64_t)hi << 32 | lo) & keep);
     }
   };
 
   // ---------------------------------------------------------------- fragments
+  auto wrap = [](int slot) { return slot >= SLOTS ? slot - SLOTS : slot; };
   i32x4 fp[2][TP], fq[2][TQ];
-  uint32_t sp[TP], sq[TQ];
-  auto frag = [&](const uint8_t* base, bool tr, int ld, int tile, int s) -> i32x4 {
+  uint32_t sp[TP] = {}, sq[TQ] = {}, sp_next[TP] = {}, sq_next[TQ] = {};
+  // tile: of 32 rows (columns) within the part at base
+  auto frag = [&](const uint8_t* base, bool tr, int tile, int s) -> i32x4 {
     if (!tr) {
       const int c = (MX ? 4 * h + s : 2 * s + h) ^ swz(r32);
       return *(const i32x4*)(base + (tile * 32 + r32) * 128 + c * 16);
     }
     const int row = 16 * s + 8 * h + ((lane & 15) >> 2), u = tile * 2 + ((lane >> 4) & 1);
-    const uint8_t* a = base + row * ld + ((u ^ (ld >= 512 ? trx<256>(row) : trx<128>(row))) << 5) + (lane & 3) * 8;
+    const uint8_t* a = base + row * 256 + ((u ^ trx(row)) << 5) + (lane & 3) * 8;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4*)a);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4*)(a + 4 * ld));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4*)(a + 4 * 256));
     return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  auto read = [&](int buf, int s, int set) {
-    const uint8_t* b = lds + buf * TL::kStage;
-#pragma unroll
-    for (int i = 0; i < TP; ++i) fp[set][i] = frag(b, kTP, BP * 2, wp * TP + i, s);
-#pragma unroll
-    for (int i = 0; i < TQ; ++i) fq[set][i] = frag(b + TL::kPBytes, kTQ, BQ * 2, wq * TQ + i, s);
+  constexpr int kPw = 128 / (TP * 32), kQw = 128 / (TQ * 32);  // waves that share a part
+  // fragment f (P's first) of a sub-step
+  auto read = [&](int f, int slot, int s, int set) {
+    if (f < TP)
+      fp[set][f] = frag(lds + wrap(slot + wp / kPw) * TL::kPart, kTP, wp % kPw * TP + f, s);
+    else
+      fq[set][f - TP] = frag(lds + wrap(slot + TL::kPP + wq / kQw) * TL::kPart, kTQ, wq % kQw * TQ + f - TP, s);
   };
   // a K-step's scales: byte s of a lane's word belongs to sub-step s
   auto read_sf = [&](int buf) {
     if constexpr (MX) {
-      const uint32_t* f = (const uint32_t*)(lds + 2 * TL::kStage + buf * TL::kSf);
+      const uint32_t* f = (const uint32_t*)(lds + SLOTS * TL::kPart + buf * TL::kSf);
 #pragma unroll
-      for (int i = 0; i < TP; ++i) sp[i] = f[((wp * TP + i) * 32 + r32) * 2 + h];
+      for (int i = 0; i < TP; ++i) sp_next[i] = f[((wp * TP + i) * 32 + r32) * 2 + h];
 #pragma unroll
-      for (int i = 0; i < TQ; ++i) sq[i] = f[(BP + (wq * TQ + i) * 32 + r32) * 2 + h];
+      for (int i = 0; i < TQ; ++i) sq_next[i] = f[(BP + (wq * TQ + i) * 32 + r32) * 2 + h];
+    }
+  };
+  auto take_sf = [&] {
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < TP; ++i) sp[i] = sp_next[i];
+#pragma unroll
+      for (int i = 0; i < TQ; ++i) sq[i] = sq_next[i];
     }
   };
   f32x16 acc[TP][TQ];
+  auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < TP; ++i)
+    for (int i = 0; i < TP; ++i)
 #pragma unroll
-    for (int j = 0; j < TQ; ++j)
+      for (int j = 0; j < TQ; ++j)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  auto mma = [&](auto sub, int set) {
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+  };
+  clear();
+  auto mma = [&](auto sub, int i, int j, int set) {
     constexpr int S = decltype(sub)::value;
+    if constexpr (MX) {
+      const i32x4 a = fp[set][i], b = fq[set][j];
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0}, i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, acc[i][j], 4, 4, S,
+          (int)sp[i], S, (int)sq[j]);
+    } else {
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fp[set][i]),
+                                                          __builtin_bit_cast(bf16x8, fq[set][j]), acc[i][j], 0, 0, 0);
+    }
+  };
+
+  // ---------------------------------------------------------------- output
+  // From the registers, 16 bytes a lane, as stores that do not wait: the loads of the next tile are under way.  A lane holds
+  // columns 8 v + 4 h .. + 4 of row r32; bf16 lanes h = 0, 1 swap so that each has 8 in a row.  Every store is issued,
+  // those out of the output with an offset that is dropped: the waits count them.
+  constexpr int kStores = TP * TQ * (F32 ? 4 : 2);
+  auto store = [&](const TileAt& t) {
+    const int q0 = t.q * BQ + wq * TQ * 32, p0 = t.p * BP + wp * TP * 32;
+    const int q_end = WG ? p.q_cols : t.hi - t.lo;
+    constexpr int kEl = F32 ? 4 : 2;
+    const uint8_t* base = p.out;
+    if (WG)
+      base += t.expert * p.out_expert + (long long)q0 * p.out_ld;
+    else if (!p.out_pair)
+      base += ((long long)t.lo + q0) * p.out_ld;
+    const __amdgpu_buffer_rsrc_t to = make_rsrc(base, kAll);
 #pragma unroll
-    for (int j = 0; j < TQ; ++j)
+    for (int j = 0; j < TQ; ++j) {
+      const int row = j * 32 + r32;
+      bool ok = q0 + row < q_end;
+      uint32_t at = (uint32_t)row * p.out_ld;
+      if (!WG && p.out_pair) {
+        const int r = p.src_info[max(min(t.lo + q0 + row, t.hi - 1), 0)];
+        ok = ok && (uint32_t)r < (uint32_t)p.npairs;
+        at = (uint32_t)r * p.out_ld;
+      }
 #pragma unroll
       for (int i = 0; i < TP; ++i) {
-        if constexpr (MX) {
-          const i32x4 a = fp[set][i], b = fq[set][j];
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0}, i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, acc[i][j], 4, 4, S,
-              (int)sp[i], S, (int)sq[j]);
-        } else {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fp[set][i]),
-                                                              __builtin_bit_cast(bf16x8, fq[set][j]), acc[i][j], 0, 0, 0);
+        const f32x16& c = acc[i][j];
+#pragma unroll
+        for (int v = 0; v < 4; v += F32 ? 1 : 2) {
+          i32x4 d;
+          int col = p0 + i * 32 + 8 * v;
+          if constexpr (F32) {
+            d = i32x4{__float_as_int(c[4 * v]), __float_as_int(c[4 * v + 1]), __float_as_int(c[4 * v + 2]), __float_as_int(c[4 * v + 3])};
+            col += 4 * h;
+          } else {
+            const auto x = __builtin_amdgcn_permlane32_swap(bf16x2_rne(c[4 * v], c[4 * v + 1]), bf16x2_rne(c[4 * v + 4], c[4 * v + 5]), false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(bf16x2_rne(c[4 * v + 2], c[4 * v + 3]), bf16x2_rne(c[4 * v + 6], c[4 * v + 7]), false, false);
+            d = i32x4{(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
+            col += 8 * h;
+          }
+          const uint32_t o = (at + (uint32_t)col * kEl) | (ok && col < p.p_cols ? 0u : kNone);
+          if constexpr (WG && F32) {
+            if (p.accumulate) {
+              const f32x4 sum = __builtin_bit_cast(f32x4, d) + __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(to, o, 0, 0));
+              d = __builtin_bit_cast(i32x4, sum);
+            }
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, d), to, o, 0, 0);
         }
       }
+    }
   };
 
   // ---------------------------------------------------------------- K loop
-  // a sub-step's reads go out between its MFMAs
-  auto order = [] {
-    constexpr int kReads = TP * (kTP ? 2 : 1) + TQ * (kTQ ? 2 : 1), kMma = TP * TQ, kEach = (kReads + kMma - 1) / kMma;
+  // A sub-step: its MFMAs, and between them the reads of the next one's fragments and the loads of HALF parts from
+  // `part` on (0: none).  (A wave that issues many loads at once waits for the address unit, 16 cycles each and shared by the
+  // waves, and feeds no MFMAs meanwhile.)
+  auto sub_step = [&](auto sub, auto first, int slot, int next_slot, int next_sub) {
+    constexpr int S = decltype(sub)::value, A = decltype(first)::value, kMma = TP * TQ;
+    constexpr int kLoads = A ? HALF * L : 0, kEvery = A ? kMma / kLoads : 1;
+    static_assert(TP + TQ <= kMma && kLoads <= kMma, "room between the MFMAs");
 #pragma unroll
-    for (int i = 0; i < kMma; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
+    for (int m = 0; m < kMma; ++m) {
+      mma(sub, m % TP, m / TP, S & 1);
+      if (m < TP + TQ) read(m, next_slot, next_sub, (S + 1) & 1);
+      if (A && m % kEvery == kEvery - 1 && m / kEvery < kLoads) {
+        const int n = m / kEvery, part = A + n / L;
+        issue(part % PT, n % L, wrap(slot + part % SLOTS));
+        // (the operand's last part of the K-step)
+        if (n % L == L - 1 && part % PT == TL::kPP - 1) advance_p();
+        if (n % L == L - 1 && part % PT == PT - 1) advance_q();
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
   };
-  // Two stages.  Fragments are read one sub-step ahead of their MFMAs.  Before the last sub-step's MFMAs a wave waits for
-  // its loads of the next stage and its reads of this one; past the barrier the next stage is whole and this one free.
-  // Stages past the last are loads of zeros that nothing reads: the loop stays one block, which the scheduler keeps as it
-  // is written.
-  if (steps > 0) {
-    places(0);
-    issue(0, 0);
-    load_sf(0);
-    places(1);
-    store_sf(0, 0);
-    __builtin_amdgcn_s_waitcnt(0);
+  // The parts of the ring go out in order, HALF of them in a trip's first sub-step, HALF in its last, each into the slot of the
+  // part SLOTS ahead of it.  Fragments are read one sub-step ahead of their MFMAs.  Before the last sub-step's MFMAs a wave
+  // waits for its loads of the next K-step and its reads of this one; past the barrier the next K-step is whole and this
+  // one's slots are free.  A workgroup goes through its tiles without draining the ring: the loads change to the next tile two
+  // K-steps ahead of the MFMAs (every tile has at least two K-steps, of zeros past its last), past the last tile they are of
+  // zeros.  The loop's body stays one block, which the scheduler keeps as it is written.
+  using I0 = std::integral_constant<int, 0>;
+  int steps = steps_of(now), ks = 0, slot = 0, buf = 0;
+  aim_p(now);
+  aim_q(now);
+  aim_sf(now);
+  load_sf();
+#pragma unroll
+  for (int n = 0; n < SLOTS - HALF; ++n) {
+    if (n % PT == 0) sources(n / PT * BK);
+#pragma unroll
+    for (int i = 0; i < L; ++i) issue(n % PT, i, n);
+    if (n % PT == TL::kPP - 1) advance_p();
+    if (n % PT == PT - 1) advance_q();
+  }
+  store_sf(0);
+  load_sf();
+  sources(2 * BK);
+  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int f = 0; f < TP + TQ; ++f) read(f, 0, 0, 0);
+  read_sf(0);
+  TileAt then{};
+  bool stored = false;
+  for (;;) {
+    const int next = wrap(slot + PT);
+    const bool change = ks == steps - 2;
+    if (change) {
+      then = walk.next(p);
+      p_live = then.ok;
+      aim_p(then);
+      if constexpr (TL::kAhead == HALF) q_live = then.ok, aim_q(then);
+      sources(0);
+    }
+    take_sf();
+    sub_step(I0{}, std::integral_constant<int, SLOTS - HALF>{}, slot, slot, 1);
+    sub_step(std::integral_constant<int, 1>{}, I0{}, slot, slot, 2);
+    sub_step(std::integral_constant<int, 2>{}, I0{}, slot, slot, 3);
+    // (keeps these MFMAs ahead of the branches below)
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) asm volatile("" : "+v"(acc[i][j]));
+    if constexpr (MX) {
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(HALF * L) | 15 << 8);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    store_sf(buf ^ 1);
+    // (the stores of a tile that has just ended lie ahead of this trip's loads and may stay under way)
+    if (stored)
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L + (MX ? 0 : kStores)));
+    else
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L));
     __builtin_amdgcn_s_barrier();
-    issue(1, 1);
-    load_sf(1);
-    places(2);
-    read(0, 0, 0);
-    read_sf(0);
-    for (int ks = 0; ks < steps; ++ks) {
-      const int buf = ks & 1;
-      read(buf, 1, 1);
-      mma(std::integral_constant<int, 0>{}, 0);
-      order();
-      read(buf, 2, 0);
-      mma(std::integral_constant<int, 1>{}, 1);
-      order();
-      read(buf, 3, 1);
-      mma(std::integral_constant<int, 2>{}, 0);
-      order();
-      store_sf(ks + 1, buf ^ 1);
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      issue(ks + 2, buf);
-      load_sf(ks + 2);
-      places(ks + 3);
-      read(buf ^ 1, 0, 0);
-      mma(std::integral_constant<int, 3>{}, 1);
-      __builtin_amdgcn_sched_barrier(0);
-      read_sf(buf ^ 1);
+    __builtin_amdgcn_sched_barrier(0);
+    if (change) {
+      if constexpr (TL::kAhead != HALF) q_live = then.ok, aim_q(then);
+      aim_sf(then);
     }
-    __builtin_amdgcn_s_waitcnt(0);  // the loads of zeros have landed before the LDS is used again
-  }
-
-  // ---------------------------------------------------------------- output
-  // Through LDS, as whole rows: a lane holds columns 8 v + 4 h .. + 4 of 32-column tile i, row r32 of 32-row tile j.
-  constexpr int kEl = F32 ? 4 : 2, kLine = BP * kEl + 16;  // (padded: rows start in different banks)
-  constexpr int kAtOnce = TL::kLds / kLine / 32 * 32 >= BQ ? BQ : TL::kLds / kLine / 32 * 32;
-  static_assert(kAtOnce >= 32, "room for a slice of rows");
-  for (int b = 0; b < BQ; b += kAtOnce) {
-    if (q0 + b > q_last) break;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < TQ; ++j) {
-      const int row0 = (wq * TQ + j) * 32 - b;
-      if (row0 < 0 || row0 >= kAtOnce) continue;
-#pragma unroll
-      for (int i = 0; i < TP; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint8_t* at = lds + (row0 + r32) * kLine + ((wp * TP + i) * 32 + 8 * v + 4 * h) * kEl;
-          const f32x16& c = acc[i][j];
-          if constexpr (F32)
-            *(f32x4*)at = f32x4{c[4 * v], c[4 * v + 1], c[4 * v + 2], c[4 * v + 3]};
-          else
-            *(uint2*)at = uint2{bf16x2_rne(c[4 * v], c[4 * v + 1]), bf16x2_rne(c[4 * v + 2], c[4 * v + 3])};
-        }
-    }
-    __syncthreads();
-    constexpr int kLineChunks = BP * kEl / 16, kCols = 16 / kEl;
-    for (int c = tid; c < kAtOnce * kLineChunks; c += kThreads) {
-      const int row = c / kLineChunks, col = p0 + c % kLineChunks * kCols, q = q0 + b + row;
-      if (q > q_last || b + row >= BQ || col >= p.p_cols) continue;
-      i32x4 v = *(const i32x4*)(lds + row * kLine + c % kLineChunks * 16);
-      long long to;
-      if (WG) {
-        to = (long long)t.expert * p.out_expert + (long long)q * p.out_ld;
-      } else {
-        int r = t.lo + q;
-        if (p.out_pair) {
-          r = p.src_info[r];
-          if ((unsigned)r >= (unsigned)p.npairs) continue;
-        }
-        to = (long long)r * p.out_ld;
-      }
-      uint8_t* o = (uint8_t*)p.out + (to + col) * kEl;
-      if constexpr (WG && F32) {
-        if (p.accumulate) {
-          const f32x4 sum = __builtin_bit_cast(f32x4, v) + *(const f32x4*)o;
-          v = __builtin_bit_cast(i32x4, sum);
-        }
-      }
-      *(i32x4*)o = v;
+    load_sf();
+    read_sf(buf ^ 1);
+    sub_step(std::integral_constant<int, 3>{}, std::integral_constant<int, SLOTS>{}, slot, next, 0);
+    sources(p_k);
+    slot = next;
+    buf ^= 1;
+    stored = ++ks == steps;
+    if (stored) {
+      store(now);
+      if (!then.ok) break;
+      now = then;
+      steps = steps_of(now);
+      ks = 0;
+      clear();
     }
   }
+  __builtin_amdgcn_s_waitcnt(0);  // the loads of zeros land before the workgroup's LDS is another's
 }
 
-template <Op O, int BP, int BQ, int WP, int WQ, bool F32>
+// Compute units of the current device (cached per device).
+int device_cus() {
+  static int cus[64] = {};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
+  if (cus[dev] == 0) {
+    int n = 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+    cus[dev] = n;
+  }
+  return cus[dev];
+}
+
+template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS, bool F32, int WHERE = 0>
 hipError_t launch_tile(GroupedParams& p, hipStream_t s) {
   p.p_tiles = (p.p_cols + BP - 1) / BP;
-  long long grid;
+  long long tiles;
   if (O == Op::WGRAD) {
     p.q_tiles = (p.q_cols + BQ - 1) / BQ;
-    grid = (long long)p.E * p.q_tiles * p.p_tiles;
+    tiles = (long long)p.E * p.q_tiles * p.p_tiles;
   } else {
     const long long groups = std::min(p.npairs, p.E);
-    grid = (p.npairs + groups * (BQ - 1)) / BQ * p.p_tiles;
+    tiles = (p.npairs + groups * (BQ - 1)) / BQ * p.p_tiles;
   }
-  if (grid <= 0) return hipSuccess;
-  grouped_kernel<O, BP, BQ, WP, WQ, F32, 8><<<dim3((unsigned)grid), dim3(64 * WP * WQ), 0, s>>>(p);
+  if (tiles <= 0) return hipSuccess;
+  // one workgroup a CU walks its tiles; a multiple of the 8 XCDs
+  const int per_cu = 163840 / GTile<O, BP, BQ, WP, WQ, SLOTS>::kLds, cus = std::max(8, device_cus() & ~7);
+  const unsigned grid = (unsigned)std::min<long long>((tiles + 7) & ~7LL, (long long)cus * per_cu);
+  grouped_kernel<O, BP, BQ, WP, WQ, SLOTS, F32, WHERE><<<dim3(grid), dim3(64 * WP * WQ), 0, s>>>(p);
   return hipGetLastError();
 }
 
 Place place(Rows r, int T, int topk) {
   const bool whole = r != Rows::TOKEN || topk == 1;
-  return Place{whole ? 0u : (uint32_t)(((1ull << 32) + topk - 1) / topk), whole ? -1 : 0, r == Rows::PLAN ? 0 : -1,
+  return Place{whole ? 0u : (uint32_t)(((1ull << 32) + topk - 1) / topk), whole ? -1 : 0, r != Rows::PLAN,
                r == Rows::TOKEN ? T : T * topk};
 }
 
@@ -501,15 +647,30 @@ GroupedParams common(const GroupedArgs& a) {
   p.K = a.k;
   p.p_cols = a.n;
   p.q_place = place(a.a_rows, a.T, a.topk);
-  p.out = a.out;
-  p.out_ld = a.n;
+  p.out = (uint8_t*)a.out;
+  p.out_ld = (uint32_t)a.n * (a.out_f32 ? 4 : 2);
   p.out_pair = a.out_rows == Rows::PAIR;
   return p;
 }
 
 template <Op O, bool F32>
 hipError_t launch_rows(GroupedParams& p, hipStream_t s) {
-  return launch_tile<O, 256, 256, 4, 2, F32>(p, s);
+  return launch_tile<O, 256, 256, 4, 2, O == Op::MX ? 9 : 10, F32>(p, s);
+}
+
+template <bool F32, int WHERE>
+hipError_t launch_wgrad(GroupedParams& p, hipStream_t s) {
+  return launch_tile<Op::WGRAD, 256, 256, 4, 2, 10, F32, WHERE>(p, s);
+}
+template <bool F32>
+hipError_t launch_wgrad(GroupedParams& p, hipStream_t s) {
+  // (no rows: src_info is not read)
+  switch (p.npairs == 0 ? 0 : (p.p_place.gathered ? 1 : 0) | (p.q_place.gathered ? 2 : 0)) {
+    case 0: return launch_wgrad<F32, 0>(p, s);
+    case 1: return launch_wgrad<F32, 1>(p, s);
+    case 2: return launch_wgrad<F32, 2>(p, s);
+    default: return launch_wgrad<F32, 3>(p, s);
+  }
 }
 
 // (the smallest tiles' extents)
@@ -527,8 +688,8 @@ bool grouped_wgrad_fits(int E, int n, int k) {
 hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s) {
   GroupedParams p = common(a);
   p.p_expert = (long long)a.n * a.k * 2;
-  p.p_ld = (a.w_kn ? a.n : a.k) * 2LL;
-  p.q_ld = a.k * 2LL;
+  p.p_ld = (uint32_t)(a.w_kn ? a.n : a.k) * 2;
+  p.q_ld = (uint32_t)a.k * 2;
   if (a.w_kn) return a.out_f32 ? launch_rows<Op::GRAD, true>(p, s) : launch_rows<Op::GRAD, false>(p, s);
   return a.out_f32 ? launch_rows<Op::FWD, true>(p, s) : launch_rows<Op::FWD, false>(p, s);
 }
@@ -536,7 +697,7 @@ hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s) {
 hipError_t launch_grouped_gemm_mxfp4(const GroupedArgs& a, hipStream_t s) {
   GroupedParams p = common(a);
   p.p_expert = (long long)a.n * (a.k / 2);
-  p.p_ld = p.q_ld = a.k / 2;
+  p.p_ld = p.q_ld = (uint32_t)a.k / 2;
   p.sf_row = a.k / 32;
   p.p_sf_expert = (long long)a.n * p.sf_row;
   p.P_sf = (const uint8_t*)a.w_sf;
@@ -552,18 +713,17 @@ hipError_t launch_grouped_wgrad(const WgradArgs& a, hipStream_t s) {
   p.npairs = a.T * a.topk;
   p.P = (const uint8_t*)a.a;
   p.Q = (const uint8_t*)a.dout;
-  p.p_ld = a.k * 2LL;
-  p.q_ld = a.n * 2LL;
+  p.p_ld = (uint32_t)a.k * 2;
+  p.q_ld = (uint32_t)a.n * 2;
   p.p_cols = a.k;
   p.q_cols = a.n;
   p.p_place = place(a.a_rows, a.T, a.topk);
   p.q_place = place(a.dout_rows, a.T, a.topk);
-  p.out = a.dw;
-  p.out_ld = a.k;
-  p.out_expert = (long long)a.n * a.k;
+  p.out = (uint8_t*)a.dw;
+  p.out_ld = (uint32_t)a.k * (a.dw_f32 ? 4 : 2);
+  p.out_expert = (long long)a.n * p.out_ld;
   p.accumulate = a.accumulate;
-  return a.dw_f32 ? launch_tile<Op::WGRAD, 256, 256, 4, 2, true>(p, s)
-                  : launch_tile<Op::WGRAD, 256, 256, 4, 2, false>(p, s);
+  return a.dw_f32 ? launch_wgrad<true>(p, s) : launch_wgrad<false>(p, s);
 }
 
 }  // namespace moe
