@@ -47,7 +47,8 @@ struct GroupedParams {
   const uint8_t* P_sf;   // MXFP4 scales
   const uint8_t* Q_sf;
   long long p_expert;    // bytes of one expert's weights
-  long long p_sf_expert;
+  long long p_sf_bytes, q_sf_bytes;
+  int n_rows;            // MXFP4: weight rows of an expert
   uint32_t p_ld, q_ld;   // bytes between rows as they lie in memory
   int p_cols, q_cols;    // extents of the output (q_cols: WGRAD only, else the expert's rows)
   int K;                 // summed length (WGRAD: the expert's rows)
@@ -61,21 +62,21 @@ struct GroupedParams {
   int p_tiles, q_tiles;  // q_tiles: WGRAD only
 };
 
-// Lane l's 16 bytes land at l + 16 l; a lane whose offset is out of the resource's bounds writes zeros.  HIDDEN: written so
-// that the compiler does not see a store to LDS -- it lets no ds_read_b64_tr pass one in flight; the kernel's own waits
-// order the two.
-constexpr uint32_t kNone = 0xFFFFFFFFu, kAll = 0xFFFFFFF0u;  // an offset, and an extent, for the two
-template <bool HIDDEN>
-MOE_DEV void lds_copy16(i32x4 rsrc, uint32_t voff, void* l) {
-  if constexpr (HIDDEN)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
-                     (uint32_t)(uintptr_t)(LDS3 void*)l),
-                 "v"(voff), "s"(rsrc)
-                 : "memory");
-  else
-    lds_load16(make_rsrc((const void*)((uint64_t)(uint32_t)rsrc[0] | (uint64_t)(uint32_t)rsrc[1] << 32), (uint32_t)rsrc[2]),
-               l, voff, 0);
+// Direct-to-LDS loads: lane l's 16 (12) bytes land at l + 16 l; what lies out of the resource's bounds is zeros.
+// Written so that the compiler does not see stores to LDS: it lets no ds_read_b64_tr pass one in flight.  The kernel's own
+// waits order the two.
+constexpr uint32_t kNone = 0xFFFFFFFFu, kAll = 0xFFFFFFF0u;  // an offset out of any resource, the largest resource
+MOE_DEV void lds_copy16(i32x4 rsrc, uint32_t voff, uint32_t l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(l), "v"(voff), "s"(rsrc)
+               : "memory");
 }
+MOE_DEV void lds_copy12(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx3 %1, %2, %3 offen lds" ::"s"(l), "v"(voff), "s"(rsrc),
+               "s"(soff)
+               : "memory");
+}
+MOE_DEV uint32_t lds_address(const void* l) { return (uint32_t)(uintptr_t)(const LDS3 void*)l; }
+
 // A value that is the same in every lane, in a scalar register.
 MOE_DEV int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 MOE_DEV const uint8_t* scalar(const uint8_t* v) {
@@ -85,15 +86,6 @@ MOE_DEV const uint8_t* scalar(const uint8_t* v) {
 MOE_DEV i32x4 resource(const void* base, uint32_t bytes) {
   const uint64_t b = (uint64_t)base;
   return i32x4{scalar((int)(uint32_t)b), scalar((int)(uint32_t)(b >> 32)), scalar((int)bytes), 0x00020000};
-}
-
-// A word of zeros, for masked lanes.
-__device__ __attribute__((aligned(16))) const uint32_t zero_words[4] = {0, 0, 0, 0};
-MOE_DEV const uint32_t* zero16_words() { return zero_words; }
-
-// (A plain store would wait for every load into LDS that is in flight.  The caller waits for this one.)
-MOE_DEV void lds_store8(void* l, uint64_t v) {
-  asm volatile("ds_write_b64 %0, %1" ::"v"((uint32_t)(uintptr_t)(LDS3 void*)l), "v"(v) : "memory");
 }
 
 MOE_DEV int wave_scan(int v) {  // inclusive
@@ -207,13 +199,15 @@ struct GTile {
   static constexpr bool kTP = O == Op::GRAD || O == Op::WGRAD, kTQ = O == Op::WGRAD;
   static constexpr int kPart = 16384, kPP = BP / 128, kPQ = BQ / 128, kParts = kPP + kPQ, kHalf = kParts / 2;
   static constexpr int kL = 16 / kWaves;  // a wave's loads of a part
-  static constexpr int kSf = O == Op::MX ? (BP + BQ) * 8 : 0;  // a K-step's scales: 8 bytes a row
+  static constexpr int kSf = O == Op::MX ? (BP + BQ) * 16 : 0;  // a K-step's scales: the words that hold a row's 8
   static constexpr int kLds = SLOTS * kPart + 2 * kSf;
   static constexpr int kBK = O == Op::MX ? 256 : 64;  // elements of a K-step
   static constexpr int kAhead = SLOTS - 2 * kParts;   // parts in flight past the next K-step's
   static_assert(BP % 128 == 0 && BQ % 128 == 0 && 128 % (TP * 32) == 0 && 128 % (TQ * 32) == 0, "a wave reads one part");
-  static_assert(16 % kWaves == 0 && kPP == kPQ && kAhead > 0 && kAhead <= kHalf, "ring");
-  static_assert(O == Op::MX || kAhead == kHalf, "P and Q change tiles together");
+  // parts that go out in a trip's sub-steps 0, 1 and 3
+  static constexpr int kOut1 = kHalf / 2 > 0 ? kHalf / 2 : 1, kOut0 = kAhead == kHalf ? 0 : kOut1;
+  static constexpr int kOut2 = kParts - kHalf - kOut0 - kOut1;
+  static_assert(16 % kWaves == 0 && kPP == kPQ && kAhead > 0 && kAhead <= kHalf && kOut2 >= 0, "ring");
 };
 
 // WHERE: bit 0: P's rows, bit 1: Q's rows are found through src_info (WGRAD; elsewhere Q's are looked up once a tile).
@@ -241,19 +235,23 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   const int chunk8 = (lane & 7) ^ swz(row8), chunk4 = ((((lane & 15) >> 1) ^ trx(row4)) << 1) | (lane & 1);
   constexpr int kStep8 = TL::kWaves * 8, kStep4 = TL::kWaves * 4;
   uint32_t voff[PT][L];  // (WGRAD through src_info: the column alone)
-  const uint8_t *p_base = nullptr, *q_base = nullptr;
-  int p_k = 0, q_k = 0;          // summed elements up to the next load's K-step
+  i32x4 p_from{}, q_from{};      // the operands' resources at the next load's K-step
+  int p_k = 0, q_k = 0;          // summed elements up to it
   int load_lo = 0, load_hi = 0;  // WGRAD: the rows of the loads' tile
+  auto extent = [&](bool isP) {  // T operands: the summed rows of a K-step that there are
+    return (uint32_t)max(min((WG ? load_hi - load_lo : p.K) - (isP ? p_k : q_k), 64), 0) * (isP ? p.p_ld : p.q_ld);
+  };
   auto column = [&](int first, int cols) { return (uint32_t)min(first / 8 + chunk4, cols / 8 - 1) * 16; };
   auto aim_p = [&](const TileAt& t) {
     p_k = 0;
+    const uint8_t* base = p.P;
     if constexpr (WG) {
       load_lo = t.lo, load_hi = t.ok ? t.hi : t.lo;
-      p_base = p.P + ((WHERE & 1) ? 0 : (long long)t.lo * p.p_ld);
+      base += (WHERE & 1) ? 0 : (long long)t.lo * p.p_ld;
     } else {
-      p_base = p.P + t.expert * p.p_expert + (kTP ? 0 : (long long)t.p * BP * p.p_ld);
+      base += t.expert * p.p_expert + (kTP ? 0 : (long long)t.p * BP * p.p_ld);
     }
-    p_base = scalar(p_base);
+    p_from = resource(base, !t.ok ? 0 : kTP && !(WHERE & 1) ? extent(true) : kAll);
 #pragma unroll
     for (int j = 0; j < TL::kPP; ++j)
 #pragma unroll
@@ -266,13 +264,13 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   };
   auto aim_q = [&](const TileAt& t) {
     q_k = 0;
-    q_base = p.Q;
+    const uint8_t* base = p.Q;
     if constexpr (WG) {
-      if (!(WHERE & 2)) q_base += (long long)t.lo * p.q_ld;
+      if (!(WHERE & 2)) base += (long long)t.lo * p.q_ld;
     } else if (!p.q_place.gathered) {
-      q_base += ((long long)t.lo + t.q * BQ) * p.q_ld;
+      base += ((long long)t.lo + t.q * BQ) * p.q_ld;
     }
-    q_base = scalar(q_base);
+    q_from = resource(base, !t.ok ? 0 : kTQ && !(WHERE & 2) ? extent(false) : kAll);
 #pragma unroll
     for (int j = 0; j < TL::kPQ; ++j)
 #pragma unroll
@@ -302,81 +300,73 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       }
     }
   };
-  // load i of part J (P's first) of the K-step that its operand has come to, into a slot
-  bool p_live = true, q_live = true;  // there is a tile to load
+  // load i of part J (P's first) of the K-step that its operand has come to, into a slot (its offset in LDS)
+  const uint32_t lds0 = lds_address(lds);
   auto issue = [&](int J, int i, int slot) {
-    const bool isP = J < TL::kPP, tr = isP ? kTP : kTQ, look = WG && (WHERE & (isP ? 1 : 2));
-    const int k0 = isP ? p_k : q_k, K = WG ? load_hi - load_lo : p.K;
-    uint32_t v = voff[J][i], extent = kAll;
-    if (look) {
+    const bool isP = J < TL::kPP, tr = isP ? kTP : kTQ;
+    const int k0 = isP ? p_k : q_k;
+    uint32_t v = voff[J][i];
+    if (WG && (WHERE & (isP ? 1 : 2))) {
       v += (uint32_t)(isP ? p.p_place : p.q_place).of(src[i]) * (isP ? p.p_ld : p.q_ld);
-      v |= i * kStep4 + row4 < K - k0 ? 0u : kNone;
-    } else if (tr) {
-      extent = (uint32_t)max(min(K - k0, 64), 0) * (isP ? p.p_ld : p.q_ld);
-    } else {
-      v |= k0 + chunk8 * (MX ? 32 : 8) < K ? 0u : kNone;
+      v = i * kStep4 + row4 < load_hi - load_lo - k0 ? v : kNone;
+    } else if (!tr) {
+      v = k0 + chunk8 * (MX ? 32 : 8) < p.K ? v : kNone;
     }
-    if (!(isP ? p_live : q_live)) extent = 0;
-    lds_copy16<kTP>(resource(isP ? p_base : q_base, extent), v, lds + slot * TL::kPart + (i * TL::kWaves + wave) * 1024);
+    lds_copy16(isP ? p_from : q_from, v, lds0 + slot + (i * TL::kWaves + wave) * 1024);
   };
   // an operand's next K-step
-  auto advance_p = [&] {
-    p_k += BK;
-    if (!(WG && (WHERE & 1))) p_base += kTP ? 64 * (long long)p.p_ld : 128;
-  };
-  auto advance_q = [&] {
-    q_k += BK;
-    if (!(WG && (WHERE & 2))) q_base += kTQ ? 64 * (long long)p.q_ld : 128;
+  auto advance = [&](i32x4& from, bool isP) {
+    const bool tr = isP ? kTP : kTQ, look = WG && (WHERE & (isP ? 1 : 2));
+    (isP ? p_k : q_k) += BK;
+    if (look) return;
+    const uint64_t base = ((uint64_t)(uint32_t)from[1] << 32 | (uint32_t)from[0]) + (tr ? 64 * (uint64_t)(isP ? p.p_ld : p.q_ld) : 128);
+    from = resource((const void*)base, tr ? extent(isP) : (uint32_t)from[2]);
   };
 
-  // MXFP4: thread -> a row's scales of a K-step, 8 bytes from an address that may be odd
-  typedef const __attribute__((address_space(1))) uint32_t* GlobalWord;
-  static_assert(!MX || BP + BQ == kThreads, "a thread for each row of scales");
-  const uint8_t* sf_base = (const uint8_t*)zero16_words();
-  uint32_t sf_shift = 0, sf[3] = {};
-  int sf_left = 0, sf_k = 0;
+  // MXFP4: the words that hold a row's 8 scales of a K-step, waves 0 .. BP / 64 - 1 P's rows, the others Q's.  A row's scales
+  // may start at any byte: the three words from the one that holds the first.
+  static_assert(!MX || (BP + BQ == kThreads && BP % 64 == 0), "a thread for each row of scales");
+  i32x4 sf_from{};
+  uint32_t sf_off = 0, sf_at = 0;
+  int sf_k = 0;                             // scales of a row up to the K-step that is read next
+  uint32_t p_shift[TP] = {}, q_shift[TQ] = {};  // where the fragments' rows start in their words, bytes
+  uint32_t p_shift_next[TP] = {}, q_shift_next[TQ] = {};
+  // the row of p or q (of the tile) whose scales row's are, in its tensor
+  auto sf_row_p = [&](const TileAt& t, int row) { return (long long)t.expert * p.n_rows + min(t.p * BP + row, p.p_cols - 1); };
+  auto sf_row_q = [&](const TileAt& t, int row) {
+    int r = max(min(t.lo + t.q * BQ + row, t.hi - 1), t.lo);
+    if (p.q_place.gathered && t.ok) r = p.q_place.of(p.src_info[r]);
+    return (long long)r;
+  };
   auto aim_sf = [&](const TileAt& t) {
     if constexpr (MX) {
-      long long at;
-      if (tid < BP) {
-        at = (long long)t.expert * p.p_sf_expert + (long long)min(t.p * BP + tid, p.p_cols - 1) * p.sf_row;
-      } else {
-        int r = max(min(t.lo + t.q * BQ + tid - BP, t.hi - 1), t.lo);
-        if (p.q_place.gathered && t.ok) r = p.q_place.of(p.src_info[r]);
-        at = (long long)r * p.sf_row;
-      }
-      const uint8_t* s = (tid < BP ? p.P_sf : p.Q_sf) + at;
-      sf_shift = (uint32_t)((uintptr_t)s & 3);
-      sf_base = s - sf_shift;
-      sf_left = t.ok ? p.sf_row : 0;
-    }
-  };
-  // the aligned words that hold a row's next 8 scales (those past its end are not read)
-  auto load_sf = [&] {
-    if constexpr (MX) {
-      const int left = sf_left > 0 ? (int)sf_shift + sf_left : 0;  // bytes from the first word to the row's end
-      const GlobalWord w = (GlobalWord)sf_base, none = (GlobalWord)zero16_words();
+      const bool isp = wave < BP / 64;
+      const uint8_t* all = isp ? p.P_sf : p.Q_sf;
+      // from the tile's first row on (gathered rows: from the tensor's first, which is below 4 GiB)
+      long long first = isp ? sf_row_p(t, 0) : p.q_place.gathered ? 0 : sf_row_q(t, 0);
+      const long long begin = first * p.sf_row & ~3LL, end = (isp ? p.p_sf_bytes : p.q_sf_bytes) + 3 & ~3LL;
+      const long long row = isp ? sf_row_p(t, tid) : sf_row_q(t, tid - BP);
+      sf_off = (uint32_t)((row * p.sf_row & ~3LL) - begin);
+      sf_from = resource(all + begin, t.ok ? (uint32_t)min(end - begin, (long long)kAll) : 0u);
+      sf_at = 0;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) sf[i] = *(4 * i < left ? w + i : none);
-      sf_k = sf_left;
-      sf_base += 8;
-      sf_left -= 8;
+      for (int i = 0; i < TP; ++i) p_shift_next[i] = (uint32_t)(sf_row_p(t, (wp * TP + i) * 32 + r32) * p.sf_row) & 3;
+#pragma unroll
+      for (int i = 0; i < TQ; ++i) q_shift_next[i] = (uint32_t)(sf_row_q(t, (wq * TQ + i) * 32 + r32) * p.sf_row) & 3;
     }
   };
-  auto store_sf = [&](int buf) {
+  auto load_sf = [&](int buf) {
     if constexpr (MX) {
-      // blocks past K: scale 2^-127 on codes of zero
-      const uint64_t keep = sf_k >= 8 ? ~0ull : sf_k <= 0 ? 0ull : (1ull << (8 * sf_k)) - 1;
-      const uint32_t lo = __builtin_amdgcn_alignbyte(sf[1], sf[0], sf_shift),
-                     hi = __builtin_amdgcn_alignbyte(sf[2], sf[1], sf_shift);
-      lds_store8(lds + SLOTS * TL::kPart + buf * TL::kSf + tid * 8, ((uint64_t)hi << 32 | lo) & keep);
+      lds_copy12(sf_from, sf_off, sf_at, lds0 + SLOTS * TL::kPart + buf * TL::kSf + wave * (64 * 16));
+      sf_at += 8;
     }
   };
 
   // ---------------------------------------------------------------- fragments
-  auto wrap = [](int slot) { return slot >= SLOTS ? slot - SLOTS : slot; };
+  constexpr int kRing = SLOTS * TL::kPart;
+  auto wrap = [](int at) { return at >= kRing ? at - kRing : at; };
   i32x4 fp[2][TP], fq[2][TQ];
-  uint32_t sp[TP] = {}, sq[TQ] = {}, sp_next[TP] = {}, sq_next[TQ] = {};
+  uint32_t sp[TP] = {}, sq[TQ] = {};
   // tile: of 32 rows (columns) within the part at base
   auto frag = [&](const uint8_t* base, bool tr, int tile, int s) -> i32x4 {
     if (!tr) {
@@ -390,30 +380,48 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   constexpr int kPw = 128 / (TP * 32), kQw = 128 / (TQ * 32);  // waves that share a part
-  // fragment f (P's first) of a sub-step
-  auto read = [&](int f, int slot, int s, int set) {
+  // fragment f (P's first) of a sub-step of the K-step whose parts this wave reads lie at bp and bq
+  auto read = [&](int f, int bp, int bq, int s, int set) {
     if (f < TP)
-      fp[set][f] = frag(lds + wrap(slot + wp / kPw) * TL::kPart, kTP, wp % kPw * TP + f, s);
+      fp[set][f] = frag(lds + bp, kTP, wp % kPw * TP + f, s);
     else
-      fq[set][f - TP] = frag(lds + wrap(slot + TL::kPP + wq / kQw) * TL::kPart, kTQ, wq % kQw * TQ + f - TP, s);
+      fq[set][f - TP] = frag(lds + bq, kTQ, wq % kQw * TQ + f - TP, s);
   };
-  // a K-step's scales: byte s of a lane's word belongs to sub-step s
+  // a K-step's scales, byte s of a lane's word for sub-step s (blocks past K: scale 2^-127, on codes of zero)
+  uint32_t sp_words[TP][2] = {}, sq_words[TQ][2] = {};
   auto read_sf = [&](int buf) {
     if constexpr (MX) {
       const uint32_t* f = (const uint32_t*)(lds + SLOTS * TL::kPart + buf * TL::kSf);
 #pragma unroll
-      for (int i = 0; i < TP; ++i) sp_next[i] = f[((wp * TP + i) * 32 + r32) * 2 + h];
+      for (int i = 0; i < TP; ++i) {
+        const uint32_t* w = f + ((wp * TP + i) * 32 + r32) * 4 + h;
+        sp_words[i][0] = w[0], sp_words[i][1] = w[1];
+      }
 #pragma unroll
-      for (int i = 0; i < TQ; ++i) sq_next[i] = f[(BP + (wq * TQ + i) * 32 + r32) * 2 + h];
+      for (int i = 0; i < TQ; ++i) {
+        const uint32_t* w = f + (BP + (wq * TQ + i) * 32 + r32) * 4 + h;
+        sq_words[i][0] = w[0], sq_words[i][1] = w[1];
+      }
     }
   };
   auto take_sf = [&] {
     if constexpr (MX) {
+      const int left = p.sf_row - sf_k;
+      const uint64_t keep = left >= 8 ? ~0ull : left <= 0 ? 0ull : (1ull << (8 * left)) - 1;
+      const uint32_t mine = h ? (uint32_t)(keep >> 32) : (uint32_t)keep;
 #pragma unroll
-      for (int i = 0; i < TP; ++i) sp[i] = sp_next[i];
+      for (int i = 0; i < TP; ++i) sp[i] = __builtin_amdgcn_alignbyte(sp_words[i][1], sp_words[i][0], p_shift[i]) & mine;
 #pragma unroll
-      for (int i = 0; i < TQ; ++i) sq[i] = sq_next[i];
+      for (int i = 0; i < TQ; ++i) sq[i] = __builtin_amdgcn_alignbyte(sq_words[i][1], sq_words[i][0], q_shift[i]) & mine;
+      sf_k += 8;
     }
+  };
+  auto take_shifts = [&] {
+    sf_k = 0;
+#pragma unroll
+    for (int i = 0; i < TP; ++i) p_shift[i] = p_shift_next[i];
+#pragma unroll
+    for (int i = 0; i < TQ; ++i) q_shift[i] = q_shift_next[i];
   };
   f32x16 acc[TP][TQ];
   auto clear = [&] {
@@ -493,95 +501,99 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   };
 
   // ---------------------------------------------------------------- K loop
-  // A sub-step: its MFMAs, and between them the reads of the next one's fragments and the loads of HALF parts from
-  // `part` on (0: none).  (A wave that issues many loads at once waits for the address unit, 16 cycles each and shared by the
-  // waves, and feeds no MFMAs meanwhile.)
-  auto sub_step = [&](auto sub, auto first, int slot, int next_slot, int next_sub) {
-    constexpr int S = decltype(sub)::value, A = decltype(first)::value, kMma = TP * TQ;
-    constexpr int kLoads = A ? HALF * L : 0, kEvery = A ? kMma / kLoads : 1;
+  // A sub-step: its MFMAs, and between them the reads of the next one's fragments and the loads of COUNT parts, those FIRST
+  // .. behind the trip's first.  (A wave that issues many loads at once waits for the address unit, 16 cycles each and
+  // shared by the waves, and feeds no MFMAs meanwhile.)
+  auto sub_step = [&](auto sub, auto first, auto count, int slot, int bp, int bq, int next_sub) {
+    constexpr int S = decltype(sub)::value, FIRST = decltype(first)::value, COUNT = decltype(count)::value, kMma = TP * TQ;
+    constexpr int kLoads = COUNT * L, kEvery = COUNT ? kMma / kLoads : 1;
     static_assert(TP + TQ <= kMma && kLoads <= kMma, "room between the MFMAs");
 #pragma unroll
     for (int m = 0; m < kMma; ++m) {
       mma(sub, m % TP, m / TP, S & 1);
-      if (m < TP + TQ) read(m, next_slot, next_sub, (S + 1) & 1);
-      if (A && m % kEvery == kEvery - 1 && m / kEvery < kLoads) {
-        const int n = m / kEvery, part = A + n / L;
-        issue(part % PT, n % L, wrap(slot + part % SLOTS));
+      if (m < TP + TQ) read(m, bp, bq, next_sub, (S + 1) & 1);
+      if (COUNT && m % kEvery == kEvery - 1 && m / kEvery < kLoads) {
+        const int n = m / kEvery, part = FIRST + n / L;
+        issue(part % PT, n % L, wrap(slot + part % SLOTS * TL::kPart));
         // (the operand's last part of the K-step)
-        if (n % L == L - 1 && part % PT == TL::kPP - 1) advance_p();
-        if (n % L == L - 1 && part % PT == PT - 1) advance_q();
+        if (n % L == L - 1 && part % PT == TL::kPP - 1) advance(p_from, true);
+        if (n % L == L - 1 && part % PT == PT - 1) advance(q_from, false);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // The parts of the ring go out in order, HALF of them in a trip's first sub-step, HALF in its last, each into the slot of the
-  // part SLOTS ahead of it.  Fragments are read one sub-step ahead of their MFMAs.  Before the last sub-step's MFMAs a wave
-  // waits for its loads of the next K-step and its reads of this one; past the barrier the next K-step is whole and this
-  // one's slots are free.  A workgroup goes through its tiles without draining the ring: the loads change to the next tile two
-  // K-steps ahead of the MFMAs (every tile has at least two K-steps, of zeros past its last), past the last tile they are of
-  // zeros.  The loop's body stays one block, which the scheduler keeps as it is written.
+  // The parts of the ring go out in order, each into the slot of the part SLOTS ahead of it.  Fragments are read one sub-step
+  // ahead of their MFMAs.  Before the last sub-step's MFMAs a wave waits for its loads of the next K-step and its reads of
+  // this one; past the barrier the next K-step is whole and this one's slots are free.  A workgroup goes through its tiles
+  // without draining the ring: the loads change to the next tile two K-steps ahead of the MFMAs (every tile has at least two
+  // K-steps, of zeros past its last), past the last tile they are of zeros.  The sub-steps stay as they are written
+  // (sched_barrier, and the accumulators pinned ahead of branches).
   using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
+  using Out0 = std::integral_constant<int, TL::kOut0>;
+  using Out1 = std::integral_constant<int, TL::kOut1>;
+  using Out2 = std::integral_constant<int, TL::kOut2>;
+  constexpr int kFill = SLOTS - TL::kOut0 - TL::kOut1 - TL::kOut2;  // parts ahead of the first trip's
   int steps = steps_of(now), ks = 0, slot = 0, buf = 0;
   aim_p(now);
   aim_q(now);
   aim_sf(now);
-  load_sf();
+  load_sf(0);
 #pragma unroll
-  for (int n = 0; n < SLOTS - HALF; ++n) {
+  for (int n = 0; n < kFill; ++n) {
     if (n % PT == 0) sources(n / PT * BK);
 #pragma unroll
-    for (int i = 0; i < L; ++i) issue(n % PT, i, n);
-    if (n % PT == TL::kPP - 1) advance_p();
-    if (n % PT == PT - 1) advance_q();
+    for (int i = 0; i < L; ++i) issue(n % PT, i, n * TL::kPart);
+    if (n % PT == TL::kPP - 1) advance(p_from, true);
+    if (n % PT == PT - 1) advance(q_from, false);
   }
-  store_sf(0);
-  load_sf();
+  load_sf(1);
   sources(2 * BK);
   __builtin_amdgcn_s_waitcnt(0);
   __builtin_amdgcn_s_barrier();
+  auto part_p = [&](int slot) { return wrap(slot + wp / kPw * TL::kPart); };
+  auto part_q = [&](int slot) { return wrap(slot + (TL::kPP + wq / kQw) * TL::kPart); };
+  int bp = part_p(0), bq = part_q(0);
 #pragma unroll
-  for (int f = 0; f < TP + TQ; ++f) read(f, 0, 0, 0);
+  for (int f = 0; f < TP + TQ; ++f) read(f, bp, bq, 0, 0);
   read_sf(0);
+  take_shifts();
   TileAt then{};
   bool stored = false;
   for (;;) {
-    const int next = wrap(slot + PT);
+    const int next = wrap(slot + PT * TL::kPart);
     const bool change = ks == steps - 2;
     if (change) {
       then = walk.next(p);
-      p_live = then.ok;
       aim_p(then);
-      if constexpr (TL::kAhead == HALF) q_live = then.ok, aim_q(then);
+      if constexpr (TL::kAhead == HALF) aim_q(then);
       sources(0);
     }
     take_sf();
-    sub_step(I0{}, std::integral_constant<int, SLOTS - HALF>{}, slot, slot, 1);
-    sub_step(std::integral_constant<int, 1>{}, I0{}, slot, slot, 2);
-    sub_step(std::integral_constant<int, 2>{}, I0{}, slot, slot, 3);
-    // (keeps these MFMAs ahead of the branches below)
+    sub_step(I0{}, std::integral_constant<int, kFill>{}, Out0{}, slot, bp, bq, 1);
+    sub_step(I1{}, std::integral_constant<int, kFill + TL::kOut0>{}, Out1{}, slot, bp, bq, 2);
+    sub_step(I2{}, std::integral_constant<int, kFill + TL::kOut0 + TL::kOut1>{}, Out2{}, slot, bp, bq, 3);
 #pragma unroll
     for (int i = 0; i < TP; ++i)
 #pragma unroll
       for (int j = 0; j < TQ; ++j) asm volatile("" : "+v"(acc[i][j]));
-    if constexpr (MX) {
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(HALF * L) | 15 << 8);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    store_sf(buf ^ 1);
     // (the stores of a tile that has just ended lie ahead of this trip's loads and may stay under way)
-    if (stored)
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L + (MX ? 0 : kStores)));
+    if (stored && TL::kAhead == HALF)
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L + kStores));
     else
       __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     if (change) {
-      if constexpr (TL::kAhead != HALF) q_live = then.ok, aim_q(then);
+      if constexpr (TL::kAhead != HALF) aim_q(then);
       aim_sf(then);
     }
-    load_sf();
+    load_sf(buf);
     read_sf(buf ^ 1);
-    sub_step(std::integral_constant<int, 3>{}, std::integral_constant<int, SLOTS>{}, slot, next, 0);
+    bp = part_p(next), bq = part_q(next);
+    sub_step(I3{}, std::integral_constant<int, SLOTS>{}, std::integral_constant<int, HALF>{}, slot, bp, bq, 0);
     sources(p_k);
     slot = next;
     buf ^= 1;
@@ -593,6 +605,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       steps = steps_of(now);
       ks = 0;
       clear();
+      take_shifts();
     }
   }
   __builtin_amdgcn_s_waitcnt(0);  // the loads of zeros land before the workgroup's LDS is another's
@@ -699,7 +712,9 @@ hipError_t launch_grouped_gemm_mxfp4(const GroupedArgs& a, hipStream_t s) {
   p.p_expert = (long long)a.n * (a.k / 2);
   p.p_ld = p.q_ld = (uint32_t)a.k / 2;
   p.sf_row = a.k / 32;
-  p.p_sf_expert = (long long)a.n * p.sf_row;
+  p.n_rows = a.n;
+  p.p_sf_bytes = (long long)a.E * a.n * p.sf_row;
+  p.q_sf_bytes = (long long)(a.a_rows == Rows::TOKEN ? a.T : p.npairs) * p.sf_row;
   p.P_sf = (const uint8_t*)a.w_sf;
   p.Q_sf = (const uint8_t*)a.a_sf;
   return a.out_f32 ? launch_rows<Op::MX, true>(p, s) : launch_rows<Op::MX, false>(p, s);
