@@ -66,13 +66,13 @@ struct GroupedParams {
 // Written so that the compiler does not see stores to LDS: it lets no ds_read_b64_tr pass one in flight.  The kernel's own
 // waits order the two.
 constexpr uint32_t kNone = 0xFFFFFFFFu, kAll = 0xFFFFFFF0u;  // an offset out of any resource, the largest resource
+// (The offsets are the lanes' own: a scalar one may wrap the check against the resource's end.)
 MOE_DEV void lds_copy16(i32x4 rsrc, uint32_t voff, uint32_t l) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(l), "v"(voff), "s"(rsrc)
                : "memory");
 }
-MOE_DEV void lds_copy12(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t l) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx3 %1, %2, %3 offen lds" ::"s"(l), "v"(voff), "s"(rsrc),
-               "s"(soff)
+MOE_DEV void lds_copy12(i32x4 rsrc, uint32_t voff, uint32_t l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx3 %1, %2, 0 offen lds" ::"s"(l), "v"(voff), "s"(rsrc)
                : "memory");
 }
 MOE_DEV uint32_t lds_address(const void* l) { return (uint32_t)(uintptr_t)(const LDS3 void*)l; }
@@ -82,6 +82,12 @@ MOE_DEV int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 MOE_DEV const uint8_t* scalar(const uint8_t* v) {
   const uint64_t b = (uint64_t)v;
   return (const uint8_t*)((uint64_t)(uint32_t)scalar((int)(uint32_t)b) | (uint64_t)(uint32_t)scalar((int)(uint32_t)(b >> 32)) << 32);
+}
+// The same value, of which the compiler knows nothing: what follows from it is computed where it is used, not kept in
+// registers through the K loop.
+MOE_DEV int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
 }
 MOE_DEV i32x4 resource(const void* base, uint32_t bytes) {
   const uint64_t b = (uint64_t)base;
@@ -112,13 +118,13 @@ struct TileAt {
 // every expert's), its workgroups in turn: what an XCD runs at once then shares few operand panels in its L2.
 template <bool WGRAD, int BQ, int GQ>
 struct Walk {
-  int e0, before, lo, hi, upto;  // lane l: rows of expert e0 + l, and the tiles up to its last
+  int e0, before, upto;  // lane l: the tiles up to expert e0 + l's last
   int at, end, step;
 
   MOE_DEV void chunk(const GroupedParams& p, int first) {
     e0 = first;
     const int e = e0 + lane_id();
-    lo = hi = 0;
+    int lo = 0, hi = 0;
     if (e < p.E) lo = row_at(p, e), hi = max(lo, row_at(p, e + 1));
     upto = before + wave_scan((hi - lo + BQ - 1) / BQ * p.p_tiles);
   }
@@ -162,8 +168,8 @@ struct Walk {
       while (at >= __builtin_amdgcn_readlane(upto, 63)) before = __builtin_amdgcn_readlane(upto, 63), chunk(p, e0 + 64);
       const int l = __ffsll((unsigned long long)__ballot(upto > at)) - 1;
       t.expert = e0 + l;
-      t.lo = __builtin_amdgcn_readlane(lo, l);
-      t.hi = __builtin_amdgcn_readlane(hi, l);
+      t.lo = row_at(p, t.expert);
+      t.hi = max(t.lo, row_at(p, t.expert + 1));
       q_tiles = (t.hi - t.lo + BQ - 1) / BQ;
       within = at - (__builtin_amdgcn_readlane(upto, l) - q_tiles * p.p_tiles);
     }
@@ -181,21 +187,40 @@ struct Walk {
   }
 };
 
-// Where 16-byte chunk c of row r lies among its row's eight (rows of 128 bytes): a 32-row operand's lanes r and r + 16
-// are read together, so both row bits take part.
-MOE_DEV int swz(int r) { return (r & 7) ^ ((r >> 4) & 1); }
+// f(0), f(1) .. with the number as a type.
+template <int FROM, int TO, class F>
+MOE_DEV void each(F&& f) {
+  if constexpr (FROM < TO) {
+    f(std::integral_constant<int, FROM>{});
+    each<FROM + 1, TO>(f);
+  }
+}
 
-// Transposed operands: the 32-byte unit u of summed row r lies at u ^ trx(r), so that the 4 rows x 2 units that 32 lanes
-// read lie in different banks.
-MOE_DEV int trx(int r) { return 2 * (r & 3); }
+// Where 16-byte chunk c of row r lies among its row's eight (rows of 128 bytes).  A read serves lanes 0-7 together with
+// 16-23: eight rows, and the two chunks that the lanes' second and third quarter differ by (bf16: 1, MXFP4: 2).
+template <bool MX>
+MOE_DEV int place_of_chunk(int c, int r) {
+  return (MX ? (c & 4) | (c & 1) << 1 | (c >> 1 & 1) : c) ^ (r & 7);
+}
+template <bool MX>
+MOE_DEV int chunk_at(int place, int r) {
+  const int c = place ^ (r & 7);
+  return MX ? (c & 4) | (c & 1) << 1 | (c >> 1 & 1) : c;
+}
+
+// Transposed operands: the 32-byte unit u of summed row r lies at u ^ trx(r), so that the 8 rows that 32 lanes read lie in
+// different banks.
+MOE_DEV int trx(int r) { return 2 * (r & 3) | (r >> 3 & 1); }
 
 // ---------------------------------------------------------------- tiles
-// BP x BQ outputs, WP x WQ waves, each TP x TQ MFMA tiles of 32 x 32.  A K-step (128 bytes of an operand's row) is staged in
-// parts of 16 KB -- 128 rows, or columns, of P or Q -- in a ring of SLOTS of them.
+// BP x BQ outputs, WP x WQ waves, each TP x TQ MFMA tiles of 16 x 16 (v_mfma_f32_16x16x32_bf16 and .._16x16x128_f8f6f4: the
+// part's power limits a loop of MFMAs alone to 2.02 and 7.19 PFLOP/s with them, to 1.80 and 6.51 with the 32 x 32 forms).  A
+// K-step (128 bytes of an operand's row) is staged in parts of 16 KB -- 128 rows, or columns, of P or Q -- in a ring of SLOTS
+// of them.
 template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS>
 struct GTile {
   static constexpr int kWaves = WP * WQ, kThreads = 64 * kWaves;
-  static constexpr int TP = BP / 32 / WP, TQ = BQ / 32 / WQ;
+  static constexpr int TP = BP / 16 / WP, TQ = BQ / 16 / WQ;
   static constexpr bool kTP = O == Op::GRAD || O == Op::WGRAD, kTQ = O == Op::WGRAD;
   static constexpr int kPart = 16384, kPP = BP / 128, kPQ = BQ / 128, kParts = kPP + kPQ, kHalf = kParts / 2;
   static constexpr int kL = 16 / kWaves;  // a wave's loads of a part
@@ -203,14 +228,13 @@ struct GTile {
   static constexpr int kLds = SLOTS * kPart + 2 * kSf;
   static constexpr int kBK = O == Op::MX ? 256 : 64;  // elements of a K-step
   static constexpr int kAhead = SLOTS - 2 * kParts;   // parts in flight past the next K-step's
-  static_assert(BP % 128 == 0 && BQ % 128 == 0 && 128 % (TP * 32) == 0 && 128 % (TQ * 32) == 0, "a wave reads one part");
-  // parts that go out in a trip's sub-steps 0, 1 and 3
-  static constexpr int kOut1 = kHalf / 2 > 0 ? kHalf / 2 : 1, kOut0 = kAhead == kHalf ? 0 : kOut1;
-  static constexpr int kOut2 = kParts - kHalf - kOut0 - kOut1;
-  static_assert(16 % kWaves == 0 && kPP == kPQ && kAhead > 0 && kAhead <= kHalf && kOut2 >= 0, "ring");
+  static_assert(BP % 128 == 0 && BQ % 128 == 0 && 128 % (TP * 16) == 0 && 128 % (TQ * 16) == 0, "a wave reads one part");
+  static_assert(TP % 2 == 0 && TQ % 4 == 0 && TP <= TQ, "the order of reads");
+  static_assert(16 % kWaves == 0 && kPP == kPQ && kAhead > 0 && kAhead <= kHalf, "ring");
 };
 
-// WHERE: bit 0: P's rows, bit 1: Q's rows are found through src_info (WGRAD; elsewhere Q's are looked up once a tile).
+// WHERE: bit 0: P's rows, bit 1: Q's rows are found through src_info (WGRAD; elsewhere Q's are looked up once a tile); MX: bit
+// 0: rows of scales are not whole words.
 // Registers: one workgroup a CU for the large tile.
 template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS, bool F32, int WHERE>
 __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams p) {
@@ -220,7 +244,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   constexpr int L = TL::kL;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TL::kLds];
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wp = wave % WP, wq = wave / WP, h = lane >> 5, r32 = lane & 31;
+  const int wp = wave % WP, wq = wave / WP, g = lane >> 4, r16 = lane & 15;
   Walk<WG, BQ, 8> walk;
   walk.begin(p);
   TileAt now = walk.next(p);  // the tile of the MFMAs; the loads run up to two K-steps ahead, into `then`
@@ -229,60 +253,74 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
 
   // ---------------------------------------------------------------- what each lane loads
   // Load i of a part: rows (i * waves + wave) * 8 + lane / 8 of 128 bytes, or (T) summed rows (i * waves + wave) * 4 + lane
-  // / 16 of 256 bytes.  Bases are scalar and move by a K-step; offsets stay.  Summed rows past the last lie past the
-  // resource's end, chunks past K get an offset that does: both load zeros.
-  const int row8 = wave * 8 + (lane >> 3), row4 = wave * 4 + (lane >> 4);
-  const int chunk8 = (lane & 7) ^ swz(row8), chunk4 = ((((lane & 15) >> 1) ^ trx(row4)) << 1) | (lane & 1);
+  // / 16 of 256 bytes.  Bases are scalar and move by a K-step, a lane's offsets stay.  Rows past the last, of the output or
+  // summed, lie past the resource's end and chunks past K get an offset that does: both load zeros.  (Columns past a T
+  // operand's last are the next row's first; what comes of them is not stored.)
   constexpr int kStep8 = TL::kWaves * 8, kStep4 = TL::kWaves * 4;
-  uint32_t voff[PT][L];  // (WGRAD through src_info: the column alone)
+  const int chunk8 = chunk_at<MX>(lane & 7, wave * 8 + (lane >> 3));
+  uint32_t p_off = 0, q_off[TL::kPQ][L] = {};  // (Q through src_info, but for WGRAD: of each row; else the first)
   i32x4 p_from{}, q_from{};      // the operands' resources at the next load's K-step
   int p_k = 0, q_k = 0;          // summed elements up to it
+  int p_rows = 0, q_rows = 0;    // rows of the output from the tile's first on (not T)
   int load_lo = 0, load_hi = 0;  // WGRAD: the rows of the loads' tile
-  auto extent = [&](bool isP) {  // T operands: the summed rows of a K-step that there are
-    return (uint32_t)max(min((WG ? load_hi - load_lo : p.K) - (isP ? p_k : q_k), 64), 0) * (isP ? p.p_ld : p.q_ld);
+  constexpr bool kLookP = WG && (WHERE & 1), kLookQ = WG && (WHERE & 2);
+  // the bytes from a resource's base on that are the operand's: T operands: of a K-step, else of the tile's rows
+  uint32_t p_skip = 0, q_skip = 0;  // T operands: the tile's first column
+  auto extent = [&](bool isP) {
+    const int k0 = isP ? p_k : q_k, rows = min(isP ? p_rows : q_rows, isP ? BP : BQ);
+    const uint32_t ld = isP ? p.p_ld : p.q_ld;
+    if (isP ? kLookP : kLookQ) return kAll;
+    if (isP ? kTP : kTQ) {
+      const int left = (WG ? load_hi - load_lo : p.K) - k0;
+      return left > 0 ? (uint32_t)min(left, 64) * ld - (isP ? p_skip : q_skip) : 0u;
+    }
+    return (uint32_t)rows * ld;
   };
-  auto column = [&](int first, int cols) { return (uint32_t)min(first / 8 + chunk4, cols / 8 - 1) * 16; };
+  // the offset of a T operand's first row and column of a part's first load
+  auto t_off = [&](uint32_t ld) {
+    const int l = fresh(lane), row = wave * 4 + (l >> 4);
+    return (uint32_t)row * ld + ((((l & 15) >> 1) ^ trx(row)) << 5) + (l & 1) * 16;
+  };
   auto aim_p = [&](const TileAt& t) {
     p_k = 0;
-    const uint8_t* base = p.P;
+    p_skip = t.p * BP * 2;
+    const uint8_t* base = p.P + (kTP ? (long long)p_skip : (long long)t.p * BP * p.p_ld);
     if constexpr (WG) {
       load_lo = t.lo, load_hi = t.ok ? t.hi : t.lo;
-      base += (WHERE & 1) ? 0 : (long long)t.lo * p.p_ld;
+      base += kLookP ? 0 : (long long)t.lo * p.p_ld;
     } else {
-      base += t.expert * p.p_expert + (kTP ? 0 : (long long)t.p * BP * p.p_ld);
+      base += t.expert * p.p_expert;
+      p_rows = p.p_cols - t.p * BP;
     }
-    p_from = resource(base, !t.ok ? 0 : kTP && !(WHERE & 1) ? extent(true) : kAll);
-#pragma unroll
-    for (int j = 0; j < TL::kPP; ++j)
-#pragma unroll
-      for (int i = 0; i < L; ++i) {
-        if constexpr (kTP)
-          voff[j][i] = column(t.p * BP + j * 128, p.p_cols) + ((WHERE & 1) ? 0 : (i * kStep4 + row4) * p.p_ld);
-        else
-          voff[j][i] = (uint32_t)min(j * 128 + i * kStep8 + row8, p.p_cols - 1 - t.p * BP) * p.p_ld + chunk8 * 16;
-      }
+    const int l = fresh(lane);
+    p_off = kLookP ? t_off(0) : kTP ? t_off(p.p_ld) : (uint32_t)(wave * 8 + (l >> 3)) * p.p_ld + chunk8 * 16;
+    p_from = resource(base, t.ok ? extent(true) : 0u);
   };
   auto aim_q = [&](const TileAt& t) {
     q_k = 0;
-    const uint8_t* base = p.Q;
+    q_skip = t.q * BQ * 2;
+    const uint8_t* base = p.Q + (kTQ ? (long long)q_skip : 0);
+    const bool look = !WG && p.q_place.gathered;
     if constexpr (WG) {
-      if (!(WHERE & 2)) base += (long long)t.lo * p.q_ld;
-    } else if (!p.q_place.gathered) {
-      base += ((long long)t.lo + t.q * BQ) * p.q_ld;
+      base += kLookQ ? 0 : (long long)t.lo * p.q_ld;
+    } else {
+      q_rows = t.hi - t.lo - t.q * BQ;
+      if (!look) base += ((long long)t.lo + t.q * BQ) * p.q_ld;
     }
-    q_from = resource(base, !t.ok ? 0 : kTQ && !(WHERE & 2) ? extent(false) : kAll);
+    const int l = fresh(lane);
+    q_off[0][0] = kLookQ ? t_off(0) : kTQ ? t_off(p.q_ld) : (uint32_t)(wave * 8 + (l >> 3)) * p.q_ld + chunk8 * 16;
+    if constexpr (!WG) {
 #pragma unroll
-    for (int j = 0; j < TL::kPQ; ++j)
+      for (int j = 0; j < TL::kPQ; ++j)
 #pragma unroll
-      for (int i = 0; i < L; ++i) {
-        if constexpr (kTQ) {
-          voff[TL::kPP + j][i] = column(t.q * BQ + j * 128, p.q_cols) + ((WHERE & 2) ? 0 : (i * kStep4 + row4) * p.q_ld);
-        } else {
-          int r = max(min(j * 128 + i * kStep8 + row8, t.hi - t.lo - 1 - t.q * BQ), 0);
-          if (p.q_place.gathered && t.ok) r = p.q_place.of(p.src_info[t.lo + t.q * BQ + r]);
-          voff[TL::kPP + j][i] = (uint32_t)r * p.q_ld + chunk8 * 16;
+        for (int i = 0; i < L; ++i) {
+          const int r = j * 128 + i * kStep8 + wave * 8 + (l >> 3);
+          q_off[j][i] = q_off[0][0] + (uint32_t)(j * 128 + i * kStep8) * p.q_ld;
+          if (look && t.ok)
+            q_off[j][i] = (uint32_t)p.q_place.of(p.src_info[t.lo + t.q * BQ + max(min(r, q_rows - 1), 0)]) * p.q_ld + chunk8 * 16;
         }
-      }
+    }
+    q_from = resource(base, !t.ok ? 0u : look ? kAll : extent(false));
   };
   // WGRAD: src_info of this lane's summed rows, by scalar loads (a vector load would have to wait for the loads into LDS
   // behind it)
@@ -304,33 +342,40 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   const uint32_t lds0 = lds_address(lds);
   auto issue = [&](int J, int i, int slot) {
     const bool isP = J < TL::kPP, tr = isP ? kTP : kTQ;
-    const int k0 = isP ? p_k : q_k;
-    uint32_t v = voff[J][i];
-    if (WG && (WHERE & (isP ? 1 : 2))) {
-      v += (uint32_t)(isP ? p.p_place : p.q_place).of(src[i]) * (isP ? p.p_ld : p.q_ld);
-      v = i * kStep4 + row4 < load_hi - load_lo - k0 ? v : kNone;
-    } else if (!tr) {
+    const int j = isP ? J : J - TL::kPP, k0 = isP ? p_k : q_k;
+    const uint32_t ld = isP ? p.p_ld : p.q_ld;
+    uint32_t v = isP ? p_off : q_off[WG ? 0 : j][WG ? 0 : i];
+    if (isP ? kLookP : kLookQ) {
+      v += (uint32_t)(isP ? p.p_place : p.q_place).of(src[i]) * ld + j * 256;
+      v = i * kStep4 + wave * 4 + g < load_hi - load_lo - k0 ? v : kNone;
+    } else if (tr) {
+      v += i * kStep4 * ld + j * 256;
+    } else {
+      if (isP) v += (j * 128 + i * kStep8) * ld;
       v = k0 + chunk8 * (MX ? 32 : 8) < p.K ? v : kNone;
     }
     lds_copy16(isP ? p_from : q_from, v, lds0 + slot + (i * TL::kWaves + wave) * 1024);
   };
   // an operand's next K-step
   auto advance = [&](i32x4& from, bool isP) {
-    const bool tr = isP ? kTP : kTQ, look = WG && (WHERE & (isP ? 1 : 2));
+    const bool tr = isP ? kTP : kTQ;
     (isP ? p_k : q_k) += BK;
-    if (look) return;
-    const uint64_t base = ((uint64_t)(uint32_t)from[1] << 32 | (uint32_t)from[0]) + (tr ? 64 * (uint64_t)(isP ? p.p_ld : p.q_ld) : 128);
-    from = resource((const void*)base, tr ? extent(isP) : (uint32_t)from[2]);
+    if (isP ? kLookP : kLookQ) return;
+    const uint64_t base = ((uint64_t)(uint32_t)from[1] << 32 | (uint32_t)from[0]) + (tr ? 64 * (isP ? p.p_ld : p.q_ld) : 128);
+    const uint32_t had = (uint32_t)from[2];
+    // (rows of 128 bytes: the resource ends where it ended, or, through src_info, nowhere)
+    from = resource((const void*)base, tr ? (had ? extent(isP) : 0u) : had == kAll || had == 0 ? had : had > 128 ? had - 128 : 0u);
   };
 
   // MXFP4: the words that hold a row's 8 scales of a K-step, waves 0 .. BP / 64 - 1 P's rows, the others Q's.  A row's scales
   // may start at any byte: the three words from the one that holds the first.
   static_assert(!MX || (BP + BQ == kThreads && BP % 64 == 0), "a thread for each row of scales");
   i32x4 sf_from{};
-  uint32_t sf_off = 0, sf_at = 0;
+  uint32_t sf_off = 0;
   int sf_k = 0;                             // scales of a row up to the K-step that is read next
-  uint32_t p_shift[TP] = {}, q_shift[TQ] = {};  // where the fragments' rows start in their words, bytes
-  uint32_t p_shift_next[TP] = {}, q_shift_next[TQ] = {};
+  // where the fragments' rows start in their words, bytes (rows 16 apart start alike)
+  constexpr bool ODD = MX && (WHERE & 1);  // rows of scales are not whole words
+  uint32_t p_shift = 0, q_shift[ODD ? TQ : 1] = {};
   // the row of p or q (of the tile) whose scales row's are, in its tensor
   auto sf_row_p = [&](const TileAt& t, int row) { return (long long)t.expert * p.n_rows + min(t.p * BP + row, p.p_cols - 1); };
   auto sf_row_q = [&](const TileAt& t, int row) {
@@ -348,111 +393,97 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       const long long row = isp ? sf_row_p(t, tid) : sf_row_q(t, tid - BP);
       sf_off = (uint32_t)((row * p.sf_row & ~3LL) - begin);
       sf_from = resource(all + begin, t.ok ? (uint32_t)min(end - begin, (long long)kAll) : 0u);
-      sf_at = 0;
+    }
+  };
+  auto aim_shifts = [&](const TileAt& t) {
+    if constexpr (ODD) {
+      p_shift = (uint32_t)((t.expert * (long long)p.n_rows + t.p * BP + r16) * p.sf_row) & 3;
 #pragma unroll
-      for (int i = 0; i < TP; ++i) p_shift_next[i] = (uint32_t)(sf_row_p(t, (wp * TP + i) * 32 + r32) * p.sf_row) & 3;
-#pragma unroll
-      for (int i = 0; i < TQ; ++i) q_shift_next[i] = (uint32_t)(sf_row_q(t, (wq * TQ + i) * 32 + r32) * p.sf_row) & 3;
+      for (int j = 0; j < TQ; ++j) q_shift[j] = (uint32_t)(sf_row_q(t, (wq * TQ + j) * 16 + r16) * p.sf_row) & 3;
     }
   };
   auto load_sf = [&](int buf) {
     if constexpr (MX) {
-      lds_copy12(sf_from, sf_off, sf_at, lds0 + SLOTS * TL::kPart + buf * TL::kSf + wave * (64 * 16));
-      sf_at += 8;
+      lds_copy12(sf_from, sf_off, lds0 + SLOTS * TL::kPart + buf * TL::kSf + wave * (64 * 16));
+      sf_off += 8;
     }
   };
 
   // ---------------------------------------------------------------- fragments
   constexpr int kRing = SLOTS * TL::kPart;
   auto wrap = [](int at) { return at >= kRing ? at - kRing : at; };
-  i32x4 fp[2][TP], fq[2][TQ];
-  uint32_t sp[TP] = {}, sq[TQ] = {};
-  // tile: of 32 rows (columns) within the part at base
+  i32x4 fp[2][TP], fq[TQ];  // (a Q fragment's registers take the next sub-step's as soon as its MFMAs are out)
+  uint32_t sp[TP / 2] = {}, sq[TQ / 2] = {};
+  const int t_row = 8 * g + (r16 >> 2);
+  const uint32_t t_lane = t_row * 256 + (trx(t_row) << 5) + (lane & 3) * 8;
+  // tile: of 16 rows (columns) within the part at base
   auto frag = [&](const uint8_t* base, bool tr, int tile, int s) -> i32x4 {
-    if (!tr) {
-      const int c = (MX ? 4 * h + s : 2 * s + h) ^ swz(r32);
-      return *(const i32x4*)(base + (tile * 32 + r32) * 128 + c * 16);
-    }
-    const int row = 16 * s + 8 * h + ((lane & 15) >> 2), u = tile * 2 + ((lane >> 4) & 1);
-    const uint8_t* a = base + row * 256 + ((u ^ trx(row)) << 5) + (lane & 3) * 8;
+    if (!tr)
+      return *(const i32x4*)(base + (tile * 16 + r16) * 128 + place_of_chunk<MX>(MX ? 2 * g + s : 4 * s + g, r16) * 16);
+    // (an exclusive or of an address that changes with the K-step, not a sum with one of a register a tile)
+    const uint32_t a = (lds_address(base) + t_lane + s * (32 * 256)) ^ (uint32_t)(tile << 5);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4*)a);
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4*)(a + 4 * 256));
     return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  constexpr int kPw = 128 / (TP * 32), kQw = 128 / (TQ * 32);  // waves that share a part
-  // fragment f (P's first) of a sub-step of the K-step whose parts this wave reads lie at bp and bq
-  auto read = [&](int f, int bp, int bq, int s, int set) {
-    if (f < TP)
-      fp[set][f] = frag(lds + bp, kTP, wp % kPw * TP + f, s);
-    else
-      fq[set][f - TP] = frag(lds + bq, kTQ, wq % kQw * TQ + f - TP, s);
-  };
-  // a K-step's scales, byte s of a lane's word for sub-step s (blocks past K: scale 2^-127, on codes of zero)
-  uint32_t sp_words[TP][2] = {}, sq_words[TQ][2] = {};
+  constexpr int kPw = 128 / (TP * 16), kQw = 128 / (TQ * 16);  // waves that share a part
+  // a fragment of a sub-step of the K-step whose parts this wave reads lie at bp and bq
+  auto read_p = [&](int i, int bp, int s) { fp[s & 1][i] = frag(lds + bp, kTP, wp % kPw * TP + i, s); };
+  auto read_q = [&](int j, int bq, int s) { fq[j] = frag(lds + bq, kTQ, wq % kQw * TQ + j, s); };
+  // a K-step's scales: lane g's blocks are 2 g and 2 g + 1, for sub-steps 0 and 1 (blocks past K: scale 2^-127, on codes of
+  // zero)
+  uint32_t sp_next[TP] = {}, sq_next[TQ] = {};
   auto read_sf = [&](int buf) {
     if constexpr (MX) {
-      const uint32_t* f = (const uint32_t*)(lds + SLOTS * TL::kPart + buf * TL::kSf);
+      typedef uint16_t __attribute__((aligned(1))) Bytes2;
+      const uint8_t* f = lds + SLOTS * TL::kPart + buf * TL::kSf + 2 * g + r16 * 16;
 #pragma unroll
-      for (int i = 0; i < TP; ++i) {
-        const uint32_t* w = f + ((wp * TP + i) * 32 + r32) * 4 + h;
-        sp_words[i][0] = w[0], sp_words[i][1] = w[1];
-      }
+      for (int i = 0; i < TP; ++i) sp_next[i] = *(const Bytes2*)(f + (wp * TP + i) * 256 + p_shift);
 #pragma unroll
-      for (int i = 0; i < TQ; ++i) {
-        const uint32_t* w = f + (BP + (wq * TQ + i) * 32 + r32) * 4 + h;
-        sq_words[i][0] = w[0], sq_words[i][1] = w[1];
-      }
+      for (int j = 0; j < TQ; ++j) sq_next[j] = *(const Bytes2*)(f + (BP + (wq * TQ + j) * 16) * 16 + (ODD ? q_shift[j] : 0));
     }
   };
+  // two tiles' in a word
   auto take_sf = [&] {
     if constexpr (MX) {
-      const int left = p.sf_row - sf_k;
-      const uint64_t keep = left >= 8 ? ~0ull : left <= 0 ? 0ull : (1ull << (8 * left)) - 1;
-      const uint32_t mine = h ? (uint32_t)(keep >> 32) : (uint32_t)keep;
+      const int left = p.sf_row - sf_k - 2 * g;
+      const uint32_t keep = left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0x00FF00FFu : 0u;
 #pragma unroll
-      for (int i = 0; i < TP; ++i) sp[i] = __builtin_amdgcn_alignbyte(sp_words[i][1], sp_words[i][0], p_shift[i]) & mine;
+      for (int i = 0; i < TP; i += 2) sp[i / 2] = (sp_next[i] | sp_next[i + 1] << 16) & keep;
 #pragma unroll
-      for (int i = 0; i < TQ; ++i) sq[i] = __builtin_amdgcn_alignbyte(sq_words[i][1], sq_words[i][0], q_shift[i]) & mine;
+      for (int j = 0; j < TQ; j += 2) sq[j / 2] = (sq_next[j] | sq_next[j + 1] << 16) & keep;
       sf_k += 8;
     }
   };
-  auto take_shifts = [&] {
-    sf_k = 0;
-#pragma unroll
-    for (int i = 0; i < TP; ++i) p_shift[i] = p_shift_next[i];
-#pragma unroll
-    for (int i = 0; i < TQ; ++i) q_shift[i] = q_shift_next[i];
-  };
-  f32x16 acc[TP][TQ];
+  f32x4 acc[TP][TQ];
   auto clear = [&] {
 #pragma unroll
     for (int i = 0; i < TP; ++i)
 #pragma unroll
-      for (int j = 0; j < TQ; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+      for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   };
   clear();
-  auto mma = [&](auto sub, int i, int j, int set) {
-    constexpr int S = decltype(sub)::value;
+  auto mma = [&](auto sub, auto place) {
+    constexpr int S = decltype(sub)::value, i = decltype(place)::value % TP, j = decltype(place)::value / TP;
     if constexpr (MX) {
-      const i32x4 a = fp[set][i], b = fq[set][j];
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0}, i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, acc[i][j], 4, 4, S,
-          (int)sp[i], S, (int)sq[j]);
+      const i32x4 a = fp[S][i], b = fq[j];
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0}, i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, acc[i][j], 4, 4,
+          S + 2 * (i & 1), (int)sp[i / 2], S + 2 * (j & 1), (int)sq[j / 2]);
     } else {
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fp[set][i]),
-                                                          __builtin_bit_cast(bf16x8, fq[set][j]), acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fp[S][i]),
+                                                          __builtin_bit_cast(bf16x8, fq[j]), acc[i][j], 0, 0, 0);
     }
   };
 
   // ---------------------------------------------------------------- output
   // From the registers, 16 bytes a lane, as stores that do not wait: the loads of the next tile are under way.  A lane holds
-  // columns 8 v + 4 h .. + 4 of row r32; bf16 lanes h = 0, 1 swap so that each has 8 in a row.  Every store is issued,
-  // those out of the output with an offset that is dropped: the waits count them.
-  constexpr int kStores = TP * TQ * (F32 ? 4 : 2);
+  // columns 4 g .. + 4 of row r16 of a 16 x 16 tile; for bf16 two neighbouring tiles' lanes swap so that each has 8 in a row:
+  // 16 rows of 64 bytes a store.  Every store is issued, those out of the output with an offset that is dropped: the waits
+  // count them.
+  constexpr int kStores = TP * TQ / (F32 ? 1 : 2);
   auto store = [&](const TileAt& t) {
-    const int q0 = t.q * BQ + wq * TQ * 32, p0 = t.p * BP + wp * TP * 32;
+    const int q0 = t.q * BQ + wq * TQ * 16, p0 = t.p * BP + wp * TP * 16;
     const int q_end = WG ? p.q_cols : t.hi - t.lo;
     constexpr int kEl = F32 ? 4 : 2;
     const uint8_t* base = p.out;
@@ -461,9 +492,10 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     else if (!p.out_pair)
       base += ((long long)t.lo + q0) * p.out_ld;
     const __amdgpu_buffer_rsrc_t to = make_rsrc(base, kAll);
+    const int l16 = fresh(r16), lg = fresh(g);
 #pragma unroll
     for (int j = 0; j < TQ; ++j) {
-      const int row = j * 32 + r32;
+      const int row = j * 16 + l16;
       bool ok = q0 + row < q_end;
       uint32_t at = (uint32_t)row * p.out_ld;
       if (!WG && p.out_pair) {
@@ -472,74 +504,66 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
         at = (uint32_t)r * p.out_ld;
       }
 #pragma unroll
-      for (int i = 0; i < TP; ++i) {
-        const f32x16& c = acc[i][j];
-#pragma unroll
-        for (int v = 0; v < 4; v += F32 ? 1 : 2) {
-          i32x4 d;
-          int col = p0 + i * 32 + 8 * v;
-          if constexpr (F32) {
-            d = i32x4{__float_as_int(c[4 * v]), __float_as_int(c[4 * v + 1]), __float_as_int(c[4 * v + 2]), __float_as_int(c[4 * v + 3])};
-            col += 4 * h;
-          } else {
-            const auto x = __builtin_amdgcn_permlane32_swap(bf16x2_rne(c[4 * v], c[4 * v + 1]), bf16x2_rne(c[4 * v + 4], c[4 * v + 5]), false, false);
-            const auto y = __builtin_amdgcn_permlane32_swap(bf16x2_rne(c[4 * v + 2], c[4 * v + 3]), bf16x2_rne(c[4 * v + 6], c[4 * v + 7]), false, false);
-            d = i32x4{(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
-            col += 8 * h;
-          }
-          const uint32_t o = (at + (uint32_t)col * kEl) | (ok && col < p.p_cols ? 0u : kNone);
-          if constexpr (WG && F32) {
-            if (p.accumulate) {
-              const f32x4 sum = __builtin_bit_cast(f32x4, d) + __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(to, o, 0, 0));
-              d = __builtin_bit_cast(i32x4, sum);
-            }
-          }
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, d), to, o, 0, 0);
+      for (int i = 0; i < TP; i += F32 ? 1 : 2) {
+        i32x4 d;
+        int col = p0 + i * 16;
+        if constexpr (F32) {
+          d = __builtin_bit_cast(i32x4, acc[i][j]);
+          col += 4 * lg;
+        } else {
+          const f32x4 u = acc[i][j], v = acc[i + 1][j];
+          const auto x = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[0], u[1]), bf16x2_rne(v[0], v[1]), false, false);
+          const auto y = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[2], u[3]), bf16x2_rne(v[2], v[3]), false, false);
+          d = i32x4{(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
+          col += 16 * (lg & 1) + 8 * (lg >> 1);
         }
+        const uint32_t o = ok && col < p.p_cols ? at + (uint32_t)col * kEl : kNone;
+        if constexpr (WG && F32) {
+          if (p.accumulate) {
+            const f32x4 sum = __builtin_bit_cast(f32x4, d) + __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(to, o, 0, 0));
+            d = __builtin_bit_cast(i32x4, sum);
+          }
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, d), to, o, 0, 0);
       }
     }
   };
 
   // ---------------------------------------------------------------- K loop
-  // A sub-step: its MFMAs, and between them the reads of the next one's fragments and the loads of COUNT parts, those FIRST
-  // .. behind the trip's first.  (A wave that issues many loads at once waits for the address unit, 16 cycles each and
-  // shared by the waves, and feeds no MFMAs meanwhile.)
-  auto sub_step = [&](auto sub, auto first, auto count, int slot, int bp, int bq, int next_sub) {
-    constexpr int S = decltype(sub)::value, FIRST = decltype(first)::value, COUNT = decltype(count)::value, kMma = TP * TQ;
-    constexpr int kLoads = COUNT * L, kEvery = COUNT ? kMma / kLoads : 1;
-    static_assert(TP + TQ <= kMma && kLoads <= kMma, "room between the MFMAs");
-#pragma unroll
-    for (int m = 0; m < kMma; ++m) {
-      mma(sub, m % TP, m / TP, S & 1);
-      if (m < TP + TQ) read(m, bp, bq, next_sub, (S + 1) & 1);
-      if (COUNT && m % kEvery == kEvery - 1 && m / kEvery < kLoads) {
-        const int n = m / kEvery, part = FIRST + n / L;
-        issue(part % PT, n % L, wrap(slot + part % SLOTS * TL::kPart));
-        // (the operand's last part of the K-step)
-        if (n % L == L - 1 && part % PT == TL::kPP - 1) advance(p_from, true);
-        if (n % L == L - 1 && part % PT == PT - 1) advance(q_from, false);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  // The parts of the ring go out in order, each into the slot of the part SLOTS ahead of it.  Fragments are read one sub-step
-  // ahead of their MFMAs.  Before the last sub-step's MFMAs a wave waits for its loads of the next K-step and its reads of
-  // this one; past the barrier the next K-step is whole and this one's slots are free.  A workgroup goes through its tiles
-  // without draining the ring: the loads change to the next tile two K-steps ahead of the MFMAs (every tile has at least two
-  // K-steps, of zeros past its last), past the last tile they are of zeros.  The sub-steps stay as they are written
+  // A trip is a K-step: two sub-steps of TQ groups of TP MFMAs, with what else goes out between them.  (A wave that issues
+  // many loads at once waits for the address unit, 16 cycles each and shared by the waves, and feeds no MFMAs meanwhile.)
+  //   sub-step 0: the reads of sub-step 1's fragments, and the loads of half of the parts
+  //   the first groups of sub-step 1; then the wait for the next K-step's loads and these reads, and the barrier: the next K-step
+  //   is whole, and this one's slots are free
+  //   the rest of sub-step 1: the reads of the next K-step's first fragments, and the loads of the other half
+  // The parts of the ring go out in order, each into the slot of the part SLOTS ahead of it.  A workgroup goes through its
+  // tiles without draining the ring: the loads change to the next tile two K-steps ahead of the MFMAs (every tile has at
+  // least two K-steps, of zeros past its last), past the last tile they are of zeros.  The order stays as it is written
   // (sched_barrier, and the accumulators pinned ahead of branches).
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  using I3 = std::integral_constant<int, 3>;
-  using Out0 = std::integral_constant<int, TL::kOut0>;
-  using Out1 = std::integral_constant<int, TL::kOut1>;
-  using Out2 = std::integral_constant<int, TL::kOut2>;
-  constexpr int kFill = SLOTS - TL::kOut0 - TL::kOut1 - TL::kOut2;  // parts ahead of the first trip's
+  constexpr int kMma = TP * TQ, kGroups = TQ / 4, kBar = kGroups * TP;  // MFMAs of a sub-step, of sub-step 1 ahead of the barrier
+  constexpr int kLoads = HALF * L;
+  // load n of the parts FIRST .. behind the trip's first, whose slot is `slot`
+  auto issue_nth = [&](int FIRST, int n, int slot) {
+    const int part = FIRST + n / L;
+    issue(part % PT, n % L, wrap(slot + part % SLOTS * TL::kPart));
+    // (the operand's last part of the K-step)
+    if (n % L == L - 1 && part % PT == TL::kPP - 1) advance(p_from, true);
+    if (n % L == L - 1 && part % PT == PT - 1) advance(q_from, false);
+  };
+  auto pin = [&] {
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) asm volatile("" : "+v"(acc[i][j]));
+  };
+  constexpr int kFill = SLOTS - HALF;  // parts ahead of the first trip's
   int steps = steps_of(now), ks = 0, slot = 0, buf = 0;
   aim_p(now);
   aim_q(now);
   aim_sf(now);
+  aim_shifts(now);
   load_sf(0);
 #pragma unroll
   for (int n = 0; n < kFill; ++n) {
@@ -557,9 +581,10 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   auto part_q = [&](int slot) { return wrap(slot + (TL::kPP + wq / kQw) * TL::kPart); };
   int bp = part_p(0), bq = part_q(0);
 #pragma unroll
-  for (int f = 0; f < TP + TQ; ++f) read(f, bp, bq, 0, 0);
+  for (int i = 0; i < TP; ++i) read_p(i, bp, 0);
+#pragma unroll
+  for (int j = 0; j < TQ; ++j) read_q(j, bq, 0);
   read_sf(0);
-  take_shifts();
   TileAt then{};
   bool stored = false;
   for (;;) {
@@ -572,13 +597,16 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       sources(0);
     }
     take_sf();
-    sub_step(I0{}, std::integral_constant<int, kFill>{}, Out0{}, slot, bp, bq, 1);
-    sub_step(I1{}, std::integral_constant<int, kFill + TL::kOut0>{}, Out1{}, slot, bp, bq, 2);
-    sub_step(I2{}, std::integral_constant<int, kFill + TL::kOut0 + TL::kOut1>{}, Out2{}, slot, bp, bq, 3);
-#pragma unroll
-    for (int i = 0; i < TP; ++i)
-#pragma unroll
-      for (int j = 0; j < TQ; ++j) asm volatile("" : "+v"(acc[i][j]));
+    each<0, kMma>([&](auto at) {
+      constexpr int m = decltype(at)::value;
+      mma(I0{}, at);
+      if (m < TP) read_p(m, bp, 1);
+      if (m % TP == TP - 1) read_q(m / TP, bq, 1);
+      if (m % (kMma / kLoads) == kMma / kLoads / 2) issue_nth(kFill, m / (kMma / kLoads), slot);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    each<0, kBar>([&](auto at) { mma(I1{}, at); });
+    pin();
     // (the stores of a tile that has just ended lie ahead of this trip's loads and may stay under way)
     if (stored && TL::kAhead == HALF)
       __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L + kStores));
@@ -590,10 +618,20 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       if constexpr (TL::kAhead != HALF) aim_q(then);
       aim_sf(then);
     }
+    // (the scales that are read next are the next tile's)
+    if (ODD && ks == steps - 1) aim_shifts(then);
     load_sf(buf);
-    read_sf(buf ^ 1);
     bp = part_p(next), bq = part_q(next);
-    sub_step(I3{}, std::integral_constant<int, SLOTS>{}, std::integral_constant<int, HALF>{}, slot, bp, bq, 0);
+    each<kBar, kMma>([&](auto at) {
+      constexpr int m = decltype(at)::value, n = m - kBar, kEvery = (kMma - kBar) / kLoads;
+      mma(I1{}, at);
+      if (n < TP) read_p(n, bp, 0);
+      if (n >= TP && n < TP + kGroups) read_q(n - TP, bq, 0);
+      if (m % TP == TP - 1) read_q(m / TP, bq, 0);
+      if (n % kEvery == kEvery / 2 && n / kEvery < kLoads) issue_nth(SLOTS, n / kEvery, slot);
+      if (n == TP + kGroups) read_sf(buf ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+    });
     sources(p_k);
     slot = next;
     buf ^= 1;
@@ -604,8 +642,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       now = then;
       steps = steps_of(now);
       ks = 0;
+      sf_k = 0;
       clear();
-      take_shifts();
     }
   }
   __builtin_amdgcn_s_waitcnt(0);  // the loads of zeros land before the workgroup's LDS is another's
@@ -668,7 +706,11 @@ GroupedParams common(const GroupedArgs& a) {
 
 template <Op O, bool F32>
 hipError_t launch_rows(GroupedParams& p, hipStream_t s) {
-  return launch_tile<O, 256, 256, 4, 2, O == Op::MX ? 9 : 10, F32>(p, s);
+  if constexpr (O == Op::MX) {
+    return p.sf_row % 4 ? launch_tile<O, 256, 256, 4, 2, 9, F32, 1>(p, s) : launch_tile<O, 256, 256, 4, 2, 9, F32>(p, s);
+  } else {
+    return launch_tile<O, 256, 256, 4, 2, 10, F32>(p, s);
+  }
 }
 
 template <bool F32, int WHERE>
