@@ -60,6 +60,7 @@ struct GroupedParams {
   int out_pair;          // rows go to src_info[r]
   int accumulate;
   int p_tiles, q_tiles;  // q_tiles: WGRAD only
+  uint32_t group_inverse;  // floor(2^32 / (8 p_tiles))
 };
 
 // Direct-to-LDS loads: lane l's 16 (12) bytes land at l + 16 l; what lies out of the resource's bounds is zeros.
@@ -106,6 +107,12 @@ MOE_DEV int wave_scan(int v) {  // inclusive
 
 // start[e], made safe against a plan that is none.
 MOE_DEV int row_at(const GroupedParams& p, int e) { return min(max(p.start[e], 0), p.npairs); }
+
+// n / d, with inverse = floor(2^32 / d) for d > 1: at most one too small.
+MOE_DEV int quotient(int n, int d, uint32_t inverse) {
+  const int q = d == 1 ? n : (int)__umulhi((uint32_t)n, inverse);
+  return q + (n - q * d >= d ? 1 : 0);
+}
 
 struct TileAt {
   bool ok;
@@ -174,15 +181,20 @@ struct Walk {
       within = at - (__builtin_amdgcn_readlane(upto, l) - q_tiles * p.p_tiles);
     }
     at += step;
-    const int group = within / (GQ * p.p_tiles), q0 = group * GQ, size = min(GQ, q_tiles - q0);
+    within = scalar(within);
+    const int group = quotient(within, GQ * p.p_tiles, p.group_inverse), q0 = group * GQ, size = min(GQ, q_tiles - q0);
     const int in = within - group * GQ * p.p_tiles;
-    t.p = in / size;
+    // (ceil(2^32 / size): exact for numbers below 2^29)
+    static_assert(GQ == 8, "the sizes below");
+    const uint32_t inverse = size == 8 ? 0x20000000u : size == 7 ? 0x24924925u : size == 6 ? 0x2AAAAAABu : size == 5 ? 0x33333334u
+                             : size == 4 ? 0x40000000u : size == 3 ? 0x55555556u : 0x80000000u;
+    t.p = size == 1 ? in : (int)__umulhi((uint32_t)in, inverse);
     t.q = q0 + in - t.p * size;
-    t.expert = __builtin_amdgcn_readfirstlane(t.expert);
-    t.lo = __builtin_amdgcn_readfirstlane(t.lo);
-    t.hi = __builtin_amdgcn_readfirstlane(t.hi);
-    t.p = __builtin_amdgcn_readfirstlane(t.p);
-    t.q = __builtin_amdgcn_readfirstlane(t.q);
+    t.expert = scalar(t.expert);
+    t.lo = scalar(t.lo);
+    t.hi = scalar(t.hi);
+    t.p = scalar(t.p);
+    t.q = scalar(t.q);
     return t;
   }
 };
@@ -249,37 +261,46 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   walk.begin(p);
   TileAt now = walk.next(p);  // the tile of the MFMAs; the loads run up to two K-steps ahead, into `then`
   if (!now.ok) return;
-  auto steps_of = [&](const TileAt& t) { return max(2, ((WG ? t.hi - t.lo : p.K) + BK - 1) / BK); };
+  // (read in every trip: not to be loaded there again)
+  const int total = scalar(p.K), sf_row = scalar(p.sf_row);
+  auto steps_of = [&](const TileAt& t) { return max(2, ((WG ? t.hi - t.lo : total) + BK - 1) / BK); };
 
   // ---------------------------------------------------------------- what each lane loads
   // Load i of a part: rows (i * waves + wave) * 8 + lane / 8 of 128 bytes, or (T) summed rows (i * waves + wave) * 4 + lane
-  // / 16 of 256 bytes.  Bases are scalar and move by a K-step, a lane's offsets stay.  Rows past the last, of the output or
+  // / 16 of 256 bytes.  Bases are scalar and move by a K-step, a lane's offsets stay until the last one.  Rows past the last, of the output or
   // summed, lie past the resource's end and chunks past K get an offset that does: both load zeros.  (Columns past a T
   // operand's last are the next row's first; what comes of them is not stored.)
   constexpr int kStep8 = TL::kWaves * 8, kStep4 = TL::kWaves * 4;
   const int chunk8 = chunk_at<MX>(lane & 7, wave * 8 + (lane >> 3));
-  uint32_t p_off = 0, q_off[TL::kPQ][L] = {};  // (Q through src_info, but for WGRAD: of each row; else the first)
+  constexpr bool kLookP = WG && (WHERE & 1), kLookQ = WG && (WHERE & 2);
+  uint32_t p_off[TL::kPP][L], q_off[TL::kPQ][L];
   i32x4 p_from{}, q_from{};      // the operands' resources at the next load's K-step
   int p_k = 0, q_k = 0;          // summed elements up to it
-  int p_rows = 0, q_rows = 0;    // rows of the output from the tile's first on (not T)
   int load_lo = 0, load_hi = 0;  // WGRAD: the rows of the loads' tile
-  constexpr bool kLookP = WG && (WHERE & 1), kLookQ = WG && (WHERE & 2);
-  // the bytes from a resource's base on that are the operand's: T operands: of a K-step, else of the tile's rows
-  uint32_t p_skip = 0, q_skip = 0;  // T operands: the tile's first column
-  auto extent = [&](bool isP) {
-    const int k0 = isP ? p_k : q_k, rows = min(isP ? p_rows : q_rows, isP ? BP : BQ);
-    const uint32_t ld = isP ? p.p_ld : p.q_ld;
-    if (isP ? kLookP : kLookQ) return kAll;
-    if (isP ? kTP : kTQ) {
-      const int left = (WG ? load_hi - load_lo : p.K) - k0;
-      return left > 0 ? (uint32_t)min(left, 64) * ld - (isP ? p_skip : q_skip) : 0u;
-    }
-    return (uint32_t)rows * ld;
+  uint32_t p_skip = 0, q_skip = 0;  // T operands: bytes ahead of the tile's first column
+  // the bytes of a T operand from its resource's base on: of a K-step
+  auto t_extent = [&](bool isP) {
+    const int left = (WG ? load_hi - load_lo : total) - (isP ? p_k : q_k);
+    return left > 0 ? (uint32_t)min(left, 64) * (isP ? p.p_ld : p.q_ld) - (isP ? p_skip : q_skip) : 0u;
   };
-  // the offset of a T operand's first row and column of a part's first load
+  // the offset of a T operand's row and column of a part's first load
   auto t_off = [&](uint32_t ld) {
     const int l = fresh(lane), row = wave * 4 + (l >> 4);
     return (uint32_t)row * ld + ((((l & 15) >> 1) ^ trx(row)) << 5) + (l & 1) * 16;
+  };
+  // src_info of this lane's rows r0 + lane / (64 / N), by scalar loads: a vector load would have to wait for the loads into
+  // LDS behind it
+  auto source = [&](auto lanes, int r0, int last) {
+    constexpr int N = decltype(lanes)::value;
+    typedef const __attribute__((address_space(4))) int* Uniform;
+    int v[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = ((Uniform)(uintptr_t)p.src_info)[max(min(r0 + j, last), 0)];
+    const int at = fresh(lane) / (64 / N);
+    int r = v[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) r = at == j ? v[j] : r;
+    return r;
   };
   auto aim_p = [&](const TileAt& t) {
     p_k = 0;
@@ -290,81 +311,100 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       base += kLookP ? 0 : (long long)t.lo * p.p_ld;
     } else {
       base += t.expert * p.p_expert;
-      p_rows = p.p_cols - t.p * BP;
     }
-    const int l = fresh(lane);
-    p_off = kLookP ? t_off(0) : kTP ? t_off(p.p_ld) : (uint32_t)(wave * 8 + (l >> 3)) * p.p_ld + chunk8 * 16;
-    p_from = resource(base, t.ok ? extent(true) : 0u);
+    const uint32_t off = kTP ? t_off(p.p_ld) : (uint32_t)(wave * 8 + (fresh(lane) >> 3)) * p.p_ld + chunk8 * 16;
+#pragma unroll
+    for (int j = 0; j < TL::kPP; ++j)
+#pragma unroll
+      for (int i = 0; i < L; ++i) p_off[j][i] = off + (kTP ? j * 256 + i * kStep4 * p.p_ld : (j * 128 + i * kStep8) * p.p_ld);
+    p_from = resource(base, !t.ok ? 0u : kLookP ? kAll : kTP ? t_extent(true) : (uint32_t)min(p.p_cols - t.p * BP, BP) * p.p_ld);
   };
   auto aim_q = [&](const TileAt& t) {
     q_k = 0;
     q_skip = t.q * BQ * 2;
     const uint8_t* base = p.Q + (kTQ ? (long long)q_skip : 0);
     const bool look = !WG && p.q_place.gathered;
-    if constexpr (WG) {
+    const int rows = t.hi - t.lo - t.q * BQ;
+    if constexpr (WG)
       base += kLookQ ? 0 : (long long)t.lo * p.q_ld;
-    } else {
-      q_rows = t.hi - t.lo - t.q * BQ;
-      if (!look) base += ((long long)t.lo + t.q * BQ) * p.q_ld;
-    }
-    const int l = fresh(lane);
-    q_off[0][0] = kLookQ ? t_off(0) : kTQ ? t_off(p.q_ld) : (uint32_t)(wave * 8 + (l >> 3)) * p.q_ld + chunk8 * 16;
-    if constexpr (!WG) {
+    else if (!look)
+      base += ((long long)t.lo + t.q * BQ) * p.q_ld;
+    const uint32_t off = kTQ ? t_off(p.q_ld) : (uint32_t)(wave * 8 + (fresh(lane) >> 3)) * p.q_ld + chunk8 * 16;
 #pragma unroll
-      for (int j = 0; j < TL::kPQ; ++j)
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-          const int r = j * 128 + i * kStep8 + wave * 8 + (l >> 3);
-          q_off[j][i] = q_off[0][0] + (uint32_t)(j * 128 + i * kStep8) * p.q_ld;
-          if (look && t.ok)
-            q_off[j][i] = (uint32_t)p.q_place.of(p.src_info[t.lo + t.q * BQ + max(min(r, q_rows - 1), 0)]) * p.q_ld + chunk8 * 16;
-        }
-    }
-    q_from = resource(base, !t.ok ? 0u : look ? kAll : extent(false));
-  };
-  // WGRAD: src_info of this lane's summed rows, by scalar loads (a vector load would have to wait for the loads into LDS
-  // behind it)
-  int src[L] = {};
-  auto sources = [&](int k0) {
-    if constexpr (WG && WHERE != 0) {
-      typedef const __attribute__((address_space(4))) int* Uniform;
+    for (int j = 0; j < TL::kPQ; ++j)
 #pragma unroll
       for (int i = 0; i < L; ++i) {
-        int v[4];
+        q_off[j][i] = off + (kTQ ? j * 256 + i * kStep4 * p.q_ld : (j * 128 + i * kStep8) * p.q_ld);
+        if (look && t.ok) {
+          const int first = t.lo + t.q * BQ;
+          q_off[j][i] = (uint32_t)p.q_place.of(source(std::integral_constant<int, 8>{}, first + j * 128 + i * kStep8 + wave * 8,
+                                                      first + rows - 1)) * p.q_ld + chunk8 * 16;
+        }
+      }
+    q_from = resource(base, !t.ok ? 0u : kLookQ || look ? kAll : kTQ ? t_extent(false) : (uint32_t)min(rows, BQ) * p.q_ld);
+  };
+  // WGRAD: the offsets of the next K-step's rows, from src_info four K-steps at a time (read also where only one operand's
+  // rows are found there)
+  int src[4][L] = {}, have = 0;
+  auto sources = [&](bool first) {
+    if constexpr (kLookP || kLookQ) {
+      if (first || have == 0) {
+        have = 4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[j] = ((Uniform)(uintptr_t)p.src_info)[max(min(load_lo + k0 + i * kStep4 + wave * 4 + j, load_hi - 1), 0)];
-        src[i] = lane < 32 ? (lane < 16 ? v[0] : v[1]) : lane < 48 ? v[2] : v[3];
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < L; ++i)
+            src[u][i] = source(std::integral_constant<int, 4>{}, load_lo + p_k + u * BK + i * kStep4 + wave * 4, load_hi - 1);
+      }
+      --have;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const bool live = p_k + i * kStep4 + wave * 4 + g < load_hi - load_lo;
+        const uint32_t p_row = live ? (uint32_t)p.p_place.of(src[0][i]) * p.p_ld + t_off(0) : kNone;
+        const uint32_t q_row = live ? (uint32_t)p.q_place.of(src[0][i]) * p.q_ld + t_off(0) : kNone;
+#pragma unroll
+        for (int j = 0; j < TL::kPP; ++j) {
+          if (kLookP) p_off[j][i] = live ? p_row + j * 256 : kNone;
+          if (kLookQ) q_off[j][i] = live ? q_row + j * 256 : kNone;
+        }
+#pragma unroll
+        for (int u = 0; u < 3; ++u) src[u][i] = src[u + 1][i];
       }
     }
   };
   // load i of part J (P's first) of the K-step that its operand has come to, into a slot (its offset in LDS)
   const uint32_t lds0 = lds_address(lds);
-  auto issue = [&](int J, int i, int slot) {
-    const bool isP = J < TL::kPP, tr = isP ? kTP : kTQ;
-    const int j = isP ? J : J - TL::kPP, k0 = isP ? p_k : q_k;
-    const uint32_t ld = isP ? p.p_ld : p.q_ld;
-    uint32_t v = isP ? p_off : q_off[WG ? 0 : j][WG ? 0 : i];
-    if (isP ? kLookP : kLookQ) {
-      v += (uint32_t)(isP ? p.p_place : p.q_place).of(src[i]) * ld + j * 256;
-      v = i * kStep4 + wave * 4 + g < load_hi - load_lo - k0 ? v : kNone;
-    } else if (tr) {
-      v += i * kStep4 * ld + j * 256;
-    } else {
-      if (isP) v += (j * 128 + i * kStep8) * ld;
-      v = k0 + chunk8 * (MX ? 32 : 8) < p.K ? v : kNone;
-    }
-    lds_copy16(isP ? p_from : q_from, v, lds0 + slot + (i * TL::kWaves + wave) * 1024);
+  auto issue = [&](int J, int i, uint32_t slot) {
+    const bool isP = J < TL::kPP;
+    lds_copy16(isP ? p_from : q_from, isP ? p_off[isP ? J : 0][i] : q_off[isP ? 0 : J - TL::kPP][i],
+               slot + (i * TL::kWaves + wave) * 1024);
   };
-  // an operand's next K-step
+  // an operand's next K-step; the last one's masks (what lies past a tile's rows does so at every K-step)
   auto advance = [&](i32x4& from, bool isP) {
-    const bool tr = isP ? kTP : kTQ;
     (isP ? p_k : q_k) += BK;
     if (isP ? kLookP : kLookQ) return;
-    const uint64_t base = ((uint64_t)(uint32_t)from[1] << 32 | (uint32_t)from[0]) + (tr ? 64 * (isP ? p.p_ld : p.q_ld) : 128);
-    const uint32_t had = (uint32_t)from[2];
-    // (rows of 128 bytes: the resource ends where it ended, or, through src_info, nowhere)
-    from = resource((const void*)base, tr ? (had ? extent(isP) : 0u) : had == kAll || had == 0 ? had : had > 128 ? had - 128 : 0u);
+    const uint32_t by = (isP ? kTP : kTQ) ? 64 * (isP ? p.p_ld : p.q_ld) : 128;
+    const uint32_t lo = (uint32_t)from[0] + by;
+    from[1] = scalar(from[1] + (lo < by ? 1 : 0));
+    from[0] = scalar((int)lo);
+  };
+  auto tail = [&](bool isP) {
+    const bool tr = isP ? kTP : kTQ;
+    const int k0 = isP ? p_k : q_k, K = WG ? load_hi - load_lo : total;
+    if ((isP ? kLookP : kLookQ) || k0 + BK <= K) return;
+    if (tr) {
+      i32x4& from = isP ? p_from : q_from;
+      if (from[2]) from[2] = scalar((int)t_extent(isP));
+    } else {
+      const bool none = k0 + chunk8 * (MX ? 32 : 8) >= K;
+#pragma unroll
+      for (int j = 0; j < TL::kPP; ++j)
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          if (isP && none) p_off[j][i] = kNone;
+          if (!isP && none) q_off[j][i] = kNone;
+        }
+    }
   };
 
   // MXFP4: the words that hold a row's 8 scales of a K-step, waves 0 .. BP / 64 - 1 P's rows, the others Q's.  A row's scales
@@ -389,17 +429,17 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       const uint8_t* all = isp ? p.P_sf : p.Q_sf;
       // from the tile's first row on (gathered rows: from the tensor's first, which is below 4 GiB)
       long long first = isp ? sf_row_p(t, 0) : p.q_place.gathered ? 0 : sf_row_q(t, 0);
-      const long long begin = first * p.sf_row & ~3LL, end = (isp ? p.p_sf_bytes : p.q_sf_bytes) + 3 & ~3LL;
+      const long long begin = first * sf_row & ~3LL, end = (isp ? p.p_sf_bytes : p.q_sf_bytes) + 3 & ~3LL;
       const long long row = isp ? sf_row_p(t, tid) : sf_row_q(t, tid - BP);
-      sf_off = (uint32_t)((row * p.sf_row & ~3LL) - begin);
+      sf_off = (uint32_t)((row * sf_row & ~3LL) - begin);
       sf_from = resource(all + begin, t.ok ? (uint32_t)min(end - begin, (long long)kAll) : 0u);
     }
   };
   auto aim_shifts = [&](const TileAt& t) {
     if constexpr (ODD) {
-      p_shift = (uint32_t)((t.expert * (long long)p.n_rows + t.p * BP + r16) * p.sf_row) & 3;
+      p_shift = (uint32_t)((t.expert * (long long)p.n_rows + t.p * BP + r16) * sf_row) & 3;
 #pragma unroll
-      for (int j = 0; j < TQ; ++j) q_shift[j] = (uint32_t)(sf_row_q(t, (wq * TQ + j) * 16 + r16) * p.sf_row) & 3;
+      for (int j = 0; j < TQ; ++j) q_shift[j] = (uint32_t)(sf_row_q(t, (wq * TQ + j) * 16 + r16) * sf_row) & 3;
     }
   };
   auto load_sf = [&](int buf) {
@@ -446,7 +486,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   // two tiles' in a word
   auto take_sf = [&] {
     if constexpr (MX) {
-      const int left = p.sf_row - sf_k - 2 * g;
+      const int left = sf_row - sf_k - 2 * g;
       const uint32_t keep = left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0x00FF00FFu : 0u;
 #pragma unroll
       for (int i = 0; i < TP; i += 2) sp[i / 2] = (sp_next[i] | sp_next[i + 1] << 16) & keep;
@@ -544,10 +584,10 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   using I1 = std::integral_constant<int, 1>;
   constexpr int kMma = TP * TQ, kGroups = TQ / 4, kBar = kGroups * TP;  // MFMAs of a sub-step, of sub-step 1 ahead of the barrier
   constexpr int kLoads = HALF * L;
-  // load n of the parts FIRST .. behind the trip's first, whose slot is `slot`
-  auto issue_nth = [&](int FIRST, int n, int slot) {
+  // load n of the parts FIRST .. behind the trip's first, whose slots are at[]
+  auto issue_nth = [&](int FIRST, int n, const uint32_t (&at)[HALF]) {
     const int part = FIRST + n / L;
-    issue(part % PT, n % L, wrap(slot + part % SLOTS * TL::kPart));
+    issue(part % PT, n % L, at[n / L]);
     // (the operand's last part of the K-step)
     if (n % L == L - 1 && part % PT == TL::kPP - 1) advance(p_from, true);
     if (n % L == L - 1 && part % PT == PT - 1) advance(q_from, false);
@@ -567,14 +607,15 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   load_sf(0);
 #pragma unroll
   for (int n = 0; n < kFill; ++n) {
-    if (n % PT == 0) sources(n / PT * BK);
+    if (n % PT == 0) sources(n == 0), tail(true);
+    if (n % PT == TL::kPP) tail(false);
 #pragma unroll
-    for (int i = 0; i < L; ++i) issue(n % PT, i, n * TL::kPart);
+    for (int i = 0; i < L; ++i) issue(n % PT, i, lds0 + n * TL::kPart);
     if (n % PT == TL::kPP - 1) advance(p_from, true);
     if (n % PT == PT - 1) advance(q_from, false);
   }
   load_sf(1);
-  sources(2 * BK);
+  sources(false);
   __builtin_amdgcn_s_waitcnt(0);
   __builtin_amdgcn_s_barrier();
   auto part_p = [&](int slot) { return wrap(slot + wp / kPw * TL::kPart); };
@@ -594,7 +635,15 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       then = walk.next(p);
       aim_p(then);
       if constexpr (TL::kAhead == HALF) aim_q(then);
-      sources(0);
+      sources(true);
+    }
+    tail(true);
+    if constexpr (TL::kAhead == HALF) tail(false);
+    uint32_t early[HALF], late[HALF];  // slots of the parts that go out ahead of the barrier and behind it
+#pragma unroll
+    for (int j = 0; j < HALF; ++j) {
+      early[j] = scalar((int)(lds0 + wrap(slot + (kFill + j) * TL::kPart)));
+      late[j] = scalar((int)(lds0 + slot + j * TL::kPart - (slot + j * TL::kPart >= kRing ? kRing : 0)));
     }
     take_sf();
     each<0, kMma>([&](auto at) {
@@ -602,7 +651,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       mma(I0{}, at);
       if (m < TP) read_p(m, bp, 1);
       if (m % TP == TP - 1) read_q(m / TP, bq, 1);
-      if (m % (kMma / kLoads) == kMma / kLoads / 2) issue_nth(kFill, m / (kMma / kLoads), slot);
+      if (m % (kMma / kLoads) == kMma / kLoads / 2) issue_nth(kFill, m / (kMma / kLoads), early);
       __builtin_amdgcn_sched_barrier(0);
     });
     each<0, kBar>([&](auto at) { mma(I1{}, at); });
@@ -618,6 +667,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       if constexpr (TL::kAhead != HALF) aim_q(then);
       aim_sf(then);
     }
+    if constexpr (TL::kAhead != HALF) tail(false);
     // (the scales that are read next are the next tile's)
     if (ODD && ks == steps - 1) aim_shifts(then);
     load_sf(buf);
@@ -628,11 +678,11 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       if (n < TP) read_p(n, bp, 0);
       if (n >= TP && n < TP + kGroups) read_q(n - TP, bq, 0);
       if (m % TP == TP - 1) read_q(m / TP, bq, 0);
-      if (n % kEvery == kEvery / 2 && n / kEvery < kLoads) issue_nth(SLOTS, n / kEvery, slot);
+      if (n % kEvery == kEvery / 2 && n / kEvery < kLoads) issue_nth(SLOTS, n / kEvery, late);
       if (n == TP + kGroups) read_sf(buf ^ 1);
       __builtin_amdgcn_sched_barrier(0);
     });
-    sources(p_k);
+    sources(false);
     slot = next;
     buf ^= 1;
     stored = ++ks == steps;
@@ -665,6 +715,7 @@ int device_cus() {
 template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS, bool F32, int WHERE = 0>
 hipError_t launch_tile(GroupedParams& p, hipStream_t s) {
   p.p_tiles = (p.p_cols + BP - 1) / BP;
+  p.group_inverse = (uint32_t)((1ull << 32) / (8 * p.p_tiles));
   long long tiles;
   if (O == Op::WGRAD) {
     p.q_tiles = (p.q_cols + BQ - 1) / BQ;
