@@ -286,7 +286,7 @@ size_t rows_of(const moe_config& c, int T, int32_t order) {
 }
 // Tensors whose rows are found through src_info are addressed by 32-bit offsets.
 bool placed(const moe_config& c, int T, int32_t order, size_t row_bytes) {
-  return order == MOE_ROWS_PLAN || rows_of(c, T, order) * row_bytes < 0xFFFFFFF0u;
+  return order == MOE_ROWS_PLAN || rows_of(c, T, order) * row_bytes < 0xFFFFF000u;
 }
 bool any_overlap(const Span& a, std::initializer_list<Span> others) {
   for (const Span& b : others)

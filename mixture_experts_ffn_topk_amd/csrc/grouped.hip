@@ -33,9 +33,9 @@ struct Place {
   int whole;         // -1: the pair itself, else 0
   int gathered;
   int places;        // the tensor's rows: a plan that is none reads nothing past them
-  MOE_DEV int of(int src) const {
-    return min(max((int)__umulhi((uint32_t)src, inverse) + (src & whole), 0), places - 1);
-  }
+  MOE_DEV int pair(int src) const { return (int)__umulhi((uint32_t)src, inverse) + (src & whole); }
+  MOE_DEV int within(int at) const { return min(max(at, 0), places - 1); }
+  MOE_DEV int of(int src) const { return within(pair(src)); }
 };
 
 struct GroupedParams {
@@ -66,8 +66,9 @@ struct GroupedParams {
 // Direct-to-LDS loads: lane l's 16 (12) bytes land at l + 16 l; what lies out of the resource's bounds is zeros.
 // Written so that the compiler does not see stores to LDS: it lets no ds_read_b64_tr pass one in flight.  The kernel's own
 // waits order the two.
-constexpr uint32_t kNone = 0xFFFFFFFFu, kAll = 0xFFFFFFF0u;  // an offset out of any resource, the largest resource
-// (The offsets are the lanes' own: a scalar one may wrap the check against the resource's end.)
+constexpr uint32_t kAll = 0xFFFFF000u, kNone = kAll;  // the largest resource, an offset out of it (with what is added)
+// (The offsets are the lanes' own: a scalar one may wrap the check against the resource's end, and the instruction's own
+// would move the place in LDS with it.)
 MOE_DEV void lds_copy16(i32x4 rsrc, uint32_t voff, uint32_t l) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(l), "v"(voff), "s"(rsrc)
                : "memory");
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   constexpr int kStep8 = TL::kWaves * 8, kStep4 = TL::kWaves * 4;
   const int chunk8 = chunk_at<MX>(lane & 7, wave * 8 + (lane >> 3));
   constexpr bool kLookP = WG && (WHERE & 1), kLookQ = WG && (WHERE & 2);
-  uint32_t p_off[TL::kPP][L], q_off[TL::kPQ][L];
+  uint32_t p_off[kTP ? 1 : TL::kPP][L], q_off[kTQ ? 1 : TL::kPQ][L];  // (T: of part 0, the others lie 256 bytes on)
   i32x4 p_from{}, q_from{};      // the operands' resources at the next load's K-step
   int p_k = 0, q_k = 0;          // summed elements up to it
   int load_lo = 0, load_hi = 0;  // WGRAD: the rows of the loads' tile
@@ -314,9 +315,9 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     }
     const uint32_t off = kTP ? t_off(p.p_ld) : (uint32_t)(wave * 8 + (fresh(lane) >> 3)) * p.p_ld + chunk8 * 16;
 #pragma unroll
-    for (int j = 0; j < TL::kPP; ++j)
+    for (int j = 0; j < (kTP ? 1 : TL::kPP); ++j)
 #pragma unroll
-      for (int i = 0; i < L; ++i) p_off[j][i] = off + (kTP ? j * 256 + i * kStep4 * p.p_ld : (j * 128 + i * kStep8) * p.p_ld);
+      for (int i = 0; i < L; ++i) p_off[j][i] = off + (kTP ? i * kStep4 : j * 128 + i * kStep8) * p.p_ld;
     p_from = resource(base, !t.ok ? 0u : kLookP ? kAll : kTP ? t_extent(true) : (uint32_t)min(p.p_cols - t.p * BP, BP) * p.p_ld);
   };
   auto aim_q = [&](const TileAt& t) {
@@ -331,10 +332,10 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       base += ((long long)t.lo + t.q * BQ) * p.q_ld;
     const uint32_t off = kTQ ? t_off(p.q_ld) : (uint32_t)(wave * 8 + (fresh(lane) >> 3)) * p.q_ld + chunk8 * 16;
 #pragma unroll
-    for (int j = 0; j < TL::kPQ; ++j)
+    for (int j = 0; j < (kTQ ? 1 : TL::kPQ); ++j)
 #pragma unroll
       for (int i = 0; i < L; ++i) {
-        q_off[j][i] = off + (kTQ ? j * 256 + i * kStep4 * p.q_ld : (j * 128 + i * kStep8) * p.q_ld);
+        q_off[j][i] = off + (kTQ ? i * kStep4 : j * 128 + i * kStep8) * p.q_ld;
         if (look && t.ok) {
           const int first = t.lo + t.q * BQ;
           q_off[j][i] = (uint32_t)p.q_place.of(source(std::integral_constant<int, 8>{}, first + j * 128 + i * kStep8 + wave * 8,
@@ -343,41 +344,68 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       }
     q_from = resource(base, !t.ok ? 0u : kLookQ || look ? kAll : kTQ ? t_extent(false) : (uint32_t)min(rows, BQ) * p.q_ld);
   };
-  // WGRAD: the offsets of the next K-step's rows, from src_info four K-steps at a time (read also where only one operand's
-  // rows are found there)
-  int src[4][L] = {}, have = 0;
-  auto sources = [&](bool first) {
+  // WGRAD: the offsets of a K-step's rows, from src_info four K-steps at a time (read also where only one operand's rows are
+  // found there); in pieces, which go between MFMAs
+  int src[4][L] = {}, have = 0, p_row[L] = {}, q_row[L] = {};
+  uint32_t p_next[L] = {}, q_next[L] = {}, t_column = 0;
+  if constexpr (kLookP || kLookQ) t_column = t_off(0);
+  auto sources = [&](int k0) {  // of the four K-steps from row k0 on
     if constexpr (kLookP || kLookQ) {
-      if (first || have == 0) {
-        have = 4;
+      have = 4;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int i = 0; i < L; ++i)
-            src[u][i] = source(std::integral_constant<int, 4>{}, load_lo + p_k + u * BK + i * kStep4 + wave * 4, load_hi - 1);
-      }
-      --have;
+        for (int i = 0; i < L; ++i)
+          src[u][i] = source(std::integral_constant<int, 4>{}, load_lo + k0 + u * BK + i * kStep4 + wave * 4, load_hi - 1);
+    }
+  };
+  constexpr int kPieces = kLookP || kLookQ ? 6 : 0;
+  auto piece = [&](int n, int k0) {  // of the offsets of the K-step at row k0
 #pragma unroll
-      for (int i = 0; i < L; ++i) {
-        const bool live = p_k + i * kStep4 + wave * 4 + g < load_hi - load_lo;
-        const uint32_t p_row = live ? (uint32_t)p.p_place.of(src[0][i]) * p.p_ld + t_off(0) : kNone;
-        const uint32_t q_row = live ? (uint32_t)p.q_place.of(src[0][i]) * p.q_ld + t_off(0) : kNone;
-#pragma unroll
-        for (int j = 0; j < TL::kPP; ++j) {
-          if (kLookP) p_off[j][i] = live ? p_row + j * 256 : kNone;
-          if (kLookQ) q_off[j][i] = live ? q_row + j * 256 : kNone;
-        }
-#pragma unroll
-        for (int u = 0; u < 3; ++u) src[u][i] = src[u + 1][i];
+    for (int i = 0; i < L; ++i) {
+      if (n == 0) {
+        if constexpr (kLookP) p_row[i] = p.p_place.pair(src[0][i]);
+        if constexpr (kLookQ) q_row[i] = p.q_place.pair(src[0][i]);
+      } else if (n == 1) {
+        if constexpr (kLookP) p_row[i] = p.p_place.within(p_row[i]);
+        if constexpr (kLookQ) q_row[i] = p.q_place.within(q_row[i]);
+      } else if (n == 2) {
+        if constexpr (kLookP) p_next[i] = (uint32_t)p_row[i] * p.p_ld;
+      } else if (n == 3) {
+        if constexpr (kLookQ) q_next[i] = (uint32_t)q_row[i] * p.q_ld;
+      } else if (n == 4) {
+        const bool live = k0 + i * kStep4 + wave * 4 + g < load_hi - load_lo;
+        if constexpr (kLookP) p_next[i] = live ? p_next[i] + t_column : kNone;
+        if constexpr (kLookQ) q_next[i] = live ? q_next[i] + t_column : kNone;
+      } else {
+        src[0][i] = src[1][i], src[1][i] = src[2][i], src[2][i] = src[3][i];
       }
     }
+    if (n == 5) --have;
+  };
+  auto take_offsets = [&] {
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      if constexpr (kLookP) p_off[0][i] = p_next[i];
+      if constexpr (kLookQ) q_off[0][i] = q_next[i];
+    }
+  };
+  auto offsets_at = [&](int k0) {
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) piece(n, k0);
+    take_offsets();
   };
   // load i of part J (P's first) of the K-step that its operand has come to, into a slot (its offset in LDS)
   const uint32_t lds0 = lds_address(lds);
-  auto issue = [&](int J, int i, uint32_t slot) {
-    const bool isP = J < TL::kPP;
-    lds_copy16(isP ? p_from : q_from, isP ? p_off[isP ? J : 0][i] : q_off[isP ? 0 : J - TL::kPP][i],
-               slot + (i * TL::kWaves + wave) * 1024);
+  auto issue = [&](auto part, int i, uint32_t slot) {
+    constexpr int J = decltype(part)::value;
+    constexpr bool isP = J < TL::kPP, tr = isP ? kTP : kTQ;
+    constexpr int j = isP ? J : J - TL::kPP;
+    const uint32_t l = slot + (i * TL::kWaves + wave) * 1024;
+    if constexpr (isP)
+      lds_copy16(p_from, p_off[tr ? 0 : j][i] + (tr ? j * 256 : 0), l);
+    else
+      lds_copy16(q_from, q_off[tr ? 0 : j][i] + (tr ? j * 256 : 0), l);
   };
   // an operand's next K-step; the last one's masks (what lies past a tile's rows does so at every K-step)
   auto advance = [&](i32x4& from, bool isP) {
@@ -398,12 +426,13 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     } else {
       const bool none = k0 + chunk8 * (MX ? 32 : 8) >= K;
 #pragma unroll
-      for (int j = 0; j < TL::kPP; ++j)
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-          if (isP && none) p_off[j][i] = kNone;
-          if (!isP && none) q_off[j][i] = kNone;
+      for (int i = 0; i < L; ++i) {
+        if (isP) {
+          for (auto& off : p_off) off[i] = none ? kNone : off[i];
+        } else {
+          for (auto& off : q_off) off[i] = none ? kNone : off[i];
         }
+      }
     }
   };
 
@@ -585,9 +614,9 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   constexpr int kMma = TP * TQ, kGroups = TQ / 4, kBar = kGroups * TP;  // MFMAs of a sub-step, of sub-step 1 ahead of the barrier
   constexpr int kLoads = HALF * L;
   // load n of the parts FIRST .. behind the trip's first, whose slots are at[]
-  auto issue_nth = [&](int FIRST, int n, const uint32_t (&at)[HALF]) {
-    const int part = FIRST + n / L;
-    issue(part % PT, n % L, at[n / L]);
+  auto issue_nth = [&](auto first, auto nth, const uint32_t (&at)[HALF]) {
+    constexpr int n = decltype(nth)::value, part = decltype(first)::value + n / L;
+    issue(std::integral_constant<int, part % PT>{}, n % L, at[n / L]);
     // (the operand's last part of the K-step)
     if (n % L == L - 1 && part % PT == TL::kPP - 1) advance(p_from, true);
     if (n % L == L - 1 && part % PT == PT - 1) advance(q_from, false);
@@ -605,17 +634,18 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   aim_sf(now);
   aim_shifts(now);
   load_sf(0);
-#pragma unroll
-  for (int n = 0; n < kFill; ++n) {
-    if (n % PT == 0) sources(n == 0), tail(true);
+  each<0, kFill>([&](auto nth) {
+    constexpr int n = decltype(nth)::value;
+    if (n == 0) sources(0);
+    if (n % PT == 0) offsets_at(n / PT * BK), tail(true);
     if (n % PT == TL::kPP) tail(false);
 #pragma unroll
-    for (int i = 0; i < L; ++i) issue(n % PT, i, lds0 + n * TL::kPart);
+    for (int i = 0; i < L; ++i) issue(std::integral_constant<int, n % PT>{}, i, lds0 + n * TL::kPart);
     if (n % PT == TL::kPP - 1) advance(p_from, true);
     if (n % PT == PT - 1) advance(q_from, false);
-  }
+  });
   load_sf(1);
-  sources(false);
+  offsets_at(2 * BK);
   __builtin_amdgcn_s_waitcnt(0);
   __builtin_amdgcn_s_barrier();
   auto part_p = [&](int slot) { return wrap(slot + wp / kPw * TL::kPart); };
@@ -635,7 +665,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       then = walk.next(p);
       aim_p(then);
       if constexpr (TL::kAhead == HALF) aim_q(then);
-      sources(true);
+      sources(0);
+      offsets_at(0);
     }
     tail(true);
     if constexpr (TL::kAhead == HALF) tail(false);
@@ -645,17 +676,21 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       early[j] = scalar((int)(lds0 + wrap(slot + (kFill + j) * TL::kPart)));
       late[j] = scalar((int)(lds0 + slot + j * TL::kPart - (slot + j * TL::kPart >= kRing ? kRing : 0)));
     }
+    const int p_k_next = p_k + BK;  // of the loads of the next trip
     take_sf();
     each<0, kMma>([&](auto at) {
       constexpr int m = decltype(at)::value;
       mma(I0{}, at);
       if (m < TP) read_p(m, bp, 1);
       if (m % TP == TP - 1) read_q(m / TP, bq, 1);
-      if (m % (kMma / kLoads) == kMma / kLoads / 2) issue_nth(kFill, m / (kMma / kLoads), early);
+      if constexpr (m % (kMma / kLoads) == kMma / kLoads / 2)
+        issue_nth(std::integral_constant<int, kFill>{}, std::integral_constant<int, m / (kMma / kLoads)>{}, early);
+      if constexpr (m % 4 == 1 && m / 4 < kPieces) piece(m / 4, p_k_next);
       __builtin_amdgcn_sched_barrier(0);
     });
     each<0, kBar>([&](auto at) { mma(I1{}, at); });
     pin();
+    if ((kLookP || kLookQ) && have == 0) sources(p_k_next + BK);
     // (the stores of a tile that has just ended lie ahead of this trip's loads and may stay under way)
     if (stored && TL::kAhead == HALF)
       __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L + kStores));
@@ -678,11 +713,12 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       if (n < TP) read_p(n, bp, 0);
       if (n >= TP && n < TP + kGroups) read_q(n - TP, bq, 0);
       if (m % TP == TP - 1) read_q(m / TP, bq, 0);
-      if (n % kEvery == kEvery / 2 && n / kEvery < kLoads) issue_nth(SLOTS, n / kEvery, late);
+      if constexpr (n % kEvery == kEvery / 2 && n / kEvery < kLoads)
+        issue_nth(std::integral_constant<int, SLOTS>{}, std::integral_constant<int, n / kEvery>{}, late);
       if (n == TP + kGroups) read_sf(buf ^ 1);
       __builtin_amdgcn_sched_barrier(0);
     });
-    sources(false);
+    take_offsets();
     slot = next;
     buf ^= 1;
     stored = ++ks == steps;
