@@ -344,19 +344,34 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       }
     q_from = resource(base, !t.ok ? 0u : kLookQ || look ? kAll : kTQ ? t_extent(false) : (uint32_t)min(rows, BQ) * p.q_ld);
   };
-  // WGRAD: the offsets of a K-step's rows, from src_info four K-steps at a time (read also where only one operand's rows are
-  // found there); in pieces, which go between MFMAs
-  int src[4][L] = {}, have = 0, p_row[L] = {}, q_row[L] = {};
+  // WGRAD: the offsets of a K-step's rows through src_info (read also where only one operand's rows are found there).  Lane l
+  // of src[v] holds that of this wave's row l % 8 of the tile's K-step 8 v + l / 8: a vector load, which has to wait for the
+  // loads into LDS behind it, for 32 K-steps, and a shuffle for each.  In pieces, which go between MFMAs.
+  constexpr int kSrc = 4;
+  int src[kSrc] = {}, src_k = 0, row[L] = {}, p_row[L] = {}, q_row[L] = {};
   uint32_t p_next[L] = {}, q_next[L] = {}, t_column = 0;
   if constexpr (kLookP || kLookQ) t_column = t_off(0);
-  auto sources = [&](int k0) {  // of the four K-steps from row k0 on
+  auto sources = [&](int k0) {  // of the K-steps from row k0 on
     if constexpr (kLookP || kLookQ) {
-      have = 4;
+      static_assert(L == 2, "8 rows a K-step");
+      const int l = fresh(lane), first = load_lo + k0 + (l >> 3) * BK + (l >> 2 & 1) * kStep4 + wave * 4 + (l & 3);
+      src_k = 0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int v = 0; v < kSrc; ++v) src[v] = p.src_info[max(min(first + v * 8 * BK, load_hi - 1), 0)];
 #pragma unroll
-        for (int i = 0; i < L; ++i)
-          src[u][i] = source(std::integral_constant<int, 4>{}, load_lo + k0 + u * BK + i * kStep4 + wave * 4, load_hi - 1);
+      for (int v = 0; v < kSrc; ++v) asm volatile("" : "+v"(src[v]));  // (waits here, not in every trip)
+    }
+  };
+  auto next_source = [&](int k0) {  // to the K-step at row k0
+    if constexpr (kLookP || kLookQ) {
+      if ((++src_k & 7) == 0) {
+        if (src_k == 8 * kSrc) {
+          sources(k0);
+        } else {
+#pragma unroll
+          for (int v = 1; v < kSrc; ++v) src[v - 1] = src[v];
+        }
+      }
     }
   };
   constexpr int kPieces = kLookP || kLookQ ? 6 : 0;
@@ -364,24 +379,23 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       if (n == 0) {
-        if constexpr (kLookP) p_row[i] = p.p_place.pair(src[0][i]);
-        if constexpr (kLookQ) q_row[i] = p.q_place.pair(src[0][i]);
+        row[i] = __builtin_amdgcn_ds_bpermute(((src_k & 7) * 8 + i * 4 + g) * 4, src[0]);
       } else if (n == 1) {
+        if constexpr (kLookP) p_row[i] = p.p_place.pair(row[i]);
+        if constexpr (kLookQ) q_row[i] = p.q_place.pair(row[i]);
+      } else if (n == 2) {
         if constexpr (kLookP) p_row[i] = p.p_place.within(p_row[i]);
         if constexpr (kLookQ) q_row[i] = p.q_place.within(q_row[i]);
-      } else if (n == 2) {
-        if constexpr (kLookP) p_next[i] = (uint32_t)p_row[i] * p.p_ld;
       } else if (n == 3) {
-        if constexpr (kLookQ) q_next[i] = (uint32_t)q_row[i] * p.q_ld;
+        if constexpr (kLookP) p_next[i] = (uint32_t)p_row[i] * p.p_ld;
       } else if (n == 4) {
+        if constexpr (kLookQ) q_next[i] = (uint32_t)q_row[i] * p.q_ld;
+      } else {
         const bool live = k0 + i * kStep4 + wave * 4 + g < load_hi - load_lo;
         if constexpr (kLookP) p_next[i] = live ? p_next[i] + t_column : kNone;
         if constexpr (kLookQ) q_next[i] = live ? q_next[i] + t_column : kNone;
-      } else {
-        src[0][i] = src[1][i], src[1][i] = src[2][i], src[2][i] = src[3][i];
       }
     }
-    if (n == 5) --have;
   };
   auto take_offsets = [&] {
 #pragma unroll
@@ -394,6 +408,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) piece(n, k0);
     take_offsets();
+    next_source(k0 + BK);
   };
   // load i of part J (P's first) of the K-step that its operand has come to, into a slot (its offset in LDS)
   const uint32_t lds0 = lds_address(lds);
@@ -690,7 +705,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     });
     each<0, kBar>([&](auto at) { mma(I1{}, at); });
     pin();
-    if ((kLookP || kLookQ) && have == 0) sources(p_k_next + BK);
+    next_source(p_k_next + BK);
     // (the stores of a tile that has just ended lie ahead of this trip's loads and may stay under way)
     if (stored && TL::kAhead == HALF)
       __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L + kStores));
