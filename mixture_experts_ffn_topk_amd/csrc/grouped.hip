@@ -23,6 +23,8 @@ namespace moe {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned U32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x3 __attribute__((ext_vector_type(3)));
 
 enum class Op { FWD, GRAD, WGRAD, MX };
 
@@ -60,7 +62,7 @@ struct GroupedParams {
   int out_pair;          // rows go to src_info[r]
   int accumulate;
   int p_tiles, q_tiles;  // q_tiles: WGRAD only
-  uint32_t group_inverse;  // floor(2^32 / (8 p_tiles))
+  uint32_t group_inverse;  // floor(2^32 / (8 p_tiles)); few rows: floor(2^32 / p_tiles)
 };
 
 // Direct-to-LDS loads: lane l's 16 (12) bytes land at l + 16 l; what lies out of the resource's bounds is zeros.
@@ -114,6 +116,8 @@ MOE_DEV int quotient(int n, int d, uint32_t inverse) {
   const int q = d == 1 ? n : (int)__umulhi((uint32_t)n, inverse);
   return q + (n - q * d >= d ? 1 : 0);
 }
+
+constexpr int kStream = 2;  // cache policy of stores: not kept
 
 struct TileAt {
   bool ok;
@@ -229,21 +233,21 @@ MOE_DEV int trx(int r) { return 2 * (r & 3) | (r >> 3 & 1); }
 // BP x BQ outputs, WP x WQ waves, each TP x TQ MFMA tiles of 16 x 16 (v_mfma_f32_16x16x32_bf16 and .._16x16x128_f8f6f4: the
 // part's power limits a loop of MFMAs alone to 2.02 and 7.19 PFLOP/s with them, to 1.80 and 6.51 with the 32 x 32 forms).  A
 // K-step (128 bytes of an operand's row) is staged in parts of 16 KB -- 128 rows, or columns, of P or Q -- in a ring of SLOTS
-// of them.
+// of them.  Two tiles: 256 x 256, one workgroup a CU, whose operands cross LDS least often, and 128 x 128, two a CU.
 template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS>
 struct GTile {
   static constexpr int kWaves = WP * WQ, kThreads = 64 * kWaves;
   static constexpr int TP = BP / 16 / WP, TQ = BQ / 16 / WQ;
   static constexpr bool kTP = O == Op::GRAD || O == Op::WGRAD, kTQ = O == Op::WGRAD;
-  static constexpr int kPart = 16384, kPP = BP / 128, kPQ = BQ / 128, kParts = kPP + kPQ, kHalf = kParts / 2;
+  static constexpr int kPart = 16384, kPP = BP / 128, kPQ = BQ / 128, kParts = kPP + kPQ;
   static constexpr int kL = 16 / kWaves;  // a wave's loads of a part
   static constexpr int kSf = O == Op::MX ? (BP + BQ) * 16 : 0;  // a K-step's scales: the words that hold a row's 8
   static constexpr int kLds = SLOTS * kPart + 2 * kSf;
   static constexpr int kBK = O == Op::MX ? 256 : 64;  // elements of a K-step
-  static constexpr int kAhead = SLOTS - 2 * kParts;   // parts in flight past the next K-step's
+  static constexpr int kEarly = SLOTS - 2 * kParts;   // parts in flight past the next K-step's
   static_assert(BP % 128 == 0 && BQ % 128 == 0 && 128 % (TP * 16) == 0 && 128 % (TQ * 16) == 0, "a wave reads one part");
   static_assert(TP % 2 == 0 && TQ % 4 == 0 && TP <= TQ, "the order of reads");
-  static_assert(16 % kWaves == 0 && kPP == kPQ && kAhead > 0 && kAhead <= kHalf, "ring");
+  static_assert(16 % kWaves == 0 && kPP == kPQ && kEarly > 0 && kEarly <= kPP, "ring");
 };
 
 // WHERE: bit 0: P's rows, bit 1: Q's rows are found through src_info (WGRAD; elsewhere Q's are looked up once a tile); MX: bit
@@ -253,7 +257,7 @@ template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS, bool F32, int WHERE>
 __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams p) {
   using TL = GTile<O, BP, BQ, WP, WQ, SLOTS>;
   constexpr bool MX = O == Op::MX, WG = O == Op::WGRAD, kTP = TL::kTP, kTQ = TL::kTQ;
-  constexpr int TP = TL::TP, TQ = TL::TQ, BK = TL::kBK, kThreads = TL::kThreads, PT = TL::kParts, HALF = TL::kHalf;
+  constexpr int TP = TL::TP, TQ = TL::TQ, BK = TL::kBK, kThreads = TL::kThreads, PT = TL::kParts, EARLY = TL::kEarly, LATE = PT - EARLY;
   constexpr int L = TL::kL;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TL::kLds];
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -345,27 +349,26 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     q_from = resource(base, !t.ok ? 0u : kLookQ || look ? kAll : kTQ ? t_extent(false) : (uint32_t)min(rows, BQ) * p.q_ld);
   };
   // WGRAD: the offsets of a K-step's rows through src_info (read also where only one operand's rows are found there).  Lane l
-  // of src[v] holds that of this wave's row l % 8 of the tile's K-step 8 v + l / 8: a vector load, which has to wait for the
-  // loads into LDS behind it, for 32 K-steps, and a shuffle for each.  In pieces, which go between MFMAs.
-  constexpr int kSrc = 4;
+  // of src[v] holds that of this wave's row l % (4 L) of the tile's K-step kEach v + l / (4 L): a vector load, which has to wait
+  // for the loads into LDS behind it, for 4 kEach K-steps, and a shuffle for each.  In pieces, which go between MFMAs.
+  constexpr int kSrc = 4, kEach = 16 / L;
   int src[kSrc] = {}, src_k = 0, row[L] = {}, p_row[L] = {}, q_row[L] = {};
   uint32_t p_next[L] = {}, q_next[L] = {}, t_column = 0;
   if constexpr (kLookP || kLookQ) t_column = t_off(0);
   auto sources = [&](int k0) {  // of the K-steps from row k0 on
     if constexpr (kLookP || kLookQ) {
-      static_assert(L == 2, "8 rows a K-step");
-      const int l = fresh(lane), first = load_lo + k0 + (l >> 3) * BK + (l >> 2 & 1) * kStep4 + wave * 4 + (l & 3);
+      const int l = fresh(lane), first = load_lo + k0 + l / (4 * L) * BK + (l >> 2) % L * kStep4 + wave * 4 + (l & 3);
       src_k = 0;
 #pragma unroll
-      for (int v = 0; v < kSrc; ++v) src[v] = p.src_info[max(min(first + v * 8 * BK, load_hi - 1), 0)];
+      for (int v = 0; v < kSrc; ++v) src[v] = p.src_info[max(min(first + v * kEach * BK, load_hi - 1), 0)];
 #pragma unroll
       for (int v = 0; v < kSrc; ++v) asm volatile("" : "+v"(src[v]));  // (waits here, not in every trip)
     }
   };
   auto next_source = [&](int k0) {  // to the K-step at row k0
     if constexpr (kLookP || kLookQ) {
-      if ((++src_k & 7) == 0) {
-        if (src_k == 8 * kSrc) {
+      if (++src_k % kEach == 0) {
+        if (src_k == kEach * kSrc) {
           sources(k0);
         } else {
 #pragma unroll
@@ -379,7 +382,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       if (n == 0) {
-        row[i] = __builtin_amdgcn_ds_bpermute(((src_k & 7) * 8 + i * 4 + g) * 4, src[0]);
+        row[i] = __builtin_amdgcn_ds_bpermute((src_k % kEach * (4 * L) + i * 4 + g) * 4, src[0]);
       } else if (n == 1) {
         if constexpr (kLookP) p_row[i] = p.p_place.pair(row[i]);
         if constexpr (kLookQ) q_row[i] = p.q_place.pair(row[i]);
@@ -486,10 +489,17 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       for (int j = 0; j < TQ; ++j) q_shift[j] = (uint32_t)(sf_row_q(t, (wq * TQ + j) * 16 + r16) * sf_row) & 3;
     }
   };
+  // kSfSteps K-steps' at a time: whole words of two (every row is a request of its own, which cost as much as 100 cycles of
+  // the loop for 64 of them)
+  constexpr int kSfSteps = ODD ? 1 : 2;
   auto load_sf = [&](int buf) {
     if constexpr (MX) {
-      lds_copy12(sf_from, sf_off, lds0 + SLOTS * TL::kPart + buf * TL::kSf + wave * (64 * 16));
-      sf_off += 8;
+      const uint32_t to = lds0 + SLOTS * TL::kPart + buf * TL::kSf + wave * (64 * 16);
+      if constexpr (ODD)
+        lds_copy12(sf_from, sf_off, to);
+      else
+        lds_copy16(sf_from, sf_off, to);
+      sf_off += 8 * kSfSteps;
     }
   };
 
@@ -516,27 +526,35 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   auto read_q = [&](int j, int bq, int s) { fq[j] = frag(lds + bq, kTQ, wq % kQw * TQ + j, s); };
   // a K-step's scales: lane g's blocks are 2 g and 2 g + 1, for sub-steps 0 and 1 (blocks past K: scale 2^-127, on codes of
   // zero)
-  uint32_t sp_next[TP] = {}, sq_next[TQ] = {};
-  auto read_sf = [&](int buf) {
+  typedef uint16_t U16x2 __attribute__((ext_vector_type(2)));
+  U16x2 sp_next[TP / 2] = {}, sq_next[TQ / 2] = {};  // two tiles' in a word
+  auto read_sf = [&](int buf, int half) {
     if constexpr (MX) {
-      typedef uint16_t __attribute__((aligned(1))) Bytes2;
-      const uint8_t* f = lds + SLOTS * TL::kPart + buf * TL::kSf + 2 * g + r16 * 16;
+      typedef uint16_t __attribute__((aligned(1))) Anywhere;
+      typedef std::conditional_t<ODD, Anywhere, uint16_t> Bytes2;
+      const uint8_t* f = lds + SLOTS * TL::kPart + buf * TL::kSf + half * 8 + 2 * g + r16 * 16;
 #pragma unroll
-      for (int i = 0; i < TP; ++i) sp_next[i] = *(const Bytes2*)(f + (wp * TP + i) * 256 + p_shift);
+      for (int i = 0; i < TP; ++i) sp_next[i / 2][i % 2] = *(const Bytes2*)(f + (wp * TP + i) * 256 + p_shift);
 #pragma unroll
-      for (int j = 0; j < TQ; ++j) sq_next[j] = *(const Bytes2*)(f + (BP + (wq * TQ + j) * 16) * 16 + (ODD ? q_shift[j] : 0));
+      for (int j = 0; j < TQ; ++j)
+        sq_next[j / 2][j % 2] = *(const Bytes2*)(f + (BP + (wq * TQ + j) * 16) * 16 + (ODD ? q_shift[j] : 0));
     }
   };
-  // two tiles' in a word
   auto take_sf = [&] {
     if constexpr (MX) {
-      const int left = sf_row - sf_k - 2 * g;
-      const uint32_t keep = left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0x00FF00FFu : 0u;
 #pragma unroll
-      for (int i = 0; i < TP; i += 2) sp[i / 2] = (sp_next[i] | sp_next[i + 1] << 16) & keep;
+      for (int i = 0; i < TP / 2; ++i) sp[i] = __builtin_bit_cast(uint32_t, sp_next[i]);
 #pragma unroll
-      for (int j = 0; j < TQ; j += 2) sq[j / 2] = (sq_next[j] | sq_next[j + 1] << 16) & keep;
+      for (int j = 0; j < TQ / 2; ++j) sq[j] = __builtin_bit_cast(uint32_t, sq_next[j]);
       sf_k += 8;
+      if (sf_k > sf_row) {
+        const int left = sf_row - sf_k + 8 - 2 * g;
+        const uint32_t keep = left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0x00FF00FFu : 0u;
+#pragma unroll
+        for (auto& word : sp) word &= keep;
+#pragma unroll
+        for (auto& word : sq) word &= keep;
+      }
     }
   };
   f32x4 acc[TP][TQ];
@@ -561,65 +579,88 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   };
 
   // ---------------------------------------------------------------- output
-  // From the registers, 16 bytes a lane, as stores that do not wait: the loads of the next tile are under way.  A lane holds
-  // columns 4 g .. + 4 of row r16 of a 16 x 16 tile; for bf16 two neighbouring tiles' lanes swap so that each has 8 in a row:
-  // 16 rows of 64 bytes a store.  Every store is issued, those out of the output with an offset that is dropped: the waits
-  // count them.
+  // From the registers, as stores that do not wait: the loads of the next tile are under way.  A lane holds columns 4 g .. + 4
+  // of row r16 of a 16 x 16 tile.  For bf16 two neighbouring tiles' lanes swap so that each has 8 in a row, and for both types
+  // lanes 8 apart then, so that a store is 8 rows of whole lines: 128 bytes.  Every store is issued, those out of the output
+  // with an offset that is dropped: the waits count them.
   constexpr int kStores = TP * TQ / (F32 ? 1 : 2);
   auto store = [&](const TileAt& t) {
-    const int q0 = t.q * BQ + wq * TQ * 16, p0 = t.p * BP + wp * TP * 16;
-    const int q_end = WG ? p.q_cols : t.hi - t.lo;
-    constexpr int kEl = F32 ? 4 : 2;
+    constexpr int kEl = F32 ? 4 : 2, kTiles = F32 ? 2 : 4;  // kTiles tiles' columns are a line
+    static_assert(TP % kTiles == 0, "lines");
+    const int q0 = t.q * BQ + wq * TQ * 16, p0 = t.p * BP + wp * TP * 16, rows = max((WG ? p.q_cols : t.hi - t.lo) - q0, 0);
     const uint8_t* base = p.out;
     if (WG)
       base += t.expert * p.out_expert + (long long)q0 * p.out_ld;
     else if (!p.out_pair)
       base += ((long long)t.lo + q0) * p.out_ld;
-    const __amdgpu_buffer_rsrc_t to = make_rsrc(base, kAll);
-    const int l16 = fresh(r16), lg = fresh(g);
+    const bool pair = !WG && p.out_pair;
+    const __amdgpu_buffer_rsrc_t to = make_rsrc(base, pair ? kAll : (uint32_t)min(rows, TQ * 16) * p.out_ld);
+    const int l16 = fresh(r16), lg = fresh(g), row8 = l16 & 7;
+    // (past the last column: past the resource, with any row)
+    constexpr uint32_t kPast = 0x80000000u;
+    uint32_t column[TP / kTiles];
+#pragma unroll
+    for (int c = 0; c < TP / kTiles; ++c) {
+      const int col = p0 + c * kTiles * 16 + (l16 >> 3) * (kTiles * 8) + (F32 ? 4 * lg : 16 * (lg & 1) + 8 * (lg >> 1));
+      column[c] = col < p.p_cols ? (uint32_t)col * kEl : kPast;
+    }
+    uint32_t at[2] = {(uint32_t)row8 * p.out_ld, (uint32_t)(row8 + 8) * p.out_ld};
 #pragma unroll
     for (int j = 0; j < TQ; ++j) {
-      const int row = j * 16 + l16;
-      bool ok = q0 + row < q_end;
-      uint32_t at = (uint32_t)row * p.out_ld;
-      if (!WG && p.out_pair) {
-        const int r = p.src_info[max(min(t.lo + q0 + row, t.hi - 1), 0)];
-        ok = ok && (uint32_t)r < (uint32_t)p.npairs;
-        at = (uint32_t)r * p.out_ld;
+      if (pair) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = j * 16 + h * 8 + row8, r = p.src_info[max(min(t.lo + q0 + row, t.hi - 1), 0)];
+          at[h] = row < rows && (uint32_t)r < (uint32_t)p.npairs ? (uint32_t)r * p.out_ld : kNone;
+        }
       }
 #pragma unroll
-      for (int i = 0; i < TP; i += F32 ? 1 : 2) {
-        i32x4 d;
-        int col = p0 + i * 16;
-        if constexpr (F32) {
-          d = __builtin_bit_cast(i32x4, acc[i][j]);
-          col += 4 * lg;
-        } else {
-          const f32x4 u = acc[i][j], v = acc[i + 1][j];
-          const auto x = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[0], u[1]), bf16x2_rne(v[0], v[1]), false, false);
-          const auto y = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[2], u[3]), bf16x2_rne(v[2], v[3]), false, false);
-          d = i32x4{(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
-          col += 16 * (lg & 1) + 8 * (lg >> 1);
-        }
-        const uint32_t o = ok && col < p.p_cols ? at + (uint32_t)col * kEl : kNone;
-        if constexpr (WG && F32) {
-          if (p.accumulate) {
-            const f32x4 sum = __builtin_bit_cast(f32x4, d) + __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(to, o, 0, 0));
-            d = __builtin_bit_cast(i32x4, sum);
+      for (int c = 0; c < TP / kTiles; ++c) {
+        i32x4 d[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = c * kTiles + h * (kTiles / 2);
+          if constexpr (F32) {
+            d[h] = __builtin_bit_cast(i32x4, acc[i][j]);
+          } else {
+            const f32x4 u = acc[i][j], v = acc[i + 1][j];
+            const auto x = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[0], u[1]), bf16x2_rne(v[0], v[1]), false, false);
+            const auto y = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[2], u[3]), bf16x2_rne(v[2], v[3]), false, false);
+            d[h] = i32x4{(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
           }
         }
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, d), to, o, 0, 0);
+        i32x4 out[2];  // rows row8: lanes 8 .. 15 take the second half of lanes 0 .. 7's; rows row8 + 8: the other way round
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          out[0][e] = __builtin_amdgcn_update_dpp(d[0][e], d[1][e], 0x128, 0xF, 0xC, false);  // row_ror:8
+          out[1][e] = __builtin_amdgcn_update_dpp(d[1][e], d[0][e], 0x128, 0xF, 0x3, false);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o = at[h] + column[c];
+          if (pair) o = at[h] == kNone || column[c] == kPast ? kNone : o;
+          if constexpr (WG && F32) {
+            if (p.accumulate) {
+              const f32x4 sum = __builtin_bit_cast(f32x4, out[h]) +
+                                __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(to, o, 0, 0));
+              out[h] = __builtin_bit_cast(i32x4, sum);
+            }
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, out[h]), to, o, 0, kStream);
+        }
       }
+      at[0] += 16 * p.out_ld, at[1] += 16 * p.out_ld;
     }
   };
 
   // ---------------------------------------------------------------- K loop
   // A trip is a K-step: two sub-steps of TQ groups of TP MFMAs, with what else goes out between them.  (A wave that issues
   // many loads at once waits for the address unit, 16 cycles each and shared by the waves, and feeds no MFMAs meanwhile.)
-  //   sub-step 0: the reads of sub-step 1's fragments, and the loads of half of the parts
+  //   sub-step 0: the reads of sub-step 1's fragments, and the loads of the first parts of the K-step two ahead (as many as the
+  //   ring has slots beside two K-steps')
   //   the first groups of sub-step 1; then the wait for the next K-step's loads and these reads, and the barrier: the next K-step
   //   is whole, and this one's slots are free
-  //   the rest of sub-step 1: the reads of the next K-step's first fragments, and the loads of the other half
+  //   the rest of sub-step 1: the reads of the next K-step's first fragments, and the loads of the other parts
   // The parts of the ring go out in order, each into the slot of the part SLOTS ahead of it.  A workgroup goes through its
   // tiles without draining the ring: the loads change to the next tile two K-steps ahead of the MFMAs (every tile has at
   // least two K-steps, of zeros past its last), past the last tile they are of zeros.  The order stays as it is written
@@ -627,9 +668,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   constexpr int kMma = TP * TQ, kGroups = TQ / 4, kBar = kGroups * TP;  // MFMAs of a sub-step, of sub-step 1 ahead of the barrier
-  constexpr int kLoads = HALF * L;
   // load n of the parts FIRST .. behind the trip's first, whose slots are at[]
-  auto issue_nth = [&](auto first, auto nth, const uint32_t (&at)[HALF]) {
+  auto issue_nth = [&](auto first, auto nth, const auto& at) {
     constexpr int n = decltype(nth)::value, part = decltype(first)::value + n / L;
     issue(std::integral_constant<int, part % PT>{}, n % L, at[n / L]);
     // (the operand's last part of the K-step)
@@ -642,14 +682,13 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
 #pragma unroll
       for (int j = 0; j < TQ; ++j) asm volatile("" : "+v"(acc[i][j]));
   };
-  constexpr int kFill = SLOTS - HALF;  // parts ahead of the first trip's
-  int steps = steps_of(now), ks = 0, slot = 0, buf = 0;
+  int steps = steps_of(now), ks = 0, slot = 0, buf = 0;  // (buf: of the scales that are read next)
   aim_p(now);
   aim_q(now);
   aim_sf(now);
   aim_shifts(now);
   load_sf(0);
-  each<0, kFill>([&](auto nth) {
+  each<0, 2 * PT>([&](auto nth) {
     constexpr int n = decltype(nth)::value;
     if (n == 0) sources(0);
     if (n % PT == 0) offsets_at(n / PT * BK), tail(true);
@@ -659,7 +698,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     if (n % PT == TL::kPP - 1) advance(p_from, true);
     if (n % PT == PT - 1) advance(q_from, false);
   });
-  load_sf(1);
+  if (kSfSteps == 1) load_sf(1);
   offsets_at(2 * BK);
   __builtin_amdgcn_s_waitcnt(0);
   __builtin_amdgcn_s_barrier();
@@ -670,7 +709,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
   for (int i = 0; i < TP; ++i) read_p(i, bp, 0);
 #pragma unroll
   for (int j = 0; j < TQ; ++j) read_q(j, bq, 0);
-  read_sf(0);
+  read_sf(0, 0);
   TileAt then{};
   bool stored = false;
   for (;;) {
@@ -679,63 +718,62 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     if (change) {
       then = walk.next(p);
       aim_p(then);
-      if constexpr (TL::kAhead == HALF) aim_q(then);
+      aim_q(then);
       sources(0);
       offsets_at(0);
     }
     tail(true);
-    if constexpr (TL::kAhead == HALF) tail(false);
-    uint32_t early[HALF], late[HALF];  // slots of the parts that go out ahead of the barrier and behind it
+    tail(false);
+    uint32_t early[EARLY], late[LATE];  // slots of the parts that go out ahead of the barrier and behind it
 #pragma unroll
-    for (int j = 0; j < HALF; ++j) {
-      early[j] = scalar((int)(lds0 + wrap(slot + (kFill + j) * TL::kPart)));
+    for (int j = 0; j < EARLY; ++j) early[j] = scalar((int)(lds0 + wrap(slot + (2 * PT + j) * TL::kPart)));
+#pragma unroll
+    for (int j = 0; j < LATE; ++j)
       late[j] = scalar((int)(lds0 + slot + j * TL::kPart - (slot + j * TL::kPart >= kRing ? kRing : 0)));
-    }
     const int p_k_next = p_k + BK;  // of the loads of the next trip
     take_sf();
     each<0, kMma>([&](auto at) {
-      constexpr int m = decltype(at)::value;
+      constexpr int m = decltype(at)::value, kEvery = kMma / (EARLY * L);
       mma(I0{}, at);
       if (m < TP) read_p(m, bp, 1);
       if (m % TP == TP - 1) read_q(m / TP, bq, 1);
-      if constexpr (m % (kMma / kLoads) == kMma / kLoads / 2)
-        issue_nth(std::integral_constant<int, kFill>{}, std::integral_constant<int, m / (kMma / kLoads)>{}, early);
-      if constexpr (m % 4 == 1 && m / 4 < kPieces) piece(m / 4, p_k_next);
+      if constexpr (m % kEvery == kEvery / 2)
+        issue_nth(std::integral_constant<int, 2 * PT>{}, std::integral_constant<int, m / kEvery>{}, early);
+      if constexpr (m % (kMma / 8) == 1 && m / (kMma / 8) < kPieces) piece(m / (kMma / 8), p_k_next);
       __builtin_amdgcn_sched_barrier(0);
     });
     each<0, kBar>([&](auto at) { mma(I1{}, at); });
     pin();
     next_source(p_k_next + BK);
     // (the stores of a tile that has just ended lie ahead of this trip's loads and may stay under way)
-    if (stored && TL::kAhead == HALF)
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L + kStores));
+    if (stored)
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(EARLY * L + kStores));
     else
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(TL::kAhead * L));
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(EARLY * L));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     if (change) {
-      if constexpr (TL::kAhead != HALF) aim_q(then);
       aim_sf(then);
     }
-    if constexpr (TL::kAhead != HALF) tail(false);
     // (the scales that are read next are the next tile's)
     if (ODD && ks == steps - 1) aim_shifts(then);
-    load_sf(buf);
+    const int ks_next = ks + 1 == steps ? 0 : ks + 1;
+    if (ks_next % kSfSteps == 0) buf ^= 1;
+    if (kSfSteps == 1 || change || (ks % kSfSteps == 0 && ks + 2 < steps)) load_sf(buf ^ 1);
     bp = part_p(next), bq = part_q(next);
     each<kBar, kMma>([&](auto at) {
-      constexpr int m = decltype(at)::value, n = m - kBar, kEvery = (kMma - kBar) / kLoads;
+      constexpr int m = decltype(at)::value, n = m - kBar, kEvery = (kMma - kBar) / (LATE * L);
       mma(I1{}, at);
       if (n < TP) read_p(n, bp, 0);
       if (n >= TP && n < TP + kGroups) read_q(n - TP, bq, 0);
       if (m % TP == TP - 1) read_q(m / TP, bq, 0);
-      if constexpr (n % kEvery == kEvery / 2 && n / kEvery < kLoads)
+      if constexpr (n % kEvery == kEvery / 2 && n / kEvery < LATE * L)
         issue_nth(std::integral_constant<int, SLOTS>{}, std::integral_constant<int, n / kEvery>{}, late);
-      if (n == TP + kGroups) read_sf(buf ^ 1);
+      if (n == TP + kGroups) read_sf(buf, ks_next % kSfSteps);
       __builtin_amdgcn_sched_barrier(0);
     });
     take_offsets();
     slot = next;
-    buf ^= 1;
     stored = ++ks == steps;
     if (stored) {
       store(now);
@@ -748,6 +786,198 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     }
   }
   __builtin_amdgcn_s_waitcnt(0);  // the loads of zeros land before the workgroup's LDS is another's
+}
+
+// ---------------------------------------------------------------- few rows
+// Where experts have few rows, the product is the weights' way through memory, and a tile of 256 rows spends its MFMAs and its
+// loads on rows that are not there.  A workgroup takes 16 TP weight rows and 16 TQ rows of an expert; its W waves share the
+// summed axis and read their parts straight from memory to the registers that the MFMAs take (a lane's 16 bytes lie side by
+// side with three others': 64 bytes a row, and the line's other half comes with the wave's next load).  No wave waits for
+// another until their sums meet in LDS, in the waves' order.  S loads of each row are under way: with 4 waves of one weight tile
+// 4 tokens' product of 28672 x 4096 reads its active experts at 6.4 TB/s (two or four weight tiles a wave 5.1 and 5.6: fewer
+// waves, less under way); MXFP4's short rows go to one wave each (128 experts, 32 tokens: 5.3 TB/s, with 4 waves 3.6).
+template <bool MX, int TP, int TQ, int W, bool F32>
+__global__ __launch_bounds__(64 * W, MX ? 2 : 4) void grouped_few_kernel(GroupedParams p) {
+  constexpr int BQ = 16 * TQ, S = 8;
+  __shared__ __attribute__((aligned(16))) float sums[W][BQ][16 * TP + 4];
+  const int lane = lane_id(), wave = scalar((int)threadIdx.x >> 6), g = lane >> 4, r16 = lane & 15;
+  // the workgroup's tile: q-tiles lie expert by expert, and each has all of its weight tiles in turn
+  int slot = quotient((int)blockIdx.x, p.p_tiles, p.group_inverse);
+  const int tile = (int)blockIdx.x - slot * p.p_tiles;
+  int expert = -1, lo = 0, hi = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    const int e = e0 + lane;
+    int from = 0, to = 0;
+    if (e < p.E) from = row_at(p, e), to = max(from, row_at(p, e + 1));
+    const int upto = wave_scan((to - from + BQ - 1) / BQ), all = __builtin_amdgcn_readlane(upto, 63);
+    if (slot < all) {
+      const int l = __ffsll((unsigned long long)__ballot(upto > slot)) - 1;
+      expert = e0 + l;
+      slot -= l ? __builtin_amdgcn_readlane(upto, l - 1) : 0;
+      lo = __builtin_amdgcn_readlane(from, l) + slot * BQ;
+      hi = __builtin_amdgcn_readlane(to, l);
+      break;
+    }
+    slot -= all;
+  }
+  if (expert < 0) return;
+
+  const int K = scalar((int)p.p_ld);  // bytes of a row
+  const int p0 = tile * 16 * TP, p_rows = min(p.p_cols - p0, 16 * TP), rows = min(hi - lo, BQ);
+  const bool look = p.q_place.gathered;
+  const __amdgpu_buffer_rsrc_t from_p = make_rsrc(p.P + expert * p.p_expert + (long long)p0 * p.p_ld, (uint32_t)p_rows * p.p_ld);
+  const __amdgpu_buffer_rsrc_t from_q = make_rsrc(p.Q + (look ? 0 : (long long)lo * p.q_ld), look ? kAll : (uint32_t)rows * p.q_ld);
+  // the tensor's row of row r of the tile
+  auto q_row = [&](int r) { return look ? p.q_place.of(p.src_info[min(lo + r, hi - 1)]) : min(r, rows - 1); };
+
+  // A trip is S * 64 bytes of each row for each wave, in lines of kLine (MXFP4, for the scales' sake: all in one); load s is
+  // 64 of them, at_load(s) bytes behind the first.
+  constexpr int kLine = MX ? S * 64 : 128, kNext = S * 64 * W;
+  auto at_load = [](int s) { return s * 64 / kLine * (kLine * W) + s * 64 % kLine; };
+  int k = wave * kLine + g * 16;  // of the lane's next load
+  uint32_t p_off[TP], q_off[TQ];
+  i32x4 part[S][TP + TQ];
+  auto load_p = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < TP; ++i) part[s][i] = bload16(from_p, (k + at_load(s) < K ? p_off[i] : kNone) + at_load(s), 0);
+  };
+  int q_end[TQ];  // K, or 0 in rows that are not there
+  auto load_q = [&](int s) {
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) part[s][TP + j] = bload16(from_q, (k + at_load(s) < q_end[j] ? q_off[j] : kNone) + at_load(s), 0);
+  };
+  // MXFP4: a trip's 4 S scales of a row lie in four lanes, lane l having S of row l / 4: the words from the one that holds
+  // the first, which the shift takes to the front.  The lane that multiplies block 4 s + g of row r16 has its word from lane
+  // 4 r16 + (4 s + g) / S by a shuffle.  (A byte's load for each block took as long as the codes.)
+  const int sf_lane = wave * (kLine / 16) + (lane & 3) * S;
+  i32x3 sf_in[MX ? TP + TQ : 1];
+  uint32_t sf[MX ? TP + TQ : 1][2], sf_off[MX ? TP + TQ : 1], sf_shift[MX ? TP + TQ : 1];
+  const long long sfp0 = ((long long)expert * p.n_rows + p0) * p.sf_row & ~3LL, sfq0 = look ? 0 : (long long)lo * p.sf_row & ~3LL;
+  const __amdgpu_buffer_rsrc_t from_psf =
+      make_rsrc(p.P_sf + sfp0, (uint32_t)min((p.p_sf_bytes + 3 & ~3LL) - sfp0, (long long)kAll));
+  const __amdgpu_buffer_rsrc_t from_qsf =
+      make_rsrc(p.Q_sf + sfq0, (uint32_t)min((p.q_sf_bytes + 3 & ~3LL) - sfq0, (long long)kAll));
+  auto aim_sf = [&](int i, long long row, long long first) {  // first: bytes of the tensor up to its resource
+    const long long at = row * p.sf_row + sf_lane;
+    sf_shift[i] = (uint32_t)at & 3;
+    sf_off[i] = (uint32_t)((at & ~3LL) - first);
+  };
+  auto load_sf = [&](int i) {
+    sf_in[i] = __builtin_bit_cast(i32x3, __builtin_amdgcn_raw_buffer_load_b96(i < TP ? from_psf : from_qsf, sf_off[i], 0, 0));
+    sf_off[i] += kNext / 16;
+  };
+  auto take_sf = [&] {
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < TP + TQ; ++i) {
+        sf[i][0] = __builtin_amdgcn_alignbyte((uint32_t)sf_in[i][1], (uint32_t)sf_in[i][0], sf_shift[i]);
+        sf[i][1] = __builtin_amdgcn_alignbyte((uint32_t)sf_in[i][2], (uint32_t)sf_in[i][1], sf_shift[i]);
+      }
+    }
+  };
+  auto scale = [&](int i, int s, bool in) {
+    const uint32_t word = (uint32_t)__builtin_amdgcn_ds_bpermute((4 * r16 + s / 2) * 4, (int)sf[i][s % 2]);
+    return (int)(in ? word >> 8 * g : 0u);
+  };
+
+#pragma unroll
+  for (int i = 0; i < TP; ++i) {
+    p_off[i] = (uint32_t)(i * 16 + r16) * p.p_ld + k;
+    if constexpr (MX) aim_sf(i, (long long)expert * p.n_rows + p0 + i * 16 + (lane >> 2), sfp0), load_sf(i);
+  }
+  int source[TQ], source_sf[TQ];
+#pragma unroll
+  for (int j = 0; j < TQ; ++j) {
+    source[j] = q_row(j * 16 + r16);
+    if constexpr (MX) source_sf[j] = q_row(j * 16 + (lane >> 2));
+  }
+#pragma unroll
+  for (int s = 0; s < S; ++s) load_p(s);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int j = 0; j < TQ; ++j) {
+    q_off[j] = (uint32_t)source[j] * p.q_ld + k;
+    q_end[j] = j * 16 + r16 < rows ? K : 0;
+    if constexpr (MX) aim_sf(TP + j, source_sf[j] + (look ? 0 : lo), sfq0), load_sf(TP + j);
+  }
+#pragma unroll
+  for (int s = 0; s < S; ++s) load_q(s);
+  f32x4 acc[TP][TQ];
+#pragma unroll
+  for (int i = 0; i < TP; ++i)
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto mma = [&](int s, int k) {
+    int scales[MX ? TP + TQ : 1];
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < TP + TQ; ++i) scales[i] = scale(i, s, k + at_load(s) < K);
+    }
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) {
+        const i32x4 a = part[s][i], b = part[s][TP + j];
+        if constexpr (MX)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0}, i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, acc[i][j], 4, 4, 0,
+              scales[i], 0, scales[TP + j]);
+        else
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                              acc[i][j], 0, 0, 0);
+      }
+  };
+  for (int k0 = wave * kLine;;) {  // (the same in every lane)
+    k0 += kNext;
+    if (k0 >= K) break;
+    take_sf();
+    k += kNext;
+#pragma unroll
+    for (int i = 0; i < TP; ++i) p_off[i] += kNext;
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) q_off[j] += kNext;
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < TP + TQ; ++i) load_sf(i);
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      mma(s, k - kNext);
+      load_p(s);
+      load_q(s);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  take_sf();
+#pragma unroll
+  for (int s = 0; s < S; ++s) mma(s, k);
+
+  // a lane holds columns 4 g .. + 4 of row r16
+#pragma unroll
+  for (int i = 0; i < TP; ++i)
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) *(f32x4*)&sums[wave][j * 16 + r16][i * 16 + 4 * g] = acc[i][j];
+  __syncthreads();
+  constexpr int kFours = 4 * TP;  // of a row
+  const uint8_t* base = p.out + (p.out_pair ? 0 : (long long)lo * p.out_ld);
+  const __amdgpu_buffer_rsrc_t to = make_rsrc(base, kAll);
+  for (int n = threadIdx.x; n < BQ * kFours; n += 64 * W) {
+    const int row = n / kFours, col = n % kFours * 4;
+    f32x4 sum = *(const f32x4*)&sums[0][row][col];
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum += *(const f32x4*)&sums[w][row][col];
+    bool ok = row < rows && col < p_rows;
+    uint32_t at = (uint32_t)row;
+    if (p.out_pair && ok) {
+      at = (uint32_t)p.src_info[lo + row];
+      ok = at < (uint32_t)p.npairs;
+    }
+    const uint32_t o = ok ? at * p.out_ld + (uint32_t)(p0 + col) * (F32 ? 4 : 2) : kNone;
+    if constexpr (F32)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum), to, o, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64(U32x2{bf16x2_rne(sum[0], sum[1]), bf16x2_rne(sum[2], sum[3])}, to, o, 0, 0);
+  }
 }
 
 // Compute units of the current device (cached per device).
@@ -783,6 +1013,23 @@ hipError_t launch_tile(GroupedParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// grouped_few_kernel's workgroups
+long long few_tiles(const GroupedParams& p, int TP, int TQ) {
+  const long long groups = std::min(p.npairs, p.E), slots = (p.npairs + groups * (16 * TQ - 1)) / (16 * TQ);
+  return slots * ((p.p_cols + 16 * TP - 1) / (16 * TP));
+}
+bool few_fits(const GroupedParams& p, int TP, int TQ, int W) { return few_tiles(p, TP, TQ) * 64 * W < 1LL << 32; }
+
+template <bool MX, int TP, int TQ, int W, bool F32>
+hipError_t launch_few(GroupedParams& p, hipStream_t s) {
+  p.p_tiles = (p.p_cols + 16 * TP - 1) / (16 * TP);
+  p.group_inverse = (uint32_t)((1ull << 32) / p.p_tiles);
+  const long long tiles = few_tiles(p, TP, TQ);
+  if (tiles == 0) return hipSuccess;
+  grouped_few_kernel<MX, TP, TQ, W, F32><<<dim3((unsigned)tiles), dim3(64 * W), 0, s>>>(p);
+  return hipGetLastError();
+}
+
 Place place(Rows r, int T, int topk) {
   const bool whole = r != Rows::TOKEN || topk == 1;
   return Place{whole ? 0u : (uint32_t)(((1ull << 32) + topk - 1) / topk), whole ? -1 : 0, r != Rows::PLAN,
@@ -808,15 +1055,33 @@ GroupedParams common(const GroupedArgs& a) {
 
 template <Op O, bool F32>
 hipError_t launch_rows(GroupedParams& p, hipStream_t s) {
+  // Rows of an expert that has any, on average, and the tiles that they make.  us measured, by rows an expert:
+  //   bf16, 8 experts of 28672 x 4096     1    4    8   16   64  128      MXFP4, 128 of 5760 x 2880    1    4    8   16   32
+  //   grouped_few_kernel                198  320  364  552                16 x 16                    137  232  270  357  548
+  //   128 x 128                         245  327  330  340  352  495      32 x 32                    163  243  261  286  387
+  //   256 x 256                         290  421  427  426  439  447      256 x 256                  231  345  351  354  361
+  // Where the tiles leave most of the part without work, the smaller ones are faster beyond that (bf16, 2 experts of 4096 x
+  // 14336, 16 rows: 76 us, 128 x 128 143; MXFP4, 32 rows: 35, 256 x 256 89).
+  const long long groups = std::max(1, std::min(p.npairs, p.E)), rows = (p.npairs + groups - 1) / groups;
+  auto tiles = [&](int n) { return groups * ((p.p_cols + n - 1) / n) * ((rows + n - 1) / n); };
+  const int cus = device_cus();
   if constexpr (O == Op::MX) {
+    if (rows <= 5 && few_fits(p, 1, 1, 1)) return launch_few<true, 1, 1, 1, F32>(p, s);
+    if ((rows <= 24 || (rows <= 128 && tiles(256) <= cus / 4)) && few_fits(p, 2, 2, 2)) return launch_few<true, 2, 2, 2, F32>(p, s);
     return p.sf_row % 4 ? launch_tile<O, 256, 256, 4, 2, 9, F32, 1>(p, s) : launch_tile<O, 256, 256, 4, 2, 9, F32>(p, s);
   } else {
+    if constexpr (O == Op::FWD)
+      if ((rows <= 4 || (rows <= 32 && tiles(128) <= cus / 2)) && few_fits(p, 1, 1, 4)) return launch_few<false, 1, 1, 4, F32>(p, s);
+    if (rows <= 64 || tiles(256) < cus) return launch_tile<O, 128, 128, 2, 2, 5, F32>(p, s);
     return launch_tile<O, 256, 256, 4, 2, 10, F32>(p, s);
   }
 }
 
 template <bool F32, int WHERE>
 hipError_t launch_wgrad(GroupedParams& p, hipStream_t s) {
+  // (16 experts of 512 x 512, 256 rows each: 11 us, with the large tile 20; from a tile a CU on the large one is as fast)
+  if ((long long)p.E * ((p.p_cols + 255) / 256) * ((p.q_cols + 255) / 256) < device_cus())
+    return launch_tile<Op::WGRAD, 128, 128, 2, 2, 5, F32, WHERE>(p, s);
   return launch_tile<Op::WGRAD, 256, 256, 4, 2, 10, F32, WHERE>(p, s);
 }
 template <bool F32>
@@ -831,7 +1096,7 @@ hipError_t launch_wgrad(GroupedParams& p, hipStream_t s) {
 }
 
 // (the smallest tiles' extents)
-constexpr int kMinP = 256, kMinQ = 256;
+constexpr int kMinP = 128, kMinQ = 128;
 
 }  // namespace
 
