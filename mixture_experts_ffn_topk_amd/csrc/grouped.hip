@@ -38,6 +38,8 @@ struct Place {
   MOE_DEV int pair(int src) const { return (int)__umulhi((uint32_t)src, inverse) + (src & whole); }
   MOE_DEV int within(int at) const { return min(max(at, 0), places - 1); }
   MOE_DEV int of(int src) const { return within(pair(src)); }
+  // the tensor's (below 4 GiB where it is gathered): what a tile's last columns would read past its last row is zeros
+  MOE_DEV uint32_t bytes(uint32_t ld) const { return (uint32_t)places * ld; }
 };
 
 struct GroupedParams {
@@ -322,7 +324,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     for (int j = 0; j < (kTP ? 1 : TL::kPP); ++j)
 #pragma unroll
       for (int i = 0; i < L; ++i) p_off[j][i] = off + (kTP ? i * kStep4 : j * 128 + i * kStep8) * p.p_ld;
-    p_from = resource(base, !t.ok ? 0u : kLookP ? kAll : kTP ? t_extent(true) : (uint32_t)min(p.p_cols - t.p * BP, BP) * p.p_ld);
+    p_from = resource(base, !t.ok ? 0u : kLookP ? p.p_place.bytes(p.p_ld) - p_skip : kTP ? t_extent(true) : (uint32_t)min(p.p_cols - t.p * BP, BP) * p.p_ld);
   };
   auto aim_q = [&](const TileAt& t) {
     q_k = 0;
@@ -346,7 +348,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
                                                       first + rows - 1)) * p.q_ld + chunk8 * 16;
         }
       }
-    q_from = resource(base, !t.ok ? 0u : kLookQ || look ? kAll : kTQ ? t_extent(false) : (uint32_t)min(rows, BQ) * p.q_ld);
+    q_from = resource(base, !t.ok ? 0u : kLookQ || look ? p.q_place.bytes(p.q_ld) - (kTQ ? q_skip : 0) : kTQ ? t_extent(false) : (uint32_t)min(rows, BQ) * p.q_ld);
   };
   // WGRAD: the offsets of a K-step's rows through src_info (read also where only one operand's rows are found there).  Lane l
   // of src[v] holds that of this wave's row l % (4 L) of the tile's K-step kEach v + l / (4 L): a vector load, which has to wait
@@ -826,7 +828,7 @@ __global__ __launch_bounds__(64 * W, MX ? 2 : 4) void grouped_few_kernel(Grouped
   const int p0 = tile * 16 * TP, p_rows = min(p.p_cols - p0, 16 * TP), rows = min(hi - lo, BQ);
   const bool look = p.q_place.gathered;
   const __amdgpu_buffer_rsrc_t from_p = make_rsrc(p.P + expert * p.p_expert + (long long)p0 * p.p_ld, (uint32_t)p_rows * p.p_ld);
-  const __amdgpu_buffer_rsrc_t from_q = make_rsrc(p.Q + (look ? 0 : (long long)lo * p.q_ld), look ? kAll : (uint32_t)rows * p.q_ld);
+  const __amdgpu_buffer_rsrc_t from_q = make_rsrc(p.Q + (look ? 0 : (long long)lo * p.q_ld), look ? p.q_place.bytes(p.q_ld) : (uint32_t)rows * p.q_ld);
   // the tensor's row of row r of the tile
   auto q_row = [&](int r) { return look ? p.q_place.of(p.src_info[min(lo + r, hi - 1)]) : min(r, rows - 1); };
 

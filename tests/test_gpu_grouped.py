@@ -107,6 +107,29 @@ def test_grouped_gemm_wgrad(T, E, k, n, kk, f32):
             assert torch.equal(dw.cpu(), 2 * want)
 
 
+def test_wgrad_reads_no_byte_past_the_rows_it_finds():
+    """A tensor that takes a whole allocation (45 MiB, half of an allocation of 90): the last tile's columns past the last
+    row's end lie past it."""
+    torch.cuda.empty_cache()
+    c = Case(8192, 2, 1)
+    whole_segment = torch.empty(8192, 2880, 2, dtype=torch.bfloat16, device="cuda")
+    del whole_segment
+    halves = [torch.zeros(8192, 2880, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    dout = torch.zeros(8192, 264, dtype=torch.bfloat16, device="cuda")
+    for a in halves:
+        a[:, 2879] = 1.0
+        dout[:] = 1.0
+        dw = torch.empty(2, 264, 2880, device="cuda")
+        c.moe.grouped_gemm_wgrad(c.T, dout, a, c.plan, dw, dout_rows="token", a_rows="token")
+        counts = torch.tensor([hi - lo for _, lo, hi in c.spans()], dtype=torch.float32)
+        assert torch.equal(dw[:, :, 2879].cpu(), counts[:, None].expand(2, 264))
+        assert not dw[:, :, :2879].any()
+        dw = torch.empty(2, 2880, 264, device="cuda")
+        c.moe.grouped_gemm_wgrad(c.T, a, dout, c.plan, dw, dout_rows="token", a_rows="token")
+        assert torch.equal(dw[:, 2879].cpu(), counts[:, None].expand(2, 264))
+        assert not dw[:, :2879].any()
+
+
 def codes(g, *shape):
     return torch.randint(0, 256, shape, generator=g, dtype=torch.uint8)
 
