@@ -231,6 +231,76 @@ MOE_DEV int chunk_at(int place, int r) {
 // different banks.
 MOE_DEV int trx(int r) { return 2 * (r & 3) | (r >> 3 & 1); }
 
+// ---------------------------------------------------------------- output
+// From the registers, as stores that do not wait: the loads of the next tile are under way.  A lane holds columns 4 g .. + 4
+// of row r16 of a 16 x 16 tile.  For bf16 two neighbouring tiles' lanes swap so that each has 8 in a row, and for both types
+// lanes 8 apart then, so that a store is 8 rows of whole lines: 128 bytes.  Every store is issued, those out of the output
+// with an offset that is dropped: the waits count them.
+// A wave's tile from column p0 on, rows of them there; pair: they go to src_info[first ..], up to last.
+template <int TP, int TQ, bool F32, bool WG>
+MOE_DEV void store_tile(const GroupedParams& p, const f32x4 (&acc)[TP][TQ], const uint8_t* base, int p0, int rows, bool pair,
+                        int first, int last) {
+  constexpr int kEl = F32 ? 4 : 2, kTiles = F32 ? 2 : 4;  // kTiles tiles' columns are a line
+  static_assert(TP % kTiles == 0, "lines");
+  const __amdgpu_buffer_rsrc_t to = make_rsrc(base, pair ? kAll : (uint32_t)min(rows, TQ * 16) * p.out_ld);
+  const int l = fresh(lane_id()), l16 = l & 15, lg = l >> 4, row8 = l16 & 7;
+  // (past the last column: past the resource, with any row)
+  constexpr uint32_t kPast = 0x80000000u;
+  uint32_t column[TP / kTiles];
+#pragma unroll
+  for (int c = 0; c < TP / kTiles; ++c) {
+    const int col = p0 + c * kTiles * 16 + (l16 >> 3) * (kTiles * 8) + (F32 ? 4 * lg : 16 * (lg & 1) + 8 * (lg >> 1));
+    column[c] = col < p.p_cols ? (uint32_t)col * kEl : kPast;
+  }
+  uint32_t at[2] = {(uint32_t)row8 * p.out_ld, (uint32_t)(row8 + 8) * p.out_ld};
+#pragma unroll
+  for (int j = 0; j < TQ; ++j) {
+    if (pair) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = j * 16 + h * 8 + row8, r = p.src_info[max(min(first + row, last), 0)];
+        at[h] = row < rows && (uint32_t)r < (uint32_t)p.npairs ? (uint32_t)r * p.out_ld : kNone;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < TP / kTiles; ++c) {
+      i32x4 d[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = c * kTiles + h * (kTiles / 2);
+        if constexpr (F32) {
+          d[h] = __builtin_bit_cast(i32x4, acc[i][j]);
+        } else {
+          const f32x4 u = acc[i][j], v = acc[i + 1][j];
+          const auto x = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[0], u[1]), bf16x2_rne(v[0], v[1]), false, false);
+          const auto y = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[2], u[3]), bf16x2_rne(v[2], v[3]), false, false);
+          d[h] = i32x4{(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
+        }
+      }
+      i32x4 out[2];  // rows row8: lanes 8 .. 15 take the second half of lanes 0 .. 7's; rows row8 + 8: the other way round
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        out[0][e] = __builtin_amdgcn_update_dpp(d[0][e], d[1][e], 0x128, 0xF, 0xC, false);  // row_ror:8
+        out[1][e] = __builtin_amdgcn_update_dpp(d[1][e], d[0][e], 0x128, 0xF, 0x3, false);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o = at[h] + column[c];
+        if (pair) o = at[h] == kNone || column[c] == kPast ? kNone : o;
+        if constexpr (WG && F32) {
+          if (p.accumulate) {
+            const f32x4 sum = __builtin_bit_cast(f32x4, out[h]) +
+                              __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(to, o, 0, 0));
+            out[h] = __builtin_bit_cast(i32x4, sum);
+          }
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, out[h]), to, o, 0, kStream);
+      }
+    }
+    at[0] += 16 * p.out_ld, at[1] += 16 * p.out_ld;
+  }
+}
+
 // ---------------------------------------------------------------- tiles
 // BP x BQ outputs, WP x WQ waves, each TP x TQ MFMA tiles of 16 x 16 (v_mfma_f32_16x16x32_bf16 and .._16x16x128_f8f6f4: the
 // part's power limits a loop of MFMAs alone to 2.02 and 7.19 PFLOP/s with them, to 1.80 and 6.51 with the 32 x 32 forms).  A
@@ -580,79 +650,16 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     }
   };
 
-  // ---------------------------------------------------------------- output
-  // From the registers, as stores that do not wait: the loads of the next tile are under way.  A lane holds columns 4 g .. + 4
-  // of row r16 of a 16 x 16 tile.  For bf16 two neighbouring tiles' lanes swap so that each has 8 in a row, and for both types
-  // lanes 8 apart then, so that a store is 8 rows of whole lines: 128 bytes.  Every store is issued, those out of the output
-  // with an offset that is dropped: the waits count them.
   constexpr int kStores = TP * TQ / (F32 ? 1 : 2);
   auto store = [&](const TileAt& t) {
-    constexpr int kEl = F32 ? 4 : 2, kTiles = F32 ? 2 : 4;  // kTiles tiles' columns are a line
-    static_assert(TP % kTiles == 0, "lines");
-    const int q0 = t.q * BQ + wq * TQ * 16, p0 = t.p * BP + wp * TP * 16, rows = max((WG ? p.q_cols : t.hi - t.lo) - q0, 0);
+    const int q0 = t.q * BQ + wq * TQ * 16, p0 = t.p * BP + wp * TP * 16;
+    const bool pair = !WG && p.out_pair;
     const uint8_t* base = p.out;
     if (WG)
       base += t.expert * p.out_expert + (long long)q0 * p.out_ld;
-    else if (!p.out_pair)
+    else if (!pair)
       base += ((long long)t.lo + q0) * p.out_ld;
-    const bool pair = !WG && p.out_pair;
-    const __amdgpu_buffer_rsrc_t to = make_rsrc(base, pair ? kAll : (uint32_t)min(rows, TQ * 16) * p.out_ld);
-    const int l16 = fresh(r16), lg = fresh(g), row8 = l16 & 7;
-    // (past the last column: past the resource, with any row)
-    constexpr uint32_t kPast = 0x80000000u;
-    uint32_t column[TP / kTiles];
-#pragma unroll
-    for (int c = 0; c < TP / kTiles; ++c) {
-      const int col = p0 + c * kTiles * 16 + (l16 >> 3) * (kTiles * 8) + (F32 ? 4 * lg : 16 * (lg & 1) + 8 * (lg >> 1));
-      column[c] = col < p.p_cols ? (uint32_t)col * kEl : kPast;
-    }
-    uint32_t at[2] = {(uint32_t)row8 * p.out_ld, (uint32_t)(row8 + 8) * p.out_ld};
-#pragma unroll
-    for (int j = 0; j < TQ; ++j) {
-      if (pair) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = j * 16 + h * 8 + row8, r = p.src_info[max(min(t.lo + q0 + row, t.hi - 1), 0)];
-          at[h] = row < rows && (uint32_t)r < (uint32_t)p.npairs ? (uint32_t)r * p.out_ld : kNone;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < TP / kTiles; ++c) {
-        i32x4 d[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = c * kTiles + h * (kTiles / 2);
-          if constexpr (F32) {
-            d[h] = __builtin_bit_cast(i32x4, acc[i][j]);
-          } else {
-            const f32x4 u = acc[i][j], v = acc[i + 1][j];
-            const auto x = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[0], u[1]), bf16x2_rne(v[0], v[1]), false, false);
-            const auto y = __builtin_amdgcn_permlane16_swap(bf16x2_rne(u[2], u[3]), bf16x2_rne(v[2], v[3]), false, false);
-            d[h] = i32x4{(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
-          }
-        }
-        i32x4 out[2];  // rows row8: lanes 8 .. 15 take the second half of lanes 0 .. 7's; rows row8 + 8: the other way round
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          out[0][e] = __builtin_amdgcn_update_dpp(d[0][e], d[1][e], 0x128, 0xF, 0xC, false);  // row_ror:8
-          out[1][e] = __builtin_amdgcn_update_dpp(d[1][e], d[0][e], 0x128, 0xF, 0x3, false);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t o = at[h] + column[c];
-          if (pair) o = at[h] == kNone || column[c] == kPast ? kNone : o;
-          if constexpr (WG && F32) {
-            if (p.accumulate) {
-              const f32x4 sum = __builtin_bit_cast(f32x4, out[h]) +
-                                __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(to, o, 0, 0));
-              out[h] = __builtin_bit_cast(i32x4, sum);
-            }
-          }
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, out[h]), to, o, 0, kStream);
-        }
-      }
-      at[0] += 16 * p.out_ld, at[1] += 16 * p.out_ld;
-    }
+    store_tile<TP, TQ, F32, WG>(p, acc, base, p0, max((WG ? p.q_cols : t.hi - t.lo) - q0, 0), pair, t.lo + q0, t.hi - 1);
   };
 
   // ---------------------------------------------------------------- K loop
@@ -982,6 +989,74 @@ __global__ __launch_bounds__(64 * W, MX ? 2 : 4) void grouped_few_kernel(Grouped
   }
 }
 
+// ---------------------------------------------------------------- weight gradients of few rows
+// With few rows an expert its gradient is written, not computed: a workgroup takes 128 x 128 of it, reads 64 rows of both
+// operands at a time into LDS, and ends with its stores on their way; others of the compute unit's four load meanwhile.  (513
+// tokens' gradients of 128 experts of 5760 x 2880, 16 rows each, bf16: 725 us, 5.9 TB/s; with the tiles above 985, whose next
+// tile waits for the stores.)
+template <bool F32, int WHERE>
+__global__ __launch_bounds__(256, 4) void grouped_wgrad_few_kernel(GroupedParams p) {
+  constexpr int kPart = 64 * 256, TP = 4, TQ = 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kPart];
+  const int lane = lane_id(), wave = scalar((int)threadIdx.x >> 6), g = lane >> 4, r16 = lane & 15;
+  const int up = quotient((int)blockIdx.x, p.p_tiles, p.group_inverse), tp = (int)blockIdx.x - up * p.p_tiles;
+  const int expert = up / p.q_tiles, tq = up - expert * p.q_tiles;
+  const int lo = scalar(row_at(p, expert)), hi = max(lo, scalar(row_at(p, expert + 1)));
+  const uint32_t lds0 = lds_address(lds);
+  f32x4 acc[TP][TQ];
+#pragma unroll
+  for (int i = 0; i < TP; ++i)
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int t_row = 8 * g + (r16 >> 2);
+  const uint32_t t_lane = t_row * 256 + (trx(t_row) << 5) + (lane & 3) * 8;
+  auto frag = [&](uint32_t part, int tile, int s) {
+    const uint32_t a = (part + t_lane + s * (32 * 256)) ^ (uint32_t)(tile << 5);
+    const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4*)a);
+    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS3 s16x4*)(a + 4 * 256));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  for (int k0 = lo; k0 < hi; k0 += 64) {
+    const int subs = hi - k0 > 32 ? 2 : 1;
+    const i32x4 from_p = resource(p.P + ((WHERE & 1) ? 0 : (long long)k0 * p.p_ld) + tp * 256, kAll);
+    const i32x4 from_q = resource(p.Q + ((WHERE & 2) ? 0 : (long long)k0 * p.q_ld) + tq * 256, kAll);
+    uint32_t p_off[4], q_off[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // rows 16 i + 4 wave + lane / 16
+      const int l = i * 16 + wave * 4 + g, r = min(k0 + l, hi - 1), src = WHERE ? p.src_info[r] : 0;
+      const uint32_t column = ((((uint32_t)r16 >> 1) ^ trx(wave * 4 + g)) << 5) + (r16 & 1) * 16;
+      const bool in = k0 + l < hi;
+      const uint32_t pr = (WHERE & 1) ? p.p_place.of(src) : r - k0, qr = (WHERE & 2) ? p.q_place.of(src) : r - k0;
+      p_off[i] = in && tp * 256 + column < p.p_ld ? pr * p.p_ld + column : kNone;
+      q_off[i] = in && tq * 256 + column < p.q_ld ? qr * p.q_ld + column : kNone;
+    }
+    if (k0 > lo) __syncthreads();  // (the rows before are read)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= 2 * subs) break;
+      lds_copy16(from_p, p_off[i], lds0 + (i * 4 + wave) * 1024);
+      lds_copy16(from_q, q_off[i], lds0 + kPart + (i * 4 + wave) * 1024);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    for (int s = 0; s < subs; ++s) {
+      bf16x8 a[TP], b[TQ];
+#pragma unroll
+      for (int i = 0; i < TP; ++i) a[i] = frag(lds0, (wave & 1) * TP + i, s);
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) b[j] = frag(lds0 + kPart, (wave >> 1) * TQ + j, s);
+#pragma unroll
+      for (int i = 0; i < TP; ++i)
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+    }
+  }
+  const int q0 = tq * 128 + (wave >> 1) * (TQ * 16);
+  store_tile<TP, TQ, F32, true>(p, acc, p.out + expert * p.out_expert + (long long)q0 * p.out_ld, tp * 128 + (wave & 1) * (TP * 16),
+                                max(p.q_cols - q0, 0), false, 0, 0);
+}
+
 // Compute units of the current device (cached per device).
 int device_cus() {
   static int cus[64] = {};
@@ -1081,6 +1156,17 @@ hipError_t launch_rows(GroupedParams& p, hipStream_t s) {
 
 template <bool F32, int WHERE>
 hipError_t launch_wgrad(GroupedParams& p, hipStream_t s) {
+  // Rows an expert, on average (us measured, 128 experts of 5760 x 2880; bf16: 16 rows 725, 48 805, 64 1112, with the large
+  // tile 985, 991, 1036; fp32: 16 1574, 64 1585, 128 2097, with it 1594, 1657, 1822):
+  const long long groups = std::max(1, std::min(p.npairs, p.E)), rows = (p.npairs + groups - 1) / groups;
+  const long long tiles = (long long)p.E * ((p.p_cols + 127) / 128) * ((p.q_cols + 127) / 128);
+  if (rows <= (F32 ? 64 : 48) && tiles * 256 < 1LL << 32) {
+    p.p_tiles = (p.p_cols + 127) / 128;
+    p.q_tiles = (p.q_cols + 127) / 128;
+    p.group_inverse = (uint32_t)((1ull << 32) / p.p_tiles);
+    grouped_wgrad_few_kernel<F32, WHERE><<<dim3((unsigned)tiles), dim3(256), 0, s>>>(p);
+    return hipGetLastError();
+  }
   // (16 experts of 512 x 512, 256 rows each: 11 us, with the large tile 20; from a tile a CU on the large one is as fast)
   if ((long long)p.E * ((p.p_cols + 255) / 256) * ((p.q_cols + 255) / 256) < device_cus())
     return launch_tile<Op::WGRAD, 128, 128, 2, 2, 5, F32, WHERE>(p, s);
