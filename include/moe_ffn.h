@@ -498,8 +498,8 @@ moe_status moe_forward_few(const moe_handle* h, int32_t num_tokens, const void* 
    expert_start_indices and (in all calls but moe_swiglu*) src_info are read.  Rows behind the last expert's
    are left as they are.  Handles of any format; sizes n and k are the call's own (a layer's gate_up: n = 2I, k =
    H; down: n = H, k = I).  A plan that is none is never followed out of a buffer.
-   num_tokens x num_topk above 2^26, n or k above 2^20, more than 2^31 tiles, and a tensor of 4 GiB and more whose rows
-   are in token or pair order are MOE_ERR_UNSUPPORTED (in the plan's order they may be any size). */
+   n or k above 2^20, more than 2^31 tiles of 128 x 128, and a tensor of 4 GiB and more whose rows are in token or pair
+   order are MOE_ERR_UNSUPPORTED (in the plan's order they may be any size).  No output overlaps the plan. */
 
 /* Where a plan row r lies in a tensor of rows. */
 typedef enum {

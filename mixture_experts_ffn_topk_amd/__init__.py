@@ -841,22 +841,34 @@ class MoEFFN:
                                                bool(accumulate), _current_stream() if stream is None else
                                                _stream(stream)), "moe_grouped_gemm_wgrad")
 
-    def quantize_mxfp4(self, x, q, sf, values=None, stream=None):
+    def quantize_mxfp4(self, x, q, sf, values=None, rows=None, cols=None, row_stride=None, stream=None):
         """moe_quantize_mxfp4: the rows of x [..., cols] (a bf16 or fp32 tensor; two dimensions with any row stride, or
-        contiguous) to packed codes q and scales sf, and values (bf16): what the codes stand for."""
+        contiguous) to packed codes q and scales sf, and values (bf16): what the codes stand for.  rows, cols and
+        row_stride (elements) go with a raw address x, which is bf16."""
         import torch
-        f32 = (cols := x.shape[-1]) and x.dtype is torch.float32
-        rows = x.numel() // max(1, cols)
-        stride = x.stride(0) if x.dim() == 2 and rows > 1 else cols
-        if x.dim() == 2 and rows > 0 and x.stride(1) == 1 and stride >= cols:
-            flat = x.as_strided((1, (rows - 1) * stride + cols), ((rows - 1) * stride + cols, 1)) if stride != cols else x
+        f32 = getattr(x, "dtype", None) is torch.float32
+        if x is None or isinstance(x, int):
+            if rows is None or cols is None:
+                raise ValueError("rows and cols are required where x is a raw address")
+            flat, stride = x, cols if row_stride is None else row_stride
         else:
-            flat, stride = x, cols  # (_need refuses other strides)
+            have = (x.numel() // max(1, x.shape[-1]), x.shape[-1]) if x.dim() else (0, 0)
+            if (rows is not None and rows != have[0]) or (cols is not None and cols != have[1]):
+                raise ValueError(f"x gives rows, cols = {have}, the call {(rows, cols)}")
+            rows, cols = have
+            stride = x.stride(0) if x.dim() == 2 and rows > 1 else cols
+            if x.dim() == 2 and rows > 0 and x.stride(1) == 1 and stride >= cols:
+                span = (rows - 1) * stride + cols
+                flat = x.as_strided((1, span), (span, 1)) if stride != cols else x
+            else:
+                flat, stride = x, cols  # (_need refuses other strides)
+            if row_stride is not None and row_stride != stride:
+                raise ValueError(f"x has a row stride of {stride}, the call {row_stride}")
         codes = _byte_types()
         xp, qp, sp, vp = self._tensors(
             [("x", flat, 0, (torch.bfloat16, torch.float32), True), ("q", q, rows * cols // 2, codes, True),
              ("sf", sf, rows * (cols // 32), codes, True), ("values", values, rows * cols * 2, (torch.bfloat16,), False)])
-        _check(self.lib.moe_quantize_mxfp4(self._h, rows, cols, xp, bool(f32), stride, qp, sp, vp,
+        _check(self.lib.moe_quantize_mxfp4(self._h, rows, cols, xp, f32, stride, qp, sp, vp,
                                            _current_stream() if stream is None else _stream(stream)),
                "moe_quantize_mxfp4")
 

@@ -277,7 +277,8 @@ bool router_supported(const moe_config& c, int T) {
 }
 
 // ---------------------------------------------------------------- products by expert
-constexpr int kGroupedMaxPairs = 1 << 26, kGroupedMaxSide = 1 << 20;
+// (T * k is below 2^26: a handle's T * k * I is below 2^31, its I at least 32.)
+constexpr int kGroupedMaxSide = 1 << 20;
 
 bool flag(int32_t v) { return v == 0 || v == 1; }
 bool row_order(int32_t v) { return v >= MOE_ROWS_PLAN && v <= MOE_ROWS_PAIR; }
@@ -294,6 +295,13 @@ bool any_overlap(const Span& a, std::initializer_list<Span> others) {
   return false;
 }
 
+Span starts_of(const moe_config& c, const moe_plan_buffers* plan) {
+  return Span{plan->expert_start_indices, ((size_t)c.num_experts + 1) * 4, 0};
+}
+Span sources_of(const moe_config& c, const moe_plan_buffers* plan, int T) {
+  return Span{plan->src_info, (size_t)T * c.num_topk * 4, 0};
+}
+
 // What moe_grouped_gemm and moe_grouped_gemm_mxfp4 share; bits: of an operand's element.
 moe_status grouped_gemm(const moe_handle* h, int32_t T, int32_t n, int32_t k, const void* a, const void* a_sf,
                         int32_t a_rows, const void* w, const void* w_sf, int32_t w_kn, const moe_plan_buffers* plan,
@@ -307,10 +315,10 @@ moe_status grouped_gemm(const moe_handle* h, int32_t T, int32_t n, int32_t k, co
   const size_t bits = mx ? 4 : 16, ar = rows_of(c, T, a_rows), wr = (size_t)c.num_experts * n;
   if (any_overlap(Span{out, rows_of(c, T, MOE_ROWS_PAIR) * n * (out_fp32 ? 4 : 2), 0},
                   {Span{a, ar * k / 8 * bits, 0}, Span{w, wr * k / 8 * bits, 0}, Span{a_sf, ar * k / 32, 0},
-                   Span{w_sf, wr * k / 32, 0}}))
+                   Span{w_sf, wr * k / 32, 0}, starts_of(c, plan), sources_of(c, plan, T)}))
     return MOE_ERR_INVALID_ARGUMENT;
-  if (out_rows == MOE_ROWS_TOKEN || (long long)T * c.num_topk > kGroupedMaxPairs || n > kGroupedMaxSide ||
-      k > kGroupedMaxSide || !moe::grouped_gemm_fits(T * c.num_topk, c.num_experts, n) ||
+  if (out_rows == MOE_ROWS_TOKEN || n > kGroupedMaxSide || k > kGroupedMaxSide ||
+      !moe::grouped_gemm_fits(T * c.num_topk, c.num_experts, n) ||
       !placed(c, T, a_rows, k / 8 * bits) || !placed(c, T, out_rows, (size_t)n * (out_fp32 ? 4 : 2)))
     return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
@@ -783,10 +791,11 @@ moe_status moe_grouped_gemm_wgrad(const moe_handle* h, int32_t T, int32_t n, int
   if (!al(dout, 16) || !al(a, 16) || !al(dw, 16)) return MOE_ERR_INVALID_ARGUMENT;
   const moe_config& c = h->cfg;
   if (any_overlap(Span{dw, (size_t)c.num_experts * n * k * (dw_fp32 ? 4 : 2), 0},
-                  {Span{dout, rows_of(c, T, dout_rows) * n * 2, 0}, Span{a, rows_of(c, T, a_rows) * k * 2, 0}}))
+                  {Span{dout, rows_of(c, T, dout_rows) * n * 2, 0}, Span{a, rows_of(c, T, a_rows) * k * 2, 0},
+                   starts_of(c, plan), sources_of(c, plan, T)}))
     return MOE_ERR_INVALID_ARGUMENT;
-  if ((accumulate && !dw_fp32) || (long long)T * c.num_topk > kGroupedMaxPairs || n > kGroupedMaxSide ||
-      k > kGroupedMaxSide || !moe::grouped_wgrad_fits(c.num_experts, n, k) || !placed(c, T, dout_rows, (size_t)n * 2) ||
+  if ((accumulate && !dw_fp32) || n > kGroupedMaxSide || k > kGroupedMaxSide ||
+      !moe::grouped_wgrad_fits(c.num_experts, n, k) || !placed(c, T, dout_rows, (size_t)n * 2) ||
       !placed(c, T, a_rows, (size_t)k * 2))
     return MOE_ERR_UNSUPPORTED;
   const moe::WgradArgs g{c.num_experts, c.num_topk, T, plan->expert_start_indices, plan->src_info, n, k, dout,
@@ -819,9 +828,10 @@ moe_status moe_swiglu(const moe_handle* h, int32_t T, const void* gu, const moe_
   if (!al(gu, 16) || !al(h_out, 16) || !al(q, 16) || !al(sf, 4)) return MOE_ERR_INVALID_ARGUMENT;
   const moe_config& c = h->cfg;
   const size_t n = (size_t)T * c.num_topk * c.intermediate_hidden;
-  const Span in{gu, n * 4, 0}, oh{h_out, n * 2, 0}, oq{q, n / 2, 0}, os{sf, n / 32, 0};
-  if (any_overlap(oh, {in, oq, os}) || any_overlap(oq, {in, os}) || any_overlap(os, {in})) return MOE_ERR_INVALID_ARGUMENT;
-  if ((long long)T * c.num_topk > kGroupedMaxPairs) return MOE_ERR_UNSUPPORTED;
+  const Span in{gu, n * 4, 0}, oh{h_out, n * 2, 0}, oq{q, n / 2, 0}, os{sf, n / 32, 0},
+      ps = starts_of(c, plan);
+  if (any_overlap(oh, {in, oq, os, ps}) || any_overlap(oq, {in, os, ps}) || any_overlap(os, {in, ps}))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (T == 0) return MOE_OK;
   const moe::SwigluArgs a{c.num_experts, T * c.num_topk, c.intermediate_hidden, plan->expert_start_indices,
                           c.activation_clamp, c.fast_math != 0, gu, nullptr, h_out, q, sf, nullptr};
@@ -837,9 +847,9 @@ moe_status moe_swiglu_backward(const moe_handle* h, int32_t T, const void* gu, c
   const size_t n = (size_t)T * c.num_topk * c.intermediate_hidden;
   // (a thread reads the gate, up and dh elements whose gradients and value it writes, no others)
   const Span ig{gu, n * 4, 4}, id{dh, n * 2, 2}, od{dgu, n * 4, 4}, oh{h_out, n * 2, 2};
-  if (!apart_or_same(od, ig) || !apart_or_same(oh, id) || any_overlap(od, {id, oh}) || any_overlap(oh, {ig}))
+  if (!apart_or_same(od, ig) || !apart_or_same(oh, id) || any_overlap(od, {id, oh, starts_of(c, plan)}) ||
+      any_overlap(oh, {ig, starts_of(c, plan)}))
     return MOE_ERR_INVALID_ARGUMENT;
-  if ((long long)T * c.num_topk > kGroupedMaxPairs) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   const moe::SwigluArgs a{c.num_experts, T * c.num_topk, c.intermediate_hidden, plan->expert_start_indices,
                           c.activation_clamp, c.fast_math != 0, gu, dh, h_out, nullptr, nullptr, dgu};

@@ -13,6 +13,7 @@
 // is staged as rows of 128 bytes and read with ds_read_b128; the others (T: transposed) as 64 summed rows of all the
 // tile's columns, read with ds_read_b64_tr_b16, which hands a lane 4 summed rows of its column.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "gemm_common.h"
@@ -1077,15 +1078,15 @@ __global__ __launch_bounds__(256, 4) void grouped_wgrad_few_kernel(GroupedParams
 
 // Compute units of the current device (cached per device).
 int device_cus() {
-  static int cus[64] = {};
+  static std::atomic<int> cus[64];
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
-  if (cus[dev] == 0) {
-    int n = 0;
+  int n = cus[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
-    cus[dev] = n;
+    cus[dev].store(n, std::memory_order_relaxed);
   }
-  return cus[dev];
+  return n;
 }
 
 template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS, bool F32, int WHERE = 0>
