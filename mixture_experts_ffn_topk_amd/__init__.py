@@ -762,18 +762,33 @@ class MoEFFN:
 
     # ---------------------------------------------------------------- products by expert outside the fused layer
     def _tensors(self, given):
-        """The addresses of (name, tensor, bytes, dtypes, required) arguments, checked as every call's are."""
-        ptrs = None
-        if not any(t is None and required for _, t, _, _, required in given):
-            ptrs = _fit([(t, size, kinds) for _, t, size, kinds, _ in given])
-        if ptrs is None:
-            for name, t, size, kinds, required in given:
-                if t is None and required:
-                    raise ValueError(f"{name} is required")
-                _need(t, name, size, kinds, required=required)
-            _on_current_gpu(**{name: t for name, t, *_ in given})
-            ptrs = [_ptr(t) for _, t, *_ in given]
-        return ptrs
+        """The addresses of (name, tensor, bytes, dtypes, required) arguments, checked as every call's are (and as _fit
+        does first in one pass)."""
+        import torch
+        cur, ptrs = None, []
+        try:
+            for _, t, nbytes, kinds, required in given:
+                if t is None and not required:
+                    ptrs.append(None)
+                elif t.dtype in kinds and t.nbytes >= nbytes and t.is_contiguous():
+                    device = t.get_device()
+                    if device != cur:
+                        if cur is not None or not t.is_cuda or device != torch._C._cuda_getDevice():
+                            break
+                        cur = device
+                    ptrs.append(t.data_ptr())
+                else:
+                    break
+            else:
+                return ptrs
+        except AttributeError:  # (None, a raw address)
+            pass
+        for name, t, size, kinds, required in given:
+            if t is None and required:
+                raise ValueError(f"{name} is required")
+            _need(t, name, size, kinds, required=required)
+        _on_current_gpu(**{name: t for name, t, *_ in given})
+        return [_ptr(t) for _, t, *_ in given]
 
     @staticmethod
     def _order(name, value):
@@ -790,9 +805,10 @@ class MoEFFN:
             if n is None or k is None:
                 raise ValueError(f"n and k are required where {what} is a raw address")
             return n, k
-        if t.dim() != 3 or t.shape[0] != self.experts:
-            raise ValueError(f"{what} must be [{self.experts}, .., ..] (got {list(t.shape)})")
-        have = (t.shape[2], t.shape[1]) if swapped else (t.shape[1], t.shape[2])
+        shape = t.shape
+        if len(shape) != 3 or shape[0] != self.experts:
+            raise ValueError(f"{what} must be [{self.experts}, .., ..] (got {list(shape)})")
+        have = (shape[2], shape[1]) if swapped else (shape[1], shape[2])
         if (n is not None and n != have[0]) or (k is not None and k != have[1]):
             raise ValueError(f"{what} gives n, k = {have}, the call {(n, k)}")
         return have
