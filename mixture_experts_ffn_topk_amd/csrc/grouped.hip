@@ -65,7 +65,7 @@ struct GroupedParams {
   int out_pair;          // rows go to src_info[r]
   int accumulate;
   int p_tiles, q_tiles;  // q_tiles: WGRAD only
-  uint32_t group_inverse;  // floor(2^32 / (8 p_tiles)); few rows: floor(2^32 / p_tiles)
+  uint32_t p_inverse;    // floor(2^32 / p_tiles), of the kernels for few rows
 };
 
 // Direct-to-LDS loads: lane l's 16 (12) bytes land at l + 16 l; what lies out of the resource's bounds is zeros.
@@ -128,7 +128,7 @@ struct TileAt {
   int q, p;            // tile indices within the expert
 };
 
-// The tiles of a workgroup, one after the other.  Tiles lie expert by expert, in groups of GQ q-tiles, within a group
+// The tiles of a workgroup, one after the other.  Tiles lie expert by expert, in groups of up to GQ q-tiles, within a group
 // p-tile by p-tile, and each XCD takes a contiguous eighth, its workgroups in turn: what an XCD runs at once then shares few
 // operand panels in its L2.  WGRAD, whose tiles cost what their expert has rows: an expert's tiles go in chunks of one for
 // each workgroup of an XCD, the chunks to the XCDs in turn, so that an XCD's workgroups walk the same rows at the same time
@@ -207,13 +207,10 @@ struct Walk {
     }
     at += step;
     within = scalar(within);
-    const int group = quotient(within, GQ * p.p_tiles, p.group_inverse), q0 = group * GQ, size = min(GQ, q_tiles - q0);
-    const int in = within - group * GQ * p.p_tiles;
-    // (ceil(2^32 / size): exact for numbers below 2^29)
-    static_assert(GQ == 8, "the sizes below");
-    const uint32_t inverse = size == 8 ? 0x20000000u : size == 7 ? 0x24924925u : size == 6 ? 0x2AAAAAABu : size == 5 ? 0x33333334u
-                             : size == 4 ? 0x40000000u : size == 3 ? 0x55555556u : 0x80000000u;
-    t.p = size == 1 ? in : (int)__umulhi((uint32_t)in, inverse);
+    // (groups of about the same size: with 9 q-tiles, 8 and 1 would leave a group whose p panels are read by one workgroup each)
+    const int groups = (q_tiles + GQ - 1) / GQ, most = (q_tiles + groups - 1) / groups;
+    const int q0 = within / (most * p.p_tiles) * most, size = min(most, q_tiles - q0), in = within - q0 * p.p_tiles;
+    t.p = in / size;
     t.q = q0 + in - t.p * size;
     t.expert = scalar(t.expert);
     t.lo = scalar(t.lo);
@@ -780,9 +777,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
       __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(EARLY * L));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    if (change) {
-      aim_sf(then);
-    }
+    if (change) aim_sf(then);
     // (the scales that are read next are the next tile's)
     if (ODD && ks == steps - 1) aim_shifts(then);
     const int ks_next = ks + 1 == steps ? 0 : ks + 1;
@@ -830,7 +825,7 @@ __global__ __launch_bounds__(64 * W, MX ? 2 : 4) void grouped_few_kernel(Grouped
   __shared__ __attribute__((aligned(16))) float sums[W][BQ][16 * TP + 4];
   const int lane = lane_id(), wave = scalar((int)threadIdx.x >> 6), g = lane >> 4, r16 = lane & 15;
   // the workgroup's tile: q-tiles lie expert by expert, and each has all of its weight tiles in turn
-  int slot = quotient((int)blockIdx.x, p.p_tiles, p.group_inverse);
+  int slot = quotient((int)blockIdx.x, p.p_tiles, p.p_inverse);
   const int tile = (int)blockIdx.x - slot * p.p_tiles;
   int expert = -1, lo = 0, hi = 0;
   for (int e0 = 0; e0 < p.E; e0 += 64) {
@@ -1018,7 +1013,7 @@ __global__ __launch_bounds__(256, 4) void grouped_wgrad_few_kernel(GroupedParams
   constexpr int kPart = 64 * 256, TP = 4, TQ = 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kPart];
   const int lane = lane_id(), wave = scalar((int)threadIdx.x >> 6), g = lane >> 4, r16 = lane & 15;
-  const int up = quotient((int)blockIdx.x, p.p_tiles, p.group_inverse), tp = (int)blockIdx.x - up * p.p_tiles;
+  const int up = quotient((int)blockIdx.x, p.p_tiles, p.p_inverse), tp = (int)blockIdx.x - up * p.p_tiles;
   const int expert = up / p.q_tiles, tq = up - expert * p.q_tiles;
   const int lo = scalar(row_at(p, expert)), hi = max(lo, scalar(row_at(p, expert + 1)));
   const uint32_t lds0 = lds_address(lds);
@@ -1092,7 +1087,6 @@ int device_cus() {
 template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS, bool F32, int WHERE = 0>
 hipError_t launch_tile(GroupedParams& p, hipStream_t s) {
   p.p_tiles = (p.p_cols + BP - 1) / BP;
-  p.group_inverse = (uint32_t)((1ull << 32) / (8 * p.p_tiles));
   long long tiles;
   if (O == Op::WGRAD) {
     p.q_tiles = (p.q_cols + BQ - 1) / BQ;
@@ -1119,7 +1113,7 @@ bool few_fits(const GroupedParams& p, int TP, int TQ, int W) { return few_tiles(
 template <bool MX, int TP, int TQ, int W, bool F32>
 hipError_t launch_few(GroupedParams& p, hipStream_t s) {
   p.p_tiles = (p.p_cols + 16 * TP - 1) / (16 * TP);
-  p.group_inverse = (uint32_t)((1ull << 32) / p.p_tiles);
+  p.p_inverse = (uint32_t)((1ull << 32) / p.p_tiles);
   const long long tiles = few_tiles(p, TP, TQ);
   if (tiles == 0) return hipSuccess;
   grouped_few_kernel<MX, TP, TQ, W, F32><<<dim3((unsigned)tiles), dim3(64 * W), 0, s>>>(p);
@@ -1182,7 +1176,7 @@ hipError_t launch_wgrad(GroupedParams& p, hipStream_t s) {
   if (rows <= (F32 ? 64 : 48) && tiles * 256 < 1LL << 32) {
     p.p_tiles = (p.p_cols + 127) / 128;
     p.q_tiles = (p.q_cols + 127) / 128;
-    p.group_inverse = (uint32_t)((1ull << 32) / p.p_tiles);
+    p.p_inverse = (uint32_t)((1ull << 32) / p.p_tiles);
     grouped_wgrad_few_kernel<F32, WHERE><<<dim3((unsigned)tiles), dim3(256), 0, s>>>(p);
     return hipGetLastError();
   }
