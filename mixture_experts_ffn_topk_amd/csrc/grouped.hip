@@ -76,11 +76,11 @@ constexpr uint32_t kAll = 0xFFFFF000u, kNone = kAll;  // the largest resource, a
 // would move the place in LDS with it.)
 MOE_DEV void lds_copy16(i32x4 rsrc, uint32_t voff, uint32_t l) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(l), "v"(voff), "s"(rsrc)
-               : "memory");
+               : "m0", "memory");
 }
 MOE_DEV void lds_copy12(i32x4 rsrc, uint32_t voff, uint32_t l) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx3 %1, %2, 0 offen lds" ::"s"(l), "v"(voff), "s"(rsrc)
-               : "memory");
+               : "m0", "memory");
 }
 MOE_DEV uint32_t lds_address(const void* l) { return (uint32_t)(uintptr_t)(const LDS3 void*)l; }
 
@@ -197,8 +197,14 @@ struct Walk {
     } else {
       t.ok = at < end;
       if (!t.ok) return t;
-      while (at >= __builtin_amdgcn_readlane(upto, 63)) before = __builtin_amdgcn_readlane(upto, 63), chunk(p, e0 + 64);
-      const int l = __ffsll((unsigned long long)__ballot(upto > at)) - 1;
+      while (at >= __builtin_amdgcn_readlane(upto, 63) && e0 + 64 < p.E)
+        before = __builtin_amdgcn_readlane(upto, 63), chunk(p, e0 + 64);
+      const unsigned long long later = __ballot(upto > at);
+      if (!later) {  // (a plan that changed meanwhile)
+        t.ok = false;
+        return t;
+      }
+      const int l = __ffsll(later) - 1;
       t.expert = e0 + l;
       t.lo = row_at(p, t.expert);
       t.hi = max(t.lo, row_at(p, t.expert + 1));

@@ -113,6 +113,13 @@ def test_many_tiles_wgrad(T, E, k, n, kk, f32, accumulate):
         check_wgrad(c, n, kk, *orders, f32, accumulate)
 
 
+@pytest.mark.parametrize("kk", [32, 64, 128, 512, 640, 1152])
+def test_mxfp4_k_steps(kk):
+    """One to five K-steps of 256, scales of whole words or not, over several tiles a workgroup."""
+    check_mx(Fixed(2, even_ids(600, 2)), 25608, kk, "token", "pair", False)
+    check_mx(Fixed(2, even_ids(600, 2)), 264, kk, "plan", "plan", True)
+
+
 def test_an_expert_with_all_rows():
     """The mean chooses the kernel for few rows, and one expert has them all."""
     c = Fixed(200, torch.full((600, 1), 7))
