@@ -70,35 +70,37 @@ struct GroupedParams {
 
 // Direct-to-LDS loads: lane l's 16 (12) bytes land at l + 16 l; what lies out of the resource's bounds is zeros.
 // Written so that the compiler does not see stores to LDS: it lets no ds_read_b64_tr pass one in flight.  The kernel's own
-// waits order the two.
+// waits order the two.  (m0 is no register that it keeps values in: it writes it right before what reads it, as here.
+// Nor does it count the five states that have to pass between a vector instruction that writes a scalar register of the
+// resource and such a load: settled() spends them where resources are made.  In the loads themselves they cost 1 %.)
 constexpr uint32_t kAll = 0xFFFFF000u, kNone = kAll;  // the largest resource, an offset out of it (with what is added)
 // (The offsets are the lanes' own: a scalar one may wrap the check against the resource's end, and the instruction's own
 // would move the place in LDS with it.)
 MOE_DEV void lds_copy16(i32x4 rsrc, uint32_t voff, uint32_t l) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(l), "v"(voff), "s"(rsrc)
-               : "m0", "memory");
+               : "memory");
 }
 MOE_DEV void lds_copy12(i32x4 rsrc, uint32_t voff, uint32_t l) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx3 %1, %2, 0 offen lds" ::"s"(l), "v"(voff), "s"(rsrc)
-               : "m0", "memory");
+               : "memory");
 }
 MOE_DEV uint32_t lds_address(const void* l) { return (uint32_t)(uintptr_t)(const LDS3 void*)l; }
 
 // A value that is the same in every lane, in a scalar register.
 MOE_DEV int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
-MOE_DEV const uint8_t* scalar(const uint8_t* v) {
-  const uint64_t b = (uint64_t)v;
-  return (const uint8_t*)((uint64_t)(uint32_t)scalar((int)(uint32_t)b) | (uint64_t)(uint32_t)scalar((int)(uint32_t)(b >> 32)) << 32);
-}
 // The same value, of which the compiler knows nothing: what follows from it is computed where it is used, not kept in
 // registers through the K loop.
 MOE_DEV int fresh(int v) {
   asm volatile("" : "+v"(v));
   return v;
 }
+MOE_DEV i32x4 settled(i32x4 rsrc) {
+  asm volatile("s_nop 4" : "+s"(rsrc));
+  return rsrc;
+}
 MOE_DEV i32x4 resource(const void* base, uint32_t bytes) {
   const uint64_t b = (uint64_t)base;
-  return i32x4{scalar((int)(uint32_t)b), scalar((int)(uint32_t)(b >> 32)), scalar((int)bytes), 0x00020000};
+  return settled(i32x4{scalar((int)(uint32_t)b), scalar((int)(uint32_t)(b >> 32)), scalar((int)bytes), 0x00020000});
 }
 
 MOE_DEV int wave_scan(int v) {  // inclusive
@@ -533,7 +535,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     if ((isP ? kLookP : kLookQ) || k0 + BK <= K) return;
     if (tr) {
       i32x4& from = isP ? p_from : q_from;
-      if (from[2]) from[2] = scalar((int)t_extent(isP));
+      if (from[2]) from = settled(i32x4{from[0], from[1], scalar((int)t_extent(isP)), from[3]});
     } else {
       const bool none = k0 + chunk8 * (MX ? 32 : 8) >= K;
 #pragma unroll
