@@ -336,7 +336,7 @@ struct GTile {
   static constexpr bool kTP = O == Op::GRAD || O == Op::WGRAD, kTQ = O == Op::WGRAD;
   static constexpr int kPart = 16384, kPP = BP / 128, kPQ = BQ / 128, kParts = kPP + kPQ;
   static constexpr int kL = 16 / kWaves;  // a wave's loads of a part
-  static constexpr int kSf = O == Op::MX ? (BP + BQ) * 16 : 0;  // a K-step's scales: the words that hold a row's 8
+  static constexpr int kSf = O == Op::MX ? (BP + BQ) * 16 : 0;  // scales: the words that hold a row's 8 (or two K-steps' 16)
   static constexpr int kLds = SLOTS * kPart + 2 * kSf;
   static constexpr int kBK = O == Op::MX ? 256 : 64;  // elements of a K-step
   static constexpr int kEarly = SLOTS - 2 * kParts;   // parts in flight past the next K-step's
@@ -352,8 +352,8 @@ template <Op O, int BP, int BQ, int WP, int WQ, int SLOTS, bool F32, int WHERE>
 __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams p) {
   using TL = GTile<O, BP, BQ, WP, WQ, SLOTS>;
   constexpr bool MX = O == Op::MX, WG = O == Op::WGRAD, kTP = TL::kTP, kTQ = TL::kTQ;
-  constexpr int TP = TL::TP, TQ = TL::TQ, BK = TL::kBK, kThreads = TL::kThreads, PT = TL::kParts, EARLY = TL::kEarly, LATE = PT - EARLY;
-  constexpr int L = TL::kL;
+  constexpr int TP = TL::TP, TQ = TL::TQ, BK = TL::kBK, kThreads = TL::kThreads, L = TL::kL;
+  constexpr int PT = TL::kParts, EARLY = TL::kEarly, LATE = PT - EARLY;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TL::kLds];
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wp = wave % WP, wq = wave / WP, g = lane >> 4, r16 = lane & 15;
@@ -367,9 +367,9 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
 
   // ---------------------------------------------------------------- what each lane loads
   // Load i of a part: rows (i * waves + wave) * 8 + lane / 8 of 128 bytes, or (T) summed rows (i * waves + wave) * 4 + lane
-  // / 16 of 256 bytes.  Bases are scalar and move by a K-step, a lane's offsets stay until the last one.  Rows past the last, of the output or
-  // summed, lie past the resource's end and chunks past K get an offset that does: both load zeros.  (Columns past a T
-  // operand's last are the next row's first; what comes of them is not stored.)
+  // / 16 of 256 bytes.  Bases are scalar and move by a K-step, a lane's offsets stay until the last one.  Rows past the
+  // last, of the output or summed, lie past the resource's end and chunks past K get an offset that does: both load zeros.
+  // (Columns past a T operand's last are the next row's first; what comes of them is not stored.)
   constexpr int kStep8 = TL::kWaves * 8, kStep4 = TL::kWaves * 4;
   const int chunk8 = chunk_at<MX>(lane & 7, wave * 8 + (lane >> 3));
   constexpr bool kLookP = WG && (WHERE & 1), kLookQ = WG && (WHERE & 2);
@@ -417,7 +417,10 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
     for (int j = 0; j < (kTP ? 1 : TL::kPP); ++j)
 #pragma unroll
       for (int i = 0; i < L; ++i) p_off[j][i] = off + (kTP ? i * kStep4 : j * 128 + i * kStep8) * p.p_ld;
-    p_from = resource(base, !t.ok ? 0u : kLookP ? p.p_place.bytes(p.p_ld) - p_skip : kTP ? t_extent(true) : (uint32_t)min(p.p_cols - t.p * BP, BP) * p.p_ld);
+    p_from = resource(base, !t.ok    ? 0u
+                            : kLookP ? p.p_place.bytes(p.p_ld) - p_skip
+                            : kTP    ? t_extent(true)
+                                     : (uint32_t)min(p.p_cols - t.p * BP, BP) * p.p_ld);
   };
   auto aim_q = [&](const TileAt& t) {
     q_k = 0;
@@ -441,7 +444,10 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
                                                       first + rows - 1)) * p.q_ld + chunk8 * 16;
         }
       }
-    q_from = resource(base, !t.ok ? 0u : kLookQ || look ? p.q_place.bytes(p.q_ld) - (kTQ ? q_skip : 0) : kTQ ? t_extent(false) : (uint32_t)min(rows, BQ) * p.q_ld);
+    q_from = resource(base, !t.ok            ? 0u
+                            : kLookQ || look ? p.q_place.bytes(p.q_ld) - (kTQ ? q_skip : 0)
+                            : kTQ            ? t_extent(false)
+                                             : (uint32_t)min(rows, BQ) * p.q_ld);
   };
   // WGRAD: the offsets of a K-step's rows through src_info (read also where only one operand's rows are found there).  Lane l
   // of src[v] holds that of this wave's row l % (4 L) of the tile's K-step kEach v + l / (4 L): a vector load, which has to wait
@@ -826,7 +832,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void grouped_kernel(GroupedParams 
 // side with three others': 64 bytes a row, and the line's other half comes with the wave's next load).  No wave waits for
 // another until their sums meet in LDS, in the waves' order.  S loads of each row are under way: with 4 waves of one weight tile
 // 4 tokens' product of 28672 x 4096 reads its active experts at 6.4 TB/s (two or four weight tiles a wave 5.1 and 5.6: fewer
-// waves, less under way); MXFP4's short rows go to one wave each (128 experts, 32 tokens: 5.3 TB/s, with 4 waves 3.6).
+// waves, less under way); MXFP4's rows, a quarter as long, go to two waves of two weight tiles (128 experts, 32 tokens: 5.4 TB/s,
+// with one wave of one tile 5.3, with four 3.6).
 template <bool MX, int TP, int TQ, int W, bool F32>
 __global__ __launch_bounds__(64 * W, MX ? 2 : 4) void grouped_few_kernel(GroupedParams p) {
   constexpr int BQ = 16 * TQ, S = 8;
@@ -857,7 +864,8 @@ __global__ __launch_bounds__(64 * W, MX ? 2 : 4) void grouped_few_kernel(Grouped
   const int p0 = tile * 16 * TP, p_rows = min(p.p_cols - p0, 16 * TP), rows = min(hi - lo, BQ);
   const bool look = p.q_place.gathered;
   const __amdgpu_buffer_rsrc_t from_p = make_rsrc(p.P + expert * p.p_expert + (long long)p0 * p.p_ld, (uint32_t)p_rows * p.p_ld);
-  const __amdgpu_buffer_rsrc_t from_q = make_rsrc(p.Q + (look ? 0 : (long long)lo * p.q_ld), look ? p.q_place.bytes(p.q_ld) : (uint32_t)rows * p.q_ld);
+  const __amdgpu_buffer_rsrc_t from_q =
+      make_rsrc(p.Q + (look ? 0 : (long long)lo * p.q_ld), look ? p.q_place.bytes(p.q_ld) : (uint32_t)rows * p.q_ld);
   // the tensor's row of row r of the tile
   auto q_row = [&](int r) { return look ? p.q_place.of(p.src_info[min(lo + r, hi - 1)]) : min(r, rows - 1); };
 
@@ -1154,22 +1162,24 @@ GroupedParams common(const GroupedArgs& a) {
 template <Op O, bool F32>
 hipError_t launch_rows(GroupedParams& p, hipStream_t s) {
   // Rows of an expert that has any, on average, and the tiles that they make.  us measured, by rows an expert:
-  //   bf16, 8 experts of 28672 x 4096     1    4    8   16   64  128      MXFP4, 128 of 5760 x 2880    1    4    8   16   32
-  //   grouped_few_kernel                198  320  364  552                16 x 16                    137  232  270  357  548
-  //   128 x 128                         245  327  330  340  352  495      32 x 32                    163  243  261  286  387
-  //   256 x 256                         290  421  427  426  439  447      256 x 256                  231  345  351  354  361
+  //   bf16, 8 experts of 28672 x 4096     1    4    8   16   64  128      MXFP4, 128 of 5760 x 2880    1    4    8   12   16   32
+  //   grouped_few_kernel                198  320  364  552                32 x 16, 2 waves           134  206  238  265  307  444
+  //   128 x 128                         245  327  330  340  352  495      32 x 32, 2 waves           162  242  260  273  286  387
+  //   256 x 256                         290  421  427  426  439  447      256 x 256                  231  345  355  358  360  369
   // Where the tiles leave most of the part without work, the smaller ones are faster beyond that (bf16, 2 experts of 4096 x
   // 14336, 16 rows: 76 us, 128 x 128 143; MXFP4, 32 rows: 35, 256 x 256 89).
   const long long groups = std::max(1, std::min(p.npairs, p.E)), rows = (p.npairs + groups - 1) / groups;
   auto tiles = [&](int n) { return groups * ((p.p_cols + n - 1) / n) * ((rows + n - 1) / n); };
   const int cus = device_cus();
   if constexpr (O == Op::MX) {
-    if (rows <= 5 && few_fits(p, 1, 1, 1)) return launch_few<true, 1, 1, 1, F32>(p, s);
-    if ((rows <= 24 || (rows <= 128 && tiles(256) <= cus / 4)) && few_fits(p, 2, 2, 2)) return launch_few<true, 2, 2, 2, F32>(p, s);
+    if (rows <= 12 && few_fits(p, 2, 1, 2)) return launch_few<true, 2, 1, 2, F32>(p, s);
+    if ((rows <= 24 || (rows <= 128 && tiles(256) <= cus / 4)) && few_fits(p, 2, 2, 2))
+      return launch_few<true, 2, 2, 2, F32>(p, s);
     return p.sf_row % 4 ? launch_tile<O, 256, 256, 4, 2, 9, F32, 1>(p, s) : launch_tile<O, 256, 256, 4, 2, 9, F32>(p, s);
   } else {
     if constexpr (O == Op::FWD)
-      if ((rows <= 4 || (rows <= 32 && tiles(128) <= cus / 2)) && few_fits(p, 1, 1, 4)) return launch_few<false, 1, 1, 4, F32>(p, s);
+      if ((rows <= 4 || (rows <= 32 && tiles(128) <= cus / 2)) && few_fits(p, 1, 1, 4))
+        return launch_few<false, 1, 1, 4, F32>(p, s);
     if (rows <= 64 || tiles(256) < cus) return launch_tile<O, 128, 128, 2, 2, 5, F32>(p, s);
     return launch_tile<O, 256, 256, 4, 2, 10, F32>(p, s);
   }

@@ -67,8 +67,8 @@ def check_wgrad(c, n, kk, d_rows, a_rows, f32, accumulate=False, seed=0):
         assert torch.equal(dw[e].cpu(), want.to(dw.dtype)), e
 
 
-# rows an expert about every change of kernel: 4 | 5 (forward), 5 | 6 and 24 | 25 (MXFP4), 48 | 49 and 64 | 65
-@pytest.mark.parametrize("rows", [1, 4, 5, 6, 15, 16, 17, 24, 25, 32, 33, 48, 49, 64, 65, 128, 129, 257])
+# rows an expert about every change of kernel: 4 | 5 (forward), 12 | 13 and 24 | 25 (MXFP4), 48 | 49 and 64 | 65
+@pytest.mark.parametrize("rows", [1, 4, 5, 6, 12, 13, 15, 16, 17, 24, 25, 32, 33, 48, 49, 64, 65, 128, 129, 257])
 @pytest.mark.parametrize("n,kk", [(264, 96), (1032, 1056)])
 def test_rows_an_expert(rows, n, kk):
     c = Fixed(3, even_ids(3 * rows, 3))
