@@ -551,8 +551,9 @@ moe_status moe_grouped_gemm_mxfp4(const moe_handle* h, int32_t num_tokens, int32
 /* The clamped SwiGLU of the plan's rows ([MegaFFN] clamp_activation; the handle's I, activation_clamp c and fast_math):
      h = g' / (1 + e^-g') * u',  g' = min(g, c), u' = clamp(u, -c, c)
    gu [T*k, 2I] bf16, gate columns first (a product with w13), h_out [T*k, I] bf16, and q, sf: MXFP4 of the unrounded
-   h (as moe_quantize_mxfp4).  h_out, or the pair q and sf, may be NULL, not all three.  A NaN stays one.  gu, h_out and
-   q 16-byte aligned, sf 4; no overlaps. */
+   h (as moe_quantize_mxfp4).  h_out, or the pair q and sf, may be NULL, not all three.  A NaN stays one; an infinite g'
+   (without a clamp) stands for its limit: infinity * u', and -infinity for 0 * u'.  gu, h_out and q 16-byte aligned, sf 4;
+   no overlaps. */
 moe_status moe_swiglu(const moe_handle* h, int32_t num_tokens, const void* gu,
                       const moe_plan_buffers* plan /* host struct */, void* h_out, void* q, void* sf,
                       hipStream_t stream);

@@ -113,11 +113,11 @@ __global__ __launch_bounds__(kThreads) void quantize_mxfp4_kernel(QuantParams p)
 }
 
 // ---------------------------------------------------------------- SwiGLU
-// Finite, for the factors that an infinite gate meets with a zero; a NaN stays one.
-MOE_DEV float finite(float g) {
-  constexpr float top = 3.402823466e38f;
-  return g > top ? top : g < -top ? -top : g;
-}
+// Finite where an infinite gate meets a zero: below its sigmoid's, above that of the backward pass's g' (1 - s) alone (the
+// value there is the infinity).  A NaN stays one.
+constexpr float kTop = 3.402823466e38f;
+MOE_DEV float finite_below(float g) { return g < -kTop ? -kTop : g; }
+MOE_DEV float finite_above(float g) { return g > kTop ? kTop : g; }
 // e^(-|g| / 2): its square may be subnormal where what it is multiplied by is not, so the square is never formed alone.
 template <bool FAST>
 MOE_DEV float half_exp(float g) {
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(SwigluArgs p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // (comparisons, not fminf: a NaN stays one)
-      const float gc = finite(g[i] > p.clamp ? p.clamp : g[i]);
+      const float gc = finite_below(g[i] > p.clamp ? p.clamp : g[i]);
       const float uc = u[i] > p.clamp ? p.clamp : u[i] < -p.clamp ? -p.clamp : u[i];
       // s = t^2 / (1 + t^2) below zero, 1 / (1 + t^2) above
       const float t = half_exp<FAST>(gc), r = inverse<FAST>(fmaf(t, t, 1.0f)), f = gc < 0.0f ? t : 1.0f;
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(SwigluArgs p) {
       o[i] = a * uc;
       if constexpr (BACK) {
         const float fr = f * r, s = fr * f;
-        dg[i] = g[i] > p.clamp ? 0.0f : d[i] * uc * fr * fmaf(gc, 1.0f - s, 1.0f) * f;
+        dg[i] = g[i] > p.clamp ? 0.0f : d[i] * uc * fr * fmaf(finite_above(gc), 1.0f - s, 1.0f) * f;
         du[i] = fabsf(u[i]) > p.clamp ? 0.0f : d[i] * a;
       }
     }
