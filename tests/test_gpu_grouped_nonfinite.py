@@ -6,7 +6,7 @@ every size, on the 256 x 256 tile."""
 import pytest
 import torch
 
-from test_gpu_grouped import LEFT, codes, gen, product, value, whole
+from test_gpu_grouped import LEFT, Case, codes, gen, product, value, whole
 from test_gpu_grouped_paths import Fixed, even_ids
 
 pytestmark = pytest.mark.gpu
@@ -145,3 +145,22 @@ def test_mxfp4_scales_of_every_size(kk):
     want, size = (product(c, x, y, "token", "pair", n) for x, y in ((av, wv), (av.abs(), wv.abs())))
     # kk - 1 sums of fp32, each rounded (or cut) by less than 2^-23 of a partial sum, which is at most `size`
     assert ((out.cpu().double() - want).abs() <= kk * 2.0 ** -23 * size).all()
+
+
+def test_gradient_of_masked_tokens_input():
+    """The rows of masked slots are not written: what the buffer held there, a NaN too, stays out of the token's gradient
+    where moe_combine adds the others up."""
+    T, E, k, H, n = 90, 4, 3, 64, 128
+    c = Case(T, E, k, seed=3, mask=0.3, H=H)
+    assert (c.ids < 0).any(1).any() and c.rows < T * k
+    g = gen(6)
+    dgu, w = whole(g, T * k, n), whole(g, E, n, H)
+    pairs = torch.full((T * k, H), NAN, dtype=torch.bfloat16, device="cuda")
+    dx = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    c.moe.grouped_gemm(T, dgu.cuda(), w.cuda(), c.plan, pairs, out_rows="pair", w_kn=True)
+    c.moe.combine(T, pairs, torch.ones((T, k), device="cuda"), c.plan, dx)
+    want = product(c, dgu, w, "plan", "pair", H, True).to(torch.bfloat16).double()
+    masked = c.ids.reshape(-1) < 0
+    assert torch.isnan(pairs.cpu()[masked]).all()
+    want[masked] = 0.0
+    assert torch.equal(dx.cpu(), want.view(T, k, H).sum(1).to(torch.bfloat16))  # (whole numbers: fp32 sums are exact)
