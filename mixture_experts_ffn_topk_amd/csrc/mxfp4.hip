@@ -118,7 +118,8 @@ __global__ __launch_bounds__(kThreads) void quantize_mxfp4_kernel(QuantParams p)
 constexpr float kTop = 3.402823466e38f;
 MOE_DEV float finite_below(float g) { return g < -kTop ? -kTop : g; }
 MOE_DEV float finite_above(float g) { return g > kTop ? kTop : g; }
-// e^(-|g| / 2): its square may be subnormal where what it is multiplied by is not, so the square is never formed alone.
+// t = e^(-|g| / 2): its square may be subnormal where what it is multiplied by is not, so neither the square nor g' times it is
+// formed alone.  (t itself is normal down to g = -174.  Below, only up columns past 2^112 would give more than bf16's zero.)
 template <bool FAST>
 MOE_DEV float half_exp(float g) {
   return FAST ? __builtin_amdgcn_exp2f(fabsf(g) * -0.7213475204444817f) : expf(fabsf(g) * -0.5f);
@@ -150,12 +151,12 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(SwigluArgs p) {
       const float uc = u[i] > p.clamp ? p.clamp : u[i] < -p.clamp ? -p.clamp : u[i];
       // s = t^2 / (1 + t^2) below zero, 1 / (1 + t^2) above
       const float t = half_exp<FAST>(gc), r = inverse<FAST>(fmaf(t, t, 1.0f)), f = gc < 0.0f ? t : 1.0f;
-      const float a = gc * (f * r) * f;
-      o[i] = a * uc;
+      const float fr = f * r, a = gc * fr;
+      o[i] = a * (f * uc);
       if constexpr (BACK) {
-        const float fr = f * r, s = fr * f;
+        const float s = fr * f;
         dg[i] = g[i] > p.clamp ? 0.0f : d[i] * uc * fr * fmaf(finite_above(gc), 1.0f - s, 1.0f) * f;
-        du[i] = fabsf(u[i]) > p.clamp ? 0.0f : d[i] * a;
+        du[i] = fabsf(u[i]) > p.clamp ? 0.0f : a * (f * d[i]);
       }
     }
     const long long chunk = row * per_row + c;

@@ -97,3 +97,10 @@ def test_an_infinite_gate_shows_in_mxfp4(fast):
     assert torch.equal(sf.cpu().long(), scale.long())
     got = torch.stack([q & 15, q >> 4], -1).flatten(-2).cpu().long()
     assert got[0, 3] == 15 and torch.equal(got[0, :32], code[0, :32]) and torch.equal(got[0, 64:], code[0, 64:])
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_large_up_columns_at_far_negative_gates(fast):
+    """g' s below fp32's normal numbers where h and its gradients are not."""
+    check((-80.0, -95.0, -100.0, -103.0, -104.5, -107.0, -110.0, -130.0, -150.0, -174.0),
+          (1000.0, -1e10, 1e20, -1e30, 1e35, INF), (0.25, -3.0, 1000.0), fast, INF)
