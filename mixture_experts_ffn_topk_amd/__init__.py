@@ -275,6 +275,19 @@ def _fit(args):
     return ptrs
 
 
+def _has_rows(t, width, group) -> bool:
+    """Whether t's last dimension, or its last ones together, are width elements, or group times as many (of a flat
+    buffer: always)."""
+    if t.dim() < 2:
+        return True
+    n = 1
+    for d in reversed(t.shape):
+        n *= d
+        if n == width or n == width * group:
+            return True
+    return False
+
+
 def _current_stream() -> int:
     """The current stream's handle (_stream(None) without making a Stream object)."""
     import torch
@@ -761,16 +774,20 @@ class MoEFFN:
                "moe_forward_few")
 
     # ---------------------------------------------------------------- products by expert outside the fused layer
-    def _tensors(self, given):
-        """The addresses of (name, tensor, bytes, dtypes, required) arguments, checked as every call's are (and as _fit
-        does first in one pass)."""
-        import torch
+    def _tensors(self, torch, given):
+        """The addresses of (name, tensor, bytes, dtypes, required, width, group) arguments, checked as every call's are (and
+        as _fit does first in one pass).  n and k come from one tensor of a call, so that another's rows may be of another
+        width and its bytes still enough: one with more bytes than the call needs has to have rows of width elements, or
+        group of them side by side (width 0: of any)."""
         cur, ptrs = None, []
         try:
-            for _, t, nbytes, kinds, required in given:
+            for _, t, nbytes, kinds, required, width, group in given:
                 if t is None and not required:
                     ptrs.append(None)
-                elif t.dtype in kinds and t.nbytes >= nbytes and t.is_contiguous():
+                    continue
+                have = t.nbytes
+                if t.dtype in kinds and t.is_contiguous() and (have == nbytes or (have > nbytes and (
+                        not width or not nbytes or _has_rows(t, width, group)))):
                     device = t.get_device()
                     if device != cur:
                         if cur is not None or not t.is_cuda or device != torch._C._cuda_getDevice():
@@ -783,10 +800,14 @@ class MoEFFN:
                 return ptrs
         except AttributeError:  # (None, a raw address)
             pass
-        for name, t, size, kinds, required in given:
+        for name, t, nbytes, kinds, required, width, group in given:
             if t is None and required:
                 raise ValueError(f"{name} is required")
-            _need(t, name, size, kinds, required=required)
+            _need(t, name, nbytes, kinds, required=required)
+            if t is None or isinstance(t, int) or not width or not nbytes:
+                continue
+            if t.nbytes > nbytes and not _has_rows(t, width, group):
+                raise ValueError(f"{name} must have rows of {width} elements (got {list(t.shape)})")
         _on_current_gpu(**{name: t for name, t, *_ in given})
         return [_ptr(t) for _, t, *_ in given]
 
@@ -796,8 +817,9 @@ class MoEFFN:
             raise ValueError(f"{name} must be one of {', '.join(ROW_ORDERS)} (got {value!r})")
         return ROW_ORDERS[value]
 
-    def _rows_of(self, order: int, T: int) -> int:
-        return T if order == 1 else T * self.topk
+    def _group(self, order: int) -> int:
+        """How many rows a token has in a tensor."""
+        return 1 if order == 1 else self.topk
 
     def _sides(self, t, what, n, k, swapped=False):
         """(n, k) of an [E, n, k] tensor ([E, k, n] swapped), or as given beside a raw address."""
@@ -813,11 +835,10 @@ class MoEFFN:
             raise ValueError(f"{what} gives n, k = {have}, the call {(n, k)}")
         return have
 
-    def _rows_args(self, plan, T):
-        import torch
+    def _rows_args(self, torch, plan, T):
         i32 = (torch.int32,)
-        return [("plan['expert_start_indices']", plan.get("expert_start_indices"), 4 * (self.experts + 1), i32, True),
-                ("plan['src_info']", plan.get("src_info"), 4 * T * self.topk, i32, True)]
+        return [("plan['expert_start_indices']", plan.get("expert_start_indices"), 4 * (self.experts + 1), i32, True, 0, 1),
+                ("plan['src_info']", plan.get("src_info"), 4 * T * self.topk, i32, True, 0, 1)]
 
     @staticmethod
     def _rows_plan(start, src=None) -> _Plan:
@@ -827,15 +848,16 @@ class MoEFFN:
                      k=None, stream=None):
         """moe_grouped_gemm: every plan row's product with its expert's weight, a bf16 and w [E, n, k] bf16 (w_kn:
         [E, k, n], the gradient of a forward product's rows), out bf16 or fp32.  Row orders: "plan", "token" (inputs
-        only), "pair".  n and k come from w (a raw address: from the call; a raw out is bf16)."""
+        only), "pair".  n and k come from w (a raw address: from the call; a raw out is bf16).  Tensors may have room for
+        more rows, and dimensions of their own: their last one, or their last ones together, are a row (or a token's k)."""
         import torch
         T, ao, oo = num_tokens, self._order("a_rows", a_rows), self._order("out_rows", out_rows)
         n, k = self._sides(w, "w", n, k, w_kn)
-        bf16, f32 = (torch.bfloat16,), getattr(out, "dtype", None) is torch.float32
+        ag, bf16, f32 = self._group(ao), (torch.bfloat16,), getattr(out, "dtype", None) is torch.float32
         ap, wp, op, sp, ip = self._tensors(
-            [("a", a, self._rows_of(ao, T) * k * 2, bf16, True), ("w", w, self.experts * n * k * 2, bf16, True),
-             ("out", out, T * self.topk * n * (4 if f32 else 2), (torch.bfloat16, torch.float32), True)] +
-            self._rows_args(plan, T))
+            torch, [("a", a, T * ag * k * 2, bf16, True, k, ag), ("w", w, self.experts * n * k * 2, bf16, True, 0, 1),
+                    ("out", out, T * self.topk * n * (4 if f32 else 2), (torch.bfloat16, torch.float32), True, n,
+                     self.topk)] + self._rows_args(torch, plan, T))
         ps = self._rows_plan(sp, ip)
         _check(self.lib.moe_grouped_gemm(self._h, T, n, k, ap, ao, wp, bool(w_kn), ctypes.byref(ps), op, f32, oo,
                                          _current_stream() if stream is None else _stream(stream)), "moe_grouped_gemm")
@@ -847,11 +869,12 @@ class MoEFFN:
         import torch
         T, do, ao = num_tokens, self._order("dout_rows", dout_rows), self._order("a_rows", a_rows)
         n, k = self._sides(dw, "dw", n, k)
+        dg, ag = self._group(do), self._group(ao)
         bf16, f32 = (torch.bfloat16,), getattr(dw, "dtype", None) is torch.float32
         dp, ap, wp, sp, ip = self._tensors(
-            [("dout", dout, self._rows_of(do, T) * n * 2, bf16, T > 0), ("a", a, self._rows_of(ao, T) * k * 2, bf16, T > 0),
-             ("dw", dw, self.experts * n * k * (4 if f32 else 2), (torch.bfloat16, torch.float32), True)] +
-            self._rows_args(plan, T))
+            torch, [("dout", dout, T * dg * n * 2, bf16, T > 0, n, dg), ("a", a, T * ag * k * 2, bf16, T > 0, k, ag),
+                    ("dw", dw, self.experts * n * k * (4 if f32 else 2), (torch.bfloat16, torch.float32), True, 0, 1)] +
+            self._rows_args(torch, plan, T))
         ps = self._rows_plan(sp, ip)
         _check(self.lib.moe_grouped_gemm_wgrad(self._h, T, n, k, dp, do, ap, ao, ctypes.byref(ps), wp, f32,
                                                bool(accumulate), _current_stream() if stream is None else
@@ -882,8 +905,10 @@ class MoEFFN:
                 raise ValueError(f"x has a row stride of {stride}, the call {row_stride}")
         codes = _byte_types()
         xp, qp, sp, vp = self._tensors(
-            [("x", flat, 0, (torch.bfloat16, torch.float32), True), ("q", q, rows * cols // 2, codes, True),
-             ("sf", sf, rows * (cols // 32), codes, True), ("values", values, rows * cols * 2, (torch.bfloat16,), False)])
+            torch, [("x", flat, 0, (torch.bfloat16, torch.float32), True, 0, 1),
+                    ("q", q, rows * cols // 2, codes, True, cols // 2, 1),
+                    ("sf", sf, rows * (cols // 32), codes, True, cols // 32, 1),
+                    ("values", values, rows * cols * 2, (torch.bfloat16,), False, cols, 1)])
         _check(self.lib.moe_quantize_mxfp4(self._h, rows, cols, xp, f32, stride, qp, sp, vp,
                                            _current_stream() if stream is None else _stream(stream)),
                "moe_quantize_mxfp4")
@@ -897,15 +922,18 @@ class MoEFFN:
         if w is None or isinstance(w, int):
             n, k = self._sides(w, "w", n, k)
         else:
-            n, half = self._sides(w, "w", n, None if k is None else k // 2)
+            n, half = self._sides(w, "w", n, None)
+            if k is not None and k != 2 * half:
+                raise ValueError(f"w gives k = {2 * half}, the call {k}")
             k = 2 * half
         codes, f32, E = _byte_types(), getattr(out, "dtype", None) is torch.float32, self.experts
-        rows = self._rows_of(ao, T)
+        ag = self._group(ao)
+        rows = T * ag
         ap, fp, wp, gp, op, sp, ip = self._tensors(
-            [("a", a, rows * (k // 2), codes, True), ("a_sf", a_sf, rows * (k // 32), codes, True),
-             ("w", w, E * n * (k // 2), codes, True), ("w_sf", w_sf, E * n * (k // 32), codes, True),
-             ("out", out, T * self.topk * n * (4 if f32 else 2), (torch.bfloat16, torch.float32), True)] +
-            self._rows_args(plan, T))
+            torch, [("a", a, rows * (k // 2), codes, True, k // 2, ag), ("a_sf", a_sf, rows * (k // 32), codes, True, k // 32, ag),
+                    ("w", w, E * n * (k // 2), codes, True, 0, 1), ("w_sf", w_sf, E * n * (k // 32), codes, True, k // 32, 1),
+                    ("out", out, T * self.topk * n * (4 if f32 else 2), (torch.bfloat16, torch.float32), True, n,
+                     self.topk)] + self._rows_args(torch, plan, T))
         ps = self._rows_plan(sp, ip)
         _check(self.lib.moe_grouped_gemm_mxfp4(self._h, T, n, k, ap, fp, ao, wp, gp, ctypes.byref(ps), op, f32, oo,
                                                _current_stream() if stream is None else _stream(stream)),
@@ -914,10 +942,12 @@ class MoEFFN:
     def swiglu(self, num_tokens, gu, plan: dict, h=None, q=None, sf=None, stream=None):
         """moe_swiglu: the clamped SwiGLU of gu [T*k, 2I] bf16 as h [T*k, I] bf16, as MXFP4 (q, sf), or both."""
         import torch
-        n, bf16, codes = num_tokens * self.topk * self.inter, (torch.bfloat16,), _byte_types()
+        I, g, bf16, codes = self.inter, self.topk, (torch.bfloat16,), _byte_types()
+        n = num_tokens * g * I
         gp, hp, qp, fp, sp = self._tensors(
-            [("gu", gu, n * 4, bf16, True), ("h", h, n * 2, bf16, q is None), ("q", q, n // 2, codes, sf is not None),
-             ("sf", sf, n // 32, codes, q is not None), self._rows_args(plan, num_tokens)[0]])
+            torch, [("gu", gu, n * 4, bf16, True, 2 * I, g), ("h", h, n * 2, bf16, q is None, I, g),
+                    ("q", q, n // 2, codes, sf is not None, I // 2, g), ("sf", sf, n // 32, codes, q is not None, I // 32, g),
+                    self._rows_args(torch, plan, num_tokens)[0]])
         ps = self._rows_plan(sp)
         _check(self.lib.moe_swiglu(self._h, num_tokens, gp, ctypes.byref(ps), hp, qp, fp,
                                    _current_stream() if stream is None else _stream(stream)), "moe_swiglu")
@@ -926,10 +956,12 @@ class MoEFFN:
         """moe_swiglu_backward: dgu [T*k, 2I] of dh [T*k, I], and the forward value h where it is given (all bf16; dgu
         may be gu itself, h may be dh)."""
         import torch
-        n, bf16 = num_tokens * self.topk * self.inter, (torch.bfloat16,)
+        I, g, bf16 = self.inter, self.topk, (torch.bfloat16,)
+        n = num_tokens * g * I
         gp, dp, op, hp, sp = self._tensors(
-            [("gu", gu, n * 4, bf16, True), ("dh", dh, n * 2, bf16, True), ("dgu", dgu, n * 4, bf16, True),
-             ("h", h, n * 2, bf16, False), self._rows_args(plan, num_tokens)[0]])
+            torch, [("gu", gu, n * 4, bf16, True, 2 * I, g), ("dh", dh, n * 2, bf16, True, I, g),
+                    ("dgu", dgu, n * 4, bf16, True, 2 * I, g), ("h", h, n * 2, bf16, False, I, g),
+                    self._rows_args(torch, plan, num_tokens)[0]])
         ps = self._rows_plan(sp)
         _check(self.lib.moe_swiglu_backward(self._h, num_tokens, gp, dp, ctypes.byref(ps), op, hp,
                                             _current_stream() if stream is None else _stream(stream)),
