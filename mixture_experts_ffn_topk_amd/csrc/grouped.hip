@@ -18,6 +18,7 @@
 
 #include "gemm_common.h"
 #include "grouped.h"
+#include "tile_walk.h"
 
 namespace moe {
 
@@ -215,11 +216,10 @@ struct Walk {
     }
     at += step;
     within = scalar(within);
-    // (groups of about the same size: with 9 q-tiles, 8 and 1 would leave a group whose p panels are read by one workgroup each)
-    const int groups = (q_tiles + GQ - 1) / GQ, most = (q_tiles + groups - 1) / groups;
-    const int q0 = within / (most * p.p_tiles) * most, size = min(most, q_tiles - q0), in = within - q0 * p.p_tiles;
-    t.p = in / size;
-    t.q = q0 + in - t.p * size;
+    const TileIn in = tile_in(within, q_tiles, p.p_tiles, GQ);
+    t.ok = in.ok;
+    t.q = in.q;
+    t.p = in.p;
     t.expert = scalar(t.expert);
     t.lo = scalar(t.lo);
     t.hi = scalar(t.hi);
