@@ -533,7 +533,7 @@ moe_status moe_grouped_gemm_wgrad(const moe_handle* h, int32_t num_tokens, int32
      per 32 columns the smallest e in [-127, 127] with 6 * 2^e >= amax; sf = e + 127 (UE8M0), q = E2M1_RNE_sat(x / 2^e)
    x [num_rows, cols] bf16 or fp32 (x_fp32), x_row_stride elements between rows; q packed E2M1 [num_rows, cols/2] (element
    2i the low nibble of byte i), sf [num_rows, cols/32]; values [num_rows, cols] bf16, or NULL: what the codes stand for
-   (6 * 2^126 is an infinity there).  Infinities saturate; zeros keep their sign; a block that holds a NaN gets sf = 255,
+   (2^128 and above, 4 * 2^126 say, are infinities there).  Infinities saturate; zeros keep their sign; a block that holds a NaN gets sf = 255,
    values of NaN and codes of no meaning.  cols a multiple of 32; x, q and values 16-byte aligned (x_row_stride with them),
    sf 4.  values may be x itself (bf16, rows without gaps); any other overlap is MOE_ERR_INVALID_ARGUMENT. */
 moe_status moe_quantize_mxfp4(const moe_handle* h, int64_t num_rows, int32_t cols, const void* x, int32_t x_fp32,

@@ -55,7 +55,7 @@ MOE_DEV void mxfp4_store(const Mxfp4& m, void* q, void* sf, long long chunk) {
   ((uint32_t*)q)[chunk] = m.codes;
   if ((chunk & 3) == 0) ((uint8_t*)sf)[chunk >> 2] = (uint8_t)m.scale;
 }
-// What the codes stand for, in bf16 (exact but for 6 * 2^126 and above, which are infinities).
+// What the codes stand for, in bf16 (exact but for 2^128 and above, 4 * 2^126 say, which are infinities).
 MOE_DEV i32x4 mxfp4_values(const Mxfp4& m) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   const float s = m.scale == 255 ? __uint_as_float(0x7FC00000u) : exp2i(m.scale - 127);
